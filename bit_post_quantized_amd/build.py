@@ -27,7 +27,8 @@ OBJDIR = os.path.join(ROOT, "_build", "obj")
 
 ARCH = "gfx950"
 SOURCES = ["abi.cpp", "pack_weights.hip", "act_quant.hip", "w4a4_gemm.hip", "w4a4_gemm_e3m2.hip",
-           "kv_int8.hip", "kv_attention.hip"]
+           "kv_int8.hip", "kv_attention.hip", "abi_serve.cpp", "w4a16_gemv.hip", "kv_blocks.hip",
+           "kv_block_attention.hip"]
 PEAKS_SOURCES = ["peaks.hip"]
 CFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

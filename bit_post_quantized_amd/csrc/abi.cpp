@@ -10,11 +10,14 @@
 #include <cstdio>
 #include <cstring>
 
+#include "abi_status.hpp"
 #include "svdq_launch.hpp"
 
+namespace svdq {
+namespace abi {
 namespace {
-
 thread_local char g_last_error[256] = {0};
+}  // namespace
 
 int fail(int status, const char* fmt, ...) {
   va_list ap;
@@ -34,13 +37,6 @@ int hip_status(hipError_t e, const char* what) {
   return fail(SVDQ_EHIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-constexpr long long kMaxElems = 1LL << 40;  // keeps every byte offset far inside size_t
-constexpr int kMaxRank = 128;
-// The KV dequantization's grid holds the tokens in its y dimension, at most 65535 blocks of 32.
-constexpr int kKvMaxTokens = 65535 * 32;
-
 int check_k(int K) {
   if (K <= 0) return fail(SVDQ_EINVAL, "K must be positive (got %d)", K);
   if (K % 64 != 0) return fail(SVDQ_ESHAPE, "K must be a multiple of 64 (got %d)", K);
@@ -54,6 +50,14 @@ int check_rank(int r) {
   return SVDQ_OK;
 }
 
+}  // namespace abi
+}  // namespace svdq
+
+using namespace svdq::abi;
+
+namespace {
+// The KV dequantization's grid holds the tokens in its y dimension, at most 65535 blocks of 32.
+constexpr int kKvMaxTokens = 65535 * 32;
 }  // namespace
 
 extern "C" {
@@ -71,7 +75,7 @@ const char* svdq_status_str(int status) {
   }
 }
 
-const char* svdq_last_error(void) { return g_last_error; }
+const char* svdq_last_error(void) { return svdq::abi::g_last_error; }
 
 static int pack_weights(const float* R, int K, int N, uint8_t* wq, uint16_t* w_scales,
                         void* stream, int e3m2, const char* name) {
