@@ -10,9 +10,11 @@
 // sums are the matrix unit's fp32.
 //  1. w4a16_prep_kernel: X^ in the matrix operand's order, its scales, and T's partial sums over
 //     slices of K (bf16 MFMA on X^ split into three bf16, which keeps all 24 bits).
-//  2. w4a16_kernel: one workgroup per 16 columns; its waves split K, each lane turns 16 nibbles of
-//     one column into fp16 per group, one fp32 FMA per output and group applies the two scales,
-//     and the waves meet in LDS, where the low-rank product and the bias join.
+//  2. w4a16_kernel: persistent workgroups of 8 waves that split K; a wave keeps its part of X^ in
+//     registers and walks over tiles of 16 columns, with the next tile's weights in flight while
+//     it computes the current one's.  A lane turns 16 nibbles of one column into fp16 per group,
+//     one fp32 FMA per output and group applies the two scales, the low-rank product is one more
+//     matrix step per 32 ranks, and the waves meet in LDS once per tile.
 #include "serve_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -21,8 +23,9 @@ namespace svdq {
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 constexpr int kFragBytes = 2048;     // one (row tile, group): 16 rows x 64 k of fp16
-constexpr int kPrepWaves = 4;
-constexpr int kMaxSlices = 16;
+constexpr int kPrepWaves = 16;       // 8 above rank 64, whose operands need the registers
+constexpr int kMaxSlices = 8;
+constexpr int kWaves = 8;            // of the main kernel
 
 // Row tiles: 16 rows each, or for fp32 output 8 rows, hi parts in matrix rows 0..7 and lo parts
 // in rows 8..15.
@@ -33,14 +36,11 @@ inline int w4a16_tiles(int M, int out_fp32) {
   return (M + rpt - 1) / rpt;
 }
 
-// Slices of K for T's partial sums: enough workgroups to be short, few enough that summing the
-// partials again in every workgroup of the main kernel (32 KB) stays cheap.
-inline int w4a16_slices(int M, int K, int r) {
-  const int G = K / kGroup;
-  int s = (G + kPrepWaves - 1) / kPrepWaves;
-  if (s > kMaxSlices) s = kMaxSlices;
-  while (s > 1 && (long long)s * M * r * 4 > 32768) --s;
-  return s;
+// Slices of K for T's partial sums: a group or so per wave of a preparing workgroup, and few
+// enough that summing the partials again in every workgroup of the main kernel stays cheap.
+inline int w4a16_slices(int K) {
+  const int s = (K / kGroup + kPrepWaves - 1) / kPrepWaves;
+  return s < kMaxSlices ? s : kMaxSlices;
 }
 
 struct W4a16Ws {
@@ -53,16 +53,13 @@ inline W4a16Ws w4a16_layout(int M, int K, int r, int out_fp32) {
   w.frags = 0;
   w.scales = tiles * G * kFragBytes;
   w.parts = w.scales + tiles * G * 16 * sizeof(float);
-  w.bytes = w.parts + (size_t)w4a16_slices(M, K, r) * M * r * sizeof(float);
+  w.bytes = w.parts + (size_t)w4a16_slices(K) * M * r * sizeof(float);
   return w;
 }
 
 size_t w4a16_workspace_bytes(int M, int K, int r, int out_fp32) {
   return w4a16_layout(M, K, r, out_fp32).bytes;
 }
-
-// The matrix operand's k order inside a lane's 8: the order in which unpack8_f16 yields them.
-__device__ __forceinline__ int frag_k(int i) { return (i >> 1) + ((i & 1) << 2); }
 
 // Eight packed nibbles -> eight exact fp16 codes, in the order k0 k4 k1 k5 k2 k6 k3 k7.  After the
 // flip of bit 3 a nibble holds c + 8; or-ed into the mantissa of 1024 it makes 1024 + (c + 8), or
@@ -87,13 +84,28 @@ __device__ __forceinline__ v4f mfma_bf16(v8bf a, v8bf b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// One workgroup per (slice of K, row tile); a wave takes every kPrepWaves-th group of the slice.
-// Lane (row l % 16, j = l / 16) holds k = 64 g + 16 j .. + 15.
-__global__ __launch_bounds__(kPrepWaves * 64) void w4a16_prep_kernel(
+// Eight fp32 -> TERMS bf16 operands that add up to them (8 bits each).
+template <int TERMS>
+__device__ __forceinline__ void split_bf16(const float* x, v8bf* out) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = x[i];
+#pragma unroll
+  for (int c = 0; c < TERMS; ++c) {
+    out[c] = to_bf16x8(y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] -= (float)out[c][i];
+  }
+}
+
+// One workgroup per (slice of K, row tile); a wave takes every WAVES-th group of the slice.
+// Lane (row l % 16, j = l / 16) holds k = 64 g + 16 j .. + 15.  RT >= r / 16 rank tiles.
+template <int RT, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void w4a16_prep_kernel(
     const uint16_t* __restrict__ X, const float* __restrict__ inv_lambda,
     const uint16_t* __restrict__ L1p, int M, int K, int r, int out_fp32, v8h* __restrict__ frags,
     float* __restrict__ scales, float* __restrict__ parts) {
-  __shared__ float red[kPrepWaves][16][17];
+  __shared__ float red[2][RT ? WAVES : 1][16][17];
   const int G = K / kGroup, slices = gridDim.x, slice = blockIdx.x, tile = blockIdx.y;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int mr = lane & 15, j = lane >> 4;
@@ -101,35 +113,39 @@ __global__ __launch_bounds__(kPrepWaves * 64) void w4a16_prep_kernel(
   const int row = tile * rpt + (mr & (rpt - 1));
   const bool live = row < M, low = out_fp32 && mr >= 8;
   const int g0 = (int)((long long)G * slice / slices), g1 = (int)((long long)G * (slice + 1) / slices);
-  const int ranks = r / 16;
 
-  v4f t[8];
+  v4f t[RT ? RT : 1];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < RT; ++i) t[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int g = g0 + wave; g < g1; g += kPrepWaves) {
+  for (int g = g0 + wave; g < g1; g += WAVES) {
     const int k0 = g * kGroup + 16 * j;
+    v8bf b[RT ? RT : 1][2];
+    // the rank rows' loads first: they do not wait for X (rows past r - 1 read row r - 1, unused)
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        b[i][s] = *reinterpret_cast<const v8bf*>(L1p + (size_t)min(16 * i + mr, r - 1) * K + k0 + 8 * s);
+    const v4u* xp = reinterpret_cast<const v4u*>(X + (size_t)min(row, M - 1) * K + k0);
+    const v4u w0 = xp[0], w1 = xp[1];
+    const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+    const v4f* lp = reinterpret_cast<const v4f*>(inv_lambda + k0);
     float x[16];
-    float amax = 0.0f;
-    if (live) {
-      const v4u* xp = reinterpret_cast<const v4u*>(X + (size_t)row * K + k0);
-      const v4u w0 = xp[0], w1 = xp[1];
-      const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-      const v4f* lp = reinterpret_cast<const v4f*>(inv_lambda + k0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const v4f l = lp[i];
-        x[4 * i] = __uint_as_float(w[2 * i] << 16) * l.x;
-        x[4 * i + 1] = __uint_as_float(w[2 * i] & 0xFFFF0000u) * l.y;
-        x[4 * i + 2] = __uint_as_float(w[2 * i + 1] << 16) * l.z;
-        x[4 * i + 3] = __uint_as_float(w[2 * i + 1] & 0xFFFF0000u) * l.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      const v4f l = lp[i];
+      x[4 * i] = __uint_as_float(w[2 * i] << 16) * l.x;
+      x[4 * i + 1] = __uint_as_float(w[2 * i] & 0xFFFF0000u) * l.y;
+      x[4 * i + 2] = __uint_as_float(w[2 * i + 1] << 16) * l.z;
+      x[4 * i + 3] = __uint_as_float(w[2 * i + 1] & 0xFFFF0000u) * l.w;
     }
+    float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(x[i]));
+    for (int i = 0; i < 16; ++i) {
+      if (!live) x[i] = 0.0f;
+      amax = __builtin_fmaxf(amax, __builtin_fabsf(x[i]));
+    }
     amax = __builtin_fmaxf(amax, __shfl_xor(amax, 16));
     amax = __builtin_fmaxf(amax, __shfl_xor(amax, 32));
     // 2^e with amax 2^-e in [2^10, 2^11) (e clamped so that both powers are normal; 0 keeps e = 0)
@@ -154,182 +170,248 @@ __global__ __launch_bounds__(kPrepWaves * 64) void w4a16_prep_kernel(
     }
     if (j == 0) scales[((size_t)tile * G + g) * 16 + mr] = up;
 
-    if (ranks) {
-      // X^ = p0 + p1 + p2, each a bf16 (8 bits at a time)
-      v8bf p[3][2];
+    if constexpr (RT > 0) {
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        float y[8];
+        v8bf p[3];
+        split_bf16<3>(x + 8 * s, p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[8 * s + i];
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int c = 0; c < 3; ++c) {
-          p[c][s] = to_bf16x8(y);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] -= (float)p[c][s][i];
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (i < ranks) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const v8bf b = *reinterpret_cast<const v8bf*>(L1p + (size_t)(16 * i + mr) * K + k0 + 8 * s);
-#pragma unroll
-            for (int c = 0; c < 3; ++c) t[i] = mfma_bf16(p[c][s], b, t[i]);
-          }
-        }
+          for (int c = 0; c < 3; ++c) t[i] = mfma_bf16(p[c], b[i][s], t[i]);
       }
     }
   }
 
   // T's partial of this slice: the waves' sums meet in LDS, one tile of 16 ranks after the other
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i < ranks) {
+  for (int i = 0; i < RT; ++i) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) red[wave][4 * j + q][mr] = t[i][q];
-      __syncthreads();
-      const int m = threadIdx.x >> 4, c = threadIdx.x & 15, out = tile * rpt + m;
-      if (m < rpt && out < M) {
-        float s = 0.0f;
+    for (int q = 0; q < 4; ++q) red[i & 1][wave][4 * j + q][mr] = t[i][q];
+    __syncthreads();
+    const int m = threadIdx.x >> 4, c = threadIdx.x & 15, out = tile * rpt + m;
+    if (m < rpt && out < M && 16 * i + c < r) {
+      float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kPrepWaves; ++w) s += red[w][m][c];
-        parts[((size_t)slice * M + out) * r + 16 * i + c] = s;
-      }
-      __syncthreads();
+      for (int w = 0; w < WAVES; ++w) s += red[i & 1][w][m][c];
+      parts[((size_t)slice * M + out) * r + 16 * i + c] = s;
     }
   }
 }
 
-// MT row tiles, WAVES waves that split K.  LDS: the waves' sums, T and the columns' L2 rows.
-template <int MT, int WAVES, bool FP32>
-__global__ __launch_bounds__(WAVES * 64) void w4a16_kernel(
+// What one wave holds of a (column tile, chunk of K): GPW groups of weights and their scales, and
+// the ranks it adds; and of X^, MT row tiles of the same groups.
+template <int GPW>
+struct Weights {
+  v2u w[GPW];
+  uint16_t s[GPW];
+  v8bf l2;
+};
+
+template <int MT, int GPW>
+struct Rows {
+  v8h a[MT][GPW][2];
+  v4f up[MT][GPW];
+};
+
+// MT row tiles; a chunk of K is kWaves * GPW groups, GPW to a wave.  HOLD: K is one chunk, and the
+// wave's X^ stays in registers for all its column tiles; otherwise it is read again per chunk,
+// one chunk ahead.
+template <int MT, int GPW, bool HOLD, bool FP32>
+__global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
     const v8h* __restrict__ frags, const float* __restrict__ scales,
     const float* __restrict__ parts, int slices, const uint8_t* __restrict__ wq,
     const uint16_t* __restrict__ w_scales, const uint16_t* __restrict__ L2p,
-    const uint16_t* __restrict__ bias, int M, int N, int K, int r, int tile0,
-    int tiles, void* __restrict__ Y) {
+    const uint16_t* __restrict__ bias, int M, int N, int K, int r, int tile0, int tiles,
+    void* __restrict__ Y) {
   constexpr int RPT = FP32 ? 8 : 16;
-  constexpr int UNROLL = 4;
-  extern __shared__ float lds[];
-  float* red = lds;                           // [WAVES][MT * 16][17]
-  float* Ts = lds + WAVES * MT * 16 * 17;     // [rows of these tiles][r]
-  const int G = K / kGroup;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  constexpr int TERMS = FP32 ? 3 : 2;  // bf16 terms of T: 24 or 16 bits
+  __shared__ float red[2][kWaves][MT * 16][17];
+  __shared__ v8bf t_lds[MT][4][TERMS][64];
+  const int G = K / kGroup, chunks = HOLD ? 1 : (G + kWaves * GPW - 1) / (kWaves * GPW);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, j = lane >> 4;
-  const int n0 = blockIdx.x * 16, n = min(n0 + c, N - 1);
-  const int g0 = (int)((long long)G * wave / WAVES), g1 = (int)((long long)G * (wave + 1) / WAVES);
   const int row0 = tile0 * RPT, rows = min(M - row0, MT * RPT);
+  const int steps = (r + 31) / 32;     // matrix steps of the low-rank product, one to a wave
 
+  // Column tiles of this workgroup.  Workgroups go to the 8 XCDs round-robin; each XCD takes a
+  // contiguous run of tiles, so that the 4 tiles that share a 128-byte line of w_scales meet in
+  // one L2.
+  const int all = (N + 15) / 16, run = (all + 7) / 8, per = gridDim.x / 8;
+  const int first = (blockIdx.x & 7) * run, end = min(first + run, all);
+  int tile = first + (int)(blockIdx.x >> 3), chunk = 0;
+  if (tile >= end) return;
+
+  auto load_x = [&](int ch, Rows<MT, GPW>& x) {
+    const int g0 = (ch * kWaves + wave) * GPW;
+#pragma unroll
+    for (int u = 0; u < GPW; ++u)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        // (a row tile past the last and a group past the last read the last one's; neither counts)
+        const size_t at = (size_t)min(tile0 + t, tiles - 1) * G + min(g0 + u, G - 1);
+        x.a[t][u][0] = (frags + at * 128)[lane];
+        x.a[t][u][1] = (frags + at * 128 + 64)[lane];
+        x.up[t][u] = reinterpret_cast<const v4f*>(scales + at * 16)[j];
+      }
+  };
+  // (uniform bases and 32-bit lane offsets: a tile's 16 rows of wq span less than 2^26 bytes)
+  auto load_w = [&](int t, int ch, Weights<GPW>& w) {
+    const int col = min(c, N - 1 - t * 16), g0 = (ch * kWaves + wave) * GPW;
+    const uint8_t* wp = wq + (size_t)t * 16 * (K / 2);
+    const uint16_t* sp = w_scales + (size_t)t * 16;
+    const uint32_t off = (uint32_t)col * (uint32_t)(K / 2) + 8 * j;
+#pragma unroll
+    for (int u = 0; u < GPW; ++u) {
+      const int g = min(g0 + u, G - 1);
+      w.w[u] = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(wp + (size_t)g * 32 + off));
+      w.s[u] = (sp + (size_t)g * N)[col];
+    }
+    if (wave < steps && ch == 0)
+      w.l2 = *reinterpret_cast<const v8bf*>(L2p + (size_t)t * 16 * r + (uint32_t)(col * r + min(32 * wave + 8 * j, r - 8)));
+  };
+
+  Weights<GPW> wa, wb;
+  Rows<MT, GPW> xa, xb;
+  load_w(tile, 0, wa);
+  load_x(0, xa);
+  // T (its slices' sum) as the low-rank product's operand; ranks past r and lo rows are 0
+  if (wave < steps) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      const int m = t * RPT + c, k = 32 * wave + 8 * j;
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+      if (c < RPT && m < rows && k < r)
+        for (int q = 0; q < slices; ++q) {
+          const v4f* pp = reinterpret_cast<const v4f*>(parts + ((size_t)q * M + row0 + m) * r + k);
+          const v4f a = pp[0], b = pp[1];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] += a[i];
+            x[4 + i] += b[i];
+          }
+        }
+      v8bf p[TERMS];
+      split_bf16<TERMS>(x, p);
+#pragma unroll
+      for (int i = 0; i < TERMS; ++i) t_lds[t][wave][i][lane] = p[i];  // (read by this wave alone)
+    }
+  }
+
+  int par = 0;
   v4f acc[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-  const uint8_t* wp = wq + (size_t)n * (K / 2) + 8 * j;
-  const uint16_t* sp = w_scales + n;
-
-  for (int g = g0; g < g1; g += UNROLL) {
-    v2u w[UNROLL];
-    uint16_t s[UNROLL];
-#pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      const int gu = min(g + u, g1 - 1);
-      w[u] = *reinterpret_cast<const v2u*>(wp + (size_t)gu * 32);
-      s[u] = sp[(size_t)gu * N];
+  // One (tile, chunk): the next one's loads, this one's products; false after the last.
+  auto step = [&](Weights<GPW>& w, Weights<GPW>& wn, Rows<MT, GPW>& x, Rows<MT, GPW>& xn) {
+    const bool last = chunk + 1 == chunks;
+    const int tile1 = last ? tile + per : tile, chunk1 = last ? 0 : chunk + 1;
+    const bool more = tile1 < end;
+    if (more) {
+      load_w(tile1, chunk1, wn);
+      if (!HOLD) load_x(chunk1, xn);
     }
+    if (chunk == 0) {
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      if (g + u < g1) {
-        const v8h b0 = unpack8_f16(w[u].x), b1 = unpack8_f16(w[u].y);
-        const float sw = half_bits_to_float(s[u]);
+      for (int t = 0; t < MT; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      if (wave < steps) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          // (a tile past the last reads the last one's operands; its results are not stored)
-          const size_t at = (size_t)min(tile0 + t, tiles - 1) * G + g + u;
-          const v8h a0 = frags[at * 128 + lane], a1 = frags[at * 128 + 64 + lane];
-          const v4f up = *reinterpret_cast<const v4f*>(scales + at * 16 + 4 * j);
-          v4f p = mfma_f16(a0, b0, v4f{0.0f, 0.0f, 0.0f, 0.0f});
-          p = mfma_f16(a1, b1, p);
+        for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(p[i], sw * up[i], acc[t][i]);
-        }
+          for (int i = 0; i < TERMS; ++i) acc[t] = mfma_bf16(t_lds[t][wave][i][lane], w.l2, acc[t]);
       }
     }
-  }
-
+    const int g0 = (chunk * kWaves + wave) * GPW;
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
+    for (int u = 0; u < GPW; ++u) {
+      const v8h b0 = unpack8_f16(w.w[u].x), b1 = unpack8_f16(w.w[u].y);
+      const float sw = g0 + u < G ? half_bits_to_float(w.s[u]) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[(wave * MT * 16 + t * 16 + 4 * j + i) * 17 + c] = acc[t][i];
-  for (int i = threadIdx.x; i < rows * r; i += WAVES * 64) {
-    float s = 0.0f;
-    for (int q = 0; q < slices; ++q) s += parts[((size_t)q * M + row0) * r + i];
-    Ts[i] = s;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < rows * 16; i += WAVES * 64) {
-    const int m = i >> 4, col = i & 15, nn = n0 + col;
-    if (nn >= N) continue;
-    const int rr = FP32 ? (m >> 3) * 16 + (m & 7) : m;
-    float y = 0.0f;
+      for (int t = 0; t < MT; ++t) {
+        v4f p = mfma_f16(x.a[t][u][0], b0, v4f{0.0f, 0.0f, 0.0f, 0.0f});
+        p = mfma_f16(x.a[t][u][1], b1, p);
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      y += red[(w * MT * 16 + rr) * 17 + col];
-      if (FP32) y += red[(w * MT * 16 + rr + 8) * 17 + col];
+        for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(p[i], sw * x.up[t][u][i], acc[t][i]);
+      }
     }
-    if (r) {
-      const v4u* lp = reinterpret_cast<const v4u*>(L2p + (size_t)nn * r);
-      float z = 0.0f;
-      for (int q = 0; q < r / 8; ++q) {
-        const v4u l = lp[q];
-        const float* tp = Ts + m * r + 8 * q;
-        const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
+    if (last) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          z = __builtin_fmaf(tp[2 * p], __uint_as_float(lw[p] << 16), z);
-          z = __builtin_fmaf(tp[2 * p + 1], __uint_as_float(lw[p] & 0xFFFF0000u), z);
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[par][wave][t * 16 + 4 * j + i][c] = acc[t][i];
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+      for (int i = threadIdx.x; i < rows * 16; i += kWaves * 64) {
+        const int m = i >> 4, col = i & 15, nn = tile * 16 + col;
+        if (nn < N) {
+          const int rr = FP32 ? (m >> 3) * 16 + (m & 7) : m;
+          float y = 0.0f;
+#pragma unroll
+          for (int q = 0; q < kWaves; ++q) {
+            y += red[par][q][rr][col];
+            if (FP32) y += red[par][q][rr + 8][col];
+          }
+          if (bias) y += bf16_bits_to_float(bias[nn]);
+          const size_t at = (size_t)(row0 + m) * N + nn;
+          if (FP32) {
+            static_cast<float*>(Y)[at] = y;
+          } else {
+            static_cast<uint16_t*>(Y)[at] = float_to_bf16_bits(y);
+          }
         }
       }
-      y += z;
+      par ^= 1;  // (the next tile's barrier separates these reads from the buffer's next writes)
     }
-    if (bias) y += bf16_bits_to_float(bias[nn]);
-    const size_t at = (size_t)(row0 + m) * N + nn;
-    if (FP32) {
-      static_cast<float*>(Y)[at] = y;
-    } else {
-      static_cast<uint16_t*>(Y)[at] = float_to_bf16_bits(y);
-    }
+    tile = tile1;
+    chunk = chunk1;
+    return more;
+  };
+  while (step(wa, wb, xa, HOLD ? xa : xb) && step(wb, wa, HOLD ? xa : xb, xa)) {
   }
 }
 
-template <int MT, int WAVES, bool FP32>
-static hipError_t launch_main(const v8h* frags, const float* scales, const float* parts,
-                              int slices, const uint8_t* wq, const uint16_t* w_scales,
-                              const uint16_t* L2p, const uint16_t* bias, int M, int N, int K,
-                              int r, int tile0, int tiles, void* Y, hipStream_t stream) {
-  const int rows = min(M - tile0 * (FP32 ? 8 : 16), MT * (FP32 ? 8 : 16));
-  const size_t lds = ((size_t)WAVES * MT * 16 * 17 + (size_t)rows * r) * sizeof(float);
-  hipLaunchKernelGGL((w4a16_kernel<MT, WAVES, FP32>), dim3((N + 15) / 16), dim3(WAVES * 64), lds,
-                     stream, frags, scales, parts, slices, wq, w_scales, L2p, bias, M, N, K, r,
-                     tile0, tiles, Y);
+struct W4a16Call {
+  const v8h* frags;
+  const float* scales;
+  const float* parts;
+  int slices;
+  const uint8_t* wq;
+  const uint16_t* w_scales;
+  const uint16_t* L2p;
+  const uint16_t* bias;
+  int M, N, K, r, tiles;
+  void* Y;
+  hipStream_t stream;
+};
+
+template <int MT, int GPW, bool HOLD, bool FP32>
+static hipError_t launch_main(const W4a16Call& a, int tile0) {
+  // one workgroup per CU, fewer where there are fewer column tiles (a multiple of 8, for the XCDs)
+  const int all = (a.N + 15) / 16, grid = all < 256 ? (all + 7) / 8 * 8 : 256;
+  hipLaunchKernelGGL((w4a16_kernel<MT, GPW, HOLD, FP32>), dim3(grid), dim3(kWaves * 64), 0,
+                     a.stream, a.frags, a.scales, a.parts, a.slices, a.wq, a.w_scales, a.L2p, a.bias,
+                     a.M, a.N, a.K, a.r, tile0, a.tiles, a.Y);
   return hipGetLastError();
 }
 
+// Up to 4 row tiles share a pass over the weights (64 bf16 rows, 32 fp32 rows).  What a wave holds
+// of X^ is 12 registers per row tile and group, 8 of them held or 4 in flight and 4 in use, so
+// more row tiles mean fewer groups to a chunk.
 template <bool FP32>
-static hipError_t launch_tiles(const v8h* frags, const float* scales, const float* parts,
-                               int slices, const uint8_t* wq, const uint16_t* w_scales,
-                               const uint16_t* L2p, const uint16_t* bias, int M, int N, int K,
-                               int r, int tiles, void* Y, hipStream_t stream) {
-  // up to 4 row tiles share a pass over the weights (64 bf16 rows, 32 fp32 rows)
-  for (int t = 0; t < tiles; t += 4) {
-    const int left = tiles - t;
+static hipError_t launch_tiles(const W4a16Call& a) {
+  const int G = a.K / kGroup;
+  for (int t = 0; t < a.tiles; t += 4) {
+    const int left = a.tiles - t;
     hipError_t e;
     if (left >= 3)
-      e = launch_main<4, 4, FP32>(frags, scales, parts, slices, wq, w_scales, L2p, bias, M, N, K, r, t, tiles, Y, stream);
+      e = G <= 2 * kWaves ? launch_main<4, 2, true, FP32>(a, t) : launch_main<4, 1, false, FP32>(a, t);
     else if (left == 2)
-      e = launch_main<2, 8, FP32>(frags, scales, parts, slices, wq, w_scales, L2p, bias, M, N, K, r, t, tiles, Y, stream);
+      e = G <= 4 * kWaves ? launch_main<2, 4, true, FP32>(a, t) : launch_main<2, 2, false, FP32>(a, t);
+    else if (G <= 4 * kWaves)
+      e = launch_main<1, 4, true, FP32>(a, t);
     else
-      e = launch_main<1, 8, FP32>(frags, scales, parts, slices, wq, w_scales, L2p, bias, M, N, K, r, t, tiles, Y, stream);
+      e = G <= 8 * kWaves ? launch_main<1, 8, true, FP32>(a, t) : launch_main<1, 4, false, FP32>(a, t);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -344,16 +426,20 @@ hipError_t launch_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const u
   v8h* frags = reinterpret_cast<v8h*>(base + w.frags);
   float* scales = reinterpret_cast<float*>(base + w.scales);
   float* parts = reinterpret_cast<float*>(base + w.parts);
-  const int tiles = w4a16_tiles(M, out_fp32), slices = w4a16_slices(M, K, r);
-  hipLaunchKernelGGL(w4a16_prep_kernel, dim3(slices, tiles), dim3(kPrepWaves * 64), 0, stream, X,
-                     inv_lambda, L1p, M, K, r, out_fp32, frags, scales, parts);
-  hipError_t e = hipGetLastError();
+  const int tiles = w4a16_tiles(M, out_fp32), slices = w4a16_slices(K);
+  const dim3 grid(slices, tiles);
+#define SVDQ_PREP(RT, WAVES)                                                                           \
+  hipLaunchKernelGGL((w4a16_prep_kernel<RT, WAVES>), grid, dim3(WAVES * 64), 0, stream, X,       \
+                     inv_lambda, L1p, M, K, r, out_fp32, frags, scales, parts)
+  if (r == 0) SVDQ_PREP(0, kPrepWaves);
+  else if (r <= 32) SVDQ_PREP(2, kPrepWaves);
+  else if (r <= 64) SVDQ_PREP(4, kPrepWaves);
+  else SVDQ_PREP(8, kPrepWaves / 2);
+#undef SVDQ_PREP
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (out_fp32)
-    return launch_tiles<true>(frags, scales, parts, slices, wq, w_scales, L2p, bias, M, N, K, r,
-                              tiles, Y, stream);
-  return launch_tiles<false>(frags, scales, parts, slices, wq, w_scales, L2p, bias, M, N, K, r,
-                             tiles, Y, stream);
+  const W4a16Call a{frags, scales, parts, slices, wq, w_scales, L2p, bias, M, N, K, r, tiles, Y, stream};
+  return out_fp32 ? launch_tiles<true>(a) : launch_tiles<false>(a);
 }
 
 }  // namespace svdq

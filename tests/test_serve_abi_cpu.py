@@ -184,16 +184,17 @@ def test_host_tensors_are_rejected(lib):
     cache = [torch.zeros(5, 2, 16, 64, dtype=torch.uint8), torch.zeros(5, 2, 64, 16, dtype=torch.uint8),
              torch.zeros(5, 2), torch.zeros(5, 2)]
     x, s = torch.zeros(3, 2, 64, dtype=torch.bfloat16), torch.zeros(3, dtype=torch.int64)
-    with pytest.raises(ValueError, match="device tensor"):
-        serve.BlockCache(*cache).append(x, x, s)
-    with pytest.raises(ValueError, match="device tensor"):
-        serve.BlockCache(*cache).read(s)
-    with pytest.raises(ValueError, match="device tensor"):
-        serve.BlockCache(*cache).attention(x, torch.zeros(1, 4, dtype=torch.int32),
-                                           torch.zeros(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), 1)
     i = torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError, match="device tensor"):
-        serve.BlockPlanner(torch.zeros(1, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), 16, 4).plan(i, i, i)
+        serve.BlockCache(*cache)
+    with pytest.raises(ValueError, match="device tensor"):
+        SB.kv_block_append(x, x, s, *cache)
+    with pytest.raises(ValueError, match="device tensor"):
+        SB.kv_block_read(s, *cache, x, x)
+    with pytest.raises(ValueError, match="device tensor"):
+        SB.kv_block_attention(x, *cache, i[None], i, torch.zeros(2, dtype=torch.int32), 1, True, 1.0, x, None)
+    with pytest.raises(ValueError, match="device tensor"):
+        serve.BlockPlanner(torch.zeros(1, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), 16, 4)
 
 
 def test_the_tiled_container_is_refused():
