@@ -61,31 +61,50 @@ size_t svdq_w4a16_workspace_bytes(int M, int N, int K, int r, int out_dtype) {
   return svdq::w4a16_workspace_bytes(M, K, r, out_dtype == SVDQ_OUT_FP32);
 }
 
-int svdq_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const uint16_t* L1p,
-                    const uint8_t* wq, const uint16_t* w_scales, const uint16_t* L2p,
-                    const uint16_t* bias, int M, int N, int K, int r, void* Y, int out_dtype,
-                    void* workspace, void* stream) {
-  if (M < 0) return fail(SVDQ_EINVAL, "M must be >= 0 (got %d)", M);
+static int check_w4a16(int N, int K) {
   if (N <= 0) return fail(SVDQ_EINVAL, "N must be positive (got %d)", N);
   if (int s = check_k(K)) return s;
+  if (N > (1 << 24)) return fail(SVDQ_ESHAPE, "N must be <= 2^24 (got %d)", N);
+  if (K / 64 > 65535) return fail(SVDQ_ESHAPE, "K / 64 must be <= 65535 (got K = %d)", K);
+  if ((long long)N * K > kMaxElems) return fail(SVDQ_ESHAPE, "problem too large");
+  return SVDQ_OK;
+}
+
+size_t svdq_w4a16_container_bytes(int N, int K) {
+  return check_w4a16(N, K) ? 0 : svdq::w4a16_container_bytes(N, K);
+}
+
+int svdq_pack_w4a16(const uint8_t* wq, const uint16_t* w_scales, int N, int K, uint8_t* container,
+                    void* stream) {
+  if (int s = check_w4a16(N, K)) return s;
+  if (!wq || !w_scales || !container) return fail(SVDQ_EINVAL, "NULL pointer");
+  if (!aligned16(wq) || !aligned16(container))
+    return fail(SVDQ_EALIGN, "wq and container must be 16-byte aligned");
+  return hip_status(svdq::launch_w4a16_pack(wq, w_scales, N, K, container, (hipStream_t)stream),
+                    "svdq_pack_w4a16");
+}
+
+int svdq_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const uint16_t* L1p,
+                    const uint8_t* container, const uint16_t* L2p, const uint16_t* bias, int M,
+                    int N, int K, int r, void* Y, int out_dtype, void* workspace, void* stream) {
+  if (M < 0) return fail(SVDQ_EINVAL, "M must be >= 0 (got %d)", M);
+  if (int s = check_w4a16(N, K)) return s;
   if (int s = check_rank(r)) return s;
   if (M > kMaxFewRows)
     return fail(SVDQ_ESHAPE, "M must be <= %d (got %d; svdq_w4a4_gemm takes more rows)",
                 kMaxFewRows, M);
-  if (N > (1 << 24)) return fail(SVDQ_ESHAPE, "N must be <= 2^24 (got %d)", N);
-  if (K / 64 > 65535) return fail(SVDQ_ESHAPE, "K / 64 must be <= 65535 (got K = %d)", K);
-  if ((long long)N * K > kMaxElems) return fail(SVDQ_ESHAPE, "problem too large");
   if (out_dtype != SVDQ_OUT_BF16 && out_dtype != SVDQ_OUT_FP32)
     return fail(SVDQ_EINVAL, "out_dtype must be SVDQ_OUT_BF16 or SVDQ_OUT_FP32");
-  if (!inv_lambda || !wq || !w_scales || (M > 0 && (!X || !Y || !workspace)))
+  if (!inv_lambda || !container || (M > 0 && (!X || !Y || !workspace)))
     return fail(SVDQ_EINVAL, "NULL pointer");
   if (r > 0 && (!L1p || !L2p)) return fail(SVDQ_EINVAL, "L1p and L2p are required when r > 0");
-  if (!aligned16(X) || !aligned16(inv_lambda) || !aligned16(wq) || !aligned16(workspace) ||
+  if (!aligned16(X) || !aligned16(inv_lambda) || !aligned16(container) || !aligned16(workspace) ||
       (r > 0 && (!aligned16(L1p) || !aligned16(L2p))))
-    return fail(SVDQ_EALIGN, "X, inv_lambda, wq, L1p, L2p and workspace must be 16-byte aligned");
+    return fail(SVDQ_EALIGN,
+                "X, inv_lambda, container, L1p, L2p and workspace must be 16-byte aligned");
   if (M == 0) return ok();
-  return hip_status(svdq::launch_w4a16_gemv(X, inv_lambda, L1p, wq, w_scales, L2p, bias, M, N, K,
-                                            r, Y, out_dtype == SVDQ_OUT_FP32, workspace,
+  return hip_status(svdq::launch_w4a16_gemv(X, inv_lambda, L1p, container, L2p, bias, M, N, K, r,
+                                            Y, out_dtype == SVDQ_OUT_FP32, workspace,
                                             (hipStream_t)stream),
                     "svdq_w4a16_gemv");
 }

@@ -5,16 +5,18 @@
 //
 // With few rows the weights are read once and used M times, so the floor is their N K / 2 bytes.
 // The products run on v_mfma_f32_16x16x32_f16: a code is an exact fp16, and an activation enters
-// as an fp16 after a power-of-two scale per (row, group) (11 significant bits, for bf16 output) or
-// as the fp16 pair hi + lo (22 bits, for fp32 output); products of 11 x 4 bits are exact and the
-// sums are the matrix unit's fp32.
+// as an fp16 after a power-of-two scale per (row, 8 groups) (11 significant bits, for bf16 output)
+// or as the fp16 pair hi + lo (22 bits, for fp32 output); products of 11 x 4 bits are exact and
+// the sums are the matrix unit's fp32.
 //  1. w4a16_prep_kernel: X^ in the matrix operand's order, its scales, and T's partial sums over
 //     slices of K (bf16 MFMA on X^ split into three bf16, which keeps all 24 bits).
 //  2. w4a16_kernel: persistent workgroups of 8 waves that split K; a wave keeps its part of X^ in
-//     registers and walks over tiles of 16 columns, with the next tile's weights in flight while
+//     registers and walks over tiles of 16 columns, with the next tiles' weights in flight while
 //     it computes the current one's.  A lane turns 16 nibbles of one column into fp16 per group,
-//     one fp32 FMA per output and group applies the two scales, the low-rank product is one more
+//     one fp32 FMA per output and group applies the weight scale, the low-rank product is one more
 //     matrix step per 32 ranks, and the waves meet in LDS once per tile.
+// The weights come in a container of the matrix operand's order (svdq_pack_w4a16): in [N, K/2] a
+// wave's load takes 32 bytes of each of 16 rows, and the scales one 2-byte load per group.
 #include "serve_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -22,10 +24,61 @@ namespace svdq {
 
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
-constexpr int kFragBytes = 2048;     // one (row tile, group): 16 rows x 64 k of fp16
+constexpr int kFragBytes = 2048;     // of X^: one (row tile, group), 16 rows x 64 k of fp16
 constexpr int kPrepWaves = 16;       // 8 above rank 64, whose operands need the registers
 constexpr int kMaxSlices = 8;
 constexpr int kWaves = 8;            // of the main kernel
+constexpr int kSeg = 8;              // groups that share an activation scale; of one container unit
+
+// Container unit (column tile t, segment s), at (t segments + s) kUnit bytes: for each of 4 pairs
+// of groups 64 lanes x 16 bytes (lane l: column 16 t + l % 16, k = 16 (l / 16) .. + 15 of either
+// group, 8 bytes of nibbles each), then fp16 scales [16 columns][8 groups].  Columns past N and
+// groups past K / 64 hold code 0 and scale 0.
+constexpr int kUnitCodes = 4096, kUnit = kUnitCodes + 256;
+
+__host__ __device__ inline int w4a16_segments(int K) { return (K / kGroup + kSeg - 1) / kSeg; }
+
+size_t w4a16_container_bytes(int N, int K) {
+  return (size_t)((N + 15) / 16) * w4a16_segments(K) * kUnit;
+}
+
+// One thread per lane of a unit.
+__global__ __launch_bounds__(256) void w4a16_pack_kernel(const uint8_t* __restrict__ wq,
+                                                         const uint16_t* __restrict__ w_scales,
+                                                         int N, int K, long long units,
+                                                         uint8_t* __restrict__ out) {
+  const long long unit = (long long)blockIdx.x * 4 + threadIdx.x / 64;
+  if (unit >= units) return;
+  const int G = K / kGroup, segs = w4a16_segments(K);
+  const int lane = threadIdx.x & 63, j = lane >> 4, seg = (int)(unit % segs);
+  const long long n = unit / segs * 16 + (lane & 15);
+  uint8_t* u = out + (size_t)unit * kUnit;
+  uint16_t s[kSeg];
+#pragma unroll
+  for (int p = 0; p < kSeg / 2; ++p) {
+    v2u w[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int g = seg * kSeg + 2 * p + e;
+      const bool live = n < N && g < G;
+      w[e] = live ? *reinterpret_cast<const v2u*>(wq + (size_t)n * (K / 2) + (size_t)g * 32 + 8 * j) : v2u{0u, 0u};
+      s[2 * p + e] = live ? w_scales[(size_t)g * N + n] : (uint16_t)0;
+    }
+    reinterpret_cast<v4u*>(u)[p * 64 + lane] = v4u{w[0].x, w[0].y, w[1].x, w[1].y};
+  }
+  if (j == 0)
+    reinterpret_cast<v4u*>(u + kUnitCodes)[lane] =
+        v4u{s[0] | (uint32_t)s[1] << 16, s[2] | (uint32_t)s[3] << 16, s[4] | (uint32_t)s[5] << 16,
+            s[6] | (uint32_t)s[7] << 16};
+}
+
+hipError_t launch_w4a16_pack(const uint8_t* wq, const uint16_t* w_scales, int N, int K,
+                             uint8_t* container, hipStream_t stream) {
+  const long long units = (long long)((N + 15) / 16) * w4a16_segments(K);
+  hipLaunchKernelGGL(w4a16_pack_kernel, dim3((unsigned)((units + 3) / 4)), dim3(256), 0, stream,
+                     wq, w_scales, N, K, units, container);
+  return hipGetLastError();
+}
 
 // Row tiles: 16 rows each, or for fp32 output 8 rows, hi parts in matrix rows 0..7 and lo parts
 // in rows 8..15.
@@ -36,10 +89,10 @@ inline int w4a16_tiles(int M, int out_fp32) {
   return (M + rpt - 1) / rpt;
 }
 
-// Slices of K for T's partial sums: a group or so per wave of a preparing workgroup, and few
-// enough that summing the partials again in every workgroup of the main kernel stays cheap.
+// Slices of K for T's partial sums: two segments (a group per wave) to a preparing workgroup, and
+// few enough that summing the partials again in every workgroup of the main kernel stays cheap.
 inline int w4a16_slices(int K) {
-  const int s = (K / kGroup + kPrepWaves - 1) / kPrepWaves;
+  const int s = (w4a16_segments(K) + 1) / 2;
   return s < kMaxSlices ? s : kMaxSlices;
 }
 
@@ -52,7 +105,7 @@ inline W4a16Ws w4a16_layout(int M, int K, int r, int out_fp32) {
   W4a16Ws w;
   w.frags = 0;
   w.scales = tiles * G * kFragBytes;
-  w.parts = w.scales + tiles * G * 16 * sizeof(float);
+  w.parts = w.scales + tiles * w4a16_segments(K) * 16 * sizeof(float);
   w.bytes = w.parts + (size_t)w4a16_slices(K) * M * r * sizeof(float);
   return w;
 }
@@ -61,19 +114,22 @@ size_t w4a16_workspace_bytes(int M, int K, int r, int out_fp32) {
   return w4a16_layout(M, K, r, out_fp32).bytes;
 }
 
-// Eight packed nibbles -> eight exact fp16 codes, in the order k0 k4 k1 k5 k2 k6 k3 k7.  After the
-// flip of bit 3 a nibble holds c + 8; or-ed into the mantissa of 1024 it makes 1024 + (c + 8), or
-// from bits 4..7 1024 + 16 (c + 8), and one packed fp16 operation takes the offset (and the 16)
-// away, exactly.
+// Eight packed nibbles -> eight exact fp16 codes, in the order k0 k4 k1 k5 k2 k6 k3 k7.  A nibble
+// with its bit 3 flipped is c + 8; in the mantissa of 1024 it makes 1024 + (c + 8), or from bits
+// 4..7 1024 + 16 (c + 8), and one packed fp16 operation takes the offset (and the 16) away,
+// exactly.  Mask, flip and exponent are one three-operand bit operation, (w & mask) ^ constant.
 __device__ __forceinline__ v8h unpack8_f16(uint32_t w) {
-  const uint32_t u = w ^ 0x88888888u, v = u >> 8;
+  constexpr int kAndXor = 0x6A;  // (a & b) ^ c
+  const uint32_t v = w >> 8;
   const v2h six = {(_Float16)0.0625f, (_Float16)0.0625f};
   const v2h off0 = {(_Float16)-1032.0f, (_Float16)-1032.0f};
   const v2h off4 = {(_Float16)-72.0f, (_Float16)-72.0f};
-  const v2h a = __builtin_bit_cast(v2h, (u & 0x000F000Fu) | 0x64006400u) + off0;
-  const v2h b = __builtin_elementwise_fma(__builtin_bit_cast(v2h, (u & 0x00F000F0u) | 0x64006400u), six, off4);
-  const v2h c = __builtin_bit_cast(v2h, (v & 0x000F000Fu) | 0x64006400u) + off0;
-  const v2h d = __builtin_elementwise_fma(__builtin_bit_cast(v2h, (v & 0x00F000F0u) | 0x64006400u), six, off4);
+  const v2h a = __builtin_bit_cast(v2h, __builtin_amdgcn_bitop3_b32(w, 0x000F000Fu, 0x64086408u, kAndXor)) + off0;
+  const v2h b = __builtin_elementwise_fma(
+      __builtin_bit_cast(v2h, __builtin_amdgcn_bitop3_b32(w, 0x00F000F0u, 0x64806480u, kAndXor)), six, off4);
+  const v2h c = __builtin_bit_cast(v2h, __builtin_amdgcn_bitop3_b32(v, 0x000F000Fu, 0x64086408u, kAndXor)) + off0;
+  const v2h d = __builtin_elementwise_fma(
+      __builtin_bit_cast(v2h, __builtin_amdgcn_bitop3_b32(v, 0x00F000F0u, 0x64806480u, kAndXor)), six, off4);
   return v8h{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
@@ -98,28 +154,34 @@ __device__ __forceinline__ void split_bf16(const float* x, v8bf* out) {
   }
 }
 
-// One workgroup per (slice of K, row tile); a wave takes every WAVES-th group of the slice.
-// Lane (row l % 16, j = l / 16) holds k = 64 g + 16 j .. + 15.  RT >= r / 16 rank tiles.
+// One workgroup per (slice of K, row tile); WAVES / kSeg segments of 8 groups at a time, a group to
+// a wave; a segment's waves share their rows' largest magnitudes in LDS.  Lane (row l % 16,
+// j = l / 16) holds k = 64 g + 16 j .. + 15.  RT >= r / 16 rank tiles.
 template <int RT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void w4a16_prep_kernel(
     const uint16_t* __restrict__ X, const float* __restrict__ inv_lambda,
     const uint16_t* __restrict__ L1p, int M, int K, int r, int out_fp32, v8h* __restrict__ frags,
     float* __restrict__ scales, float* __restrict__ parts) {
   __shared__ float red[2][RT ? WAVES : 1][16][17];
-  const int G = K / kGroup, slices = gridDim.x, slice = blockIdx.x, tile = blockIdx.y;
+  __shared__ float top[2][WAVES][16];
+  const int G = K / kGroup, segs = w4a16_segments(K);
+  const int slices = gridDim.x, slice = blockIdx.x, tile = blockIdx.y;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int mr = lane & 15, j = lane >> 4;
   const int rpt = w4a16_rows_per_tile(out_fp32);
   const int row = tile * rpt + (mr & (rpt - 1));
   const bool live = row < M, low = out_fp32 && mr >= 8;
-  const int g0 = (int)((long long)G * slice / slices), g1 = (int)((long long)G * (slice + 1) / slices);
+  const int s0 = (int)((long long)segs * slice / slices), s1 = (int)((long long)segs * (slice + 1) / slices);
 
   v4f t[RT ? RT : 1];
 #pragma unroll
   for (int i = 0; i < RT; ++i) t[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int g = g0 + wave; g < g1; g += WAVES) {
-    const int k0 = g * kGroup + 16 * j;
+  int par = 0;
+  for (int sb = s0; sb < s1; sb += WAVES / kSeg, par ^= 1) {
+    const int seg = sb + wave / kSeg, want = seg * kSeg + wave % kSeg;
+    const bool mine = seg < s1 && want < G;  // (the others read the last group and store nothing)
+    const int g = min(want, G - 1), k0 = g * kGroup + 16 * j;
     v8bf b[RT ? RT : 1][2];
     // the rank rows' loads first: they do not wait for X (rows past r - 1 read row r - 1, unused)
 #pragma unroll
@@ -143,11 +205,15 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_prep_kernel(
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      if (!live) x[i] = 0.0f;
+      if (!live || !mine) x[i] = 0.0f;
       amax = __builtin_fmaxf(amax, __builtin_fabsf(x[i]));
     }
     amax = __builtin_fmaxf(amax, __shfl_xor(amax, 16));
     amax = __builtin_fmaxf(amax, __shfl_xor(amax, 32));
+    if (j == 0) top[par][wave][mr] = amax;
+    __syncthreads();  // (the next round's buffer is the other one)
+#pragma unroll
+    for (int q = 0; q < kSeg; ++q) amax = __builtin_fmaxf(amax, top[par][wave / kSeg * kSeg + q][mr]);
     // 2^e with amax 2^-e in [2^10, 2^11) (e clamped so that both powers are normal; 0 keeps e = 0)
     int e = (int)(__float_as_uint(amax) >> 23) - 127 - 10;
     e = amax == 0.0f ? 0 : max(e, -110);
@@ -160,15 +226,17 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_prep_kernel(
       const _Float16 hi = (_Float16)y;
       h[i] = low ? (_Float16)(y - (float)hi) : hi;
     }
-    const size_t base = ((size_t)tile * G + g) * 128;
+    if (mine) {
+      const size_t base = ((size_t)tile * G + g) * 128;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      v8h f;
+      for (int s = 0; s < 2; ++s) {
+        v8h f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = h[8 * s + (i >> 1) + ((i & 1) << 2)];
-      frags[base + s * 64 + lane] = f;
+        for (int i = 0; i < 8; ++i) f[i] = h[8 * s + (i >> 1) + ((i & 1) << 2)];
+        frags[base + s * 64 + lane] = f;
+      }
+      if (j == 0 && wave % kSeg == 0) scales[((size_t)tile * segs + seg) * 16 + mr] = up;
     }
-    if (j == 0) scales[((size_t)tile * G + g) * 16 + mr] = up;
 
     if constexpr (RT > 0) {
 #pragma unroll
@@ -199,44 +267,44 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_prep_kernel(
   }
 }
 
-// What one wave holds of a (column tile, chunk of K): GPW groups of weights and their scales, and
-// the ranks it adds; and of X^, MT row tiles of the same groups.
+// What one wave holds of a (column tile, chunk of K): GPW groups of codes and their scales (fp16
+// pairs), and the ranks it adds; and of X^, MT row tiles of the same groups.
 template <int GPW>
 struct Weights {
-  v2u w[GPW];
-  uint16_t s[GPW];
+  v4u w[GPW / 2];
+  uint32_t s[GPW / 2];
   v8bf l2;
 };
 
 template <int MT, int GPW>
 struct Rows {
   v8h a[MT][GPW][2];
-  v4f up[MT][GPW];
+  v4f up[MT];  // the scales of its rows 4 j + i: a wave's groups lie in one segment
 };
 
 // MT row tiles; a chunk of K is kWaves * GPW groups, GPW to a wave.  HOLD: K is one chunk, and the
-// wave's X^ stays in registers for all its column tiles; otherwise it is read again per chunk,
-// one chunk ahead.
-template <int MT, int GPW, bool HOLD, bool FP32>
+// wave's X^ stays in registers for all its column tiles; otherwise it is read again per chunk, a
+// chunk ahead.  STAGES - 1 steps of weights are in flight.  RANK: there is a low-rank branch.
+template <int MT, int GPW, bool HOLD, bool FP32, bool RANK>
 __global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
     const v8h* __restrict__ frags, const float* __restrict__ scales,
-    const float* __restrict__ parts, int slices, const uint8_t* __restrict__ wq,
-    const uint16_t* __restrict__ w_scales, const uint16_t* __restrict__ L2p,
-    const uint16_t* __restrict__ bias, int M, int N, int K, int r, int tile0, int tiles,
-    void* __restrict__ Y) {
+    const float* __restrict__ parts, int slices, const uint8_t* __restrict__ container,
+    const uint16_t* __restrict__ L2p, const uint16_t* __restrict__ bias, int M, int N, int K,
+    int r, int tile0, int tiles, void* __restrict__ Y) {
   constexpr int RPT = FP32 ? 8 : 16;
   constexpr int TERMS = FP32 ? 3 : 2;  // bf16 terms of T: 24 or 16 bits
   __shared__ float red[2][kWaves][MT * 16][17];
-  __shared__ v8bf t_lds[MT][4][TERMS][64];
-  const int G = K / kGroup, chunks = HOLD ? 1 : (G + kWaves * GPW - 1) / (kWaves * GPW);
+  __shared__ v8bf t_lds[RANK ? MT : 1][4][TERMS][64];
+  static_assert(kSeg % GPW == 0 && GPW % 2 == 0, "a wave's groups are pairs of one segment");
+  const int G = K / kGroup, segs = w4a16_segments(K);
+  const int chunks = HOLD ? 1 : (G + kWaves * GPW - 1) / (kWaves * GPW);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, j = lane >> 4;
   const int row0 = tile0 * RPT, rows = min(M - row0, MT * RPT);
-  const int steps = (r + 31) / 32;     // matrix steps of the low-rank product, one to a wave
+  const int steps = RANK ? (r + 31) / 32 : 0;  // matrix steps of the low-rank product, one to a wave
 
-  // Column tiles of this workgroup.  Workgroups go to the 8 XCDs round-robin; each XCD takes a
-  // contiguous run of tiles, so that the 4 tiles that share a 128-byte line of w_scales meet in
-  // one L2.
+  // Column tiles of this workgroup; each XCD (workgroups go to the 8 round-robin) takes a
+  // contiguous run of them.
   const int all = (N + 15) / 16, run = (all + 7) / 8, per = gridDim.x / 8;
   const int first = (blockIdx.x & 7) * run, end = min(first + run, all);
   int tile = first + (int)(blockIdx.x >> 3), chunk = 0;
@@ -245,36 +313,54 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
   auto load_x = [&](int ch, Rows<MT, GPW>& x) {
     const int g0 = (ch * kWaves + wave) * GPW;
 #pragma unroll
-    for (int u = 0; u < GPW; ++u)
+    for (int t = 0; t < MT; ++t) {
+      // (a row tile past the last and a group past the last read the last one's; neither counts)
+      const int tt = min(tile0 + t, tiles - 1);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        // (a row tile past the last and a group past the last read the last one's; neither counts)
-        const size_t at = (size_t)min(tile0 + t, tiles - 1) * G + min(g0 + u, G - 1);
-        x.a[t][u][0] = (frags + at * 128)[lane];
-        x.a[t][u][1] = (frags + at * 128 + 64)[lane];
-        x.up[t][u] = reinterpret_cast<const v4f*>(scales + at * 16)[j];
+      for (int u = 0; u < GPW; ++u) {
+        const v8h* f = frags + ((size_t)tt * G + min(g0 + u, G - 1)) * 128;
+        x.a[t][u][0] = f[lane];
+        x.a[t][u][1] = f[64 + lane];
       }
-  };
-  // (uniform bases and 32-bit lane offsets: a tile's 16 rows of wq span less than 2^26 bytes)
-  auto load_w = [&](int t, int ch, Weights<GPW>& w) {
-    const int col = min(c, N - 1 - t * 16), g0 = (ch * kWaves + wave) * GPW;
-    const uint8_t* wp = wq + (size_t)t * 16 * (K / 2);
-    const uint16_t* sp = w_scales + (size_t)t * 16;
-    const uint32_t off = (uint32_t)col * (uint32_t)(K / 2) + 8 * j;
-#pragma unroll
-    for (int u = 0; u < GPW; ++u) {
-      const int g = min(g0 + u, G - 1);
-      w.w[u] = __builtin_nontemporal_load(reinterpret_cast<const v2u*>(wp + (size_t)g * 32 + off));
-      w.s[u] = (sp + (size_t)g * N)[col];
+      x.up[t] = reinterpret_cast<const v4f*>(scales + ((size_t)tt * segs + min(g0 / kSeg, segs - 1)) * 16)[j];
     }
-    if (wave < steps && ch == 0)
-      w.l2 = *reinterpret_cast<const v8bf*>(L2p + (size_t)t * 16 * r + (uint32_t)(col * r + min(32 * wave + 8 * j, r - 8)));
+  };
+  // Loads without branches, so that the next step's are all in flight while this one's are waited
+  // for; a step that is not there (spread = 0) reads one address.
+  auto load_w = [&](int t, int ch, int spread, Weights<GPW>& w) {
+    const int g0 = (ch * kWaves + wave) * GPW, seg = min(g0 / kSeg, segs - 1);
+    const uint8_t* u = container + ((size_t)t * segs + seg) * kUnit;
+    const uint8_t* codes = u + (g0 % kSeg) * 512 + lane * 16 * spread;
+#pragma unroll
+    for (int p = 0; p < GPW / 2; ++p) w.w[p] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(codes + p * 1024));
+    const uint32_t* sp = reinterpret_cast<const uint32_t*>(u + kUnitCodes + (g0 % kSeg) * 2 + c * 16 * spread);
+#pragma unroll
+    for (int p = 0; p < GPW / 2; ++p) w.s[p] = sp[p];
+    if constexpr (RANK) {
+      const int n = min(t * 16 + c, N - 1);
+      w.l2 = *reinterpret_cast<const v8bf*>(L2p + (size_t)n * r + min(32 * wave + 8 * j, r - 8));
+    }
+  };
+  // the (tile, chunk) after one
+  auto after = [&](int& t, int& ch) {
+    const bool wrap = ch + 1 >= chunks;
+    t += wrap ? per : 0;
+    ch = wrap ? 0 : ch + 1;
   };
 
-  Weights<GPW> wa, wb;
+  constexpr int STAGES = HOLD ? 3 : 2;
+  Weights<GPW> wa, wb, wc;
   Rows<MT, GPW> xa, xb;
-  load_w(tile, 0, wa);
-  load_x(0, xa);
+  int tile2 = tile, chunk2 = 0;  // what the next load reads
+  auto load_next = [&](Weights<GPW>& w, Rows<MT, GPW>& x) {
+    const bool there = tile2 < end;
+    load_w(there ? tile2 : tile, chunk2, there, w);
+    if (!HOLD) load_x(chunk2, x);
+    after(tile2, chunk2);
+  };
+  if (HOLD) load_x(0, xa);
+  load_next(wa, xa);
+  if (STAGES == 3) load_next(wb, xa);
   // T (its slices' sum) as the low-rank product's operand; ranks past r and lo rows are 0
   if (wave < steps) {
 #pragma unroll
@@ -302,38 +388,41 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
 
   int par = 0;
   v4f acc[MT];
-  // One (tile, chunk): the next one's loads, this one's products; false after the last.
+  // One (tile, chunk): loads ahead, this one's products; false after the last.
   auto step = [&](Weights<GPW>& w, Weights<GPW>& wn, Rows<MT, GPW>& x, Rows<MT, GPW>& xn) {
-    const bool last = chunk + 1 == chunks;
-    const int tile1 = last ? tile + per : tile, chunk1 = last ? 0 : chunk + 1;
-    const bool more = tile1 < end;
-    if (more) {
-      load_w(tile1, chunk1, wn);
-      if (!HOLD) load_x(chunk1, xn);
-    }
+    load_next(wn, xn);
     if (chunk == 0) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      if (wave < steps) {
+      if (RANK && wave < steps) {
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int i = 0; i < TERMS; ++i) acc[t] = mfma_bf16(t_lds[t][wave][i][lane], w.l2, acc[t]);
       }
     }
-    const int g0 = (chunk * kWaves + wave) * GPW;
+    v4f part[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) part[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int u = 0; u < GPW; ++u) {
-      const v8h b0 = unpack8_f16(w.w[u].x), b1 = unpack8_f16(w.w[u].y);
-      const float sw = g0 + u < G ? half_bits_to_float(w.s[u]) : 0.0f;
+      const v4u q = w.w[u / 2];
+      const v8h b0 = unpack8_f16(u & 1 ? q.z : q.x), b1 = unpack8_f16(u & 1 ? q.w : q.y);
+      const float sw = half_bits_to_float((uint16_t)(u & 1 ? w.s[u / 2] >> 16 : w.s[u / 2]));
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         v4f p = mfma_f16(x.a[t][u][0], b0, v4f{0.0f, 0.0f, 0.0f, 0.0f});
         p = mfma_f16(x.a[t][u][1], b1, p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(p[i], sw * x.up[t][u][i], acc[t][i]);
+        for (int i = 0; i < 4; ++i) part[t][i] = __builtin_fmaf(p[i], sw, part[t][i]);
       }
     }
+    const bool counts = (chunk * kWaves + wave) * GPW < G;
+    const bool last = chunk + 1 == chunks;
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(part[t][i], counts ? x.up[t][i] : 0.0f, acc[t][i]);
     if (last) {
 #pragma unroll
       for (int t = 0; t < MT; ++t)
@@ -363,11 +452,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
       }
       par ^= 1;  // (the next tile's barrier separates these reads from the buffer's next writes)
     }
-    tile = tile1;
-    chunk = chunk1;
-    return more;
+    after(tile, chunk);
+    return tile < end;
   };
-  while (step(wa, wb, xa, HOLD ? xa : xb) && step(wb, wa, HOLD ? xa : xb, xa)) {
+  if constexpr (STAGES == 3) {
+    while (step(wa, wc, xa, xa) && step(wb, wa, xa, xa) && step(wc, wb, xa, xa)) {
+    }
+  } else {
+    while (step(wa, wb, xa, xb) && step(wb, wa, xb, xa)) {
+    }
   }
 }
 
@@ -376,8 +469,7 @@ struct W4a16Call {
   const float* scales;
   const float* parts;
   int slices;
-  const uint8_t* wq;
-  const uint16_t* w_scales;
+  const uint8_t* container;
   const uint16_t* L2p;
   const uint16_t* bias;
   int M, N, K, r, tiles;
@@ -385,42 +477,38 @@ struct W4a16Call {
   hipStream_t stream;
 };
 
-template <int MT, int GPW, bool HOLD, bool FP32>
+template <int MT, int GPW, bool FP32, bool RANK>
 static hipError_t launch_main(const W4a16Call& a, int tile0) {
   // one workgroup per CU, fewer where there are fewer column tiles (a multiple of 8, for the XCDs)
   const int all = (a.N + 15) / 16, grid = all < 256 ? (all + 7) / 8 * 8 : 256;
-  hipLaunchKernelGGL((w4a16_kernel<MT, GPW, HOLD, FP32>), dim3(grid), dim3(kWaves * 64), 0,
-                     a.stream, a.frags, a.scales, a.parts, a.slices, a.wq, a.w_scales, a.L2p, a.bias,
-                     a.M, a.N, a.K, a.r, tile0, a.tiles, a.Y);
+#define SVDQ_MAIN(HOLD)                                                                            \
+  hipLaunchKernelGGL((w4a16_kernel<MT, GPW, HOLD, FP32, RANK>), dim3(grid), dim3(kWaves * 64), 0,  \
+                     a.stream, a.frags, a.scales, a.parts, a.slices, a.container, a.L2p, a.bias,   \
+                     a.M, a.N, a.K, a.r, tile0, a.tiles, a.Y)
+  if (a.K / kGroup <= kWaves * GPW) SVDQ_MAIN(true);
+  else SVDQ_MAIN(false);
+#undef SVDQ_MAIN
   return hipGetLastError();
 }
 
 // Up to 4 row tiles share a pass over the weights (64 bf16 rows, 32 fp32 rows).  What a wave holds
-// of X^ is 12 registers per row tile and group, 8 of them held or 4 in flight and 4 in use, so
-// more row tiles mean fewer groups to a chunk.
-template <bool FP32>
+// of X^ is 8 registers per row tile and group, so more row tiles mean fewer groups to a chunk.
+template <bool FP32, bool RANK>
 static hipError_t launch_tiles(const W4a16Call& a) {
-  const int G = a.K / kGroup;
   for (int t = 0; t < a.tiles; t += 4) {
     const int left = a.tiles - t;
-    hipError_t e;
-    if (left >= 3)
-      e = G <= 2 * kWaves ? launch_main<4, 2, true, FP32>(a, t) : launch_main<4, 1, false, FP32>(a, t);
-    else if (left == 2)
-      e = G <= 4 * kWaves ? launch_main<2, 4, true, FP32>(a, t) : launch_main<2, 2, false, FP32>(a, t);
-    else if (G <= 4 * kWaves)
-      e = launch_main<1, 4, true, FP32>(a, t);
-    else
-      e = G <= 8 * kWaves ? launch_main<1, 8, true, FP32>(a, t) : launch_main<1, 4, false, FP32>(a, t);
+    const hipError_t e = left >= 3 ? launch_main<4, 2, FP32, RANK>(a, t)
+                         : left == 2 ? launch_main<2, 4, FP32, RANK>(a, t)
+                                     : launch_main<1, 8, FP32, RANK>(a, t);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
 hipError_t launch_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const uint16_t* L1p,
-                             const uint8_t* wq, const uint16_t* w_scales, const uint16_t* L2p,
-                             const uint16_t* bias, int M, int N, int K, int r, void* Y,
-                             int out_fp32, void* workspace, hipStream_t stream) {
+                             const uint8_t* container, const uint16_t* L2p, const uint16_t* bias,
+                             int M, int N, int K, int r, void* Y, int out_fp32, void* workspace,
+                             hipStream_t stream) {
   const W4a16Ws w = w4a16_layout(M, K, r, out_fp32);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   v8h* frags = reinterpret_cast<v8h*>(base + w.frags);
@@ -428,7 +516,7 @@ hipError_t launch_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const u
   float* parts = reinterpret_cast<float*>(base + w.parts);
   const int tiles = w4a16_tiles(M, out_fp32), slices = w4a16_slices(K);
   const dim3 grid(slices, tiles);
-#define SVDQ_PREP(RT, WAVES)                                                                           \
+#define SVDQ_PREP(RT, WAVES)                                                                     \
   hipLaunchKernelGGL((w4a16_prep_kernel<RT, WAVES>), grid, dim3(WAVES * 64), 0, stream, X,       \
                      inv_lambda, L1p, M, K, r, out_fp32, frags, scales, parts)
   if (r == 0) SVDQ_PREP(0, kPrepWaves);
@@ -438,8 +526,9 @@ hipError_t launch_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const u
 #undef SVDQ_PREP
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const W4a16Call a{frags, scales, parts, slices, wq, w_scales, L2p, bias, M, N, K, r, tiles, Y, stream};
-  return out_fp32 ? launch_tiles<true>(a) : launch_tiles<false>(a);
+  const W4a16Call a{frags, scales, parts, slices, container, L2p, bias, M, N, K, r, tiles, Y, stream};
+  if (out_fp32) return r ? launch_tiles<true, true>(a) : launch_tiles<true, false>(a);
+  return r ? launch_tiles<false, true>(a) : launch_tiles<false, false>(a);
 }
 
 }  // namespace svdq

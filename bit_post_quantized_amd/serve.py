@@ -54,23 +54,24 @@ def _stream(device: torch.device) -> int:
 
 class DecodeLinear:
     """The SVDQuant linear of ``layer.PackedWeights`` (nibble container) for up to 64 rows, with
-    the activations kept at 16 bits (``svdq_w4a16_gemv``).  The weights are checked and bound when
-    the object is made."""
+    the activations kept at 16 bits (``svdq_w4a16_gemv``).  The weights are checked, laid out for
+    it (``svdq_pack_w4a16``; ``pw.wq`` is not kept) and bound when the object is made."""
 
     def __init__(self, pw: layer.PackedWeights):
         if pw.e3m2:
             raise ValueError("DecodeLinear reads the nibble container (e3m2=False)")
-        self.pw = pw
         self.K, self.N, self.rank = K, N, r = pw.K, pw.N, pw.rank
+        if tuple(pw.wq.shape) != (N, K // 2):
+            raise ValueError(f"DecodeLinear: wq must have shape {(N, K // 2)} (got {tuple(pw.wq.shape)})")
+        self.container = torch.empty(B.svdq_w4a16_container_bytes(N, K), dtype=_U8, device=pw.wq.device)
+        B.svdq_pack_w4a16(pw.wq, pw.w_scales, self.container)
         a = binding._Args("svdq_w4a16_gemv")
         l1, l2 = (pw.L1p, pw.L2p) if r else (None, None)
         self._weights = (a(pw.inv_lambda, 4 * K, "inv_lambda", _F32, (K,)),
-                         a(l1, 2 * r * K, "L1p", _BF16, (r, K)),
-                         a(pw.wq, N * (K // 2), "wq", _U8, (N, K // 2)),
-                         a(pw.w_scales, 2 * (K // 64) * N, "w_scales", torch.float16, (K // 64, N)),
+                         a(l1, 2 * r * K, "L1p", _BF16, (r, K)), a(self.container, 0, "container"),
                          a(l2, 2 * N * r, "L2p", _BF16, (N, r)),
                          a(pw.bias, 2 * N, "bias", _BF16, (N,)))
-        self._held = (pw.inv_lambda, l1, pw.wq, pw.w_scales, l2, pw.bias)
+        self._held = (pw.inv_lambda, l1, self.container, l2, pw.bias)
         self.device = a.device
         self._call = B.load().svdq_w4a16_gemv
 
@@ -92,8 +93,7 @@ class DecodeLinear:
             if status:
                 binding._check("svdq_w4a16_gemv", status)
         else:
-            inv, l1, wq, ws, l2, bias = self._held
-            B.svdq_w4a16_gemv(X, inv, l1, wq, ws, l2, bias, self.rank, out, workspace)
+            B.svdq_w4a16_gemv(X, *self._held, self.rank, out, workspace)
         return out
 
 

@@ -17,8 +17,10 @@ from .binding import SVDQ_OUT_BF16, SVDQ_OUT_FP32, _Args, _out_dtype
 _P, _I, _L, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _SIGNATURES = {
     "svdq_serve_version": ([], _I),
+    "svdq_w4a16_container_bytes": ([_I, _I], _Z),
+    "svdq_pack_w4a16": ([_P, _P, _I, _I, _P, _P], _I),
     "svdq_w4a16_workspace_bytes": ([_I] * 5, _Z),
-    "svdq_w4a16_gemv": ([_P] * 7 + [_I] * 4 + [_P, _I, _P, _P], _I),
+    "svdq_w4a16_gemv": ([_P] * 6 + [_I] * 4 + [_P, _I, _P, _P], _I),
     "kv_block_plan": ([_P, _P, _I, _P, _I, _I, _P, _I, _P, _P, _P, _I, _P, _P, _P, _P, _P], _I),
     "kv_block_release": ([_P, _P, _I, _P, _I, _I, _P, _I, _P, _P, _P, _P], _I),
     "kv_block_append": ([_P, _P, _L, _L, _P] + [_I] * 5 + [_P] * 5, _I),
@@ -81,21 +83,39 @@ def svdq_w4a16_workspace_bytes(M: int, N: int, K: int, r: int, out_dtype: int) -
     return load().svdq_w4a16_workspace_bytes(M, N, K, r, out_dtype)
 
 
+def svdq_w4a16_container_bytes(N: int, K: int) -> int:
+    """Bytes of svdq_w4a16_gemv's weight container for N columns of K codes."""
+    return load().svdq_w4a16_container_bytes(N, K)
+
+
+def svdq_pack_w4a16(wq: torch.Tensor, w_scales: torch.Tensor, container: torch.Tensor,
+                    stream=None) -> None:
+    """wq uint8 [N, K/2], w_scales fp16 [K/64, N] (from svdq_pack_weights) -> container uint8
+    [svdq_w4a16_container_bytes(N, K)]."""
+    fn = "svdq_pack_w4a16"
+    N, half_k = wq.shape
+    K = 2 * half_k
+    a = _Args(fn)
+    args = (a(wq, N * half_k, "wq", _U8), a(w_scales, 2 * (K // 64) * N, "w_scales", _F16, (K // 64, N)),
+            N, K, a(container, svdq_w4a16_container_bytes(N, K), "container", _U8))
+    _call(fn, a, args, stream)
+
+
 def svdq_w4a16_gemv(X: torch.Tensor, inv_lambda: torch.Tensor, L1p: Optional[torch.Tensor],
-                    wq: torch.Tensor, w_scales: torch.Tensor, L2p: Optional[torch.Tensor],
+                    container: torch.Tensor, L2p: Optional[torch.Tensor],
                     bias: Optional[torch.Tensor], r: int, Y: torch.Tensor,
                     workspace: Optional[torch.Tensor], stream=None) -> None:
-    """X bf16 [M, K] (M <= 64), inv_lambda fp32 [K], L1p bf16 [r, K], wq uint8 [N, K/2],
-    w_scales fp16 [K/64, N], L2p bf16 [N, r], bias bf16 [N] -> Y [M, N], bf16 or fp32."""
+    """X bf16 [M, K] (M <= 64), inv_lambda fp32 [K], L1p bf16 [r, K], container (from
+    svdq_pack_w4a16), L2p bf16 [N, r], bias bf16 [N] -> Y [M, N], bf16 or fp32."""
     fn = "svdq_w4a16_gemv"
     M, K = X.shape
-    N = wq.shape[0]
+    N = Y.shape[1]
     out = _out_dtype(fn, Y)
     need = svdq_w4a16_workspace_bytes(M, N, K, r, out)
     a = _Args(fn)
     args = (a(X, 2 * M * K, "X", _BF16, (M, K)), a(inv_lambda, 4 * K, "inv_lambda", _F32, (K,)),
-            a(L1p, 2 * r * K, "L1p", _BF16, (r, K)), a(wq, N * (K // 2), "wq", _U8, (N, K // 2)),
-            a(w_scales, 2 * (K // 64) * N, "w_scales", _F16, (K // 64, N)),
+            a(L1p, 2 * r * K, "L1p", _BF16, (r, K)),
+            a(container, svdq_w4a16_container_bytes(N, K), "container", _U8),
             a(L2p, 2 * N * r, "L2p", _BF16, (N, r)), a(bias, 2 * N, "bias", _BF16, (N,)),
             M, N, K, r, a(Y, Y.element_size() * M * N, "Y", None, (M, N)), out,
             a(workspace, need, "workspace"))

@@ -42,6 +42,21 @@ extern "C" {
 int svdq_serve_version(void);
 
 /*
+ * svdq_pack_w4a16 — relayout of svdq_pack_weights' INT4 codes and scales for svdq_w4a16_gemv
+ * (offline weight preparation; the codes and scales are copied, not rounded, and wq need not be
+ * kept).  Unit (t, s) of the container, at (t ceil(K / 512) + s) * 4352 bytes, holds columns
+ * 16 t .. + 15 and the 64-groups g = 8 s .. + 7: for each pair of groups 64 lanes of 16 bytes
+ * (lane l: column 16 t + l % 16, the 8 bytes of wq with k = 64 g + 16 (l / 16) .. + 15 of the even,
+ * then of the odd group), then the scales fp16 [16 columns][8 groups]; what lies past N or K is 0.
+ *   wq         uint8 [N, K/2] (16B), w_scales  fp16 [K/64, N], as written by svdq_pack_weights
+ *   container  uint8 [svdq_w4a16_container_bytes(N, K)]  16B
+ *   1 <= N <= 2^24, K % 64 == 0, 64 <= K <= 64 * 65535 (the size is 0 outside these limits).
+ */
+size_t svdq_w4a16_container_bytes(int N, int K);
+int svdq_pack_w4a16(const uint8_t* wq, const uint16_t* w_scales, int N, int K, uint8_t* container,
+                    void* stream);
+
+/*
  * svdq_w4a16_gemv — the linear layer on few rows (decoding: 1 to 64 tokens), with the INT4
  * weights of svdq_pack_weights and the activations kept at 16 bits (no activation codes), in
  * fp32:
@@ -50,7 +65,7 @@ int svdq_serve_version(void);
  *   X           bf16 [M, K]  16B;  inv_lambda  fp32 [K]  16B
  *   L1p         bf16 [r, K] (16B), L2p  bf16 [N, r] (16B), as for svdq_quantize_act and
  *               svdq_w4a4_gemm; may be NULL when r == 0
- *   wq, w_scales   as written by svdq_pack_weights (wq: 16B)
+ *   container   as written by svdq_pack_w4a16  16B
  *   bias        bf16 [N] or NULL
  *   Y           [M, N], bf16 or fp32 by out_dtype (enum svdq_out_dtype)
  *   workspace   device scratch of svdq_w4a16_workspace_bytes(M, N, K, r, out_dtype) bytes (16B),
@@ -59,13 +74,13 @@ int svdq_serve_version(void);
  *   0 <= M <= 64 (more rows: svdq_w4a4_gemm), 1 <= N <= 2^24, K % 64 == 0,
  *   64 <= K <= 64 * 65535, 0 <= r <= 128, r % 16 == 0.
  * For SVDQ_OUT_BF16 an activation enters the products rounded to 11 significant bits, for
- * SVDQ_OUT_FP32 to 22; every product with a 4-bit code is exact and every sum is in fp32.
+ * SVDQ_OUT_FP32 to 22 (of values within 2^24 of the largest of its row's 512); every product with
+ * a 4-bit code is exact and every sum is in fp32.
  */
 size_t svdq_w4a16_workspace_bytes(int M, int N, int K, int r, int out_dtype);
 int svdq_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const uint16_t* L1p,
-                    const uint8_t* wq, const uint16_t* w_scales, const uint16_t* L2p,
-                    const uint16_t* bias, int M, int N, int K, int r, void* Y, int out_dtype,
-                    void* workspace, void* stream);
+                    const uint8_t* container, const uint16_t* L2p, const uint16_t* bias, int M,
+                    int N, int K, int r, void* Y, int out_dtype, void* workspace, void* stream);
 
 /*
  * kv_block_plan — the bookkeeping of one step, on the device: from each request's cached tokens

@@ -30,8 +30,10 @@ int main() {
       (void)svdq_w4a16_workspace_bytes(M, INT_MAX, K, 128, 1);
       (void)svdq_w4a16_workspace_bytes(M, 1, K, INT_MAX, 0);
       for (int N : {INT_MIN, INT_MAX})
-        EXPECT(svdq_w4a16_gemv(u16(), f32(), u16(), u8(), u16(), u16(), nullptr, M, N, K, 16, p, 0, p,
-                               nullptr) != SVDQ_OK);
+        EXPECT(svdq_w4a16_gemv(u16(), f32(), u16(), u8(), u16(), nullptr, M, N, K, 16, p, 0, p, nullptr) !=
+               SVDQ_OK);
+      (void)svdq_w4a16_container_bytes(M, K);
+      EXPECT(svdq_pack_w4a16(u8(), u16(), INT_MAX, K, u8(), nullptr) != SVDQ_OK);
     }
   for (int n : ends)
     for (int w : ends)

@@ -132,6 +132,26 @@ def test_same_bits_every_time_on_streams_and_in_graphs(gpu_lib):
     check(host64(first), *ref(x), 1024, False)
 
 
+@pytest.mark.parametrize("N,K", [(16, 512), (1, 64), (50, 704), (33, 1024)])
+def test_container_layout(gpu_lib, N, K):
+    rng = np.random.default_rng(N)
+    wq = rng.integers(0, 256, (N, K // 2)).astype(np.uint8)
+    ws = rng.integers(0, 1 << 15, (K // 64, N)).astype(np.uint16)
+    G, segs, tiles = K // 64, -(-K // 512), -(-N // 16)
+    got = torch.full((SB.svdq_w4a16_container_bytes(N, K),), 0xEE, dtype=torch.uint8, device="cuda")
+    SB.svdq_pack_w4a16(to_dev(wq), to_dev(ws.view(np.float16)), got)
+    want = np.zeros((tiles, segs, 4352), np.uint8)
+    for n in range(N):
+        for g in range(G):
+            unit = want[n // 16, g // 8]
+            for j in range(4):
+                at = (g % 8) // 2 * 1024 + (16 * j + n % 16) * 16 + g % 2 * 8
+                unit[at:at + 8] = wq[n, 32 * g + 8 * j:32 * g + 8 * j + 8]
+            at = 4096 + (n % 16) * 16 + g % 8 * 2
+            unit[at:at + 2] = ws[g, n:n + 1].view(np.uint8)
+    np.testing.assert_array_equal(got.cpu().numpy(), want.reshape(-1))
+
+
 def test_refusals(gpu_lib):
     x, pw, _ = make(29, 2, 128, 32, 16, False)
     lin = serve.DecodeLinear(pw)
@@ -139,7 +159,7 @@ def test_refusals(gpu_lib):
         lin(torch.zeros(65, 128, dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(ValueError, match="X must be"):
         lin(torch.zeros(2, 128, dtype=torch.float16, device="cuda"))
-    with pytest.raises(ValueError, match="inv_lambda must have shape"):
+    with pytest.raises(ValueError, match="inv_lambda must have shape"):  # K of X against the weights
         lin(torch.zeros(2, 192, dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(ValueError, match="X must be contiguous"):
         lin(torch.zeros(2, 256, dtype=torch.bfloat16, device="cuda")[:, ::2])

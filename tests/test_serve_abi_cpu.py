@@ -40,8 +40,8 @@ def test_every_declared_symbol_is_exported(lib):
 def test_gemv_validation(lib):
     f = lib.svdq_w4a16_gemv
 
-    def call(M=1, N=16, K=64, r=0, X=F, inv=F, l1=F, wq=F, ws=F, l2=F, bias=None, Y=F, out=0, wsp=F):
-        return f(X, inv, l1, wq, ws, l2, bias, M, N, K, r, Y, out, wsp, None)
+    def call(M=1, N=16, K=64, r=0, X=F, inv=F, l1=F, wt=F, l2=F, bias=None, Y=F, out=0, wsp=F):
+        return f(X, inv, l1, wt, l2, bias, M, N, K, r, Y, out, wsp, None)
 
     assert call(M=-1) == EINVAL and call(N=0) == EINVAL and call(K=0) == EINVAL and call(r=-16) == EINVAL
     assert call(K=100) == ESHAPE and call(r=24) == ESHAPE and call(r=144) == ESHAPE
@@ -49,9 +49,9 @@ def test_gemv_validation(lib):
     assert call(N=(1 << 24) + 1) == ESHAPE and call(K=64 * 65536) == ESHAPE
     assert call(N=1 << 24, K=64 * 65535) == ESHAPE      # N K past 2^40
     assert call(out=2) == EINVAL
-    assert call(X=None) == EINVAL and call(Y=None) == EINVAL and call(wsp=None) == EINVAL
+    assert call(X=None) == EINVAL and call(Y=None) == EINVAL and call(wsp=None) == EINVAL and call(wt=None) == EINVAL
     assert call(r=16, l1=None) == EINVAL and call(r=16, l2=None) == EINVAL
-    for k in ("X", "inv", "wq", "wsp"):
+    for k in ("X", "inv", "wt", "wsp"):
         assert call(**{k: ODD}) == EALIGN
     assert call(r=16, l1=ODD) == EALIGN and call(r=16, l2=ODD) == EALIGN
     assert call(M=0) == OK and call(M=0, X=None, Y=None, wsp=None) == OK
@@ -59,7 +59,13 @@ def test_gemv_validation(lib):
     assert w(0, 16, 64, 0, 0) == 0 and w(65, 16, 64, 0, 0) == 0 and w(1, 16, 100, 0, 0) == 0
     # one row tile of 16 rows x 64 k of fp16, its 16 scales, and T's partials
     assert w(1, 16, 64, 16, 0) == 2048 + 64 + 16 * 4
-    assert w(9, 16, 128, 0, 1) == 2 * 2 * (2048 + 64)   # fp32 output: 8 rows to a tile
+    assert w(9, 16, 128, 0, 1) == 2 * (2 * 2048 + 64)   # fp32 output: 8 rows to a tile
+    p, c = lib.svdq_pack_w4a16, lib.svdq_w4a16_container_bytes
+    assert p(F, F, 0, 64, F, None) == EINVAL and p(F, F, 16, 65, F, None) == ESHAPE
+    assert p(None, F, 16, 64, F, None) == EINVAL and p(F, F, 16, 64, None, None) == EINVAL
+    assert p(ODD, F, 16, 64, F, None) == EALIGN and p(F, F, 16, 64, ODD, None) == EALIGN
+    assert c(16, 512) == 4352 and c(17, 576) == 4 * 4352 and c(0, 512) == 0 and c(16, 100) == 0
+    assert c(1 << 24, 64 * 65535) == 0
 
 
 def test_plan_and_release_validation(lib):
@@ -142,10 +148,13 @@ def _cases():
     names = list(cache)
     plan = dict(block_tables=([n, width], i32), free_blocks=([9], i32), free_count=([1], i32))
     return [
-        (SB.svdq_w4a16_gemv, ["X", "inv_lambda", "L1p", "wq", "w_scales", "L2p", "bias", "r", "Y", "workspace"],
-         dict(X=([M, K], bf16), inv_lambda=([K], f32), L1p=([R, K], bf16), wq=([N, K // 2], u8),
-              w_scales=([K // 64, N], f16), L2p=([N, R], bf16), bias=([N], bf16), Y=([M, N], bf16),
-              workspace=([SB.svdq_w4a16_workspace_bytes(M, N, K, R, 0)], u8)), dict(r=R)),
+        (SB.svdq_pack_w4a16, ["wq", "w_scales", "container"],
+         dict(wq=([N, K // 2], u8), w_scales=([K // 64, N], f16),
+              container=([SB.svdq_w4a16_container_bytes(N, K)], u8)), {}),
+        (SB.svdq_w4a16_gemv, ["X", "inv_lambda", "L1p", "container", "L2p", "bias", "r", "Y", "workspace"],
+         dict(X=([M, K], bf16), inv_lambda=([K], f32), L1p=([R, K], bf16),
+              container=([SB.svdq_w4a16_container_bytes(N, K)], u8), L2p=([N, R], bf16), bias=([N], bf16),
+              Y=([M, N], bf16), workspace=([SB.svdq_w4a16_workspace_bytes(M, N, K, R, 0)], u8)), dict(r=R)),
         (SB.kv_block_plan, ["ctx_lens", "new_lens", "block_tables", "block_size", "free_blocks", "free_count",
                             "cu_rows", "seq_lens", "positions", "slots", "status", "free_count_out"],
          dict(plan, ctx_lens=([n], i32), new_lens=([n], i32), cu_rows=([n + 1], i32), seq_lens=([n], i32),
