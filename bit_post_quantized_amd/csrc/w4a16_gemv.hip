@@ -25,8 +25,7 @@ namespace svdq {
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
 constexpr int kFragBytes = 2048;     // of X^: one (row tile, group), 16 rows x 64 k of fp16
-constexpr int kPrepWaves = 16;       // 8 above rank 64, whose operands need the registers
-constexpr int kMaxSlices = 8;
+constexpr int kMaxSlices = 32;       // of K, in the preparing kernel
 constexpr int kWaves = 8;            // of the main kernel
 constexpr int kSeg = 8;              // groups that share an activation scale; of one container unit
 
@@ -89,10 +88,10 @@ inline int w4a16_tiles(int M, int out_fp32) {
   return (M + rpt - 1) / rpt;
 }
 
-// Slices of K for T's partial sums: two segments (a group per wave) to a preparing workgroup, and
-// few enough that summing the partials again in every workgroup of the main kernel stays cheap.
+// Slices of K for T's partial sums: one segment (a group per wave) to a preparing workgroup, as far
+// as summing the partials again in every workgroup of the main kernel stays cheap.
 inline int w4a16_slices(int K) {
-  const int s = (w4a16_segments(K) + 1) / 2;
+  const int s = w4a16_segments(K);
   return s < kMaxSlices ? s : kMaxSlices;
 }
 
@@ -154,16 +153,16 @@ __device__ __forceinline__ void split_bf16(const float* x, v8bf* out) {
   }
 }
 
-// One workgroup per (slice of K, row tile); WAVES / kSeg segments of 8 groups at a time, a group to
-// a wave; a segment's waves share their rows' largest magnitudes in LDS.  Lane (row l % 16,
-// j = l / 16) holds k = 64 g + 16 j .. + 15.  RT >= r / 16 rank tiles.
-template <int RT, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void w4a16_prep_kernel(
+// One workgroup per (slice of K, row tile); a segment of 8 groups at a time, a group to a wave; the
+// waves share their rows' largest magnitudes in LDS.  Lane (row l % 16, j = l / 16) holds
+// k = 64 g + 16 j .. + 15.  RT >= r / 16 rank tiles.
+template <int RT>
+__global__ __launch_bounds__(kSeg * 64) void w4a16_prep_kernel(
     const uint16_t* __restrict__ X, const float* __restrict__ inv_lambda,
     const uint16_t* __restrict__ L1p, int M, int K, int r, int out_fp32, v8h* __restrict__ frags,
     float* __restrict__ scales, float* __restrict__ parts) {
-  __shared__ float red[2][RT ? WAVES : 1][16][17];
-  __shared__ float top[2][WAVES][16];
+  __shared__ float red[RT ? RT : 1][kSeg][16][17];
+  __shared__ float top[2][kSeg][16];
   const int G = K / kGroup, segs = w4a16_segments(K);
   const int slices = gridDim.x, slice = blockIdx.x, tile = blockIdx.y;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -178,10 +177,9 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_prep_kernel(
   for (int i = 0; i < RT; ++i) t[i] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
   int par = 0;
-  for (int sb = s0; sb < s1; sb += WAVES / kSeg, par ^= 1) {
-    const int seg = sb + wave / kSeg, want = seg * kSeg + wave % kSeg;
-    const bool mine = seg < s1 && want < G;  // (the others read the last group and store nothing)
-    const int g = min(want, G - 1), k0 = g * kGroup + 16 * j;
+  for (int seg = s0; seg < s1; ++seg, par ^= 1) {
+    const bool mine = seg * kSeg + wave < G;  // (the others read the last group and store nothing)
+    const int g = min(seg * kSeg + wave, G - 1), k0 = g * kGroup + 16 * j;
     v8bf b[RT ? RT : 1][2];
     // the rank rows' loads first: they do not wait for X (rows past r - 1 read row r - 1, unused)
 #pragma unroll
@@ -213,7 +211,7 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_prep_kernel(
     if (j == 0) top[par][wave][mr] = amax;
     __syncthreads();  // (the next round's buffer is the other one)
 #pragma unroll
-    for (int q = 0; q < kSeg; ++q) amax = __builtin_fmaxf(amax, top[par][wave / kSeg * kSeg + q][mr]);
+    for (int q = 0; q < kSeg; ++q) amax = __builtin_fmaxf(amax, top[par][q][mr]);
     // 2^e with amax 2^-e in [2^10, 2^11) (e clamped so that both powers are normal; 0 keeps e = 0)
     int e = (int)(__float_as_uint(amax) >> 23) - 127 - 10;
     e = amax == 0.0f ? 0 : max(e, -110);
@@ -235,7 +233,7 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_prep_kernel(
         for (int i = 0; i < 8; ++i) f[i] = h[8 * s + (i >> 1) + ((i & 1) << 2)];
         frags[base + s * 64 + lane] = f;
       }
-      if (j == 0 && wave % kSeg == 0) scales[((size_t)tile * segs + seg) * 16 + mr] = up;
+      if (j == 0 && wave == 0) scales[((size_t)tile * segs + seg) * 16 + mr] = up;
     }
 
     if constexpr (RT > 0) {
@@ -251,18 +249,21 @@ __global__ __launch_bounds__(WAVES * 64) void w4a16_prep_kernel(
     }
   }
 
-  // T's partial of this slice: the waves' sums meet in LDS, one tile of 16 ranks after the other
+  // T's partial of this slice: the waves' sums meet in LDS
+  if constexpr (RT > 0) {
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) red[i & 1][wave][4 * j + q][mr] = t[i][q];
+      for (int q = 0; q < 4; ++q) red[i][wave][4 * j + q][mr] = t[i][q];
     __syncthreads();
-    const int m = threadIdx.x >> 4, c = threadIdx.x & 15, out = tile * rpt + m;
-    if (m < rpt && out < M && 16 * i + c < r) {
-      float s = 0.0f;
+    for (int o = threadIdx.x; o < RT * 256; o += kSeg * 64) {
+      const int i = o >> 8, m = (o >> 4) & 15, c = o & 15, out = tile * rpt + m;
+      if (m < rpt && out < M && 16 * i + c < r) {
+        float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) s += red[i & 1][w][m][c];
-      parts[((size_t)slice * M + out) * r + 16 * i + c] = s;
+        for (int w = 0; w < kSeg; ++w) s += red[i][w][m][c];
+        parts[((size_t)slice * M + out) * r + 16 * i + c] = s;
+      }
     }
   }
 }
@@ -370,14 +371,21 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = 0.0f;
       if (c < RPT && m < rows && k < r)
-        for (int q = 0; q < slices; ++q) {
-          const v4f* pp = reinterpret_cast<const v4f*>(parts + ((size_t)q * M + row0 + m) * r + k);
-          const v4f a = pp[0], b = pp[1];
+        for (int q = 0; q < slices; q += 8) {
+          v4f a[8], b[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] += a[i];
-            x[4 + i] += b[i];
+          for (int e = 0; e < 8; ++e) {
+            const v4f* pp = reinterpret_cast<const v4f*>(parts + ((size_t)min(q + e, slices - 1) * M + row0 + m) * r + k);
+            a[e] = pp[0];
+            b[e] = pp[1];
           }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[i] += q + e < slices ? a[e][i] : 0.0f;
+              x[4 + i] += q + e < slices ? b[e][i] : 0.0f;
+            }
         }
       v8bf p[TERMS];
       split_bf16<TERMS>(x, p);
@@ -497,7 +505,8 @@ template <bool FP32, bool RANK>
 static hipError_t launch_tiles(const W4a16Call& a) {
   for (int t = 0; t < a.tiles; t += 4) {
     const int left = a.tiles - t;
-    const hipError_t e = left >= 3 ? launch_main<4, 2, FP32, RANK>(a, t)
+    const hipError_t e = left >= 4   ? launch_main<4, 2, FP32, RANK>(a, t)
+                         : left == 3 ? launch_main<3, 2, FP32, RANK>(a, t)
                          : left == 2 ? launch_main<2, 4, FP32, RANK>(a, t)
                                      : launch_main<1, 8, FP32, RANK>(a, t);
     if (e != hipSuccess) return e;
@@ -516,13 +525,13 @@ hipError_t launch_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const u
   float* parts = reinterpret_cast<float*>(base + w.parts);
   const int tiles = w4a16_tiles(M, out_fp32), slices = w4a16_slices(K);
   const dim3 grid(slices, tiles);
-#define SVDQ_PREP(RT, WAVES)                                                                     \
-  hipLaunchKernelGGL((w4a16_prep_kernel<RT, WAVES>), grid, dim3(WAVES * 64), 0, stream, X,       \
-                     inv_lambda, L1p, M, K, r, out_fp32, frags, scales, parts)
-  if (r == 0) SVDQ_PREP(0, kPrepWaves);
-  else if (r <= 32) SVDQ_PREP(2, kPrepWaves);
-  else if (r <= 64) SVDQ_PREP(4, kPrepWaves);
-  else SVDQ_PREP(8, kPrepWaves / 2);
+#define SVDQ_PREP(RT)                                                                            \
+  hipLaunchKernelGGL(w4a16_prep_kernel<RT>, grid, dim3(kSeg * 64), 0, stream, X, inv_lambda,     \
+                     L1p, M, K, r, out_fp32, frags, scales, parts)
+  if (r == 0) SVDQ_PREP(0);
+  else if (r <= 32) SVDQ_PREP(2);
+  else if (r <= 64) SVDQ_PREP(4);
+  else SVDQ_PREP(8);
 #undef SVDQ_PREP
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
