@@ -207,81 +207,254 @@ hipError_t launch_kv_block_release(const int32_t* seq, const uint8_t* done, int 
 // ------------------------------------------------------------------------------------ append
 // A run is the rows of one block: it begins at a row whose predecessor is not the slot before it,
 // or at a block's first slot, and goes on while the slots ascend inside the block.  One workgroup
-// per (tile of kAppendTile rows, head, K or V) handles the runs that begin in its tile, one after
-// the other: amax over the run, the scale, the old codes where it grew, the new codes.
+// per (window of rows, head, K or V) writes the runs that begin in its window.  Every wave finds
+// them by itself: a lane looks at one row, and the rows where a run breaks are three 64-bit masks.
+//  - Short runs (up to kShort rows: decoding) go to groups of D / 8 lanes, one run to a group, all
+//    at once.
+//  - A long run (a prompt's block) takes the whole workgroup: its rows are read once, 8 channels
+//    and 4 consecutive rows to a thread and step, all loads before the largest magnitude is known;
+//    K's codes are stored as they are, V's go through LDS to become rows of tokens.
+// The append of 20000 rows moves 123 MB (2 bytes in and 1 out for K and V) and is bound by that.
 constexpr int kAppendThreads = 256;
-constexpr int kAppendTile = 4;
+constexpr int kShort = 4;
+constexpr int kMaxBlock = 128;  // tokens
+
+__host__ __device__ inline int append_window(int bs) { return bs < 32 ? 16 : 32; }
 
 // One value -> code + 128, for s != 0 and rcp = fl32(1 / s).  The correction-step quotient needs a
 // normal reciprocal; below 2^-100 the division itself is used.
-__device__ __forceinline__ uint32_t kv_code(float x, float s, float rcp) {
+__device__ __forceinline__ float kv_code(float x, float s, float rcp) {
   const float t = s >= 0x1p-100f ? rne_quotient(x, s, rcp) : __builtin_rintf(x / s);
-  return (uint32_t)(int)(__builtin_amdgcn_fmed3f(t, -127.0f, 127.0f) + 128.0f);
+  return __builtin_amdgcn_fmed3f(t, -127.0f, 127.0f) + 128.0f;
+}
+
+// Eight bf16 of a 16-byte load as fp32.
+__device__ __forceinline__ void bf16x8(v4u w, float* x) {
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(ws[e] << 16);
+    x[2 * e + 1] = __uint_as_float(ws[e] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ float amax8(v4u w, float amax) {
+  float x[8];
+  bf16x8(w, x);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = __builtin_fmaxf(amax, __builtin_fabsf(x[e]));
+  return amax;
+}
+
+// Codes of one row's 8 channels (byte e: channel e).  zero: the block's scale is 0.
+__device__ __forceinline__ v2u codes8(v4u w, float s, float rcp, bool zero) {
+  float x[8];
+  bf16x8(w, x);
+  v2u c = {0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float q = zero ? 128.0f : kv_code(x[e], s, rcp);
+    if (e < 4) c.x = __builtin_amdgcn_cvt_pk_u8_f32(q, e, c.x);
+    else c.y = __builtin_amdgcn_cvt_pk_u8_f32(q, e - 4, c.y);
+  }
+  return c;
+}
+
+// The first `n` bytes of a dword of codes under a grown scale; the others as they are.
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio, int n) {
+  uint32_t r = 0u;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float c = (float)((w >> (8 * e)) & 0xFFu);
+    r = __builtin_amdgcn_cvt_pk_u8_f32(__builtin_rintf((c - 128.0f) * ratio) + 128.0f, e, r);
+  }
+  const uint32_t keep = n >= 4 ? 0u : ~0u << (8 * n);
+  return (r & ~keep) | (w & keep);
 }
 
 template <int D>
 __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
     const uint16_t* __restrict__ kx, const uint16_t* __restrict__ vx, int64_t k_stride,
     int64_t v_stride, const int64_t* __restrict__ slots, int rows, int shift, BlockCacheView c) {
-  constexpr int TPR = D / 8;                     // threads per token row, 8 channels each
-  constexpr int PER = kAppendThreads / TPR;      // tokens per pass
+  constexpr int TPR = D / 8;                       // lanes per row, 8 channels each
+  constexpr int GROUPS = kAppendThreads / TPR;
+  constexpr int STEPS = kMaxBlock / 4 / GROUPS;    // of 4 rows per group, for the longest run
+  constexpr int PITCH = kMaxBlock + 4;             // of a channel's tokens in LDS, bytes
   __shared__ float wmax[kAppendThreads / 64];
+  __shared__ __attribute__((aligned(16))) uint8_t vt[D * PITCH];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int h = blockIdx.y, is_v = blockIdx.z, bs = 1 << shift;
-  const uint16_t* x = is_v ? vx : kx;
+  const int part = tid % TPR, group = tid / TPR;
   const int64_t stride = is_v ? v_stride : k_stride;
+  const uint16_t* x = (is_v ? vx : kx) + (size_t)h * D + 8 * part;
+  uint8_t* const cache = is_v ? c.v_codes : c.k_codes;
+  float* const scales = is_v ? c.v_scale : c.k_scale;
   const int64_t limit = (int64_t)c.num_blocks << shift;
-  const int row0 = blockIdx.x * kAppendTile;
-  for (int t = row0; t < min(row0 + kAppendTile, rows); ++t) {
-    const int64_t slot = slots[t];
-    if (slot < 0 || slot >= limit) continue;
-    const int off = (int)(slot & (bs - 1));
-    if (off != 0 && t > 0 && slots[t - 1] == slot - 1) continue;  // inside a run
-    int n = 1;
-    while (off + n < bs && t + n < rows && slots[t + n] == slot + n) ++n;
-    const size_t bh = (size_t)(slot >> shift) * c.heads + h;
-    uint8_t* codes = (is_v ? c.v_codes : c.k_codes) + bh * bs * D;
-    float* scale = (is_v ? c.v_scale : c.k_scale) + bh;
-    const int part = tid % TPR, first = tid / TPR;
-    float amax = 0.0f;
-    for (int i = first; i < n; i += PER) {
-      const v4u w = *reinterpret_cast<const v4u*>(x + (size_t)(t + i) * stride + (size_t)h * D + 8 * part);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  const int window = append_window(bs), row0 = blockIdx.x * window;
+
+  // rows row0 + 0 .. 191: where a run (or a row without a token) begins
+  uint64_t brk[3], lead = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        amax = __builtin_fmaxf(amax, __builtin_fabsf(__uint_as_float(ws[e] << 16)));
-        amax = __builtin_fmaxf(amax, __builtin_fabsf(__uint_as_float(ws[e] & 0xFFFF0000u)));
+  for (int q = 0; q < 3; ++q) {
+    const int t = row0 + 64 * q + lane;
+    const int64_t s = t < rows ? slots[t] : -1, before = t > 0 && t < rows ? slots[t - 1] : -2;
+    const bool valid = s >= 0 && s < limit;
+    brk[q] = __ballot(!valid || (s & (bs - 1)) == 0 || before != s - 1);
+    if (q == 0) lead = __ballot(valid && lane < window) & brk[0];
+  }
+  auto length = [&](int i) {  // rows of the run that begins at row0 + i
+    const uint64_t m = i < 63 ? brk[0] >> (i + 1) : 0;
+    if (m) return __builtin_ctzll(m) + 1;
+    if (brk[1]) return 64 + __builtin_ctzll(brk[1]) - i;
+    return 128 + (brk[2] ? __builtin_ctzll(brk[2]) : 64) - i;
+  };
+  uint64_t shorts = 0;
+  for (uint64_t m = lead; m; m &= m - 1) {
+    const int i = __builtin_ctzll(m);
+    if (length(i) <= kShort) shorts |= 1ull << i;
+  }
+
+  // ---- long runs, the whole workgroup
+  for (uint64_t m = lead & ~shorts; m; m &= m - 1) {
+    const int i0 = __builtin_ctzll(m), n = length(i0), t = row0 + i0;
+    const int64_t slot = slots[t];
+    const int off = (int)(slot & (bs - 1));
+    const size_t bh = (size_t)(slot >> shift) * c.heads + h;
+    uint8_t* codes = cache + bh * bs * D;
+    v4u w[STEPS][4];
+    float amax = 0.0f;
+#pragma unroll
+    for (int p = 0; p < STEPS; ++p)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = 4 * (group + GROUPS * p) + r;  // (rows past the run read its last one)
+        if (4 * GROUPS * p < n) w[p][r] = *reinterpret_cast<const v4u*>(x + (size_t)(t + min(i, n - 1)) * stride);
       }
-    }
+    const float old = off == 0 ? 0.0f : scales[bh];
+#pragma unroll
+    for (int p = 0; p < STEPS; ++p)
+      if (4 * GROUPS * p < n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) amax = amax8(w[p][r], amax);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o));
-    __syncthreads();
     if (lane == 0) wmax[wave] = amax;
-    __syncthreads();
+    __syncthreads();  // (also: every thread has read the old scale)
 #pragma unroll
-    for (int w = 0; w < kAppendThreads / 64; ++w) amax = __builtin_fmaxf(amax, wmax[w]);
-    const float old = off == 0 ? 0.0f : *scale;
+    for (int q = 0; q < kAppendThreads / 64; ++q) amax = __builtin_fmaxf(amax, wmax[q]);
     const float s = __builtin_fmaxf(old, amax / 127.0f);
-    __syncthreads();  // (every thread has read the old scale)
-    if (tid == 0) *scale = s;
+    const bool zero = s == 0.0f;
+    const float s1 = zero ? 1.0f : s, rcp = 1.0f / s1;
+    if (tid == 0) scales[bh] = s;
     if (off > 0 && s > old) {
       const float ratio = old / s;
-      for (int i = tid; i < off * D; i += kAppendThreads) {
-        const int at = is_v ? (i / off) * bs + i % off : i;
-        codes[at] = (uint8_t)(int)(__builtin_rintf(((float)codes[at] - 128.0f) * ratio) + 128.0f);
+      if (is_v) {
+        const int dw = (off + 3) / 4;  // dwords of a channel's earlier tokens
+        for (int i = tid; i < D * dw; i += kAppendThreads) {
+          uint32_t* p = reinterpret_cast<uint32_t*>(codes + (size_t)(i / dw) * bs) + i % dw;
+          *p = rescale4(*p, ratio, off - 4 * (i % dw));
+        }
+      } else {
+        for (int i = tid; i < off * D / 4; i += kAppendThreads) {
+          uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
+          *p = rescale4(*p, ratio, 4);
+        }
       }
     }
-    const float s1 = s == 0.0f ? 1.0f : s, rcp = 1.0f / s1;
-    for (int i = first; i < n; i += PER) {
-      const v4u w = *reinterpret_cast<const v4u*>(x + (size_t)(t + i) * stride + (size_t)h * D + 8 * part);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float f = __uint_as_float(e & 1 ? ws[e >> 1] & 0xFFFF0000u : ws[e >> 1] << 16);
-        const uint32_t q = s == 0.0f ? 128u : kv_code(f, s1, rcp);
-        const int d = 8 * part + e;
-        codes[is_v ? d * bs + off + i : (off + i) * D + d] = (uint8_t)q;
+    for (int p = 0; p < STEPS; ++p) {
+      const int i = 4 * (group + GROUPS * p);
+      if (i >= n) continue;
+      v2u q[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) q[r] = codes8(w[p][r], s1, rcp, zero);
+      if (!is_v) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (i + r < n) *reinterpret_cast<v2u*>(codes + (size_t)(off + i + r) * D + 8 * part) = q[r];
+      } else {
+        // four tokens of each of 8 channels as a dword: bytes e of q[0..3]
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t sel = 0x0C0C0400u + 0x0101u * (e & 3);
+          const uint32_t a = e < 4 ? q[0].x : q[0].y, b = e < 4 ? q[1].x : q[1].y;
+          const uint32_t d = e < 4 ? q[2].x : q[2].y, f = e < 4 ? q[3].x : q[3].y;
+          const uint32_t lo = __builtin_amdgcn_perm(b, a, sel), hi = __builtin_amdgcn_perm(f, d, sel);
+          *reinterpret_cast<uint32_t*>(&vt[(8 * part + e) * PITCH + i]) = lo | (hi << 16);
+        }
       }
+    }
+    if (is_v) {
+      __syncthreads();  // (the earlier tokens' rescaled dwords are written before bytes beside them)
+      // rows of tokens to the block: 16 bytes at a time where a chunk is whole and in step with
+      // LDS (off a multiple of 4), else its bytes
+      const int c0 = off >> 4, c1 = (off + n + 15) >> 4, nc = c1 - c0;
+      for (int i = tid; i < D * nc; i += kAppendThreads) {
+        const int d = i / nc, ch = c0 + i % nc;
+        const int lo = max(off, 16 * ch), hi = min(off + n, 16 * ch + 16);
+        const uint8_t* from = &vt[d * PITCH + lo - off];
+        uint8_t* to = codes + (size_t)d * bs + lo;
+        if (hi - lo == 16 && (off & 3) == 0) {
+          const uint32_t* f4 = reinterpret_cast<const uint32_t*>(from);
+          *reinterpret_cast<v4u*>(to) = v4u{f4[0], f4[1], f4[2], f4[3]};
+        } else {
+          for (int b = 0; b < hi - lo; ++b) to[b] = from[b];
+        }
+      }
+    }
+    __syncthreads();  // (wmax and vt before the next run)
+  }
+
+  // ---- short runs, one to a group of lanes
+  for (int k = group; k < __popcll(shorts); k += GROUPS) {
+    uint64_t m = shorts;
+    for (int q = 0; q < k; ++q) m &= m - 1;
+    const int i0 = __builtin_ctzll(m), n = length(i0), t = row0 + i0;
+    const int64_t slot = slots[t];
+    const int off = (int)(slot & (bs - 1));
+    const size_t bh = (size_t)(slot >> shift) * c.heads + h;
+    uint8_t* codes = cache + bh * bs * D;
+    v4u w[kShort];
+#pragma unroll
+    for (int r = 0; r < kShort; ++r) w[r] = *reinterpret_cast<const v4u*>(x + (size_t)(t + min(r, n - 1)) * stride);
+    const float old = off == 0 ? 0.0f : scales[bh];
+    float amax = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kShort; ++r) amax = amax8(w[r], amax);
+#pragma unroll
+    for (int o = 1; o < TPR; o <<= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o));
+    const float s = __builtin_fmaxf(old, amax / 127.0f);
+    const bool zero = s == 0.0f;
+    const float s1 = zero ? 1.0f : s, rcp = 1.0f / s1;
+    if (part == 0) scales[bh] = s;  // (the group's lanes have read it: they are one wave's)
+    const bool grew = off > 0 && s > old;
+    const float ratio = grew ? old / s : 1.0f;
+    if (!is_v) {
+      if (grew)
+        for (int i = 0; i < off; ++i) {
+          v2u* p = reinterpret_cast<v2u*>(codes + (size_t)i * D + 8 * part);
+          const v2u q = *p;
+          *p = v2u{rescale4(q.x, ratio, 4), rescale4(q.y, ratio, 4)};
+        }
+#pragma unroll
+      for (int r = 0; r < kShort; ++r)
+        if (r < n) *reinterpret_cast<v2u*>(codes + (size_t)(off + r) * D + 8 * part) = codes8(w[r], s1, rcp, zero);
+    } else {
+      if (grew)
+        for (int i = 0; i < off; i += 4)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            uint32_t* p = reinterpret_cast<uint32_t*>(codes + (size_t)(8 * part + e) * bs + i);
+            *p = rescale4(*p, ratio, off - i);
+          }
+#pragma unroll
+      for (int r = 0; r < kShort; ++r)
+        if (r < n) {
+          const v2u q = codes8(w[r], s1, rcp, zero);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            codes[(size_t)(8 * part + e) * bs + off + r] = (uint8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
+        }
     }
   }
 }
@@ -289,7 +462,8 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
 hipError_t launch_kv_block_append(const uint16_t* k, const uint16_t* v, int64_t k_stride,
                                   int64_t v_stride, const int64_t* slots, int rows,
                                   const BlockCacheView& c, hipStream_t stream) {
-  const dim3 grid((rows + kAppendTile - 1) / kAppendTile, c.heads, 2);
+  const int window = append_window(c.bs);
+  const dim3 grid((rows + window - 1) / window, c.heads, 2);
   const int shift = __builtin_ctz(c.bs);
   if (c.dim == 128)
     hipLaunchKernelGGL(kv_block_append_kernel<128>, grid, dim3(kAppendThreads), 0, stream, k, v,
@@ -301,51 +475,88 @@ hipError_t launch_kv_block_append(const uint16_t* k, const uint16_t* v, int64_t 
 }
 
 // -------------------------------------------------------------------------------------- read
-// One thread per (row, head, 8 channels).
+// One workgroup per (window of 16 * 256 / D rows, head, K or V).  K: a thread per 8 channels of a
+// row.  V: a thread per channel and 16 rows; where these are 16 consecutive slots at a multiple of
+// 16 their codes are one 16-byte load, otherwise a byte per row; the values go through LDS to
+// become rows of channels.
 template <int D>
 __global__ __launch_bounds__(256) void kv_block_read_kernel(const int64_t* __restrict__ slots,
                                                             int rows, int shift, BlockCacheView c,
                                                             uint16_t* __restrict__ k_out,
                                                             uint16_t* __restrict__ v_out) {
-  constexpr int TPR = D / 8;
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int part = (int)(i % TPR);
-  const long long rh = i / TPR;
-  const int h = (int)(rh % c.heads), bs = 1 << shift;
-  const long long t = rh / c.heads;
-  if (t >= rows) return;
-  const int64_t slot = slots[t];
-  if (slot < 0 || slot >= ((int64_t)c.num_blocks << shift)) return;
-  const int off = (int)(slot & (bs - 1));
-  const size_t bh = (size_t)(slot >> shift) * c.heads + h;
-  const size_t out = ((size_t)t * c.heads + h) * D + 8 * part;
-  const float ks = c.k_scale[bh], vs = c.v_scale[bh];
-  const v2u kw = *reinterpret_cast<const v2u*>(c.k_codes + (bh * bs + off) * D + 8 * part);
-  const uint8_t* vp = c.v_codes + (bh * D + 8 * part) * bs + off;
-  float kf[8], vf[8];
+  constexpr int TPR = D / 8, W = 16 * 256 / D, PER = 256 / TPR;
+  __shared__ __attribute__((aligned(16))) uint16_t vt[W][D + 8];
+  const int tid = threadIdx.x, bs = 1 << shift, h = blockIdx.y;
+  const int64_t limit = (int64_t)c.num_blocks << shift;
+  const int row0 = blockIdx.x * W, part = tid % TPR;
+  auto block_head = [&](int64_t slot) { return (size_t)(slot >> shift) * c.heads + h; };
+  if (blockIdx.z == 0) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    kf[e] = ((float)(((e < 4 ? kw.x : kw.y) >> (8 * (e & 3))) & 0xFFu) - 128.0f) * ks;
-    vf[e] = ((float)vp[(size_t)e * bs] - 128.0f) * vs;
+    for (int p = 0; p < W / PER; ++p) {
+      const int t = row0 + tid / TPR + PER * p;
+      if (t >= rows) continue;
+      const int64_t slot = slots[t];
+      if (slot < 0 || slot >= limit) continue;
+      const size_t bh = block_head(slot);
+      const float s = c.k_scale[bh];
+      const v2u w = *reinterpret_cast<const v2u*>(c.k_codes + (bh * bs + (slot & (bs - 1))) * D + 8 * part);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = ((float)(((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 0xFFu) - 128.0f) * s;
+      *reinterpret_cast<v4u*>(k_out + ((size_t)t * c.heads + h) * D + 8 * part) =
+          v4u{pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]), pack2_bf16(x[4], x[5]), pack2_bf16(x[6], x[7])};
+    }
+    return;
   }
-  *reinterpret_cast<v4u*>(k_out + out) = v4u{pack2_bf16(kf[0], kf[1]), pack2_bf16(kf[2], kf[3]),
-                                             pack2_bf16(kf[4], kf[5]), pack2_bf16(kf[6], kf[7])};
-  *reinterpret_cast<v4u*>(v_out + out) = v4u{pack2_bf16(vf[0], vf[1]), pack2_bf16(vf[2], vf[3]),
-                                             pack2_bf16(vf[4], vf[5]), pack2_bf16(vf[6], vf[7])};
+  {
+    const int d = tid % D, i0 = 16 * (tid / D), t0 = row0 + i0;
+    const int64_t slot = t0 < rows ? slots[t0] : -1;
+    bool run = slot >= 0 && slot < limit && (slot & 15) == 0 && t0 + 16 <= rows;
+    if (run) {
+#pragma unroll
+      for (int i = 1; i < 16; ++i) run = run && slots[t0 + i] == slot + i;
+    }
+    if (run) {
+      const size_t bh = block_head(slot);
+      const float s = c.v_scale[bh];
+      const v4u w = *reinterpret_cast<const v4u*>(c.v_codes + (bh * D + d) * bs + (slot & (bs - 1)));
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        vt[i0 + i][d] = float_to_bf16_bits(((float)((ws[i >> 2] >> (8 * (i & 3))) & 0xFFu) - 128.0f) * s);
+    } else {
+      for (int i = 0; i < 16 && t0 + i < rows; ++i) {
+        const int64_t si = slots[t0 + i];
+        if (si < 0 || si >= limit) continue;
+        const size_t bh = block_head(si);
+        vt[i0 + i][d] = float_to_bf16_bits(
+            ((float)c.v_codes[(bh * D + d) * bs + (si & (bs - 1))] - 128.0f) * c.v_scale[bh]);
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < W / PER; ++p) {
+    const int i = tid / TPR + PER * p, t = row0 + i;
+    if (t >= rows) continue;
+    const int64_t slot = slots[t];
+    if (slot < 0 || slot >= limit) continue;
+    *reinterpret_cast<v4u*>(v_out + ((size_t)t * c.heads + h) * D + 8 * part) =
+        *reinterpret_cast<const v4u*>(&vt[i][8 * part]);
+  }
 }
 
 hipError_t launch_kv_block_read(const int64_t* slots, int rows, const BlockCacheView& c,
                                 uint16_t* k_out, uint16_t* v_out, hipStream_t stream) {
-  const long long threads = (long long)rows * c.heads * (c.dim / 8);
-  const long long grid = (threads + 255) / 256;
-  if (grid > 0x7FFFFFFFLL) return hipErrorInvalidConfiguration;
+  const int window = 16 * 256 / c.dim;
+  const dim3 grid((rows + window - 1) / window, c.heads, 2);
   const int shift = __builtin_ctz(c.bs);
   if (c.dim == 128)
-    hipLaunchKernelGGL(kv_block_read_kernel<128>, dim3((unsigned)grid), dim3(256), 0, stream,
-                       slots, rows, shift, c, k_out, v_out);
+    hipLaunchKernelGGL(kv_block_read_kernel<128>, grid, dim3(256), 0, stream, slots, rows, shift, c,
+                       k_out, v_out);
   else
-    hipLaunchKernelGGL(kv_block_read_kernel<64>, dim3((unsigned)grid), dim3(256), 0, stream,
-                       slots, rows, shift, c, k_out, v_out);
+    hipLaunchKernelGGL(kv_block_read_kernel<64>, grid, dim3(256), 0, stream, slots, rows, shift, c,
+                       k_out, v_out);
   return hipGetLastError();
 }
 
