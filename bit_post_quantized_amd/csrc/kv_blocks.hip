@@ -219,13 +219,34 @@ constexpr int kAppendThreads = 256;
 constexpr int kShort = 4;
 constexpr int kMaxBlock = 128;  // tokens
 
-__host__ __device__ inline int append_window(int bs) { return bs < 32 ? 16 : 32; }
+// Rows of a window: a block's worth (at most 64) where that makes enough workgroups, so that a
+// prompt's window begins a run; less for few rows, where a window's short runs would queue up.
+inline int append_window(int rows, int heads, int bs) {
+  int w = bs < 64 ? bs : 64;
+  while (w > 16 && (long long)(rows / w) * heads * 2 < 2048) w /= 2;
+  return w;
+}
 
-// One value -> code + 128, for s != 0 and rcp = fl32(1 / s).  The correction-step quotient needs a
-// normal reciprocal; below 2^-100 the division itself is used.
-__device__ __forceinline__ float kv_code(float x, float s, float rcp) {
-  const float t = s >= 0x1p-100f ? rne_quotient(x, s, rcp) : __builtin_rintf(x / s);
-  return __builtin_amdgcn_fmed3f(t, -127.0f, 127.0f) + 128.0f;
+// What turns a value into a code + 128 under the block scale s: the correctly rounded quotient
+// (div_rn) plus 1.5 2^23 + 128, whose low byte is then the code to the nearest even.  |x / s| is at
+// most 127 (1 + 2^-23), so no code needs a clamp.  The correction step needs a normal reciprocal,
+// so a scale below 2^-80 and its values are taken 2^64 times larger (exact, the quotient is the
+// same).  s = 0: every value of the block is 0, and so is every quotient by 1.
+struct Coder {
+  float s, rcp;
+  bool tiny;
+};
+
+__device__ __forceinline__ Coder coder_of(float s) {
+  Coder k;
+  k.tiny = s < 0x1p-80f;
+  k.s = s == 0.0f ? 1.0f : k.tiny ? s * 0x1p64f : s;
+  k.rcp = 1.0f / k.s;
+  return k;
+}
+
+__device__ __forceinline__ uint32_t kv_code_bits(float x, Coder k) {
+  return __float_as_uint(div_rn(x, k.s, k.rcp) + 12583040.0f);
 }
 
 // Eight bf16 of a 16-byte load as fp32.
@@ -246,18 +267,23 @@ __device__ __forceinline__ float amax8(v4u w, float amax) {
   return amax;
 }
 
-// Codes of one row's 8 channels (byte e: channel e).  zero: the block's scale is 0.
-__device__ __forceinline__ v2u codes8(v4u w, float s, float rcp, bool zero) {
+// Codes of one row's 8 channels (byte e: channel e).
+__device__ __forceinline__ v2u codes8(v4u w, Coder k) {
   float x[8];
   bf16x8(w, x);
-  v2u c = {0u, 0u};
+  if (k.tiny)
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float q = zero ? 128.0f : kv_code(x[e], s, rcp);
-    if (e < 4) c.x = __builtin_amdgcn_cvt_pk_u8_f32(q, e, c.x);
-    else c.y = __builtin_amdgcn_cvt_pk_u8_f32(q, e - 4, c.y);
-  }
-  return c;
+    for (int e = 0; e < 8; ++e) x[e] *= 0x1p64f;
+  uint32_t b[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) b[e] = kv_code_bits(x[e], k);
+  // the low bytes of four words -> one dword
+  auto low4 = [](const uint32_t* v) {
+    const uint32_t lo = __builtin_amdgcn_perm(v[1], v[0], 0x0C0C0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(v[3], v[2], 0x04000C0Cu);
+    return lo | hi;
+  };
+  return v2u{low4(b), low4(b + 4)};
 }
 
 // The first `n` bytes of a dword of codes under a grown scale; the others as they are.
@@ -272,35 +298,41 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio, int n) {
   return (r & ~keep) | (w & keep);
 }
 
-template <int D>
+// STEPS: of 4 rows per group of lanes, for the longest run.
+template <int D, int STEPS>
 __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
     const uint16_t* __restrict__ kx, const uint16_t* __restrict__ vx, int64_t k_stride,
-    int64_t v_stride, const int64_t* __restrict__ slots, int rows, int shift, BlockCacheView c) {
+    int64_t v_stride, const int64_t* __restrict__ slots, int rows, int shift, int window,
+    BlockCacheView c) {
   constexpr int TPR = D / 8;                       // lanes per row, 8 channels each
   constexpr int GROUPS = kAppendThreads / TPR;
-  constexpr int STEPS = kMaxBlock / 4 / GROUPS;    // of 4 rows per group, for the longest run
-  constexpr int PITCH = kMaxBlock + 4;             // of a channel's tokens in LDS, bytes
+  constexpr int PITCH = 4 * GROUPS * STEPS + 4;    // of a channel's tokens in LDS, bytes
   __shared__ float wmax[kAppendThreads / 64];
   __shared__ __attribute__((aligned(16))) uint8_t vt[D * PITCH];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int h = blockIdx.y, is_v = blockIdx.z, bs = 1 << shift;
+  // head fastest: the workgroups that run together read whole rows between them
+  const int h = blockIdx.x % c.heads, is_v = blockIdx.x / c.heads & 1, bs = 1 << shift;
   const int part = tid % TPR, group = tid / TPR;
   const int64_t stride = is_v ? v_stride : k_stride;
   const uint16_t* x = (is_v ? vx : kx) + (size_t)h * D + 8 * part;
   uint8_t* const cache = is_v ? c.v_codes : c.k_codes;
   float* const scales = is_v ? c.v_scale : c.k_scale;
   const int64_t limit = (int64_t)c.num_blocks << shift;
-  const int window = append_window(bs), row0 = blockIdx.x * window;
+  const int row0 = (int)(blockIdx.x / c.heads >> 1) * window;
 
   // rows row0 + 0 .. 191: where a run (or a row without a token) begins
   uint64_t brk[3], lead = 0;
+  int64_t first64 = -1;  // slot of row row0 + lane
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-    const int t = row0 + 64 * q + lane;
-    const int64_t s = t < rows ? slots[t] : -1, before = t > 0 && t < rows ? slots[t - 1] : -2;
-    const bool valid = s >= 0 && s < limit;
-    brk[q] = __ballot(!valid || (s & (bs - 1)) == 0 || before != s - 1);
-    if (q == 0) lead = __ballot(valid && lane < window) & brk[0];
+    const int t = row0 + 64 * q + lane, at = min(t, rows - 1);
+    const int64_t s = slots[at], before = slots[max(at - 1, 0)];
+    const bool valid = t < rows && s >= 0 && s < limit;
+    brk[q] = __ballot(!valid || (s & (bs - 1)) == 0 || at == 0 || before != s - 1);
+    if (q == 0) {
+      lead = __ballot(valid && lane < window) & brk[0];
+      first64 = s;
+    }
   }
   auto length = [&](int i) {  // rows of the run that begins at row0 + i
     const uint64_t m = i < 63 ? brk[0] >> (i + 1) : 0;
@@ -317,7 +349,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
   // ---- long runs, the whole workgroup
   for (uint64_t m = lead & ~shorts; m; m &= m - 1) {
     const int i0 = __builtin_ctzll(m), n = length(i0), t = row0 + i0;
-    const int64_t slot = slots[t];
+    const int64_t slot = __shfl(first64, i0);
     const int off = (int)(slot & (bs - 1));
     const size_t bh = (size_t)(slot >> shift) * c.heads + h;
     uint8_t* codes = cache + bh * bs * D;
@@ -343,8 +375,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
 #pragma unroll
     for (int q = 0; q < kAppendThreads / 64; ++q) amax = __builtin_fmaxf(amax, wmax[q]);
     const float s = __builtin_fmaxf(old, amax / 127.0f);
-    const bool zero = s == 0.0f;
-    const float s1 = zero ? 1.0f : s, rcp = 1.0f / s1;
+    const Coder coder = coder_of(s);
     if (tid == 0) scales[bh] = s;
     if (off > 0 && s > old) {
       const float ratio = old / s;
@@ -367,7 +398,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
       if (i >= n) continue;
       v2u q[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) q[r] = codes8(w[p][r], s1, rcp, zero);
+      for (int r = 0; r < 4; ++r) q[r] = codes8(w[p][r], coder);
       if (!is_v) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
@@ -424,8 +455,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
 #pragma unroll
     for (int o = 1; o < TPR; o <<= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o));
     const float s = __builtin_fmaxf(old, amax / 127.0f);
-    const bool zero = s == 0.0f;
-    const float s1 = zero ? 1.0f : s, rcp = 1.0f / s1;
+    const Coder coder = coder_of(s);
     if (part == 0) scales[bh] = s;  // (the group's lanes have read it: they are one wave's)
     const bool grew = off > 0 && s > old;
     const float ratio = grew ? old / s : 1.0f;
@@ -438,7 +468,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
         }
 #pragma unroll
       for (int r = 0; r < kShort; ++r)
-        if (r < n) *reinterpret_cast<v2u*>(codes + (size_t)(off + r) * D + 8 * part) = codes8(w[r], s1, rcp, zero);
+        if (r < n) *reinterpret_cast<v2u*>(codes + (size_t)(off + r) * D + 8 * part) = codes8(w[r], coder);
     } else {
       if (grew)
         for (int i = 0; i < off; i += 4)
@@ -450,7 +480,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
 #pragma unroll
       for (int r = 0; r < kShort; ++r)
         if (r < n) {
-          const v2u q = codes8(w[r], s1, rcp, zero);
+          const v2u q = codes8(w[r], coder);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             codes[(size_t)(8 * part + e) * bs + off + r] = (uint8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
@@ -462,101 +492,139 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
 hipError_t launch_kv_block_append(const uint16_t* k, const uint16_t* v, int64_t k_stride,
                                   int64_t v_stride, const int64_t* slots, int rows,
                                   const BlockCacheView& c, hipStream_t stream) {
-  const int window = append_window(c.bs);
-  const dim3 grid((rows + window - 1) / window, c.heads, 2);
+  const int window = append_window(rows, c.heads, c.bs);
+  const long long n = (long long)((rows + window - 1) / window) * c.heads * 2;
+  if (n > 0x7FFFFFFFLL) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)n);
   const int shift = __builtin_ctz(c.bs);
-  if (c.dim == 128)
-    hipLaunchKernelGGL(kv_block_append_kernel<128>, grid, dim3(kAppendThreads), 0, stream, k, v,
-                       k_stride, v_stride, slots, rows, shift, c);
-  else
-    hipLaunchKernelGGL(kv_block_append_kernel<64>, grid, dim3(kAppendThreads), 0, stream, k, v,
-                       k_stride, v_stride, slots, rows, shift, c);
+#define SVDQ_APPEND(D, STEPS)                                                                       \
+  hipLaunchKernelGGL((kv_block_append_kernel<D, STEPS>), grid, dim3(kAppendThreads), 0, stream, k, v, \
+                     k_stride, v_stride, slots, rows, shift, window, c)
+  if (c.dim == 64) SVDQ_APPEND(64, 1);
+  else if (c.bs <= 64) SVDQ_APPEND(128, 1);
+  else SVDQ_APPEND(128, 2);
+#undef SVDQ_APPEND
   return hipGetLastError();
 }
 
 // -------------------------------------------------------------------------------------- read
-// One workgroup per (window of 16 * 256 / D rows, head, K or V).  K: a thread per 8 channels of a
-// row.  V: a thread per channel and 16 rows; where these are 16 consecutive slots at a multiple of
-// 16 their codes are one 16-byte load, otherwise a byte per row; the values go through LDS to
-// become rows of channels.
+// One workgroup per (window of 64 rows, head, K or V), head fastest, so that the workgroups that run
+// together write whole rows between them.  K: a thread per 8 channels of a row.  V: a thread per
+// channel and 16 rows at a time; where these are 16 slots in a row from a multiple of 16 on, save
+// those without a token, their codes are one 16-byte load, otherwise a byte per row; the values go
+// through LDS to become rows of channels.
+constexpr int kReadRows = 64;
+
 template <int D>
 __global__ __launch_bounds__(256) void kv_block_read_kernel(const int64_t* __restrict__ slots,
                                                             int rows, int shift, BlockCacheView c,
                                                             uint16_t* __restrict__ k_out,
                                                             uint16_t* __restrict__ v_out) {
-  constexpr int TPR = D / 8, W = 16 * 256 / D, PER = 256 / TPR;
+  constexpr int TPR = D / 8, W = kReadRows, PER = 256 / TPR;
   __shared__ __attribute__((aligned(16))) uint16_t vt[W][D + 8];
-  const int tid = threadIdx.x, bs = 1 << shift, h = blockIdx.y;
+  const int tid = threadIdx.x, bs = 1 << shift;
+  const int h = blockIdx.x % c.heads, is_v = blockIdx.x / c.heads & 1;
+  const int window = blockIdx.x / c.heads >> 1;
   const int64_t limit = (int64_t)c.num_blocks << shift;
-  const int row0 = blockIdx.x * W, part = tid % TPR;
+  const int row0 = window * W, part = tid % TPR, lane = tid & 63;
   auto block_head = [&](int64_t slot) { return (size_t)(slot >> shift) * c.heads + h; };
-  if (blockIdx.z == 0) {
+  // Every wave holds the window's 64 slots, a row to a lane, and which rows have a token.
+  const int64_t slot = slots[min(row0 + lane, rows - 1)];
+  const uint64_t live = __ballot(row0 + lane < rows && slot >= 0 && slot < limit);
+  // (c - 128) s in one rounding: 128 s is exact
+  if (!is_v) {
+    v2u w[W / PER];
+    float s[W / PER];
+#pragma unroll
+    for (int p = 0; p < W / PER; ++p) {  // (rows without a token read slot 0's)
+      const int i = tid / TPR + PER * p;
+      const int64_t si = __shfl(slot, i), at = live >> i & 1 ? si : 0;
+      const size_t bh = block_head(at);
+      s[p] = c.k_scale[bh];
+      w[p] = *reinterpret_cast<const v2u*>(c.k_codes + (bh * bs + (at & (bs - 1))) * D + 8 * part);
+    }
 #pragma unroll
     for (int p = 0; p < W / PER; ++p) {
-      const int t = row0 + tid / TPR + PER * p;
-      if (t >= rows) continue;
-      const int64_t slot = slots[t];
-      if (slot < 0 || slot >= limit) continue;
-      const size_t bh = block_head(slot);
-      const float s = c.k_scale[bh];
-      const v2u w = *reinterpret_cast<const v2u*>(c.k_codes + (bh * bs + (slot & (bs - 1))) * D + 8 * part);
+      const int i = tid / TPR + PER * p;
+      if (!(live >> i & 1)) continue;
       float x[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = ((float)(((e < 4 ? w.x : w.y) >> (8 * (e & 3))) & 0xFFu) - 128.0f) * s;
-      *reinterpret_cast<v4u*>(k_out + ((size_t)t * c.heads + h) * D + 8 * part) =
-          v4u{pack2_bf16(x[0], x[1]), pack2_bf16(x[2], x[3]), pack2_bf16(x[4], x[5]), pack2_bf16(x[6], x[7])};
+      for (int e = 0; e < 8; ++e)
+        x[e] = __builtin_fmaf((float)(((e < 4 ? w[p].x : w[p].y) >> (8 * (e & 3))) & 0xFFu), s[p], -128.0f * s[p]);
+      *reinterpret_cast<v8bf*>(k_out + ((size_t)(row0 + i) * c.heads + h) * D + 8 * part) = to_bf16x8(x);
     }
     return;
   }
-  {
-    const int d = tid % D, i0 = 16 * (tid / D), t0 = row0 + i0;
-    const int64_t slot = t0 < rows ? slots[t0] : -1;
-    bool run = slot >= 0 && slot < limit && (slot & 15) == 0 && t0 + 16 <= rows;
-    if (run) {
+  // where row i - (i mod 16) would be if a lane's 16 rows ran on from it, against the first's
+  const int here = (int)(live >> (lane & 48)) & 0xFFFF;
+  const int64_t base = slot - (lane & 15), lead = __shfl(base, (lane & 48) + (here ? __builtin_ctz(here) : 0));
+  const uint64_t odd = __ballot((live >> lane & 1) && (base != lead || (base & 15) != 0));
+  constexpr int PARTS = W * D / (16 * 256);  // 16-row parts of the window to a thread
+  const int d = tid % D;
+  v4u w[PARTS];
+  float s[PARTS];
 #pragma unroll
-      for (int i = 1; i < 16; ++i) run = run && slots[t0 + i] == slot + i;
-    }
-    if (run) {
-      const size_t bh = block_head(slot);
-      const float s = c.v_scale[bh];
-      const v4u w = *reinterpret_cast<const v4u*>(c.v_codes + (bh * D + d) * bs + (slot & (bs - 1)));
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  for (int q = 0; q < PARTS; ++q) {
+    const int i0 = __builtin_amdgcn_readfirstlane(16 * (tid / D + 256 / D * q));
+    const int64_t first = __shfl(lead, i0);
+    const bool run = (live >> i0 & 0xFFFF) && !(odd >> i0 & 0xFFFF);
+    const int64_t at = run ? first : 0;
+    const size_t bh = block_head(at);
+    s[q] = c.v_scale[bh];
+    w[q] = *reinterpret_cast<const v4u*>(c.v_codes + (bh * D + d) * bs + (at & (bs - 1)));
+  }
+#pragma unroll
+  for (int q = 0; q < PARTS; ++q) {
+    const int i0 = __builtin_amdgcn_readfirstlane(16 * (tid / D + 256 / D * q));
+    float x[16];
+    if (!(odd >> i0 & 0xFFFF)) {
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        vt[i0 + i][d] = float_to_bf16_bits(((float)((ws[i >> 2] >> (8 * (i & 3))) & 0xFFu) - 128.0f) * s);
+        x[i] = __builtin_fmaf((float)((w[q][i >> 2] >> (8 * (i & 3))) & 0xFFu), s[q], -128.0f * s[q]);
     } else {
-      for (int i = 0; i < 16 && t0 + i < rows; ++i) {
-        const int64_t si = slots[t0 + i];
-        if (si < 0 || si >= limit) continue;
-        const size_t bh = block_head(si);
-        vt[i0 + i][d] = float_to_bf16_bits(
-            ((float)c.v_codes[(bh * D + d) * bs + (si & (bs - 1))] - 128.0f) * c.v_scale[bh]);
+      uint8_t b[16];
+      float t[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int64_t si = __shfl(slot, i0 + i), at = live >> (i0 + i) & 1 ? si : 0;
+        const size_t bh = block_head(at);
+        b[i] = c.v_codes[(bh * D + d) * bs + (at & (bs - 1))];
+        t[i] = c.v_scale[bh];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf((float)b[i], t[i], -128.0f * t[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; i += 8) {
+      const v4u u = __builtin_bit_cast(v4u, to_bf16x8(x + i));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        vt[i0 + i + 2 * e][d] = (uint16_t)u[e];
+        vt[i0 + i + 2 * e + 1][d] = (uint16_t)(u[e] >> 16);
       }
     }
   }
   __syncthreads();
 #pragma unroll
   for (int p = 0; p < W / PER; ++p) {
-    const int i = tid / TPR + PER * p, t = row0 + i;
-    if (t >= rows) continue;
-    const int64_t slot = slots[t];
-    if (slot < 0 || slot >= limit) continue;
-    *reinterpret_cast<v4u*>(v_out + ((size_t)t * c.heads + h) * D + 8 * part) =
-        *reinterpret_cast<const v4u*>(&vt[i][8 * part]);
+    const int i = tid / TPR + PER * p;
+    if (live >> i & 1)
+      *reinterpret_cast<v4u*>(v_out + ((size_t)(row0 + i) * c.heads + h) * D + 8 * part) =
+          *reinterpret_cast<const v4u*>(&vt[i][8 * part]);
   }
 }
 
 hipError_t launch_kv_block_read(const int64_t* slots, int rows, const BlockCacheView& c,
                                 uint16_t* k_out, uint16_t* v_out, hipStream_t stream) {
-  const int window = 16 * 256 / c.dim;
-  const dim3 grid((rows + window - 1) / window, c.heads, 2);
+  const long long grid = (long long)((rows + kReadRows - 1) / kReadRows) * c.heads * 2;
+  if (grid > 0x7FFFFFFFLL) return hipErrorInvalidConfiguration;
   const int shift = __builtin_ctz(c.bs);
   if (c.dim == 128)
-    hipLaunchKernelGGL(kv_block_read_kernel<128>, grid, dim3(256), 0, stream, slots, rows, shift, c,
-                       k_out, v_out);
+    hipLaunchKernelGGL(kv_block_read_kernel<128>, dim3((unsigned)grid), dim3(256), 0, stream,
+                       slots, rows, shift, c, k_out, v_out);
   else
-    hipLaunchKernelGGL(kv_block_read_kernel<64>, grid, dim3(256), 0, stream, slots, rows, shift, c,
-                       k_out, v_out);
+    hipLaunchKernelGGL(kv_block_read_kernel<64>, dim3((unsigned)grid), dim3(256), 0, stream, slots,
+                       rows, shift, c, k_out, v_out);
   return hipGetLastError();
 }
 
