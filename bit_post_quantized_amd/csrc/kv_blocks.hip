@@ -207,14 +207,17 @@ hipError_t launch_kv_block_release(const int32_t* seq, const uint8_t* done, int 
 // ------------------------------------------------------------------------------------ append
 // A run is the rows of one block: it begins at a row whose predecessor is not the slot before it,
 // or at a block's first slot, and goes on while the slots ascend inside the block.  One workgroup
-// per (window of rows, head, K or V) writes the runs that begin in its window.  Every wave finds
-// them by itself: a lane looks at one row, and the rows where a run breaks are three 64-bit masks.
+// per (window of rows, head) writes the runs that begin in its window, K's and V's rows together.
+// Every wave finds them by itself: a lane looks at one row, and the rows where a run breaks are
+// three 64-bit masks.
 //  - Short runs (up to kShort rows: decoding) go to groups of D / 8 lanes, one run to a group, all
 //    at once.
 //  - A long run (a prompt's block) takes the whole workgroup: its rows are read once, 8 channels
 //    and 4 consecutive rows to a thread and step, all loads before the largest magnitude is known;
 //    K's codes are stored as they are, V's go through LDS to become rows of tokens.
-// The append of 20000 rows moves 123 MB (2 bytes in and 1 out for K and V) and is bound by that.
+// 20000 rows of 8 x 128 (82 MB in, 41 MB out) take 28 us, 4.4 TB/s: the loads alone 21 (4 TB/s),
+// the coding 2 of the rest.  Measured: plain stores 31 us; K and V in workgroups of their own
+// the same; coding with a clamp and float conversions 45.
 constexpr int kAppendThreads = 256;
 constexpr int kShort = 4;
 constexpr int kMaxBlock = 128;  // tokens
@@ -223,7 +226,7 @@ constexpr int kMaxBlock = 128;  // tokens
 // prompt's window begins a run; less for few rows, where a window's short runs would queue up.
 inline int append_window(int rows, int heads, int bs) {
   int w = bs < 64 ? bs : 64;
-  while (w > 16 && (long long)(rows / w) * heads * 2 < 2048) w /= 2;
+  while (w > 16 && (long long)(rows / w) * heads < 1024) w /= 2;
   return w;
 }
 
@@ -259,12 +262,24 @@ __device__ __forceinline__ void bf16x8(v4u w, float* x) {
   }
 }
 
-__device__ __forceinline__ float amax8(v4u w, float amax) {
-  float x[8];
-  bf16x8(w, x);
+// Largest magnitudes as bf16 bits without the sign, two to a dword (they order like integers).
+typedef uint16_t v2s __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(v2s, a), __builtin_bit_cast(v2s, b)));
+}
+
+__device__ __forceinline__ uint32_t amax8(v4u w, uint32_t amax) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) amax = __builtin_fmaxf(amax, __builtin_fabsf(x[e]));
+  for (int e = 0; e < 4; ++e) amax = pk_max(amax, w[e] & 0x7FFF7FFFu);
   return amax;
+}
+
+// ... over the lanes that differ in the bits below `lanes`, as fp32 in every one of them.
+__device__ __forceinline__ float amax_lanes(uint32_t amax, int lanes) {
+  amax = pk_max(amax, amax >> 16);
+  for (int o = 1; o < lanes; o <<= 1) amax = pk_max(amax, __shfl_xor(amax, o));
+  return __uint_as_float(amax << 16);
 }
 
 // Codes of one row's 8 channels (byte e: channel e).
@@ -298,6 +313,18 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio, int n) {
   return (r & ~keep) | (w & keep);
 }
 
+// The codes of a block's first `off` tokens under a grown scale: K's rows or V's rows of tokens, the
+// dwords i, i + step, ... of them.
+template <int D, bool V>
+__device__ __forceinline__ void rescale_block(uint8_t* codes, int bs, int off, float ratio, int i, int step) {
+  const int dw = (off + 3) / 4;  // V: dwords of a channel's earlier tokens
+  for (; i < (V ? D * dw : off * D / 4); i += step) {
+    uint32_t* p = V ? reinterpret_cast<uint32_t*>(codes + (size_t)(i / dw) * bs) + i % dw
+                    : reinterpret_cast<uint32_t*>(codes) + i;
+    *p = rescale4(*p, ratio, V ? off - 4 * (i % dw) : 4);
+  }
+}
+
 // STEPS: of 4 rows per group of lanes, for the longest run.
 template <int D, int STEPS>
 __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
@@ -307,18 +334,16 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
   constexpr int TPR = D / 8;                       // lanes per row, 8 channels each
   constexpr int GROUPS = kAppendThreads / TPR;
   constexpr int PITCH = 4 * GROUPS * STEPS + 4;    // of a channel's tokens in LDS, bytes
-  __shared__ float wmax[kAppendThreads / 64];
+  __shared__ float wmax[2][kAppendThreads / 64];
   __shared__ __attribute__((aligned(16))) uint8_t vt[D * PITCH];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   // head fastest: the workgroups that run together read whole rows between them
-  const int h = blockIdx.x % c.heads, is_v = blockIdx.x / c.heads & 1, bs = 1 << shift;
+  const int h = blockIdx.x % c.heads, bs = 1 << shift;
   const int part = tid % TPR, group = tid / TPR;
-  const int64_t stride = is_v ? v_stride : k_stride;
-  const uint16_t* x = (is_v ? vx : kx) + (size_t)h * D + 8 * part;
-  uint8_t* const cache = is_v ? c.v_codes : c.k_codes;
-  float* const scales = is_v ? c.v_scale : c.k_scale;
+  kx += (size_t)h * D + 8 * part;
+  vx += (size_t)h * D + 8 * part;
   const int64_t limit = (int64_t)c.num_blocks << shift;
-  const int row0 = (int)(blockIdx.x / c.heads >> 1) * window;
+  const int row0 = (int)(blockIdx.x / c.heads) * window;
 
   // rows row0 + 0 .. 191: where a run (or a row without a token) begins
   uint64_t brk[3], lead = 0;
@@ -352,85 +377,81 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
     const int64_t slot = __shfl(first64, i0);
     const int off = (int)(slot & (bs - 1));
     const size_t bh = (size_t)(slot >> shift) * c.heads + h;
-    uint8_t* codes = cache + bh * bs * D;
-    v4u w[STEPS][4];
-    float amax = 0.0f;
+    uint8_t* const kc = c.k_codes + bh * bs * D;
+    uint8_t* const vc = c.v_codes + bh * bs * D;
+    v4u wk[STEPS][4], wv[STEPS][4];
 #pragma unroll
     for (int p = 0; p < STEPS; ++p)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int i = 4 * (group + GROUPS * p) + r;  // (rows past the run read its last one)
-        if (4 * GROUPS * p < n) w[p][r] = *reinterpret_cast<const v4u*>(x + (size_t)(t + min(i, n - 1)) * stride);
+        // (rows past the run read its last one)
+        const size_t at = (size_t)(t + min(4 * (group + GROUPS * p) + r, n - 1));
+        wk[p][r] = *reinterpret_cast<const v4u*>(kx + at * k_stride);
+        wv[p][r] = *reinterpret_cast<const v4u*>(vx + at * v_stride);
       }
-    const float old = off == 0 ? 0.0f : scales[bh];
+    const float k_old = off == 0 ? 0.0f : c.k_scale[bh], v_old = off == 0 ? 0.0f : c.v_scale[bh];
+    uint32_t k_top = 0, v_top = 0;
 #pragma unroll
     for (int p = 0; p < STEPS; ++p)
-      if (4 * GROUPS * p < n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) amax = amax8(w[p][r], amax);
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o));
-    if (lane == 0) wmax[wave] = amax;
-    __syncthreads();  // (also: every thread has read the old scale)
-#pragma unroll
-    for (int q = 0; q < kAppendThreads / 64; ++q) amax = __builtin_fmaxf(amax, wmax[q]);
-    const float s = __builtin_fmaxf(old, amax / 127.0f);
-    const Coder coder = coder_of(s);
-    if (tid == 0) scales[bh] = s;
-    if (off > 0 && s > old) {
-      const float ratio = old / s;
-      if (is_v) {
-        const int dw = (off + 3) / 4;  // dwords of a channel's earlier tokens
-        for (int i = tid; i < D * dw; i += kAppendThreads) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(codes + (size_t)(i / dw) * bs) + i % dw;
-          *p = rescale4(*p, ratio, off - 4 * (i % dw));
-        }
-      } else {
-        for (int i = tid; i < off * D / 4; i += kAppendThreads) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(codes) + i;
-          *p = rescale4(*p, ratio, 4);
-        }
+      for (int r = 0; r < 4; ++r) {
+        k_top = amax8(wk[p][r], k_top);
+        v_top = amax8(wv[p][r], v_top);
       }
+    float ka = amax_lanes(k_top, 64), va = amax_lanes(v_top, 64);
+    if (lane == 0) {
+      wmax[0][wave] = ka;
+      wmax[1][wave] = va;
     }
+    __syncthreads();  // (also: every thread has read the old scales)
+#pragma unroll
+    for (int q = 0; q < kAppendThreads / 64; ++q) {
+      ka = __builtin_fmaxf(ka, wmax[0][q]);
+      va = __builtin_fmaxf(va, wmax[1][q]);
+    }
+    const float ks = __builtin_fmaxf(k_old, ka / 127.0f), vs = __builtin_fmaxf(v_old, va / 127.0f);
+    const Coder kk = coder_of(ks), vk = coder_of(vs);
+    if (tid == 0) {
+      c.k_scale[bh] = ks;
+      c.v_scale[bh] = vs;
+    }
+    if (off > 0 && ks > k_old) rescale_block<D, false>(kc, bs, off, k_old / ks, tid, kAppendThreads);
+    if (off > 0 && vs > v_old) rescale_block<D, true>(vc, bs, off, v_old / vs, tid, kAppendThreads);
 #pragma unroll
     for (int p = 0; p < STEPS; ++p) {
       const int i = 4 * (group + GROUPS * p);
       if (i >= n) continue;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const v2u q = codes8(wk[p][r], kk);
+        if (i + r < n) __builtin_nontemporal_store(q, reinterpret_cast<v2u*>(kc + (size_t)(off + i + r) * D + 8 * part));
+      }
+      // four tokens of each of 8 channels as a dword: bytes e of q[0..3]
       v2u q[4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) q[r] = codes8(w[p][r], coder);
-      if (!is_v) {
+      for (int r = 0; r < 4; ++r) q[r] = codes8(wv[p][r], vk);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (i + r < n) *reinterpret_cast<v2u*>(codes + (size_t)(off + i + r) * D + 8 * part) = q[r];
-      } else {
-        // four tokens of each of 8 channels as a dword: bytes e of q[0..3]
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t sel = 0x0C0C0400u + 0x0101u * (e & 3);
-          const uint32_t a = e < 4 ? q[0].x : q[0].y, b = e < 4 ? q[1].x : q[1].y;
-          const uint32_t d = e < 4 ? q[2].x : q[2].y, f = e < 4 ? q[3].x : q[3].y;
-          const uint32_t lo = __builtin_amdgcn_perm(b, a, sel), hi = __builtin_amdgcn_perm(f, d, sel);
-          *reinterpret_cast<uint32_t*>(&vt[(8 * part + e) * PITCH + i]) = lo | (hi << 16);
-        }
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t lo_sel = 0x0C0C0400u + 0x0101u * (e & 3), hi_sel = 0x04000C0Cu + 0x01010000u * (e & 3);
+        const uint32_t lo = e < 4 ? __builtin_amdgcn_perm(q[1].x, q[0].x, lo_sel) : __builtin_amdgcn_perm(q[1].y, q[0].y, lo_sel);
+        const uint32_t hi = e < 4 ? __builtin_amdgcn_perm(q[3].x, q[2].x, hi_sel) : __builtin_amdgcn_perm(q[3].y, q[2].y, hi_sel);
+        *reinterpret_cast<uint32_t*>(&vt[(8 * part + e) * PITCH + i]) = lo | hi;
       }
     }
-    if (is_v) {
-      __syncthreads();  // (the earlier tokens' rescaled dwords are written before bytes beside them)
-      // rows of tokens to the block: 16 bytes at a time where a chunk is whole and in step with
-      // LDS (off a multiple of 4), else its bytes
-      const int c0 = off >> 4, c1 = (off + n + 15) >> 4, nc = c1 - c0;
-      for (int i = tid; i < D * nc; i += kAppendThreads) {
-        const int d = i / nc, ch = c0 + i % nc;
-        const int lo = max(off, 16 * ch), hi = min(off + n, 16 * ch + 16);
-        const uint8_t* from = &vt[d * PITCH + lo - off];
-        uint8_t* to = codes + (size_t)d * bs + lo;
-        if (hi - lo == 16 && (off & 3) == 0) {
-          const uint32_t* f4 = reinterpret_cast<const uint32_t*>(from);
-          *reinterpret_cast<v4u*>(to) = v4u{f4[0], f4[1], f4[2], f4[3]};
-        } else {
-          for (int b = 0; b < hi - lo; ++b) to[b] = from[b];
-        }
+    __syncthreads();  // (the earlier tokens' rescaled dwords are written before bytes beside them)
+    // V's rows of tokens to the block: 16 bytes at a time where a chunk is whole and in step with
+    // LDS (off a multiple of 4), else its bytes
+    const int c0 = off >> 4, c1 = (off + n + 15) >> 4, nc = c1 - c0;
+    for (int i = tid; i < D * nc; i += kAppendThreads) {
+      const int d = i / nc, ch = c0 + i % nc;
+      const int lo = max(off, 16 * ch), hi = min(off + n, 16 * ch + 16);
+      const uint8_t* from = &vt[d * PITCH + lo - off];
+      uint8_t* to = vc + (size_t)d * bs + lo;
+      if (hi - lo == 16 && (off & 3) == 0) {
+        const uint32_t* f4 = reinterpret_cast<const uint32_t*>(from);
+        __builtin_nontemporal_store(v4u{f4[0], f4[1], f4[2], f4[3]}, reinterpret_cast<v4u*>(to));
+      } else {
+        for (int b = 0; b < hi - lo; ++b) to[b] = from[b];
       }
     }
     __syncthreads();  // (wmax and vt before the next run)
@@ -444,48 +465,48 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
     const int64_t slot = slots[t];
     const int off = (int)(slot & (bs - 1));
     const size_t bh = (size_t)(slot >> shift) * c.heads + h;
-    uint8_t* codes = cache + bh * bs * D;
-    v4u w[kShort];
+    uint8_t* const kc = c.k_codes + bh * bs * D;
+    uint8_t* const vc = c.v_codes + bh * bs * D;
+    v4u wk[kShort], wv[kShort];
 #pragma unroll
-    for (int r = 0; r < kShort; ++r) w[r] = *reinterpret_cast<const v4u*>(x + (size_t)(t + min(r, n - 1)) * stride);
-    const float old = off == 0 ? 0.0f : scales[bh];
-    float amax = 0.0f;
+    for (int r = 0; r < kShort; ++r) {
+      wk[r] = *reinterpret_cast<const v4u*>(kx + (size_t)(t + min(r, n - 1)) * k_stride);
+      wv[r] = *reinterpret_cast<const v4u*>(vx + (size_t)(t + min(r, n - 1)) * v_stride);
+    }
+    const float k_old = off == 0 ? 0.0f : c.k_scale[bh], v_old = off == 0 ? 0.0f : c.v_scale[bh];
+    uint32_t k_top = 0, v_top = 0;
 #pragma unroll
-    for (int r = 0; r < kShort; ++r) amax = amax8(w[r], amax);
+    for (int r = 0; r < kShort; ++r) {
+      k_top = amax8(wk[r], k_top);
+      v_top = amax8(wv[r], v_top);
+    }
+    const float ks = __builtin_fmaxf(k_old, amax_lanes(k_top, TPR) / 127.0f);
+    const float vs = __builtin_fmaxf(v_old, amax_lanes(v_top, TPR) / 127.0f);
+    const Coder kk = coder_of(ks), vk = coder_of(vs);
+    if (part == 0) {  // (the group's lanes have read them: they are one wave's)
+      c.k_scale[bh] = ks;
+      c.v_scale[bh] = vs;
+    }
+    // (a lane rescales the dwords that it writes codes beside: its own channels' rows of V)
+    if (off > 0 && ks > k_old) rescale_block<D, false>(kc, bs, off, k_old / ks, part, TPR);
+    if (off > 0 && vs > v_old) {
+      const float ratio = v_old / vs;
+      for (int i = 0; i < off; i += 4)
 #pragma unroll
-    for (int o = 1; o < TPR; o <<= 1) amax = __builtin_fmaxf(amax, __shfl_xor(amax, o));
-    const float s = __builtin_fmaxf(old, amax / 127.0f);
-    const Coder coder = coder_of(s);
-    if (part == 0) scales[bh] = s;  // (the group's lanes have read it: they are one wave's)
-    const bool grew = off > 0 && s > old;
-    const float ratio = grew ? old / s : 1.0f;
-    if (!is_v) {
-      if (grew)
-        for (int i = 0; i < off; ++i) {
-          v2u* p = reinterpret_cast<v2u*>(codes + (size_t)i * D + 8 * part);
-          const v2u q = *p;
-          *p = v2u{rescale4(q.x, ratio, 4), rescale4(q.y, ratio, 4)};
-        }
-#pragma unroll
-      for (int r = 0; r < kShort; ++r)
-        if (r < n) *reinterpret_cast<v2u*>(codes + (size_t)(off + r) * D + 8 * part) = codes8(w[r], coder);
-    } else {
-      if (grew)
-        for (int i = 0; i < off; i += 4)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            uint32_t* p = reinterpret_cast<uint32_t*>(codes + (size_t)(8 * part + e) * bs + i);
-            *p = rescale4(*p, ratio, off - i);
-          }
-#pragma unroll
-      for (int r = 0; r < kShort; ++r)
-        if (r < n) {
-          const v2u q = codes8(w[r], coder);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            codes[(size_t)(8 * part + e) * bs + off + r] = (uint8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
+        for (int e = 0; e < 8; ++e) {
+          uint32_t* p = reinterpret_cast<uint32_t*>(vc + (size_t)(8 * part + e) * bs + i);
+          *p = rescale4(*p, ratio, off - i);
         }
     }
+#pragma unroll
+    for (int r = 0; r < kShort; ++r)
+      if (r < n) {
+        *reinterpret_cast<v2u*>(kc + (size_t)(off + r) * D + 8 * part) = codes8(wk[r], kk);
+        const v2u q = codes8(wv[r], vk);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          vc[(size_t)(8 * part + e) * bs + off + r] = (uint8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
+      }
   }
 }
 
@@ -493,7 +514,7 @@ hipError_t launch_kv_block_append(const uint16_t* k, const uint16_t* v, int64_t 
                                   int64_t v_stride, const int64_t* slots, int rows,
                                   const BlockCacheView& c, hipStream_t stream) {
   const int window = append_window(rows, c.heads, c.bs);
-  const long long n = (long long)((rows + window - 1) / window) * c.heads * 2;
+  const long long n = (long long)((rows + window - 1) / window) * c.heads;
   if (n > 0x7FFFFFFFLL) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)n);
   const int shift = __builtin_ctz(c.bs);
