@@ -215,9 +215,10 @@ hipError_t launch_kv_block_release(const int32_t* seq, const uint8_t* done, int 
 //  - A long run (a prompt's block) takes the whole workgroup: its rows are read once, 8 channels
 //    and 4 consecutive rows to a thread and step, all loads before the largest magnitude is known;
 //    K's codes are stored as they are, V's go through LDS to become rows of tokens.
-// 20000 rows of 8 x 128 (82 MB in, 41 MB out) take 28 us, 4.4 TB/s: the loads alone 21 (4 TB/s),
-// the coding 2 of the rest.  Measured: plain stores 31 us; K and V in workgroups of their own
-// the same; coding with a clamp and float conversions 45.
+// 20000 rows of 8 x 128 (82 MB in, 41 MB out) take 31 us, 4 TB/s: the loads alone 21, the coding 2
+// of the rest.  Measured: non-temporal stores 28 us, but the read of the codes that follows takes
+// 3 us longer; K and V in workgroups of their own the same; a clamp and float conversions in the
+// coding 45 us.
 constexpr int kAppendThreads = 256;
 constexpr int kShort = 4;
 constexpr int kMaxBlock = 128;  // tokens
@@ -424,7 +425,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const v2u q = codes8(wk[p][r], kk);
-        if (i + r < n) __builtin_nontemporal_store(q, reinterpret_cast<v2u*>(kc + (size_t)(off + i + r) * D + 8 * part));
+        if (i + r < n) *reinterpret_cast<v2u*>(kc + (size_t)(off + i + r) * D + 8 * part) = q;
       }
       // four tokens of each of 8 channels as a dword: bytes e of q[0..3]
       v2u q[4];
@@ -449,7 +450,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
       uint8_t* to = vc + (size_t)d * bs + lo;
       if (hi - lo == 16 && (off & 3) == 0) {
         const uint32_t* f4 = reinterpret_cast<const uint32_t*>(from);
-        __builtin_nontemporal_store(v4u{f4[0], f4[1], f4[2], f4[3]}, reinterpret_cast<v4u*>(to));
+        *reinterpret_cast<v4u*>(to) = v4u{f4[0], f4[1], f4[2], f4[3]};
       } else {
         for (int b = 0; b < hi - lo; ++b) to[b] = from[b];
       }
