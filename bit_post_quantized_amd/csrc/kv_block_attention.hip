@@ -4,17 +4,21 @@
 //
 // One pass over the codes with a running maximum and sum.  The query rows of one request that
 // share a cached head (rows x heads / kv_heads of them) fill the columns of the matrix
-// instructions, 16 to a tile; a wave takes 64 tokens at a time:
+// instructions, 16 to a tile, against 64 tokens at a time:
 //     S^T [64 tokens x 16 rows] = codes_K [64 x D] Q^T,     O^T [D x 16] += codes_V^T [D x 64] P^T
 // on v_mfma_f32_16x16x32_f16.  Codes are exact fp16; a query enters as its bf16 bits scaled by a
 // power of two per row, which fp16 holds exactly down to 2^-22 of the row's largest; a weight
 // enters PV as fp16 (11 bits).  A block's scale multiplies whole tiles, so it is applied to scores
-// and weights and never to codes.  The K rows go to the matrix rows in such an order that a
-// lane's 16 scores are those of 16 consecutive tokens of one row: its P is then the second
-// product's operand as it stands, and it shares one block, hence one pair of scales.
+// and weights and never to codes.  The K rows go to the matrix rows in such an order that a lane's
+// scores are those of consecutive tokens of one row: its P is then the second product's operand as
+// it stands, and 8 or 16 of its scores share one pair of scales.
 //
-// With few rows the tokens are split over workgroups (chunks), and kv_block_combine_kernel joins
-// the chunks' maxima, sums and outputs.
+// Two kernels.  Few rows (one or two tiles: decoding) are bound by the codes' bytes: every wave
+// walks over tokens of its own, straight from memory to registers, and the waves meet at the end.
+// More rows (drafts, prompts) are bound by the softmax's vector work: the waves share the tokens,
+// whose codes become fp16 once, in LDS, and own their rows.  With few workgroups the tokens are
+// split over more of them (chunks), and kv_block_combine_kernel joins the chunks' maxima, sums and
+// outputs.
 #include "serve_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -22,12 +26,13 @@ namespace svdq {
 
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
-constexpr int kTile = 64;         // tokens per wave step
+constexpr int kTile = 64;         // tokens per step
 constexpr int kWaves = 4;
 constexpr float kLog2e = 1.4426950408889634f;
-// Weights are held 2^14 too large (the sum too, so it cancels): an fp16 weight then keeps its 11
-// bits down to 2^-28 of the row's largest and something of it to 2^-38, however long the row.
-constexpr float kShift = 14.0f;
+// Weights are held 2^10 too large (the sum too, so it cancels): an fp16 weight then keeps its 11
+// bits down to 2^-24 of the row's largest and something of it to 2^-34, however long the row.  The
+// running maximum follows a new one only when that is 2^4 ahead, so a weight stays below 2^15.
+constexpr float kShift = 10.0f, kLazy = 4.0f;
 
 // Four codes + 128 (bytes) -> four exact fp16: a byte in the mantissa of 1024 is 1024 + c + 128.
 __device__ __forceinline__ void codes4_f16(uint32_t w, v2h& lo, v2h& hi) {
@@ -51,8 +56,22 @@ __device__ __forceinline__ v4f mfma16(v8h a, v8h b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// The largest of the four lanes l % 16 + 16 {0, 1, 2, 3}, in all of them.
+__device__ __forceinline__ float max_quads(float x) {
+  const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+__device__ __forceinline__ float sum_quads(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
 // What one workgroup works on, from its linear id: cached head fastest (the workgroups of one
-// run of blocks read neighbouring memory), then the chunk, the row group, the request.
+// run of blocks read neighbouring memory, and with 8 heads an XCD keeps to one), then the chunk,
+// the row group, the request.
 struct Work {
   int h, chunk, group, b;
 };
@@ -69,7 +88,133 @@ __device__ __forceinline__ Work work_of(int kv_heads, int chunks, int groups) {
   return w;
 }
 
-// RT tiles of 16 rows.
+// The rows and tokens of a workgroup that takes `span` rows (row x head, head fastest) from
+// group * span on.
+struct Range {
+  int row0, n, vrows, len, hg;
+  __device__ __forceinline__ Range(const BlockAttention& a, int b) {
+    row0 = min(max(a.cu[b], 0), a.rows);
+    n = min(max(a.cu[b + 1], row0), a.rows) - row0;
+    hg = a.heads / a.cache.heads;
+    vrows = min(n, a.max_rows) * hg;
+    len = min(max(a.seq[b], 0), a.width << __builtin_ctz(a.cache.bs));
+  }
+  // tokens that row vr sees
+  __device__ __forceinline__ int limit(const BlockAttention& a, int vr) const {
+    return a.causal ? min(len, max(len - n + vr / hg + 1, 0)) : len;
+  }
+  __device__ __forceinline__ size_t out_row(const BlockAttention& a, int h, int vr) const {
+    return (size_t)(row0 + vr / hg) * a.heads + h * hg + vr % hg;
+  }
+};
+
+// 16 (SEG of 64 channels) of a query's channels per lane as fp16, scaled by a power of two that
+// puts the row's largest into [2^8, 2^9); returns what turns a code product into a log2 score
+// (never negative: the query takes the sign of sm_scale).
+template <int SEG>
+__device__ __forceinline__ float scale_query(const BlockAttention& a, float (*x)[16]) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int s = 0; s < SEG; ++s)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) amax = __builtin_fmaxf(amax, __builtin_fabsf(x[s][e]));
+  amax = max_quads(amax);
+  int e2 = (int)(__float_as_uint(amax) >> 23) - 127 - 8;
+  e2 = amax == 0.0f ? 0 : max(e2, -110);
+  const float down = __builtin_copysignf(__uint_as_float((uint32_t)(127 - e2) << 23), a.sm_scale);
+#pragma unroll
+  for (int s = 0; s < SEG; ++s)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[s][e] *= down;
+  return __builtin_fabsf(a.sm_scale) * kLog2e * __uint_as_float((uint32_t)(127 + e2) << 23);
+}
+
+__device__ __forceinline__ void bf16x16(const uint16_t* p0, const uint16_t* p1, float* x) {
+  const v4u w0 = *reinterpret_cast<const v4u*>(p0), w1 = *reinterpret_cast<const v4u*>(p1);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    x[e] = __uint_as_float(e & 1 ? w0[e >> 1] & 0xFFFF0000u : w0[e >> 1] << 16);
+    x[8 + e] = __uint_as_float(e & 1 ? w1[e >> 1] & 0xFFFF0000u : w1[e >> 1] << 16);
+  }
+}
+
+// The scales of a lane's two runs of tokens, and how far its row sees into each: of run g's 8
+// scores sc[2 g], sc[2 g + 1] those of tokens below seen[g].
+struct Runs {
+  float ks[2], lv[2], ivs[2];
+};
+
+// One softmax step of one tile of rows: the lane's 16 code products become weights (pf, the second
+// product's operand), and m, l, o follow.  A weight carries its run's V scale: it is 2^(score +
+// log2 vs), and the sum takes vs out again, so the codes of V stay codes.  (A zero V scale belongs
+// to codes that are all zero, so 1 serves for it.)
+template <int DT>
+__device__ __forceinline__ void softmax_step(v4f* sc, float fac, const Runs& r, bool masked,
+                                             const int* seen, float& m, float& l, v4f* o, v8h* pf) {
+  const float f0 = fac * r.ks[0], f1 = fac * r.ks[1];
+  float mx;
+  if (masked) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float x = __builtin_fmaf(sc[t][i], t < 2 ? f0 : f1, r.lv[t >> 1]);
+        sc[t][i] = 4 * (t & 1) + i < seen[t >> 1] ? x : -__builtin_inff();
+      }
+    mx = -__builtin_inff();
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) mx = __builtin_fmaxf(__builtin_fmaxf(mx, sc[t][i]), sc[t][i + 1]);
+  } else {
+    float top[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      top[g] = __builtin_fmaxf(sc[2 * g][0], sc[2 * g][1]);
+#pragma unroll
+      for (int e = 2; e < 8; e += 2)
+        top[g] = __builtin_fmaxf(__builtin_fmaxf(top[g], sc[2 * g + (e >> 2)][e & 3]), sc[2 * g + (e >> 2)][(e & 3) + 1]);
+    }
+    mx = __builtin_fmaxf(__builtin_fmaf(top[0], f0, r.lv[0]), __builtin_fmaf(top[1], f1, r.lv[1]));
+  }
+  mx = max_quads(mx);
+  if (__any(mx > m + kLazy)) {
+    const float mn = __builtin_fmaxf(m, mx);
+    const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
+    m = mn;
+    l *= alpha;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[d][i] *= alpha;
+  }
+  const float off = (m == -__builtin_inff() ? 0.0f : m) - kShift;
+  float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      v2f x;
+      if (masked) {
+        x = v2f{sc[t][i] - off, sc[t][i + 1] - off};
+      } else {
+        const float f = t < 2 ? f0 : f1, c = r.lv[t >> 1] - off;
+        x = v2f{__builtin_fmaf(sc[t][i], f, c), __builtin_fmaf(sc[t][i + 1], f, c)};
+      }
+      x = v2f{__builtin_amdgcn_exp2f(x.x), __builtin_amdgcn_exp2f(x.y)};
+      sum[t >> 1] += x.x + x.y;  // (in fp32: a run of small V scale counts in the sum all the same)
+      const v2h p = __builtin_convertvector(x, v2h);
+      pf[t >> 1][4 * (t & 1) + i] = p.x;
+      pf[t >> 1][4 * (t & 1) + i + 1] = p.y;
+    }
+  l = __builtin_fmaf(sum[0], r.ivs[0], l);
+  l = __builtin_fmaf(sum[1], r.ivs[1], l);
+}
+
+// ------------------------------------------------------------------------------------ few rows
+// RT tiles of 16 rows.  A wave's lane (c = l % 16, j = l / 16) scores tokens 16 j .. + 15 of its
+// tile for row c: K's row of matrix row 4 j' + i of product t is token 16 j' + 4 t + i.  The next
+// tile's codes are in flight while this one's are used.
 template <int D, int RT>
 __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(BlockAttention a,
                                                                             int chunks, int groups,
@@ -78,172 +223,151 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
   __shared__ float o_lds[kWaves][16][D + 4];
   __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
   const Work wk = work_of(a.cache.heads, chunks, groups);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, j = lane >> 4;
-  const int KV = a.cache.heads, hg = a.heads / KV, shift = __builtin_ctz(a.cache.bs);
-  const int row0 = min(max(a.cu[wk.b], 0), a.rows), row1 = min(max(a.cu[wk.b + 1], row0), a.rows);
-  const int n = row1 - row0;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, j = lane >> 4;
+  const int KV = a.cache.heads, shift = __builtin_ctz(a.cache.bs);
+  const Range rg(a, wk.b);
   const int vr0 = wk.group * 16 * RT;               // first row (row x head) of this workgroup
-  const int vrows = min(n, a.max_rows) * hg;
-  if (vr0 >= vrows) return;
-  const int len = min(max(a.seq[wk.b], 0), a.width << shift);
-  // rows in [vr0, vr0 + 16 RT) see at most `top` tokens
-  const int last = min(vr0 + 16 * RT, vrows) - 1;
-  const int top = a.causal ? min(len, max(len - n + last / hg + 1, 0)) : len;
+  if (vr0 >= rg.vrows) return;
+  const int top = rg.limit(a, min(vr0 + 16 * RT, rg.vrows) - 1);
   const int t0 = wk.chunk * chunk_tokens, t1 = min(t0 + chunk_tokens, top);
   if (chunks > 1 && t0 >= t1) return;               // (the combine knows which chunks there are)
   const int32_t* table = a.tables + (size_t)wk.b * a.width;
 
+  // the blocks of this lane's K rows (16 tokens from base + 16 (c / 4)) and of its 16 scores and V
+  // columns (from base + 16 j); -1 where there are none
+  struct Pages {
+    int k, v;
+  };
+  auto load_pages = [&](int base) {
+    const int tk = base + 16 * (c >> 2), tv = base + 16 * j;
+    Pages p{table[min(tk, t1 - 1) >> shift], table[min(tv, t1 - 1) >> shift]};
+    if (tk >= t1 || (unsigned)p.k >= (unsigned)a.cache.num_blocks) p.k = -1;
+    if (tv >= t1 || (unsigned)p.v >= (unsigned)a.cache.num_blocks) p.v = -1;
+    return p;
+  };
+  struct Codes {
+    v4u k[4][SEG], v[DT];
+    float ks, vs;
+  };
+  const int mask = a.cache.bs - 1;
+  auto load_codes = [&](int base, Pages p, Codes& w) {
+    const size_t bk = (size_t)max(p.k, 0) * KV + wk.h, bv = (size_t)max(p.v, 0) * KV + wk.h;
+    const int tk = (base + 16 * (c >> 2)) & mask, tv = (base + 16 * j) & mask;
+    const uint8_t* kp = a.cache.k_codes + (bk * a.cache.bs + tk + (c & 3)) * D + 16 * j;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int s = 0; s < SEG; ++s) w.k[t][s] = *reinterpret_cast<const v4u*>(kp + 4 * t * D + 64 * s);
+    const uint8_t* vp = a.cache.v_codes + (bv * D + c) * a.cache.bs + tv;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) w.v[d] = *reinterpret_cast<const v4u*>(vp + (size_t)16 * d * a.cache.bs);
+    w.ks = a.cache.k_scale[bv];
+    w.vs = a.cache.v_scale[bv];
+  };
+
   v8h qf[RT][SEG][2];
-  float fac[RT];
+  float fac[RT], m[RT], l[RT];
   int limit[RT];
+  v4f o[RT][DT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    const int vr = min(vr0 + 16 * t + c, vrows - 1), i = vr / hg;
-    limit[t] = a.causal ? min(len, max(len - n + i + 1, 0)) : len;
-    const uint16_t* qp = a.q + (size_t)(row0 + i) * a.q_stride + (size_t)(wk.h * hg + vr % hg) * D + 16 * j;
+    const int vr = min(vr0 + 16 * t + c, rg.vrows - 1);
+    limit[t] = rg.limit(a, vr);
+    const uint16_t* qp = a.q + (size_t)(rg.row0 + vr / rg.hg) * a.q_stride + (size_t)(wk.h * rg.hg + vr % rg.hg) * D + 16 * j;
     float x[SEG][16];
-    float amax = 0.0f;
 #pragma unroll
-    for (int s = 0; s < SEG; ++s) {
-      const v4u w0 = *reinterpret_cast<const v4u*>(qp + 64 * s), w1 = *reinterpret_cast<const v4u*>(qp + 64 * s + 8);
-      const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        x[s][e] = __uint_as_float(e & 1 ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16);
-        amax = __builtin_fmaxf(amax, __builtin_fabsf(x[s][e]));
-      }
-    }
-    amax = __builtin_fmaxf(amax, __shfl_xor(amax, 16));
-    amax = __builtin_fmaxf(amax, __shfl_xor(amax, 32));
-    int e2 = (int)(__float_as_uint(amax) >> 23) - 127 - 8;  // amax 2^-e2 in [2^8, 2^9)
-    e2 = amax == 0.0f ? 0 : max(e2, -110);
-    const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-    fac[t] = a.sm_scale * kLog2e * __uint_as_float((uint32_t)(127 + e2) << 23);
+    for (int s = 0; s < SEG; ++s) bf16x16(qp + 64 * s, qp + 64 * s + 8, x[s]);
+    fac[t] = scale_query<SEG>(a, x);
 #pragma unroll
     for (int s = 0; s < SEG; ++s)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) qf[t][s][e >> 3][e & 7] = (_Float16)(x[s][e] * down);
-  }
-
-  v4f o[RT][DT];
-  float m[RT], l[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
+      for (int e = 0; e < 16; ++e) qf[t][s][e >> 3][e & 7] = (_Float16)x[s][e];
     m[t] = -__builtin_inff();
     l[t] = 0.0f;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[t][d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  for (int base = t0 + wave * kTile; base < t1; base += kWaves * kTile) {
-    // the blocks of this lane's K rows (16 tokens from base + 16 (c / 4)) and of its 16 scores and
-    // V columns (from base + 16 j); -1 where there are none
-    const int tk = base + 16 * (c >> 2), tv = base + 16 * j;
-    int pk = tk < t1 ? table[tk >> shift] : -1, pv = tv < t1 ? table[tv >> shift] : -1;
-    if ((unsigned)pk >= (unsigned)a.cache.num_blocks) pk = -1;
-    if ((unsigned)pv >= (unsigned)a.cache.num_blocks) pv = -1;
-    const size_t bk = (size_t)max(pk, 0) * KV + wk.h, bv = (size_t)max(pv, 0) * KV + wk.h;
-    const int mask = a.cache.bs - 1;
-    v4u kw[4][SEG], vw[DT];
-    const uint8_t* kp = a.cache.k_codes + (bk * a.cache.bs + (tk & mask) + (c & 3)) * D + 16 * j;
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int s = 0; s < SEG; ++s) kw[t][s] = *reinterpret_cast<const v4u*>(kp + 4 * t * D + 64 * s);
-    const uint8_t* vp = a.cache.v_codes + (bv * D + c) * a.cache.bs + (tv & mask);
-#pragma unroll
-    for (int d = 0; d < DT; ++d) vw[d] = *reinterpret_cast<const v4u*>(vp + (size_t)16 * d * a.cache.bs);
-    float ks = 0.0f, vs = 1.0f;
-    if (pv >= 0) {
-      ks = a.cache.k_scale[bv];
-      vs = a.cache.v_scale[bv];
-    }
-    // A weight carries its block's V scale: it is 2^(score + log2 vs), and the sum takes vs out
-    // again.  A zero scale belongs to codes that are all zero, so any scale serves.
-    if (vs == 0.0f) vs = 1.0f;
-    const float lv = __builtin_amdgcn_logf(vs), ivs = 1.0f / vs;
-
+  constexpr int STEP = kWaves * kTile;
+  auto step = [&](int base, Pages p, const Codes& w) {
+    Runs r;
+    const float vs = p.v < 0 || w.vs == 0.0f ? 1.0f : w.vs;
+    r.ks[0] = r.ks[1] = p.v < 0 ? 0.0f : w.ks;
+    r.lv[0] = r.lv[1] = __builtin_amdgcn_logf(vs);
+    r.ivs[0] = r.ivs[1] = __builtin_amdgcn_rcpf(vs);
     v4f sc[RT][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       v8h ka[SEG][2];
 #pragma unroll
-      for (int s = 0; s < SEG; ++s) codes16_f16(kw[t][s], ka[s][0], ka[s][1]);
+      for (int s = 0; s < SEG; ++s) codes16_f16(w.k[t][s], ka[s][0], ka[s][1]);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
+      for (int q = 0; q < RT; ++q) {
         v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int s = 0; s < SEG; ++s) {
-          x = mfma16(ka[s][0], qf[r][s][0], x);
-          x = mfma16(ka[s][1], qf[r][s][1], x);
+          x = mfma16(ka[s][0], qf[q][s][0], x);
+          x = mfma16(ka[s][1], qf[q][s][1], x);
         }
-        sc[r][t] = x;
+        sc[q][t] = x;
       }
     }
     v8h pf[RT][2];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const float f = fac[r] * ks;
-      const int seen = pv >= 0 ? limit[r] - tv : 0;  // of this lane's 16 tokens
-      float mx = -__builtin_inff();
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = __builtin_fmaf(sc[r][t][i], f, lv);
-          sc[r][t][i] = 4 * t + i < seen ? x : -__builtin_inff();
-          mx = __builtin_fmaxf(mx, sc[r][t][i]);
-        }
-      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16));
-      mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
-      const float mn = __builtin_fmaxf(m[r], mx);
-      const float off = (mn == -__builtin_inff() ? 0.0f : mn) - kShift;
-      const float alpha = __builtin_amdgcn_exp2f(m[r] - (off + kShift));
-      m[r] = mn;
-      float sum = 0.0f;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = __builtin_amdgcn_exp2f(sc[r][t][i] - off);
-          sum += p;
-          pf[r][t >> 1][4 * (t & 1) + i] = (_Float16)p;
-        }
-      l[r] = __builtin_fmaf(l[r], alpha, sum * ivs);
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[r][d][i] *= alpha;
+    for (int q = 0; q < RT; ++q) {
+      const int n = p.v < 0 ? 0 : limit[q] - (base + 16 * j);  // of this lane's 16 tokens
+      const int seen[2] = {n, n - 8};
+      softmax_step<DT>(sc[q], fac[q], r, __any(n < 16), seen, m[q], l[q], o[q], pf[q]);
     }
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
       v8h va, vb;
-      codes16_f16(vw[d], va, vb);
+      codes16_f16(w.v[d], va, vb);
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        o[r][d] = mfma16(va, pf[r][0], o[r][d]);
-        o[r][d] = mfma16(vb, pf[r][1], o[r][d]);
+      for (int q = 0; q < RT; ++q) {
+        o[q][d] = mfma16(va, pf[q][0], o[q][d]);
+        o[q][d] = mfma16(vb, pf[q][1], o[q][d]);
       }
+    }
+  };
+  int base = t0 + wave * kTile;
+  if (base < t1) {
+    Pages pa = load_pages(base), pb = load_pages(base + STEP);
+    Codes wa, wb;
+    load_codes(base, pa, wa);
+    for (;;) {
+      // (past the last tile the pages are -1 and block 0 is read, unused)
+      load_codes(base + STEP, pb, wb);
+      Pages pc = load_pages(base + 2 * STEP);
+      step(base, pa, wa);
+      base += STEP;
+      if (base >= t1) break;
+      load_codes(base + STEP, pc, wa);
+      pa = load_pages(base + 2 * STEP);
+      step(base, pb, wb);
+      base += STEP;
+      if (base >= t1) break;
+      pb = pa;
+      pa = pc;
     }
   }
 
   // ---- the waves meet, one tile of 16 rows after the other
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    float ls = l[r];
-    ls += __shfl_xor(ls, 16);
-    ls += __shfl_xor(ls, 32);
+  for (int q = 0; q < RT; ++q) {
+    const float ls = sum_quads(l[q]);
     __syncthreads();
     if (j == 0) {
-      m_lds[wave][c] = m[r];
+      m_lds[wave][c] = m[q];
       l_lds[wave][c] = ls;
     }
 #pragma unroll
-    for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f*>(&o_lds[wave][c][16 * d + 4 * j]) = o[r][d];
+    for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f*>(&o_lds[wave][c][16 * d + 4 * j]) = o[q][d];
     __syncthreads();
     for (int e = threadIdx.x; e < 16 * D; e += kWaves * 64) {
-      const int row = e / D, d = e % D, vr = vr0 + 16 * r + row;
-      if (vr >= vrows) continue;
+      const int row = e / D, d = e % D, vr = vr0 + 16 * q + row;
+      if (vr >= rg.vrows) continue;
       float mm = -__builtin_inff();
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) mm = __builtin_fmaxf(mm, m_lds[w][row]);
@@ -255,12 +379,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
         sum = __builtin_fmaf(l_lds[w][row], f, sum);
         out = __builtin_fmaf(o_lds[w][row][d], f, out);
       }
-      const size_t at = (size_t)(row0 + vr / hg) * a.heads + wk.h * hg + vr % hg;
+      const size_t at = rg.out_row(a, wk.h, vr);
       if (chunks == 1) {
         a.out[at * D + d] = float_to_bf16_bits(sum == 0.0f ? 0.0f : out / sum);
       } else {
-        float* ws = a.ws + (at * chunks + wk.chunk) * (D + 2);
-        ws[2 + d] = out;
+        float* ws = a.ws + (at * chunks + wk.chunk) * (D + 4);
+        ws[4 + d] = out;
         if (d == 0) {
           ws[0] = mm;
           ws[1] = sum;
@@ -270,57 +394,321 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
   }
 }
 
-// Joins the chunks of one (row, head): D threads, each one channel.
+// ----------------------------------------------------------------------------------- more rows
+// A workgroup takes 64 RT rows, 16 RT to a wave, and walks over its tokens with them, 64 at a time.
+// Their codes come two tiles ahead, 16 bytes per thread and load, and become fp16 in LDS one tile
+// ahead (double buffered, one barrier per tile): K as [token][D], its 16-byte slots permuted within
+// the row so that 16 matrix rows read 16 different bank groups, V as [channel][token] with a slot
+// of padding.  Lane (c, j) scores tokens 32 g + 8 j .. + 7 (g = 0, 1) for row c: K's row of matrix
+// row 4 j' + i of product t = 2 g + e is token 32 g + 8 j' + 4 e + i.
 template <int D>
-__global__ __launch_bounds__(D) void kv_block_combine_kernel(BlockAttention a, int chunks,
-                                                             int chunk_tokens, int span) {
-  const int hg = a.heads / a.cache.heads, shift = __builtin_ctz(a.cache.bs);
+struct TileLds {
+  uint16_t k[kTile][D];
+  uint16_t v[D][kTile + 8];
+};
+
+template <int D>
+__device__ __forceinline__ int k_slot(int token, int slot) {
+  return D == 64 ? slot ^ ((token >> 3 & 3) * 2 | (token >> 1 & 1)) : slot ^ ((token >> 3 & 3) * 4 | (token & 3));
+}
+
+template <int D, int RT>
+__global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel(
+    BlockAttention a, int chunks, int groups, int chunk_tokens) {
+  constexpr int DT = D / 16, STEPS = D / 32, LOADS = D / 64;
+  __shared__ __attribute__((aligned(16))) TileLds<D> lds[2];
+  const Work wk = work_of(a.cache.heads, chunks, groups);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, j = lane >> 4;
+  const int KV = a.cache.heads, shift = __builtin_ctz(a.cache.bs);
+  const Range rg(a, wk.b);
+  const int vr0 = wk.group * 64 * RT;
+  if (vr0 >= rg.vrows) return;
+  const int top = rg.limit(a, min(vr0 + 64 * RT, rg.vrows) - 1), low = rg.limit(a, vr0);
+  const int t0 = wk.chunk * chunk_tokens, t1 = min(t0 + chunk_tokens, top);
+  if (chunks > 1 && t0 >= t1) return;
+  const int32_t* table = a.tables + (size_t)wk.b * a.width;
+
+  // the four 16-token parts of a tile: their blocks (-1 where there is none) and scales, uniform
+  struct Parts {
+    int page[4];
+    float ks[4], vs[4];
+  };
+  auto load_parts = [&](int base) {
+    Parts p;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int t = base + 16 * k;
+      p.page[k] = table[max(min(t, t1 - 1), 0) >> shift];
+      if (t >= t1 || (unsigned)p.page[k] >= (unsigned)a.cache.num_blocks) p.page[k] = -1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const size_t at = (size_t)max(p.page[k], 0) * KV + wk.h;
+      p.ks[k] = a.cache.k_scale[at];
+      p.vs[k] = a.cache.v_scale[at];
+    }
+    return p;
+  };
+  struct Codes {
+    v4u k[LOADS], v[LOADS];
+  };
+  const int mask = a.cache.bs - 1;
+  auto page_of = [](const Parts& p, int part) {
+    const int lo = part & 1 ? p.page[1] : p.page[0], hi = part & 1 ? p.page[3] : p.page[2];
+    return max(part & 2 ? hi : lo, 0);
+  };
+  auto load_codes = [&](int base, const Parts& p, Codes& w) {
+#pragma unroll
+    for (int q = 0; q < LOADS; ++q) {
+      const int token = tid / (D / 16) + 256 / (D / 16) * q, col = tid % (D / 16);
+      const size_t bk = (size_t)page_of(p, token >> 4) * KV + wk.h;
+      w.k[q] = *reinterpret_cast<const v4u*>(a.cache.k_codes + (bk * a.cache.bs + ((base + token) & mask)) * D + 16 * col);
+      const int d = tid / 4 + 64 * q, part = tid & 3;
+      const size_t bv = (size_t)page_of(p, part) * KV + wk.h;
+      w.v[q] = *reinterpret_cast<const v4u*>(a.cache.v_codes + (bv * D + d) * a.cache.bs + ((base + 16 * part) & mask));
+    }
+  };
+  auto store_codes = [&](const Codes& w, TileLds<D>& to) {
+#pragma unroll
+    for (int q = 0; q < LOADS; ++q) {
+      const int token = tid / (D / 16) + 256 / (D / 16) * q, col = tid % (D / 16);
+      v8h x, y;
+      codes16_f16(w.k[q], x, y);
+      *reinterpret_cast<v8h*>(&to.k[token][8 * k_slot<D>(token, 2 * col)]) = x;
+      *reinterpret_cast<v8h*>(&to.k[token][8 * k_slot<D>(token, 2 * col + 1)]) = y;
+      const int d = tid / 4 + 64 * q, part = tid & 3;
+      codes16_f16(w.v[q], x, y);
+      *reinterpret_cast<v8h*>(&to.v[d][16 * part]) = x;
+      *reinterpret_cast<v8h*>(&to.v[d][16 * part + 8]) = y;
+    }
+  };
+
+  v8h qf[RT][STEPS];
+  float fac[RT], m[RT], l[RT];
+  int limit[RT];
+  v4f o[RT][DT];
+  const int first = vr0 + 16 * RT * wave;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const int vr = min(first + 16 * t + c, rg.vrows - 1);
+    limit[t] = rg.limit(a, vr);
+    const uint16_t* qp = a.q + (size_t)(rg.row0 + vr / rg.hg) * a.q_stride + (size_t)(wk.h * rg.hg + vr % rg.hg) * D + 8 * j;
+    float x[STEPS / 2][16];
+#pragma unroll
+    for (int s = 0; s < STEPS / 2; ++s) bf16x16(qp + 64 * s, qp + 64 * s + 32, x[s]);
+    fac[t] = scale_query<STEPS / 2>(a, x);
+#pragma unroll
+    for (int s = 0; s < STEPS / 2; ++s)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) qf[t][2 * s + (e >> 3)][e & 7] = (_Float16)x[s][e];
+    m[t] = -__builtin_inff();
+    l[t] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[t][d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+
+  auto compute = [&](int base, const Parts& p, const TileLds<D>& in) {
+    v4f sc[RT][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+#pragma unroll
+      for (int q = 0; q < RT; ++q) sc[q][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+      const int token = 32 * (t >> 1) + 8 * (c >> 2) + 4 * (t & 1) + (c & 3);
+#pragma unroll
+      for (int s = 0; s < STEPS; ++s) {
+        const v8h ka = *reinterpret_cast<const v8h*>(&in.k[token][8 * k_slot<D>(token, 4 * s + j)]);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) sc[q][t] = mfma16(ka, qf[q][s], sc[q][t]);
+      }
+    }
+    // this lane's runs: tokens 32 g + 8 j .. + 7 lie in part 2 g + j / 2
+    Runs r;
+    bool there[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const bool odd = j >> 1;
+      there[g] = (odd ? p.page[2 * g + 1] : p.page[2 * g]) >= 0;
+      const float ks = odd ? p.ks[2 * g + 1] : p.ks[2 * g];
+      float vs = odd ? p.vs[2 * g + 1] : p.vs[2 * g];
+      vs = !there[g] || vs == 0.0f ? 1.0f : vs;
+      r.ks[g] = there[g] ? ks : 0.0f;
+      r.lv[g] = __builtin_amdgcn_logf(vs);
+      r.ivs[g] = __builtin_amdgcn_rcpf(vs);
+    }
+    const bool masked = base + kTile > low || (p.page[0] | p.page[1] | p.page[2] | p.page[3]) < 0;
+    v8h pf[RT][2];
+#pragma unroll
+    for (int q = 0; q < RT; ++q) {
+      const int n = limit[q] - (base + 8 * j);
+      const int seen[2] = {there[0] ? n : 0, there[1] ? n - 32 : 0};
+      softmax_step<DT>(sc[q], fac[q], r, masked, seen, m[q], l[q], o[q], pf[q]);
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      const v8h va = *reinterpret_cast<const v8h*>(&in.v[16 * d + c][8 * j]);
+      const v8h vb = *reinterpret_cast<const v8h*>(&in.v[16 * d + c][32 + 8 * j]);
+#pragma unroll
+      for (int q = 0; q < RT; ++q) {
+        o[q][d] = mfma16(va, pf[q][0], o[q][d]);
+        o[q][d] = mfma16(vb, pf[q][1], o[q][d]);
+      }
+    }
+  };
+  auto barrier = [] {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  };
+
+  if (t0 < t1) {
+    Parts p0 = load_parts(t0), p1 = load_parts(t0 + kTile);
+    Codes w;
+    load_codes(t0, p0, w);
+    store_codes(w, lds[0]);
+    load_codes(t0 + kTile, p1, w);
+    barrier();
+    int buf = 0;
+    for (int base = t0; base < t1; base += kTile, buf ^= 1) {
+      // (past the last tile the pages are -1 and block 0 is read, unused)
+      store_codes(w, lds[buf ^ 1]);
+      const Parts p2 = load_parts(base + 2 * kTile);
+      load_codes(base + 2 * kTile, p2, w);
+      if (first < rg.vrows) compute(base, p0, lds[buf]);  // (a wave without rows only helps to load)
+      p0 = p1;
+      p1 = p2;
+      barrier();
+    }
+  }
+
+#pragma unroll
+  for (int q = 0; q < RT; ++q) {
+    const int vr = first + 16 * q + c;
+    const float sum = sum_quads(l[q]);
+    if (vr >= rg.vrows) continue;
+    const size_t at = rg.out_row(a, wk.h, vr);
+    if (chunks == 1) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        *reinterpret_cast<v2u*>(a.out + at * D + 16 * d + 4 * j) =
+            v2u{pack2_bf16(o[q][d][0] * inv, o[q][d][1] * inv), pack2_bf16(o[q][d][2] * inv, o[q][d][3] * inv)};
+    } else {
+      float* ws = a.ws + (at * chunks + wk.chunk) * (D + 4);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f*>(ws + 4 + 16 * d + 4 * j) = o[q][d];
+      if (j == 0) {
+        ws[0] = m[q];
+        ws[1] = sum;
+      }
+    }
+  }
+}
+
+// --------------------------------------------------------------------------------------- join
+// Joins the chunks of one (row, head).  256 threads: the chunks' weights 2^(m_k - M) go through
+// LDS, then a thread adds one channel of every (256 / D)-th chunk, several loads in flight.
+constexpr int kJoinThreads = 256;
+constexpr int kMaxChunks = 1024;
+
+template <int D>
+__global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAttention a, int chunks,
+                                                                        int chunk_tokens, int span) {
+  constexpr int PARTS = kJoinThreads / D;
+  __shared__ float f_lds[kMaxChunks];
+  __shared__ float red[2][kJoinThreads / 64];
+  __shared__ float o_lds[PARTS][D];
   unsigned id = blockIdx.x;
   const int h = id % a.heads;
   id /= a.heads;
   const int i = id % a.max_rows, b = id / a.max_rows;
-  const int row0 = min(max(a.cu[b], 0), a.rows), row1 = min(max(a.cu[b + 1], row0), a.rows);
-  const int n = row1 - row0;
-  if (i >= n) return;
-  const int len = min(max(a.seq[b], 0), a.width << shift);
-  // the chunks that the workgroup of this row's group wrote: those below the tokens its last row sees
-  const int vrows = min(n, a.max_rows) * hg, vr = i * hg + h % hg;
-  const int last = min((vr / span + 1) * span, vrows) - 1;
-  const int top = a.causal ? min(len, max(len - n + last / hg + 1, 0)) : len;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const Range rg(a, b);
+  if (i >= rg.n) return;
+  // the chunks that the workgroups of this row's group wrote: those below the tokens its last row sees
+  const int vr = i * rg.hg + h % rg.hg;
+  const int top = rg.limit(a, min((vr / span + 1) * span, rg.vrows) - 1);
   const int used = min((top + chunk_tokens - 1) / chunk_tokens, chunks);
-  const size_t at = (size_t)(row0 + i) * a.heads + h;
-  const float* ws = a.ws + at * chunks * (D + 2);
+  const size_t at = (size_t)(rg.row0 + i) * a.heads + h;
+  const float* ws = a.ws + at * chunks * (D + 4);
+  // four chunks to a thread at most: their maxima and sums
+  float m[kMaxChunks / kJoinThreads], s[kMaxChunks / kJoinThreads];
   float mm = -__builtin_inff();
-  for (int k = 0; k < used; ++k) mm = __builtin_fmaxf(mm, ws[(size_t)k * (D + 2)]);
-  const float off = mm == -__builtin_inff() ? 0.0f : mm;
-  float sum = 0.0f, out = 0.0f;
-  for (int k = 0; k < used; ++k) {
-    const float* p = ws + (size_t)k * (D + 2);
-    const float f = __builtin_amdgcn_exp2f(p[0] - off);
-    sum = __builtin_fmaf(p[1], f, sum);
-    out = __builtin_fmaf(p[2 + threadIdx.x], f, out);
+#pragma unroll
+  for (int q = 0; q < kMaxChunks / kJoinThreads; ++q) {
+    const int k = tid + kJoinThreads * q;
+    const v2f ms = *reinterpret_cast<const v2f*>(ws + (size_t)min(k, max(used - 1, 0)) * (D + 4));
+    m[q] = k < used ? ms.x : -__builtin_inff();
+    s[q] = k < used ? ms.y : 0.0f;
+    mm = __builtin_fmaxf(mm, m[q]);
   }
-  a.out[at * D + threadIdx.x] = float_to_bf16_bits(sum == 0.0f ? 0.0f : out / sum);
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) mm = __builtin_fmaxf(mm, __shfl_xor(mm, x));
+  if (lane == 0) red[0][wave] = mm;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 64; ++w) mm = __builtin_fmaxf(mm, red[0][w]);
+  const float off = mm == -__builtin_inff() ? 0.0f : mm;
+  float sum = 0.0f;
+#pragma unroll
+  for (int q = 0; q < kMaxChunks / kJoinThreads; ++q) {
+    const int k = tid + kJoinThreads * q;
+    const float f = __builtin_amdgcn_exp2f(m[q] - off);
+    if (k < used) f_lds[k] = f;
+    sum = __builtin_fmaf(s[q], f, sum);
+  }
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
+  if (lane == 0) red[1][wave] = sum;
+  __syncthreads();
+  sum = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinThreads / 64; ++w) sum += red[1][w];
+  const int d = tid % D, part = tid / D;
+  float out = 0.0f;
+  for (int k = part; k < used; k += 8 * PARTS) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = ws[(size_t)min(k + u * PARTS, used - 1) * (D + 4) + 4 + d];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (k + u * PARTS < used) out = __builtin_fmaf(v[u], f_lds[k + u * PARTS], out);
+  }
+  o_lds[part][d] = out;
+  __syncthreads();
+  if (part == 0) {
+#pragma unroll
+    for (int p = 1; p < PARTS; ++p) out += o_lds[p][d];
+    a.out[at * D + d] = float_to_bf16_bits(sum == 0.0f ? 0.0f : out / sum);
+  }
 }
 
-// How a call is split, from its sizes alone.
+// How a call is split, from its sizes alone.  Up to 16 rows (row x head) per request and cached head,
+// 32 of 64 channels (128 would need more registers than there are), go to the few-rows kernel; more to the other, 128 to a workgroup, or 64 where that would leave
+// CUs idle or rows empty.
 struct Split {
+  bool few;
   int rt, groups, chunks, chunk_tokens;
+  int span() const { return (few ? 16 : 64) * rt; }
 };
 
-static Split split_of(int requests, int max_rows, int heads, int kv_heads, int width, int bs) {
+static Split split_of(int requests, int max_rows, int heads, int kv_heads, int dim, int width, int bs) {
   Split s;
   const long long vrows = (long long)max_rows * (heads / kv_heads);
-  s.rt = vrows > 16 ? 2 : 1;
-  s.groups = (int)((vrows + 16 * s.rt - 1) / (16 * s.rt));
+  s.few = vrows <= (dim == 64 ? 32 : 16);
+  s.rt = s.few ? (vrows > 16 ? 2 : 1) : (vrows > 64 ? 2 : 1);
+  s.groups = (int)((vrows + s.span() - 1) / s.span());
   const long long natural = (long long)requests * kv_heads * s.groups;
   const long long tokens = (long long)width * bs;
-  const long long want = (1024 + natural - 1) / natural;              // workgroups for 256 CUs
-  const long long most = (tokens + kWaves * kTile - 1) / (kWaves * kTile);
+  // enough workgroups for 256 CUs, each with a few tiles to itself
+  const int unit = s.few ? kWaves * kTile : 4 * kTile;
+  const long long want = ((s.few ? 1024 : 512) + natural - 1) / natural;
+  long long most = (tokens + unit - 1) / unit;
+  if (most > kMaxChunks) most = kMaxChunks;
   long long chunks = want < most ? want : most;
   if (chunks < 1) chunks = 1;
   long long per = (tokens + chunks - 1) / chunks;
-  per = (per + kWaves * kTile - 1) / (kWaves * kTile) * (kWaves * kTile);
+  per = (per + unit - 1) / unit * unit;
   s.chunk_tokens = (int)per;
   s.chunks = (int)((tokens + per - 1) / per);
   return s;
@@ -329,26 +717,28 @@ static Split split_of(int requests, int max_rows, int heads, int kv_heads, int w
 size_t kv_block_attention_ws_bytes(int requests, int rows, int max_rows, int heads, int kv_heads,
                                    int dim, int width, int bs) {
   if (requests <= 0 || rows <= 0) return 0;
-  const Split s = split_of(requests, max_rows, heads, kv_heads, width, bs);
-  return s.chunks == 1 ? 0 : (size_t)rows * heads * s.chunks * (dim + 2) * sizeof(float);
+  const Split s = split_of(requests, max_rows, heads, kv_heads, dim, width, bs);
+  return s.chunks == 1 ? 0 : (size_t)rows * heads * s.chunks * (dim + 4) * sizeof(float);
 }
 
 template <int D>
 static hipError_t launch(const BlockAttention& a, hipStream_t stream) {
-  const Split s = split_of(a.requests, a.max_rows, a.heads, a.cache.heads, a.width, a.cache.bs);
+  const Split s = split_of(a.requests, a.max_rows, a.heads, a.cache.heads, D, a.width, a.cache.bs);
   const long long grid = (long long)a.requests * s.groups * s.chunks * a.cache.heads;
   const long long joins = (long long)a.requests * a.max_rows * a.heads;
   if (grid > 0x7FFFFFFFLL || (s.chunks > 1 && joins > 0x7FFFFFFFLL)) return hipErrorInvalidConfiguration;
-  if (s.rt == 1)
-    hipLaunchKernelGGL((kv_block_attention_kernel<D, 1>), dim3((unsigned)grid), dim3(kWaves * 64), 0, stream, a,
-                       s.chunks, s.groups, s.chunk_tokens);
-  else
-    hipLaunchKernelGGL((kv_block_attention_kernel<D, 2>), dim3((unsigned)grid), dim3(kWaves * 64), 0, stream, a,
-                       s.chunks, s.groups, s.chunk_tokens);
+#define SVDQ_ATTEND(KERNEL, RT)                                                                  \
+  hipLaunchKernelGGL((KERNEL<D, RT>), dim3((unsigned)grid), dim3(kWaves * 64), 0, stream, a,     \
+                     s.chunks, s.groups, s.chunk_tokens)
+  if (s.few && s.rt == 1) SVDQ_ATTEND(kv_block_attention_kernel, 1);
+  else if (s.few) SVDQ_ATTEND(kv_block_attention_kernel, (D == 64 ? 2 : 1));
+  else if (s.rt == 1) SVDQ_ATTEND(kv_block_attention_rows_kernel, 1);
+  else SVDQ_ATTEND(kv_block_attention_rows_kernel, 2);
+#undef SVDQ_ATTEND
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || s.chunks == 1) return e;
-  hipLaunchKernelGGL(kv_block_combine_kernel<D>, dim3((unsigned)joins), dim3(D), 0, stream, a, s.chunks,
-                     s.chunk_tokens, 16 * s.rt);
+  hipLaunchKernelGGL(kv_block_combine_kernel<D>, dim3((unsigned)joins), dim3(kJoinThreads), 0, stream,
+                     a, s.chunks, s.chunk_tokens, s.span());
   return hipGetLastError();
 }
 
