@@ -19,6 +19,8 @@
 // whose codes become fp16 once, in LDS, and own their rows.  With few workgroups the tokens are
 // split over more of them (chunks), and kv_block_combine_kernel joins the chunks' maxima, sums and
 // outputs.
+#include <type_traits>
+
 #include "serve_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -62,6 +64,11 @@ __device__ __forceinline__ float max_quads(float x) {
   x = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
   const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
   return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+
+// The IEEE maximum (a NaN stays one): the form that needs no canonical operands.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 
 __device__ __forceinline__ float sum_quads(float x) {
@@ -148,12 +155,12 @@ struct Runs {
 // product's operand), and m, l, o follow.  A weight carries its run's V scale: it is 2^(score +
 // log2 vs), and the sum takes vs out again, so the codes of V stay codes.  (A zero V scale belongs
 // to codes that are all zero, so 1 serves for it.)
-template <int DT>
-__device__ __forceinline__ void softmax_step(v4f* sc, float fac, const Runs& r, bool masked,
-                                             const int* seen, float& m, float& l, v4f* o, v8h* pf) {
+template <int DT, bool MASKED>
+__device__ __forceinline__ void softmax_step(v4f* sc, float fac, const Runs& r, const int* seen,
+                                             float& m, float& l, v4f* o, v8h* pf) {
   const float f0 = fac * r.ks[0], f1 = fac * r.ks[1];
   float mx;
-  if (masked) {
+  if constexpr (MASKED) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -165,15 +172,15 @@ __device__ __forceinline__ void softmax_step(v4f* sc, float fac, const Runs& r, 
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) mx = __builtin_fmaxf(__builtin_fmaxf(mx, sc[t][i]), sc[t][i + 1]);
+      for (int i = 0; i < 4; i += 2) mx = max3(mx, sc[t][i], sc[t][i + 1]);
   } else {
     float top[2];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      top[g] = __builtin_fmaxf(sc[2 * g][0], sc[2 * g][1]);
+      top[g] = __builtin_elementwise_maximum(sc[2 * g][0], sc[2 * g][1]);
 #pragma unroll
       for (int e = 2; e < 8; e += 2)
-        top[g] = __builtin_fmaxf(__builtin_fmaxf(top[g], sc[2 * g + (e >> 2)][e & 3]), sc[2 * g + (e >> 2)][(e & 3) + 1]);
+        top[g] = max3(top[g], sc[2 * g + (e >> 2)][e & 3], sc[2 * g + (e >> 2)][(e & 3) + 1]);
     }
     mx = __builtin_fmaxf(__builtin_fmaf(top[0], f0, r.lv[0]), __builtin_fmaf(top[1], f1, r.lv[1]));
   }
@@ -195,7 +202,7 @@ __device__ __forceinline__ void softmax_step(v4f* sc, float fac, const Runs& r, 
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {
       v2f x;
-      if (masked) {
+      if constexpr (MASKED) {
         x = v2f{sc[t][i] - off, sc[t][i + 1] - off};
       } else {
         const float f = t < 2 ? f0 : f1, c = r.lv[t >> 1] - off;
@@ -234,25 +241,28 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
   if (chunks > 1 && t0 >= t1) return;               // (the combine knows which chunks there are)
   const int32_t* table = a.tables + (size_t)wk.b * a.width;
 
-  // the blocks of this lane's K rows (16 tokens from base + 16 (c / 4)) and of its 16 scores and V
-  // columns (from base + 16 j); -1 where there are none
+  // the table's entries for this lane's K rows (16 tokens from base + 16 (c / 4)) and for its 16
+  // scores and V columns (from base + 16 j); they are looked at one step later, so that the loads
+  // stay in flight meanwhile
   struct Pages {
     int k, v;
   };
   auto load_pages = [&](int base) {
-    const int tk = base + 16 * (c >> 2), tv = base + 16 * j;
-    Pages p{table[min(tk, t1 - 1) >> shift], table[min(tv, t1 - 1) >> shift]};
-    if (tk >= t1 || (unsigned)p.k >= (unsigned)a.cache.num_blocks) p.k = -1;
-    if (tv >= t1 || (unsigned)p.v >= (unsigned)a.cache.num_blocks) p.v = -1;
-    return p;
+    return Pages{table[min(base + 16 * (c >> 2), t1 - 1) >> shift], table[min(base + 16 * j, t1 - 1) >> shift]};
   };
   struct Codes {
     v4u k[4][SEG], v[DT];
     float ks, vs;
+    bool there;  // this lane's 16 tokens
   };
   const int mask = a.cache.bs - 1;
   auto load_codes = [&](int base, Pages p, Codes& w) {
-    const size_t bk = (size_t)max(p.k, 0) * KV + wk.h, bv = (size_t)max(p.v, 0) * KV + wk.h;
+    // a block of no token, or outside the pool, is read as block 0 and left out
+    const bool k_there = base + 16 * (c >> 2) < t1 && (unsigned)p.k < (unsigned)a.cache.num_blocks;
+    w.there = base + 16 * j < t1 && (unsigned)p.v < (unsigned)a.cache.num_blocks;
+    p.k = k_there ? p.k : 0;
+    p.v = w.there ? p.v : 0;
+    const size_t bk = (size_t)p.k * KV + wk.h, bv = (size_t)p.v * KV + wk.h;
     const int tk = (base + 16 * (c >> 2)) & mask, tv = (base + 16 * j) & mask;
     const uint8_t* kp = a.cache.k_codes + (bk * a.cache.bs + tk + (c & 3)) * D + 16 * j;
 #pragma unroll
@@ -290,10 +300,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
   }
 
   constexpr int STEP = kWaves * kTile;
-  auto step = [&](int base, Pages p, const Codes& w) {
+  auto step = [&](int base, const Codes& w) {
     Runs r;
-    const float vs = p.v < 0 || w.vs == 0.0f ? 1.0f : w.vs;
-    r.ks[0] = r.ks[1] = p.v < 0 ? 0.0f : w.ks;
+    const float vs = w.there && w.vs != 0.0f ? w.vs : 1.0f;
+    r.ks[0] = r.ks[1] = w.there ? w.ks : 0.0f;
     r.lv[0] = r.lv[1] = __builtin_amdgcn_logf(vs);
     r.ivs[0] = r.ivs[1] = __builtin_amdgcn_rcpf(vs);
     v4f sc[RT][4];
@@ -316,9 +326,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
     v8h pf[RT][2];
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
-      const int n = p.v < 0 ? 0 : limit[q] - (base + 16 * j);  // of this lane's 16 tokens
+      const int n = w.there ? limit[q] - (base + 16 * j) : 0;  // of this lane's 16 tokens
       const int seen[2] = {n, n - 8};
-      softmax_step<DT>(sc[q], fac[q], r, __any(n < 16), seen, m[q], l[q], o[q], pf[q]);
+      softmax_step<DT, true>(sc[q], fac[q], r, seen, m[q], l[q], o[q], pf[q]);
     }
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
@@ -333,23 +343,22 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
   };
   int base = t0 + wave * kTile;
   if (base < t1) {
-    Pages pa = load_pages(base), pb = load_pages(base + STEP);
+    // pages two steps ahead, codes one (past the last tile block 0 is read, unused)
+    Pages p = load_pages(base);
     Codes wa, wb;
-    load_codes(base, pa, wa);
+    load_codes(base, p, wa);
+    p = load_pages(base + STEP);
     for (;;) {
-      // (past the last tile the pages are -1 and block 0 is read, unused)
-      load_codes(base + STEP, pb, wb);
-      Pages pc = load_pages(base + 2 * STEP);
-      step(base, pa, wa);
+      load_codes(base + STEP, p, wb);
+      p = load_pages(base + 2 * STEP);
+      step(base, wa);
       base += STEP;
       if (base >= t1) break;
-      load_codes(base + STEP, pc, wa);
-      pa = load_pages(base + 2 * STEP);
-      step(base, pb, wb);
+      load_codes(base + STEP, p, wa);
+      p = load_pages(base + 2 * STEP);
+      step(base, wb);
       base += STEP;
       if (base >= t1) break;
-      pb = pa;
-      pa = pc;
     }
   }
 
@@ -429,43 +438,66 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
   if (chunks > 1 && t0 >= t1) return;
   const int32_t* table = a.tables + (size_t)wk.b * a.width;
 
-  // the four 16-token parts of a tile: their blocks (-1 where there is none) and scales, uniform
-  struct Parts {
-    int page[4];
-    float ks[4], vs[4];
+  // The four 16-token parts of a tile: lane l holds the table's entry for part l % 4 and the part's
+  // scales; readlane makes them uniform where they are used.  The entry is looked at one step
+  // later, so that the load stays in flight meanwhile; -1: a block of no token, or outside the pool.
+  auto load_page = [&](int base) { return table[max(min(base + 16 * (lane & 3), t1 - 1), 0) >> shift]; };
+  auto checked = [&](int base, int page) {
+    return base + 16 * (lane & 3) < t1 && (unsigned)page < (unsigned)a.cache.num_blocks ? page : -1;
   };
-  auto load_parts = [&](int base) {
-    Parts p;
+  struct Parts {
+    int page;
+    float ks, vs;
+  };
+  auto load_parts = [&](int page) {
+    const size_t at = (size_t)max(page, 0) * KV + wk.h;
+    return Parts{page, a.cache.k_scale[at], a.cache.v_scale[at]};
+  };
+  // this lane's runs of a tile, tokens 32 g + 8 j .. + 7, lie in part 2 g + j / 2
+  struct Tile {
+    Runs r;
+    bool there[2], all;  // all: no part is missing (uniform)
+  };
+  auto tile_of = [&](const Parts& p) {
+    Tile t;
+    t.all = true;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int t = base + 16 * k;
-      p.page[k] = table[max(min(t, t1 - 1), 0) >> shift];
-      if (t >= t1 || (unsigned)p.page[k] >= (unsigned)a.cache.num_blocks) p.page[k] = -1;
+    for (int g = 0; g < 2; ++g) {
+      const int page0 = __builtin_amdgcn_readlane(p.page, 2 * g), page1 = __builtin_amdgcn_readlane(p.page, 2 * g + 1);
+      t.all = t.all && page0 >= 0 && page1 >= 0;
+      auto scale = [&](float x) {
+        const float x0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 2 * g));
+        const float x1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 2 * g + 1));
+        return j >> 1 ? x1 : x0;
+      };
+      t.there[g] = (j >> 1 ? page1 : page0) >= 0;
+      float vs = scale(p.vs);
+      vs = t.there[g] && vs != 0.0f ? vs : 1.0f;
+      t.r.ks[g] = t.there[g] ? scale(p.ks) : 0.0f;
+      t.r.lv[g] = __builtin_amdgcn_logf(vs);
+      t.r.ivs[g] = __builtin_amdgcn_rcpf(vs);
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const size_t at = (size_t)max(p.page[k], 0) * KV + wk.h;
-      p.ks[k] = a.cache.k_scale[at];
-      p.vs[k] = a.cache.v_scale[at];
-    }
-    return p;
+    return t;
   };
   struct Codes {
     v4u k[LOADS], v[LOADS];
   };
   const int mask = a.cache.bs - 1;
-  auto page_of = [](const Parts& p, int part) {
-    const int lo = part & 1 ? p.page[1] : p.page[0], hi = part & 1 ? p.page[3] : p.page[2];
-    return max(part & 2 ? hi : lo, 0);
-  };
-  auto load_codes = [&](int base, const Parts& p, Codes& w) {
+  auto load_codes = [&](int base, int pages, Codes& w) {
+    int page[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) page[k] = max(__builtin_amdgcn_readlane(pages, k), 0);
+    auto page_of = [&](int part) {
+      const int lo = part & 1 ? page[1] : page[0], hi = part & 1 ? page[3] : page[2];
+      return part & 2 ? hi : lo;
+    };
 #pragma unroll
     for (int q = 0; q < LOADS; ++q) {
       const int token = tid / (D / 16) + 256 / (D / 16) * q, col = tid % (D / 16);
-      const size_t bk = (size_t)page_of(p, token >> 4) * KV + wk.h;
+      const size_t bk = (size_t)page_of(token >> 4) * KV + wk.h;
       w.k[q] = *reinterpret_cast<const v4u*>(a.cache.k_codes + (bk * a.cache.bs + ((base + token) & mask)) * D + 16 * col);
       const int d = tid / 4 + 64 * q, part = tid & 3;
-      const size_t bv = (size_t)page_of(p, part) * KV + wk.h;
+      const size_t bv = (size_t)page_of(part) * KV + wk.h;
       w.v[q] = *reinterpret_cast<const v4u*>(a.cache.v_codes + (bv * D + d) * a.cache.bs + ((base + 16 * part) & mask));
     }
   };
@@ -508,7 +540,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
     for (int d = 0; d < DT; ++d) o[t][d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  auto compute = [&](int base, const Parts& p, const TileLds<D>& in) {
+  auto products = [&](int base, const Tile& tl, const TileLds<D>& in, auto masked) {
     v4f sc[RT][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -522,27 +554,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
         for (int q = 0; q < RT; ++q) sc[q][t] = mfma16(ka, qf[q][s], sc[q][t]);
       }
     }
-    // this lane's runs: tokens 32 g + 8 j .. + 7 lie in part 2 g + j / 2
-    Runs r;
-    bool there[2];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const bool odd = j >> 1;
-      there[g] = (odd ? p.page[2 * g + 1] : p.page[2 * g]) >= 0;
-      const float ks = odd ? p.ks[2 * g + 1] : p.ks[2 * g];
-      float vs = odd ? p.vs[2 * g + 1] : p.vs[2 * g];
-      vs = !there[g] || vs == 0.0f ? 1.0f : vs;
-      r.ks[g] = there[g] ? ks : 0.0f;
-      r.lv[g] = __builtin_amdgcn_logf(vs);
-      r.ivs[g] = __builtin_amdgcn_rcpf(vs);
-    }
-    const bool masked = base + kTile > low || (p.page[0] | p.page[1] | p.page[2] | p.page[3]) < 0;
     v8h pf[RT][2];
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
       const int n = limit[q] - (base + 8 * j);
-      const int seen[2] = {there[0] ? n : 0, there[1] ? n - 32 : 0};
-      softmax_step<DT>(sc[q], fac[q], r, masked, seen, m[q], l[q], o[q], pf[q]);
+      const int seen[2] = {tl.there[0] ? n : 0, tl.there[1] ? n - 32 : 0};
+      softmax_step<DT, decltype(masked)::value>(sc[q], fac[q], tl.r, seen, m[q], l[q], o[q], pf[q]);
     }
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
@@ -562,21 +579,32 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
   };
 
   if (t0 < t1) {
-    Parts p0 = load_parts(t0), p1 = load_parts(t0 + kTile);
+    // tile by tile: pages three ahead, codes and scales two, fp16 in LDS one (past the last tile
+    // the pages are -1 and block 0 is read, unused)
+    int page = checked(t0, load_page(t0));
     Codes w;
-    load_codes(t0, p0, w);
+    load_codes(t0, page, w);
+    Parts p = load_parts(page);
+    page = checked(t0 + kTile, load_page(t0 + kTile));
     store_codes(w, lds[0]);
-    load_codes(t0 + kTile, p1, w);
+    Tile now = tile_of(p);
+    load_codes(t0 + kTile, page, w);
+    p = load_parts(page);
+    page = load_page(t0 + 2 * kTile);
     barrier();
     int buf = 0;
     for (int base = t0; base < t1; base += kTile, buf ^= 1) {
-      // (past the last tile the pages are -1 and block 0 is read, unused)
       store_codes(w, lds[buf ^ 1]);
-      const Parts p2 = load_parts(base + 2 * kTile);
-      load_codes(base + 2 * kTile, p2, w);
-      if (first < rg.vrows) compute(base, p0, lds[buf]);  // (a wave without rows only helps to load)
-      p0 = p1;
-      p1 = p2;
+      const Tile next = tile_of(p);
+      page = checked(base + 2 * kTile, page);
+      load_codes(base + 2 * kTile, page, w);
+      p = load_parts(page);
+      page = load_page(base + 3 * kTile);
+      if (first < rg.vrows) {  // (a wave without rows only helps to load)
+        if (now.all && base + kTile <= low) products(base, now, lds[buf], std::false_type());
+        else products(base, now, lds[buf], std::true_type());
+      }
+      now = next;
       barrier();
     }
   }
