@@ -19,8 +19,6 @@
 // whose codes become fp16 once, in LDS, and own their rows.  With few workgroups the tokens are
 // split over more of them (chunks), and kv_block_combine_kernel joins the chunks' maxima, sums and
 // outputs.
-#include <type_traits>
-
 #include "serve_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -151,71 +149,97 @@ struct Runs {
   float ks[2], lv[2], ivs[2];
 };
 
-// One softmax step of one tile of rows: the lane's 16 code products become weights (pf, the second
-// product's operand), and m, l, o follow.  A weight carries its run's V scale: it is 2^(score +
-// log2 vs), and the sum takes vs out again, so the codes of V stay codes.  (A zero V scale belongs
-// to codes that are all zero, so 1 serves for it.)
-template <int DT, bool MASKED>
-__device__ __forceinline__ void softmax_step(v4f* sc, float fac, const Runs& r, const int* seen,
-                                             float& m, float& l, v4f* o, v8h* pf) {
-  const float f0 = fac * r.ks[0], f1 = fac * r.ks[1];
-  float mx;
-  if constexpr (MASKED) {
+// One softmax step of RT tiles of rows: the lane's 16 code products of each become weights (pf, the
+// second product's operand), and m, l, o follow.  A weight carries its run's V scale: it is
+// 2^(score + log2 vs), and the sum takes vs out again, so the codes of V stay codes.  (A zero V scale
+// belongs to codes that are all zero, so 1 serves for it.)  The tiles of rows go through it
+// together, with one branch for all: each is a chain of dependent operations, and two chains fill
+// each other's gaps.
+template <int RT, int DT>
+__device__ __forceinline__ void softmax_step(v4f (*sc)[4], const float* fac, const Runs& r, bool masked,
+                                             const int (*seen)[2], float* m, float* l, v4f (*o)[DT],
+                                             v8h (*pf)[2]) {
+  float f[RT][2], add[2] = {r.lv[0], r.lv[1]}, mx[RT];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+  for (int q = 0; q < RT; ++q) {
+    f[q][0] = fac[q] * r.ks[0];
+    f[q][1] = fac[q] * r.ks[1];
+  }
+  if (masked) {  // (uniform) the products become scores here
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float x = __builtin_fmaf(sc[t][i], t < 2 ? f0 : f1, r.lv[t >> 1]);
-        sc[t][i] = 4 * (t & 1) + i < seen[t >> 1] ? x : -__builtin_inff();
+    for (int q = 0; q < RT; ++q) {
+      float x = -__builtin_inff();
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float y = __builtin_fmaf(sc[q][t][i], f[q][t >> 1], add[t >> 1]);
+          sc[q][t][i] = 4 * (t & 1) + i < seen[q][t >> 1] ? y : -__builtin_inff();
+        }
+        x = max3(max3(x, sc[q][t][0], sc[q][t][1]), sc[q][t][2], sc[q][t][3]);
       }
-    mx = -__builtin_inff();
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) mx = max3(mx, sc[t][i], sc[t][i + 1]);
+      mx[q] = x;
+      f[q][0] = f[q][1] = 1.0f;
+    }
+    add[0] = add[1] = 0.0f;
   } else {
-    float top[2];
+#pragma unroll
+    for (int q = 0; q < RT; ++q) {
+      float x[2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const v4f a = sc[q][2 * g], b = sc[q][2 * g + 1];
+        x[g] = max3(max3(__builtin_elementwise_maximum(a[0], a[1]), a[2], a[3]), b[0], b[1]);
+        x[g] = max3(x[g], b[2], b[3]);
+        x[g] = __builtin_fmaf(x[g], f[q][g], add[g]);
+      }
+      mx[q] = __builtin_elementwise_maximum(x[0], x[1]);
+    }
+  }
+  bool ahead = false;
+#pragma unroll
+  for (int q = 0; q < RT; ++q) {
+    mx[q] = max_quads(mx[q]);
+    ahead = ahead || mx[q] > m[q] + kLazy;
+  }
+  if (__any(ahead)) {
+#pragma unroll
+    for (int q = 0; q < RT; ++q) {
+      const float mn = __builtin_fmaxf(m[q], mx[q]);
+      const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[q] - mn);
+      m[q] = mn;
+      l[q] *= alpha;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[q][d][i] *= alpha;
+    }
+  }
+  float c[RT][2], sum[RT][2];
+#pragma unroll
+  for (int q = 0; q < RT; ++q)
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      top[g] = __builtin_elementwise_maximum(sc[2 * g][0], sc[2 * g][1]);
-#pragma unroll
-      for (int e = 2; e < 8; e += 2)
-        top[g] = max3(top[g], sc[2 * g + (e >> 2)][e & 3], sc[2 * g + (e >> 2)][(e & 3) + 1]);
+      c[q][g] = add[g] + kShift - (m[q] == -__builtin_inff() ? 0.0f : m[q]);
+      sum[q][g] = 0.0f;
     }
-    mx = __builtin_fmaxf(__builtin_fmaf(top[0], f0, r.lv[0]), __builtin_fmaf(top[1], f1, r.lv[1]));
-  }
-  mx = max_quads(mx);
-  if (__any(mx > m + kLazy)) {
-    const float mn = __builtin_fmaxf(m, mx);
-    const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
-    m = mn;
-    l *= alpha;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[d][i] *= alpha;
-  }
-  const float off = (m == -__builtin_inff() ? 0.0f : m) - kShift;
-  float sum[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int t = 0; t < 4; ++t)
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      v2f x;
-      if constexpr (MASKED) {
-        x = v2f{sc[t][i] - off, sc[t][i + 1] - off};
-      } else {
-        const float f = t < 2 ? f0 : f1, c = r.lv[t >> 1] - off;
-        x = v2f{__builtin_fmaf(sc[t][i], f, c), __builtin_fmaf(sc[t][i + 1], f, c)};
+    for (int i = 0; i < 4; i += 2)
+#pragma unroll
+      for (int q = 0; q < RT; ++q) {
+        const float f0 = f[q][t >> 1], c0 = c[q][t >> 1];
+        const v2f x = {__builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][t][i], f0, c0)),
+                       __builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][t][i + 1], f0, c0))};
+        sum[q][t >> 1] += x.x + x.y;  // (in fp32: a run of small V scale counts in the sum all the same)
+        const v2h p = __builtin_convertvector(x, v2h);
+        pf[q][t >> 1][4 * (t & 1) + i] = p.x;
+        pf[q][t >> 1][4 * (t & 1) + i + 1] = p.y;
       }
-      x = v2f{__builtin_amdgcn_exp2f(x.x), __builtin_amdgcn_exp2f(x.y)};
-      sum[t >> 1] += x.x + x.y;  // (in fp32: a run of small V scale counts in the sum all the same)
-      const v2h p = __builtin_convertvector(x, v2h);
-      pf[t >> 1][4 * (t & 1) + i] = p.x;
-      pf[t >> 1][4 * (t & 1) + i + 1] = p.y;
-    }
-  l = __builtin_fmaf(sum[0], r.ivs[0], l);
-  l = __builtin_fmaf(sum[1], r.ivs[1], l);
+#pragma unroll
+  for (int q = 0; q < RT; ++q)
+    l[q] = __builtin_fmaf(sum[q][1], r.ivs[1], __builtin_fmaf(sum[q][0], r.ivs[0], l[q]));
 }
 
 // ------------------------------------------------------------------------------------ few rows
@@ -324,12 +348,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
       }
     }
     v8h pf[RT][2];
+    int seen[RT][2];
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
       const int n = w.there ? limit[q] - (base + 16 * j) : 0;  // of this lane's 16 tokens
-      const int seen[2] = {n, n - 8};
-      softmax_step<DT, true>(sc[q], fac[q], r, seen, m[q], l[q], o[q], pf[q]);
+      seen[q][0] = n;
+      seen[q][1] = n - 8;
     }
+    softmax_step<RT, DT>(sc, fac, r, true, seen, m, l, o, pf);
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
       v8h va, vb;
@@ -456,26 +482,20 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
   // this lane's runs of a tile, tokens 32 g + 8 j .. + 7, lie in part 2 g + j / 2
   struct Tile {
     Runs r;
-    bool there[2], all;  // all: no part is missing (uniform)
+    uint32_t there;  // bit k: part k is there (uniform)
   };
   auto tile_of = [&](const Parts& p) {
+    const bool there = p.page >= 0;
+    const float vs = there && p.vs != 0.0f ? p.vs : 1.0f, ks = there ? p.ks : 0.0f;
+    const float lv = __builtin_amdgcn_logf(vs), ivs = __builtin_amdgcn_rcpf(vs);
     Tile t;
-    t.all = true;
+    t.there = (uint32_t)__ballot(there) & 15u;
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const int page0 = __builtin_amdgcn_readlane(p.page, 2 * g), page1 = __builtin_amdgcn_readlane(p.page, 2 * g + 1);
-      t.all = t.all && page0 >= 0 && page1 >= 0;
-      auto scale = [&](float x) {
-        const float x0 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 2 * g));
-        const float x1 = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), 2 * g + 1));
-        return j >> 1 ? x1 : x0;
-      };
-      t.there[g] = (j >> 1 ? page1 : page0) >= 0;
-      float vs = scale(p.vs);
-      vs = t.there[g] && vs != 0.0f ? vs : 1.0f;
-      t.r.ks[g] = t.there[g] ? scale(p.ks) : 0.0f;
-      t.r.lv[g] = __builtin_amdgcn_logf(vs);
-      t.r.ivs[g] = __builtin_amdgcn_rcpf(vs);
+      const int from = 2 * g + (j >> 1);
+      t.r.ks[g] = __shfl(ks, from);
+      t.r.lv[g] = __shfl(lv, from);
+      t.r.ivs[g] = __shfl(ivs, from);
     }
     return t;
   };
@@ -540,27 +560,32 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
     for (int d = 0; d < DT; ++d) o[t][d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  auto products = [&](int base, const Tile& tl, const TileLds<D>& in, auto masked) {
+  // K's slot of step s is the same for every token of this lane's matrix row
+  const int token0 = 8 * (c >> 2) + (c & 3);
+  int k_at[STEPS];
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) k_at[s] = token0 * D + 8 * k_slot<D>(token0, 4 * s + j);
+  auto products = [&](int base, const Tile& tl, const TileLds<D>& in) {
     v4f sc[RT][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
 #pragma unroll
-      for (int q = 0; q < RT; ++q) sc[q][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      const int token = 32 * (t >> 1) + 8 * (c >> 2) + 4 * (t & 1) + (c & 3);
-#pragma unroll
       for (int s = 0; s < STEPS; ++s) {
-        const v8h ka = *reinterpret_cast<const v8h*>(&in.k[token][8 * k_slot<D>(token, 4 * s + j)]);
+        const v8h ka = *reinterpret_cast<const v8h*>(&in.k[0][0] + k_at[s] + (32 * (t >> 1) + 4 * (t & 1)) * D);
 #pragma unroll
-        for (int q = 0; q < RT; ++q) sc[q][t] = mfma16(ka, qf[q][s], sc[q][t]);
+        for (int q = 0; q < RT; ++q) sc[q][t] = mfma16(ka, qf[q][s], s ? sc[q][t] : v4f{0.0f, 0.0f, 0.0f, 0.0f});
       }
     }
+    const bool masked = tl.there != 15u || base + kTile > low;  // (uniform)
     v8h pf[RT][2];
+    int seen[RT][2];
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
       const int n = limit[q] - (base + 8 * j);
-      const int seen[2] = {tl.there[0] ? n : 0, tl.there[1] ? n - 32 : 0};
-      softmax_step<DT, decltype(masked)::value>(sc[q], fac[q], tl.r, seen, m[q], l[q], o[q], pf[q]);
+      seen[q][0] = tl.there >> (j >> 1) & 1 ? n : 0;
+      seen[q][1] = tl.there >> (2 + (j >> 1)) & 1 ? n - 32 : 0;
     }
+    softmax_step<RT, DT>(sc, fac, tl.r, masked, seen, m, l, o, pf);
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
       const v8h va = *reinterpret_cast<const v8h*>(&in.v[16 * d + c][8 * j]);
@@ -600,10 +625,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
       load_codes(base + 2 * kTile, page, w);
       p = load_parts(page);
       page = load_page(base + 3 * kTile);
-      if (first < rg.vrows) {  // (a wave without rows only helps to load)
-        if (now.all && base + kTile <= low) products(base, now, lds[buf], std::false_type());
-        else products(base, now, lds[buf], std::true_type());
-      }
+      if (first < rg.vrows) products(base, now, lds[buf]);  // (a wave without rows only helps to load)
       now = next;
       barrier();
     }
