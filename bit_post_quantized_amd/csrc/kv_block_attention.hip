@@ -59,9 +59,9 @@ __device__ __forceinline__ v4f mfma16(v8h a, v8h b, v4f c) {
 // The largest of the four lanes l % 16 + 16 {0, 1, 2, 3}, in all of them.
 __device__ __forceinline__ float max_quads(float x) {
   const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  x = __builtin_fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  x = __builtin_elementwise_maximum(__uint_as_float(a[0]), __uint_as_float(a[1]));
   const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __builtin_fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+  return __builtin_elementwise_maximum(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
 // The IEEE maximum (a NaN stays one): the form that needs no canonical operands.
@@ -431,8 +431,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
 
 // ----------------------------------------------------------------------------------- more rows
 // A workgroup takes 64 RT rows, 16 RT to a wave, and walks over its tokens with them, 64 at a time.
-// Their codes come two tiles ahead, 16 bytes per thread and load, and become fp16 in LDS one tile
-// ahead (double buffered, one barrier per tile): K as [token][D], its 16-byte slots permuted within
+// Their codes come a tile or two ahead, 16 bytes per thread and load, and become fp16 in LDS: for 64
+// channels a tile ahead (double buffered, one barrier per tile), for 128 in one buffer, whose two
+// barriers cost less than a third workgroup on the CU gains.  K lies there as [token][D], its 16-byte slots permuted within
 // the row so that 16 matrix rows read 16 different bank groups, V as [channel][token] with a slot
 // of padding.  Lane (c, j) scores tokens 32 g + 8 j .. + 7 (g = 0, 1) for row c: K's row of matrix
 // row 4 j' + i of product t = 2 g + e is token 32 g + 8 j' + 4 e + i.
@@ -451,7 +452,8 @@ template <int D, int RT>
 __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel(
     BlockAttention a, int chunks, int groups, int chunk_tokens) {
   constexpr int DT = D / 16, STEPS = D / 32, LOADS = D / 64;
-  __shared__ __attribute__((aligned(16))) TileLds<D> lds[2];
+  constexpr int BUFS = D == 64 ? 2 : 1;
+  __shared__ __attribute__((aligned(16))) TileLds<D> lds[BUFS];
   const Work wk = work_of(a.cache.heads, chunks, groups);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, j = lane >> 4;
@@ -604,30 +606,45 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
   };
 
   if (t0 < t1) {
-    // tile by tile: pages three ahead, codes and scales two, fp16 in LDS one (past the last tile
-    // the pages are -1 and block 0 is read, unused)
+    // tile by tile: pages two or three ahead, codes and scales one or two, fp16 in LDS (past the
+    // last tile block 0 is read, unused)
     int page = checked(t0, load_page(t0));
     Codes w;
     load_codes(t0, page, w);
     Parts p = load_parts(page);
-    page = checked(t0 + kTile, load_page(t0 + kTile));
-    store_codes(w, lds[0]);
-    Tile now = tile_of(p);
-    load_codes(t0 + kTile, page, w);
-    p = load_parts(page);
-    page = load_page(t0 + 2 * kTile);
-    barrier();
-    int buf = 0;
-    for (int base = t0; base < t1; base += kTile, buf ^= 1) {
-      store_codes(w, lds[buf ^ 1]);
-      const Tile next = tile_of(p);
-      page = checked(base + 2 * kTile, page);
-      load_codes(base + 2 * kTile, page, w);
+    if constexpr (BUFS == 2) {
+      page = checked(t0 + kTile, load_page(t0 + kTile));
+      store_codes(w, lds[0]);
+      Tile now = tile_of(p);
+      load_codes(t0 + kTile, page, w);
       p = load_parts(page);
-      page = load_page(base + 3 * kTile);
-      if (first < rg.vrows) products(base, now, lds[buf]);  // (a wave without rows only helps to load)
-      now = next;
+      page = load_page(t0 + 2 * kTile);
       barrier();
+      int buf = 0;
+      for (int base = t0; base < t1; base += kTile, buf ^= 1) {
+        store_codes(w, lds[buf ^ 1]);
+        const Tile next = tile_of(p);
+        page = checked(base + 2 * kTile, page);
+        load_codes(base + 2 * kTile, page, w);
+        p = load_parts(page);
+        page = load_page(base + 3 * kTile);
+        if (first < rg.vrows) products(base, now, lds[buf]);  // (a wave without rows only helps to load)
+        now = next;
+        barrier();
+      }
+    } else {
+      page = load_page(t0 + kTile);
+      for (int base = t0; base < t1; base += kTile) {
+        store_codes(w, lds[0]);
+        const Tile now = tile_of(p);
+        page = checked(base + kTile, page);
+        load_codes(base + kTile, page, w);
+        p = load_parts(page);
+        page = load_page(base + 2 * kTile);
+        barrier();
+        if (first < rg.vrows) products(base, now, lds[0]);
+        barrier();
+      }
     }
   }
 
