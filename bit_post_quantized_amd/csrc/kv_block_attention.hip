@@ -504,23 +504,29 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
   struct Codes {
     v4u k[LOADS], v[LOADS];
   };
+  // K: a wave loads 16 tokens or fewer of one part, so the block is uniform; V: a thread loads 16
+  // tokens of one channel in part tid % 4, the one whose table entry its lane holds.
   const int mask = a.cache.bs - 1;
-  auto load_codes = [&](int base, int pages, Codes& w) {
-    int page[4];
+  const uint32_t block_bytes = (uint32_t)KV * a.cache.bs * D;
+  const uint32_t head_bytes = (uint32_t)wk.h * a.cache.bs * D;
+  uint32_t k_off[LOADS];
+  const uint8_t* v_base[LOADS];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) page[k] = max(__builtin_amdgcn_readlane(pages, k), 0);
-    auto page_of = [&](int part) {
-      const int lo = part & 1 ? page[1] : page[0], hi = part & 1 ? page[3] : page[2];
-      return part & 2 ? hi : lo;
-    };
+  for (int q = 0; q < LOADS; ++q) {
+    const int token = tid / (D / 16) + 256 / (D / 16) * q;
+    k_off[q] = head_bytes + (token & mask) * D + 16 * (tid % (D / 16));
+    v_base[q] = a.cache.v_codes + head_bytes + (tid / 4 + 64 * q) * a.cache.bs + (16 * (tid & 3) & mask);
+  }
+  auto load_codes = [&](int base, int pages, Codes& w) {
+    const int in = base & mask;  // (a tile begins inside a block of 128 only)
+    const uint64_t at = (uint64_t)(uint32_t)max(pages, 0) * block_bytes + in;
 #pragma unroll
     for (int q = 0; q < LOADS; ++q) {
-      const int token = tid / (D / 16) + 256 / (D / 16) * q, col = tid % (D / 16);
-      const size_t bk = (size_t)page_of(token >> 4) * KV + wk.h;
-      w.k[q] = *reinterpret_cast<const v4u*>(a.cache.k_codes + (bk * a.cache.bs + ((base + token) & mask)) * D + 16 * col);
-      const int d = tid / 4 + 64 * q, part = tid & 3;
-      const size_t bv = (size_t)page_of(part) * KV + wk.h;
-      w.v[q] = *reinterpret_cast<const v4u*>(a.cache.v_codes + (bv * D + d) * a.cache.bs + ((base + 16 * part) & mask));
+      const int part = (wave * 64 / (D / 16) + 256 / (D / 16) * q) >> 4;
+      const uint32_t page = (uint32_t)max(__builtin_amdgcn_readlane(pages, part), 0);
+      const uint8_t* k = a.cache.k_codes + ((uint64_t)page * block_bytes + in * D);
+      w.k[q] = *reinterpret_cast<const v4u*>(k + k_off[q]);
+      w.v[q] = *reinterpret_cast<const v4u*>(v_base[q] + at);
     }
   };
   auto store_codes = [&](const Codes& w, TileLds<D>& to) {
