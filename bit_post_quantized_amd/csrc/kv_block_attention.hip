@@ -430,13 +430,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
 }
 
 // ----------------------------------------------------------------------------------- more rows
-// A workgroup takes 64 RT rows, 16 RT to a wave, and walks over its tokens with them, 64 at a time.
+// A workgroup takes 16 RT rows per wave and walks over its tokens with them, 64 at a time.
 // Their codes come a tile or two ahead, 16 bytes per thread and load, and become fp16 in LDS: for 64
 // channels a tile ahead (double buffered, one barrier per tile), for 128 in one buffer, whose two
-// barriers cost less than a third workgroup on the CU gains.  K lies there as [token][D], its 16-byte slots permuted within
-// the row so that 16 matrix rows read 16 different bank groups, V as [channel][token] with a slot
-// of padding.  Lane (c, j) scores tokens 32 g + 8 j .. + 7 (g = 0, 1) for row c: K's row of matrix
-// row 4 j' + i of product t = 2 g + e is token 32 g + 8 j' + 4 e + i.
+// barriers cost less than a third workgroup on the CU gains (66 against 71 us for 2 x 5 rows of 32
+// heads before 131071 tokens).  K lies there as [token][D], its 16-byte slots permuted within the
+// row so that 16 matrix rows read 16 different bank groups, V as [channel][token] with a slot of
+// padding.  Lane (c, j) scores tokens 32 g + 8 j .. + 7 (g = 0, 1) for row c: K's row of matrix row
+// 4 j' + i of product t = 2 g + e is token 32 g + 8 j' + 4 e + i.
 template <int D>
 struct TileLds {
   uint16_t k[kTile][D];
@@ -448,10 +449,10 @@ __device__ __forceinline__ int k_slot(int token, int slot) {
   return D == 64 ? slot ^ ((token >> 3 & 3) * 2 | (token >> 1 & 1)) : slot ^ ((token >> 3 & 3) * 4 | (token & 3));
 }
 
-template <int D, int RT>
-__global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel(
+template <int D, int RT, int WAVES>
+__global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_attention_rows_kernel(
     BlockAttention a, int chunks, int groups, int chunk_tokens) {
-  constexpr int DT = D / 16, STEPS = D / 32, LOADS = D / 64;
+  constexpr int DT = D / 16, STEPS = D / 32, THREADS = 64 * WAVES, ITEMS = 8 * D / THREADS;
   constexpr int BUFS = D == 64 ? 2 : 1;
   __shared__ __attribute__((aligned(16))) TileLds<D> lds[BUFS];
   const Work wk = work_of(a.cache.heads, chunks, groups);
@@ -459,9 +460,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
   const int c = lane & 15, j = lane >> 4;
   const int KV = a.cache.heads, shift = __builtin_ctz(a.cache.bs);
   const Range rg(a, wk.b);
-  const int vr0 = wk.group * 64 * RT;
+  constexpr int ROWS = 16 * RT * WAVES;
+  const int vr0 = (groups - 1 - wk.group) * ROWS;  // the rows that see most tokens begin first
   if (vr0 >= rg.vrows) return;
-  const int top = rg.limit(a, min(vr0 + 64 * RT, rg.vrows) - 1), low = rg.limit(a, vr0);
+  const int top = rg.limit(a, min(vr0 + ROWS, rg.vrows) - 1);
   const int t0 = wk.chunk * chunk_tokens, t1 = min(t0 + chunk_tokens, top);
   if (chunks > 1 && t0 >= t1) return;
   const int32_t* table = a.tables + (size_t)wk.b * a.width;
@@ -501,46 +503,44 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
     }
     return t;
   };
+  // A tile's codes are 4 D pieces of 16 bytes each for K and V, ITEMS of them to a thread.  K: a
+  // wave takes 16 tokens or fewer of one part, so the block is uniform; V: a thread takes 16 tokens
+  // of one channel in part tid % 4, the one whose table entry its lane holds.
   struct Codes {
-    v4u k[LOADS], v[LOADS];
+    v4u x[ITEMS];
   };
-  // K: a wave loads 16 tokens or fewer of one part, so the block is uniform; V: a thread loads 16
-  // tokens of one channel in part tid % 4, the one whose table entry its lane holds.
   const int mask = a.cache.bs - 1;
   const uint32_t block_bytes = (uint32_t)KV * a.cache.bs * D;
-  const uint32_t head_bytes = (uint32_t)wk.h * a.cache.bs * D;
-  uint32_t k_off[LOADS];
-  const uint8_t* v_base[LOADS];
+  auto is_k = [&](int i) { return ITEMS == 1 ? wave < WAVES / 2 : i < ITEMS / 2; };
+  auto piece = [&](int i) { return tid + THREADS * i - (is_k(i) ? 0 : 4 * D); };
+  uint32_t off[ITEMS];
 #pragma unroll
-  for (int q = 0; q < LOADS; ++q) {
-    const int token = tid / (D / 16) + 256 / (D / 16) * q;
-    k_off[q] = head_bytes + (token & mask) * D + 16 * (tid % (D / 16));
-    v_base[q] = a.cache.v_codes + head_bytes + (tid / 4 + 64 * q) * a.cache.bs + (16 * (tid & 3) & mask);
+  for (int i = 0; i < ITEMS; ++i) {
+    const int x = piece(i), token = x / (D / 16);
+    off[i] = (uint32_t)wk.h * a.cache.bs * D +
+             (is_k(i) ? (token & mask) * D + 16 * (x % (D / 16)) : x / 4 * a.cache.bs + (16 * (x & 3) & mask));
   }
   auto load_codes = [&](int base, int pages, Codes& w) {
     const int in = base & mask;  // (a tile begins inside a block of 128 only)
-    const uint64_t at = (uint64_t)(uint32_t)max(pages, 0) * block_bytes + in;
 #pragma unroll
-    for (int q = 0; q < LOADS; ++q) {
-      const int part = (wave * 64 / (D / 16) + 256 / (D / 16) * q) >> 4;
-      const uint32_t page = (uint32_t)max(__builtin_amdgcn_readlane(pages, part), 0);
-      const uint8_t* k = a.cache.k_codes + ((uint64_t)page * block_bytes + in * D);
-      w.k[q] = *reinterpret_cast<const v4u*>(k + k_off[q]);
-      w.v[q] = *reinterpret_cast<const v4u*>(v_base[q] + at);
+    for (int i = 0; i < ITEMS; ++i) {
+      const int part = ((wave * 64 + THREADS * i) / (D / 16) >> 4) & 3;
+      const uint32_t uniform = (uint32_t)max(__builtin_amdgcn_readlane(pages, part), 0);
+      const uint32_t page = is_k(i) ? uniform : (uint32_t)max(pages, 0);
+      const uint8_t* codes = is_k(i) ? a.cache.k_codes + in * D : a.cache.v_codes + in;
+      w.x[i] = *reinterpret_cast<const v4u*>(codes + (uint64_t)page * block_bytes + off[i]);
     }
   };
   auto store_codes = [&](const Codes& w, TileLds<D>& to) {
 #pragma unroll
-    for (int q = 0; q < LOADS; ++q) {
-      const int token = tid / (D / 16) + 256 / (D / 16) * q, col = tid % (D / 16);
-      v8h x, y;
-      codes16_f16(w.k[q], x, y);
-      *reinterpret_cast<v8h*>(&to.k[token][8 * k_slot<D>(token, 2 * col)]) = x;
-      *reinterpret_cast<v8h*>(&to.k[token][8 * k_slot<D>(token, 2 * col + 1)]) = y;
-      const int d = tid / 4 + 64 * q, part = tid & 3;
-      codes16_f16(w.v[q], x, y);
-      *reinterpret_cast<v8h*>(&to.v[d][16 * part]) = x;
-      *reinterpret_cast<v8h*>(&to.v[d][16 * part + 8]) = y;
+    for (int i = 0; i < ITEMS; ++i) {
+      const int x = piece(i), token = x / (D / 16), col = x % (D / 16);
+      v8h lo, hi;
+      codes16_f16(w.x[i], lo, hi);
+      uint16_t* at = is_k(i) ? &to.k[token][8 * k_slot<D>(token, 2 * col)] : &to.v[x / 4][16 * (x & 3)];
+      uint16_t* next = is_k(i) ? &to.k[token][8 * k_slot<D>(token, 2 * col + 1)] : at + 8;
+      *reinterpret_cast<v8h*>(at) = lo;
+      *reinterpret_cast<v8h*>(next) = hi;
     }
   };
 
@@ -549,6 +549,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
   int limit[RT];
   v4f o[RT][DT];
   const int first = vr0 + 16 * RT * wave;
+  // what the wave's first and last row see (a wave without rows only helps to load)
+  const int low = rg.limit(a, min(first, rg.vrows - 1));
+  const int high = first < rg.vrows ? rg.limit(a, min(first + 16 * RT, rg.vrows) - 1) : 0;
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int vr = min(first + 16 * t + c, rg.vrows - 1);
@@ -634,7 +637,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
         load_codes(base + 2 * kTile, page, w);
         p = load_parts(page);
         page = load_page(base + 3 * kTile);
-        if (first < rg.vrows) products(base, now, lds[buf]);  // (a wave without rows only helps to load)
+        if (base < high) products(base, now, lds[buf]);
         now = next;
         barrier();
       }
@@ -648,7 +651,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
         p = load_parts(page);
         page = load_page(base + 2 * kTile);
         barrier();
-        if (first < rg.vrows) products(base, now, lds[0]);
+        if (base < high) products(base, now, lds[0]);
         barrier();
       }
     }
@@ -679,9 +682,67 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_rows_kernel
 }
 
 // --------------------------------------------------------------------------------------- join
-// Joins the chunks of one (row, head).  256 threads: the chunks' weights 2^(m_k - M) go through
-// LDS, then a thread adds one channel of every (256 / D)-th chunk, several loads in flight.
 constexpr int kJoinThreads = 256;
+
+// The chunks that were written of row i, head h of a request: those below the tokens that the last
+// row of its group sees.
+__device__ __forceinline__ int chunks_of(const BlockAttention& a, const Range& rg, int i, int h, int chunks,
+                                         int chunk_tokens, int span) {
+  const int vr = i * rg.hg + h % rg.hg;
+  const int top = rg.limit(a, min((vr / span + 1) * span, rg.vrows) - 1);
+  return min((top + chunk_tokens - 1) / chunk_tokens, chunks);
+}
+
+// Joins up to kFewChunks chunks: a lane adds four channels of a (row, head), and the
+// lanes of a (row, head) find its chunks' weights 2^(m_k - M) together, one chunk each.  (A workgroup
+// per (row, head), as below, takes 110 us more than this for 2 chunks of 2950 rows x 24 heads.)
+constexpr int kFewChunks = 16;
+
+template <int D>
+__global__ __launch_bounds__(kJoinThreads) void kv_block_join_kernel(BlockAttention a, int chunks,
+                                                                     int chunk_tokens, int span, unsigned joins) {
+  constexpr int LANES = D / 4;
+  const int lane = threadIdx.x & (LANES - 1);
+  unsigned id = blockIdx.x * (kJoinThreads / LANES) + threadIdx.x / LANES;
+  if (id >= joins) return;
+  const int h = id % a.heads;
+  id /= a.heads;
+  const int i = id % a.max_rows, b = id / a.max_rows;
+  const Range rg(a, b);
+  if (i >= rg.n) return;
+  const int used = chunks_of(a, rg, i, h, chunks, chunk_tokens, span);
+  const size_t at = (size_t)(rg.row0 + i) * a.heads + h;
+  const float* ws = a.ws + at * chunks * (D + 4);
+  const v2f ms = *reinterpret_cast<const v2f*>(ws + min(lane, max(used - 1, 0)) * (D + 4));
+  const float m = lane < used ? ms.x : -__builtin_inff();
+  float mm = m;
+#pragma unroll
+  for (int x = 1; x < LANES; x <<= 1) mm = __builtin_fmaxf(mm, __shfl_xor(mm, x));
+  const float f = __builtin_amdgcn_exp2f(m - (mm == -__builtin_inff() ? 0.0f : mm));
+  float sum = lane < used ? ms.y * f : 0.0f;
+#pragma unroll
+  for (int x = 1; x < LANES; x <<= 1) sum += __shfl_xor(sum, x);
+  v4f out = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k = 0; k < used; k += 4) {
+    v4f v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const v4f*>(ws + min(k + u, used - 1) * (D + 4) + 4 + 4 * lane);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float w = __shfl(f, k + u, LANES);
+      if (k + u < used)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = __builtin_fmaf(v[u][e], w, out[e]);
+    }
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  *reinterpret_cast<v2u*>(a.out + at * D + 4 * lane) =
+      v2u{pack2_bf16(out[0] * inv, out[1] * inv), pack2_bf16(out[2] * inv, out[3] * inv)};
+}
+
+// Joins more chunks of few rows, one (row, head) per workgroup (a lane of the kernel above would add
+// them one after the other).  256 threads: the chunks' weights 2^(m_k - M) go through
+// LDS, then a thread adds one channel of every (256 / D)-th chunk, several loads in flight.
 constexpr int kMaxChunks = 1024;
 
 template <int D>
@@ -698,10 +759,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Range rg(a, b);
   if (i >= rg.n) return;
-  // the chunks that the workgroups of this row's group wrote: those below the tokens its last row sees
-  const int vr = i * rg.hg + h % rg.hg;
-  const int top = rg.limit(a, min((vr / span + 1) * span, rg.vrows) - 1);
-  const int used = min((top + chunk_tokens - 1) / chunk_tokens, chunks);
+  const int used = chunks_of(a, rg, i, h, chunks, chunk_tokens, span);
   const size_t at = (size_t)(rg.row0 + i) * a.heads + h;
   const float* ws = a.ws + at * chunks * (D + 4);
   // four chunks to a thread at most: their maxima and sums
@@ -756,16 +814,27 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
   }
 }
 
-// How a call is split, from its sizes alone.  Up to 16 rows (row x head) per request and cached head,
-// 32 of 64 channels (128 would need more registers than there are), go to the few-rows kernel; more to the other, 128 to a workgroup, or 64 where that would leave
-// CUs idle or rows empty.
+// How a batch is cut, from sizes the host knows (lengths are the device's).  Up to 16 query rows per
+// cached head (32 at 64 channels) the few-rows kernel: at 5 rows of 8 heads it would need three row
+// tiles and spill.  Above, a workgroup takes 64 rows, or 128 if there are more: at 64 channels in
+// eight waves of 16 (85 against 97 us for four of 32 on 4 prompts of 475..1000 rows: more waves to
+// hide the softmax's latency), at 128 in four waves of 32 (454 against 605 us on 4096 rows before
+// 8192 tokens: an LDS read feeds two products).
+//
+// Few rows: the codes are read at 5.2 TB/s by one workgroup on each CU, and a join costs 5 us, so
+// tokens are cut only as far as that fills (32768 tokens, 8 heads: 174 us uncut, 22.1 in 32 chunks,
+// 24.1 in 64, 30.8 in 128; 24 requests of 2048, 8 heads: 12.4 uncut, 17.5 in two).  A chunk is 16384
+// tokens at most, so that one long request among short ones does not end up in few workgroups.
+// More rows: cut so that the workgroups fit the chip at once, if the tiles saved (1.2 us each) take
+// longer than the join (6 us and its bytes at 4 TB/s): 2 x 5 rows before 131071 tokens 91 us in 32
+// chunks, 66 in 64, 60 in 96; 2 prompts of 1024 rows, 12 heads: 22.7 us uncut, 30 in two.
 struct Split {
   bool few;
   int rt, groups, chunks, chunk_tokens;
   int span() const { return (few ? 16 : 64) * rt; }
 };
 
-static Split split_of(int requests, int max_rows, int heads, int kv_heads, int dim, int width, int bs) {
+static Split split_of(int requests, int rows, int max_rows, int heads, int kv_heads, int dim, int width, int bs) {
   Split s;
   const long long vrows = (long long)max_rows * (heads / kv_heads);
   s.few = vrows <= (dim == 64 ? 32 : 16);
@@ -773,12 +842,21 @@ static Split split_of(int requests, int max_rows, int heads, int kv_heads, int d
   s.groups = (int)((vrows + s.span() - 1) / s.span());
   const long long natural = (long long)requests * kv_heads * s.groups;
   const long long tokens = (long long)width * bs;
-  // enough workgroups for 256 CUs, each with a few tiles to itself
   const int unit = s.few ? kWaves * kTile : 4 * kTile;
-  const long long want = ((s.few ? 1024 : 512) + natural - 1) / natural;
-  long long most = (tokens + unit - 1) / unit;
-  if (most > kMaxChunks) most = kMaxChunks;
-  long long chunks = want < most ? want : most;
+  long long chunks = (s.few ? 256 : s.rt == 1 ? 768 : 512) / natural;
+  if (s.few) {
+    const long long least = (tokens + 16383) / 16384;
+    if (chunks < least) chunks = least;
+  }
+  const long long most = (tokens + unit - 1) / unit;
+  if (chunks > most) chunks = most;
+  if (chunks > kMaxChunks) chunks = kMaxChunks;
+  if (!s.few && chunks > 1) {
+    long long joins = (long long)requests * max_rows;
+    joins = (joins < rows ? joins : rows) * heads;
+    const long long saved = tokens / kTile * (chunks - 1) / chunks * 1200;  // ns
+    if (saved < 6000 + joins * chunks * (dim + 4) * 8 / 4000) chunks = 1;
+  }
   if (chunks < 1) chunks = 1;
   long long per = (tokens + chunks - 1) / chunks;
   per = (per + unit - 1) / unit * unit;
@@ -790,28 +868,37 @@ static Split split_of(int requests, int max_rows, int heads, int kv_heads, int d
 size_t kv_block_attention_ws_bytes(int requests, int rows, int max_rows, int heads, int kv_heads,
                                    int dim, int width, int bs) {
   if (requests <= 0 || rows <= 0) return 0;
-  const Split s = split_of(requests, max_rows, heads, kv_heads, dim, width, bs);
+  const Split s = split_of(requests, rows, max_rows, heads, kv_heads, dim, width, bs);
   return s.chunks == 1 ? 0 : (size_t)rows * heads * s.chunks * (dim + 4) * sizeof(float);
 }
 
 template <int D>
 static hipError_t launch(const BlockAttention& a, hipStream_t stream) {
-  const Split s = split_of(a.requests, a.max_rows, a.heads, a.cache.heads, D, a.width, a.cache.bs);
+  const Split s = split_of(a.requests, a.rows, a.max_rows, a.heads, a.cache.heads, D, a.width, a.cache.bs);
   const long long grid = (long long)a.requests * s.groups * s.chunks * a.cache.heads;
   const long long joins = (long long)a.requests * a.max_rows * a.heads;
-  if (grid > 0x7FFFFFFFLL || (s.chunks > 1 && joins > 0x7FFFFFFFLL)) return hipErrorInvalidConfiguration;
-#define SVDQ_ATTEND(KERNEL, RT)                                                                  \
-  hipLaunchKernelGGL((KERNEL<D, RT>), dim3((unsigned)grid), dim3(kWaves * 64), 0, stream, a,     \
+  const int each = s.chunks <= kFewChunks ? kJoinThreads / (D / 4) : 1;
+  const long long join_grid = (joins + each - 1) / each;
+  // a launch has fewer than 2^32 threads
+  if (grid >= 1 << 23 || (s.chunks > 1 && join_grid >= 1 << 24)) return hipErrorInvalidConfiguration;
+#define SVDQ_ATTEND(WAVES, ...)                                                                  \
+  hipLaunchKernelGGL((__VA_ARGS__), dim3((unsigned)grid), dim3(WAVES * 64), 0, stream, a,        \
                      s.chunks, s.groups, s.chunk_tokens)
-  if (s.few && s.rt == 1) SVDQ_ATTEND(kv_block_attention_kernel, 1);
-  else if (s.few) SVDQ_ATTEND(kv_block_attention_kernel, (D == 64 ? 2 : 1));
-  else if (s.rt == 1) SVDQ_ATTEND(kv_block_attention_rows_kernel, 1);
-  else SVDQ_ATTEND(kv_block_attention_rows_kernel, 2);
+  if (s.few && s.rt == 1) SVDQ_ATTEND(kWaves, kv_block_attention_kernel<D, 1>);
+  else if (s.few) SVDQ_ATTEND(kWaves, kv_block_attention_kernel<D, (D == 64 ? 2 : 1)>);  // (128: never)
+  else if (s.rt == 1) SVDQ_ATTEND(4, kv_block_attention_rows_kernel<D, 1, 4>);
+  else if constexpr (D == 64) SVDQ_ATTEND(8, kv_block_attention_rows_kernel<D, 1, 8>);
+  else SVDQ_ATTEND(4, kv_block_attention_rows_kernel<D, 2, 4>);
 #undef SVDQ_ATTEND
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || s.chunks == 1) return e;
-  hipLaunchKernelGGL(kv_block_combine_kernel<D>, dim3((unsigned)joins), dim3(kJoinThreads), 0, stream,
-                     a, s.chunks, s.chunk_tokens, s.span());
+  if (s.chunks <= kFewChunks) {
+    hipLaunchKernelGGL(kv_block_join_kernel<D>, dim3((unsigned)join_grid), dim3(kJoinThreads), 0, stream,
+                       a, s.chunks, s.chunk_tokens, s.span(), (unsigned)joins);
+  } else {
+    hipLaunchKernelGGL(kv_block_combine_kernel<D>, dim3((unsigned)join_grid), dim3(kJoinThreads), 0, stream,
+                       a, s.chunks, s.chunk_tokens, s.span());
+  }
   return hipGetLastError();
 }
 
