@@ -434,20 +434,22 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
 // Their codes come a tile or two ahead, 16 bytes per thread and load, and become fp16 in LDS: for 64
 // channels a tile ahead (double buffered, one barrier per tile), for 128 in one buffer, whose two
 // barriers cost less than a third workgroup on the CU gains (66 against 71 us for 2 x 5 rows of 32
-// heads before 131071 tokens).  K lies there as [token][D], its 16-byte slots permuted within the
-// row so that 16 matrix rows read 16 different bank groups, V as [channel][token] with a slot of
-// padding.  Lane (c, j) scores tokens 32 g + 8 j .. + 7 (g = 0, 1) for row c: K's row of matrix row
-// 4 j' + i of product t = 2 g + e is token 32 g + 8 j' + 4 e + i.
+// heads before 131071 tokens).  K lies there as [token][D], V as [channel][token], the 16-byte slots
+// of both permuted within the row so that the 16 lanes which read a matrix operand, or write 16
+// pieces, meet 16 different bank groups.  Lane (c, j) scores tokens 32 g + 8 j .. + 7 (g = 0, 1) for
+// row c: K's row of matrix row 4 j' + i of product t = 2 g + e is token 32 g + 8 j' + 4 e + i.
 template <int D>
 struct TileLds {
   uint16_t k[kTile][D];
-  uint16_t v[D][kTile + 8];
+  uint16_t v[D][kTile];
 };
 
 template <int D>
 __device__ __forceinline__ int k_slot(int token, int slot) {
   return D == 64 ? slot ^ ((token >> 3 & 3) * 2 | (token >> 1 & 1)) : slot ^ ((token >> 3 & 3) * 4 | (token & 3));
 }
+
+__device__ __forceinline__ int v_slot(int d, int slot) { return slot ^ (d >> 1 & 7); }
 
 template <int D, int RT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_attention_rows_kernel(
@@ -537,8 +539,8 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
       const int x = piece(i), token = x / (D / 16), col = x % (D / 16);
       v8h lo, hi;
       codes16_f16(w.x[i], lo, hi);
-      uint16_t* at = is_k(i) ? &to.k[token][8 * k_slot<D>(token, 2 * col)] : &to.v[x / 4][16 * (x & 3)];
-      uint16_t* next = is_k(i) ? &to.k[token][8 * k_slot<D>(token, 2 * col + 1)] : at + 8;
+      uint16_t* at = is_k(i) ? &to.k[token][8 * k_slot<D>(token, 2 * col)] : &to.v[x / 4][8 * v_slot(x / 4, 2 * (x & 3))];
+      uint16_t* next = is_k(i) ? &to.k[token][8 * k_slot<D>(token, 2 * col + 1)] : &to.v[x / 4][8 * v_slot(x / 4, 2 * (x & 3) + 1)];
       *reinterpret_cast<v8h*>(at) = lo;
       *reinterpret_cast<v8h*>(next) = hi;
     }
@@ -576,6 +578,7 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
   int k_at[STEPS];
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) k_at[s] = token0 * D + 8 * k_slot<D>(token0, 4 * s + j);
+  const int va_at = c * kTile + 8 * v_slot(c, j), vb_at = c * kTile + 8 * v_slot(c, 4 + j);
   auto products = [&](int base, const Tile& tl, const TileLds<D>& in) {
     v4f sc[RT][4];
 #pragma unroll
@@ -599,8 +602,8 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
     softmax_step<RT, DT>(sc, fac, tl.r, masked, seen, m, l, o, pf);
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
-      const v8h va = *reinterpret_cast<const v8h*>(&in.v[16 * d + c][8 * j]);
-      const v8h vb = *reinterpret_cast<const v8h*>(&in.v[16 * d + c][32 + 8 * j]);
+      const v8h va = *reinterpret_cast<const v8h*>(&in.v[16 * d][0] + va_at);
+      const v8h vb = *reinterpret_cast<const v8h*>(&in.v[16 * d][0] + vb_at);
 #pragma unroll
       for (int q = 0; q < RT; ++q) {
         o[q][d] = mfma16(va, pf[q][0], o[q][d]);
