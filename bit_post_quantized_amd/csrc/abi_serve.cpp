@@ -54,13 +54,6 @@ extern "C" {
 
 int svdq_serve_version(void) { return SVDQ_SERVE_VERSION; }
 
-size_t svdq_w4a16_workspace_bytes(int M, int N, int K, int r, int out_dtype) {
-  if (M <= 0 || M > kMaxFewRows || N <= 0 || K <= 0 || K % 64 != 0 || K / 64 > 65535 || r < 0 ||
-      r > kMaxRank)
-    return 0;
-  return svdq::w4a16_workspace_bytes(M, K, r, out_dtype == SVDQ_OUT_FP32);
-}
-
 static int check_w4a16(int N, int K) {
   if (N <= 0) return fail(SVDQ_EINVAL, "N must be positive (got %d)", N);
   if (int s = check_k(K)) return s;
@@ -68,6 +61,11 @@ static int check_w4a16(int N, int K) {
   if (K / 64 > 65535) return fail(SVDQ_ESHAPE, "K / 64 must be <= 65535 (got K = %d)", K);
   if ((long long)N * K > kMaxElems) return fail(SVDQ_ESHAPE, "problem too large");
   return SVDQ_OK;
+}
+
+size_t svdq_w4a16_workspace_bytes(int M, int N, int K, int r, int out_dtype) {
+  if (M <= 0 || M > kMaxFewRows || r < 0 || r > kMaxRank || check_w4a16(N, K)) return 0;
+  return svdq::w4a16_workspace_bytes(M, N, K, r, out_dtype == SVDQ_OUT_FP32);
 }
 
 size_t svdq_w4a16_container_bytes(int N, int K) {

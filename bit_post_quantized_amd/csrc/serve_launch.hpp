@@ -13,7 +13,7 @@ size_t w4a16_container_bytes(int N, int K);
 hipError_t launch_w4a16_pack(const uint8_t* wq, const uint16_t* w_scales, int N, int K,
                              uint8_t* container, hipStream_t stream);
 
-size_t w4a16_workspace_bytes(int M, int K, int r, int out_fp32);
+size_t w4a16_workspace_bytes(int M, int N, int K, int r, int out_fp32);
 hipError_t launch_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const uint16_t* L1p,
                              const uint8_t* container, const uint16_t* L2p, const uint16_t* bias,
                              int M, int N, int K, int r, void* Y, int out_fp32, void* workspace,

@@ -95,22 +95,57 @@ inline int w4a16_slices(int K) {
   return s < kMaxSlices ? s : kMaxSlices;
 }
 
-struct W4a16Ws {
-  size_t frags, scales, parts, bytes;  // byte offsets and the total
+// Up to 4 row tiles share a pass over the weights (64 bf16 rows, 32 fp32 rows).  What a wave holds
+// of X^ is 8 registers per row tile and group, so more row tiles mean fewer groups to a chunk.
+constexpr int kMaxTiles = 4;
+constexpr int groups_per_wave(int tiles) { return tiles <= 2 ? 8 : 4; }
+
+// How a pass is cut.  One persistent workgroup per CU.  Where K is more than a workgroup's waves
+// hold of X^, it is cut into chunks: the workgroups of a column tile take one each and their sums go
+// through memory (shares), or with few rows one workgroup walks over them all and reads X^ again.
+struct W4a16Pass {
+  int rows, shares, grid;
+  bool loop;
 };
 
-inline W4a16Ws w4a16_layout(int M, int K, int r, int out_fp32) {
+inline W4a16Pass w4a16_pass(int M, int N, int K, int tile0, int tiles, int out_fp32) {
+  const int rpt = w4a16_rows_per_tile(out_fp32);
+  const int mt = tiles - tile0 < kMaxTiles ? tiles - tile0 : kMaxTiles;
+  const int per = kWaves * groups_per_wave(mt), chunks = (K / kGroup + per - 1) / per;
+  W4a16Pass p;
+  p.rows = M - tile0 * rpt < mt * rpt ? M - tile0 * rpt : mt * rpt;
+  p.loop = chunks > 1 && mt == 1;
+  p.shares = p.loop ? 1 : chunks;
+  // a multiple of 8, for the XCDs
+  const int run = ((N + 15) / 16 + 7) / 8, most = 32 / p.shares < 1 ? 1 : 32 / p.shares;
+  p.grid = 8 * p.shares * (run < most ? run : most);
+  return p;
+}
+
+struct W4a16Ws {
+  size_t frags, scales, parts, partial, bytes;  // byte offsets and the total
+};
+
+inline W4a16Ws w4a16_layout(int M, int N, int K, int r, int out_fp32) {
   const size_t tiles = w4a16_tiles(M, out_fp32), G = K / kGroup;
   W4a16Ws w;
   w.frags = 0;
   w.scales = tiles * G * kFragBytes;
   w.parts = w.scales + tiles * w4a16_segments(K) * 16 * sizeof(float);
-  w.bytes = w.parts + (size_t)w4a16_slices(K) * M * r * sizeof(float);
+  w.partial = w.parts + (size_t)w4a16_slices(K) * M * r * sizeof(float);
+  w.partial = (w.partial + 15) / 16 * 16;
+  size_t most = 0;
+  for (int t = 0; t < (int)tiles; t += kMaxTiles) {
+    const W4a16Pass p = w4a16_pass(M, N, K, t, (int)tiles, out_fp32);
+    const size_t need = p.shares == 1 ? 0 : (size_t)p.shares * p.rows * ((N + 15) / 16 * 16) * sizeof(float);
+    most = need > most ? need : most;
+  }
+  w.bytes = w.partial + most;
   return w;
 }
 
-size_t w4a16_workspace_bytes(int M, int K, int r, int out_fp32) {
-  return w4a16_layout(M, K, r, out_fp32).bytes;
+size_t w4a16_workspace_bytes(int M, int N, int K, int r, int out_fp32) {
+  return w4a16_layout(M, N, K, r, out_fp32).bytes;
 }
 
 // Eight packed nibbles -> eight exact fp16 codes, in the order k0 k4 k1 k5 k2 k6 k3 k7.  A nibble
@@ -287,28 +322,29 @@ struct Rows {
 // wave's X^ stays in registers for all its column tiles; otherwise it is read again per chunk, a
 // chunk ahead.  STAGES - 1 steps of weights are in flight.  RANK: there is a low-rank branch.
 template <int MT, int GPW, bool HOLD, bool FP32, bool RANK>
-__global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
+__global__ __launch_bounds__(kWaves * 64, 1) void w4a16_kernel(
     const v8h* __restrict__ frags, const float* __restrict__ scales,
     const float* __restrict__ parts, int slices, const uint8_t* __restrict__ container,
     const uint16_t* __restrict__ L2p, const uint16_t* __restrict__ bias, int M, int N, int K,
-    int r, int tile0, int tiles, void* __restrict__ Y) {
+    int r, int tile0, int tiles, int shares, float* __restrict__ partial, void* __restrict__ Y) {
   constexpr int RPT = FP32 ? 8 : 16;
   constexpr int TERMS = FP32 ? 3 : 2;  // bf16 terms of T: 24 or 16 bits
-  __shared__ float red[2][kWaves][MT * 16][17];
+  __shared__ __attribute__((aligned(16))) float red[2][kWaves][MT * 16][17];
   __shared__ v8bf t_lds[RANK ? MT : 1][4][TERMS][64];
   static_assert(kSeg % GPW == 0 && GPW % 2 == 0, "a wave's groups are pairs of one segment");
   const int G = K / kGroup, segs = w4a16_segments(K);
-  const int chunks = HOLD ? 1 : (G + kWaves * GPW - 1) / (kWaves * GPW);
+  const int chunks = (G + kWaves * GPW - 1) / (kWaves * GPW);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, j = lane >> 4;
   const int row0 = tile0 * RPT, rows = min(M - row0, MT * RPT);
   const int steps = RANK ? (r + 31) / 32 : 0;  // matrix steps of the low-rank product, one to a wave
 
   // Column tiles of this workgroup; each XCD (workgroups go to the 8 round-robin) takes a
-  // contiguous run of them.
-  const int all = (N + 15) / 16, run = (all + 7) / 8, per = gridDim.x / 8;
+  // contiguous run of them.  HOLD: a workgroup has one chunk, and 'shares' of them share a tile.
+  const int all = (N + 15) / 16, run = (all + 7) / 8, per = gridDim.x / 8 / shares;
   const int first = (blockIdx.x & 7) * run, end = min(first + run, all);
-  int tile = first + (int)(blockIdx.x >> 3), chunk = 0;
+  const int share = HOLD ? (int)(blockIdx.x >> 3) % shares : 0;
+  int tile = first + (int)(blockIdx.x >> 3) / shares, chunk = share;
   if (tile >= end) return;
 
   auto load_x = [&](int ch, Rows<MT, GPW>& x) {
@@ -317,11 +353,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
     for (int t = 0; t < MT; ++t) {
       // (a row tile past the last and a group past the last read the last one's; neither counts)
       const int tt = min(tile0 + t, tiles - 1);
+      // rows past the last are not stored, so they may be the last one's: fewer bytes to read
+      const int most = min(RPT, M - tt * RPT) - 1;
+      const int at = 16 * j + (FP32 ? (c & 8) + min(c & 7, most) : min(c, most));
 #pragma unroll
       for (int u = 0; u < GPW; ++u) {
         const v8h* f = frags + ((size_t)tt * G + min(g0 + u, G - 1)) * 128;
-        x.a[t][u][0] = f[lane];
-        x.a[t][u][1] = f[64 + lane];
+        x.a[t][u][0] = f[at];
+        x.a[t][u][1] = f[64 + at];
       }
       x.up[t] = reinterpret_cast<const v4f*>(scales + ((size_t)tt * segs + min(g0 / kSeg, segs - 1)) * 16)[j];
     }
@@ -344,54 +383,69 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
   };
   // the (tile, chunk) after one
   auto after = [&](int& t, int& ch) {
-    const bool wrap = ch + 1 >= chunks;
+    const bool wrap = HOLD || ch + 1 >= chunks;
     t += wrap ? per : 0;
-    ch = wrap ? 0 : ch + 1;
+    ch = HOLD ? share : wrap ? 0 : ch + 1;
   };
 
-  constexpr int STAGES = HOLD ? 3 : 2;
+  constexpr int STAGES = HOLD && !(MT == 2 && GPW == 8) ? 3 : 2;  // (as far as the registers go)
   Weights<GPW> wa, wb, wc;
   Rows<MT, GPW> xa, xb;
-  int tile2 = tile, chunk2 = 0;  // what the next load reads
+  int tile2 = tile, chunk2 = chunk;  // what the next load reads
   auto load_next = [&](Weights<GPW>& w, Rows<MT, GPW>& x) {
     const bool there = tile2 < end;
     load_w(there ? tile2 : tile, chunk2, there, w);
     if (!HOLD) load_x(chunk2, x);
     after(tile2, chunk2);
   };
-  if (HOLD) load_x(0, xa);
+  if (HOLD) load_x(share, xa);
   load_next(wa, xa);
   if (STAGES == 3) load_next(wb, xa);
-  // T (its slices' sum) as the low-rank product's operand; ranks past r and lo rows are 0
-  if (wave < steps) {
+  auto barrier = [] {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  };
+  // T (its slices' sum) as the low-rank product's operand; ranks past r and lo rows are 0.  All
+  // threads add, four elements of every fold-th slice each, eight loads in flight; then a wave splits
+  // a (row tile, matrix step) into its bf16 terms.
+  if (RANK && share == 0) {
+    static_assert(sizeof(red) >= MT * 16 * 128 * 4, "the sums fit where the waves meet");
+    v4f* sums = reinterpret_cast<v4f*>(&red[0][0][0][0]);
+    const int quads = rows * r / 4, fold = max(1, min(kWaves * 64 / quads, slices));
+    for (int i = threadIdx.x; i < quads * fold; i += kWaves * 64) {
+      const int from = i / quads, at = i % quads;
+      const v4f* pp = reinterpret_cast<const v4f*>(parts + (size_t)row0 * r) + at;
+      v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int q = from; q < slices; q += 8 * fold) {
+        v4f v[8];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const int m = t * RPT + c, k = 32 * wave + 8 * j;
+        for (int e = 0; e < 8; ++e) v[e] = pp[(size_t)min(q + e * fold, slices - 1) * (M * r / 4)];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k] += q + e * fold < slices ? v[e][k] : 0.0f;
+      }
+      sums[i] = x;
+    }
+    barrier();
+    for (int task = wave; task < MT * steps; task += kWaves) {
+      const int t = task / steps, st = task % steps, m = t * RPT + c, k = 32 * st + 8 * j;
       float x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = 0.0f;
       if (c < RPT && m < rows && k < r)
-        for (int q = 0; q < slices; q += 8) {
-          v4f a[8], b[8];
+        for (int p = 0; p < fold; ++p) {
+          const v4f* q = sums + p * quads + (m * r + k) / 4;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const v4f* pp = reinterpret_cast<const v4f*>(parts + ((size_t)min(q + e, slices - 1) * M + row0 + m) * r + k);
-            a[e] = pp[0];
-            b[e] = pp[1];
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[i] += q + e < slices ? a[e][i] : 0.0f;
-              x[4 + i] += q + e < slices ? b[e][i] : 0.0f;
-            }
+          for (int i = 0; i < 8; ++i) x[i] += q[i >> 2][i & 3];
         }
       v8bf p[TERMS];
       split_bf16<TERMS>(x, p);
 #pragma unroll
-      for (int i = 0; i < TERMS; ++i) t_lds[t][wave][i][lane] = p[i];  // (read by this wave alone)
+      for (int i = 0; i < TERMS; ++i) t_lds[t][st][i][lane] = p[i];
     }
+    barrier();
   }
 
   int par = 0;
@@ -399,10 +453,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
   // One (tile, chunk): loads ahead, this one's products; false after the last.
   auto step = [&](Weights<GPW>& w, Weights<GPW>& wn, Rows<MT, GPW>& x, Rows<MT, GPW>& xn) {
     load_next(wn, xn);
-    if (chunk == 0) {
+    if (HOLD || chunk == 0) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-      if (RANK && wave < steps) {
+      if (RANK && share == 0 && wave < steps) {
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -426,7 +480,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
       }
     }
     const bool counts = (chunk * kWaves + wave) * GPW < G;
-    const bool last = chunk + 1 == chunks;
+    const bool last = HOLD || chunk + 1 == chunks;
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -436,9 +490,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) red[par][wave][t * 16 + 4 * j + i][c] = acc[t][i];
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+      barrier();
       for (int i = threadIdx.x; i < rows * 16; i += kWaves * 64) {
         const int m = i >> 4, col = i & 15, nn = tile * 16 + col;
         if (nn < N) {
@@ -448,6 +500,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
           for (int q = 0; q < kWaves; ++q) {
             y += red[par][q][rr][col];
             if (FP32) y += red[par][q][rr + 8][col];
+          }
+          if (HOLD && shares > 1) {
+            partial[((size_t)share * rows + m) * (all * 16) + nn] = y;
+            continue;
           }
           if (bias) y += bf16_bits_to_float(bias[nn]);
           const size_t at = (size_t)(row0 + m) * N + nn;
@@ -472,6 +528,38 @@ __global__ __launch_bounds__(kWaves * 64, 2) void w4a16_kernel(
   }
 }
 
+// Adds the shares of a pass and the bias; a thread has four columns of a row.
+template <bool FP32>
+__global__ __launch_bounds__(256) void w4a16_sum_kernel(const float* __restrict__ partial, int shares,
+                                                        const uint16_t* __restrict__ bias, int rows,
+                                                        int row0, int N, void* __restrict__ Y) {
+  const int quads = (N + 15) / 16 * 4, at = blockIdx.x * 256 + threadIdx.x;
+  if (at >= rows * quads) return;
+  const int m = at / quads, n = at % quads * 4;
+  v4f y = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int q = 0; q < shares; q += 4) {
+    v4f v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      v[u] = reinterpret_cast<const v4f*>(partial)[(size_t)min(q + u, shares - 1) * rows * quads + at];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] += q + u < shares ? v[u][i] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (n + i < N) {
+      const float z = bias ? y[i] + bf16_bits_to_float(bias[n + i]) : y[i];
+      const size_t to = (size_t)(row0 + m) * N + n + i;
+      if (FP32) {
+        static_cast<float*>(Y)[to] = z;
+      } else {
+        static_cast<uint16_t*>(Y)[to] = float_to_bf16_bits(z);
+      }
+    }
+}
+
 struct W4a16Call {
   const v8h* frags;
   const float* scales;
@@ -481,34 +569,41 @@ struct W4a16Call {
   const uint16_t* L2p;
   const uint16_t* bias;
   int M, N, K, r, tiles;
+  float* partial;
   void* Y;
   hipStream_t stream;
 };
 
 template <int MT, int GPW, bool FP32, bool RANK>
 static hipError_t launch_main(const W4a16Call& a, int tile0) {
-  // one workgroup per CU, fewer where there are fewer column tiles (a multiple of 8, for the XCDs)
-  const int all = (a.N + 15) / 16, grid = all < 256 ? (all + 7) / 8 * 8 : 256;
+  const W4a16Pass p = w4a16_pass(a.M, a.N, a.K, tile0, a.tiles, FP32);
 #define SVDQ_MAIN(HOLD)                                                                            \
-  hipLaunchKernelGGL((w4a16_kernel<MT, GPW, HOLD, FP32, RANK>), dim3(grid), dim3(kWaves * 64), 0,  \
-                     a.stream, a.frags, a.scales, a.parts, a.slices, a.container, a.L2p, a.bias,   \
-                     a.M, a.N, a.K, a.r, tile0, a.tiles, a.Y)
-  if (a.K / kGroup <= kWaves * GPW) SVDQ_MAIN(true);
-  else SVDQ_MAIN(false);
+  hipLaunchKernelGGL((w4a16_kernel<MT, GPW, HOLD, FP32, RANK>), dim3(p.grid), dim3(kWaves * 64),   \
+                     0, a.stream, a.frags, a.scales, a.parts, a.slices, a.container, a.L2p,        \
+                     a.bias, a.M, a.N, a.K, a.r, tile0, a.tiles, p.shares, a.partial, a.Y)
+  if constexpr (MT == 1) {
+    if (p.loop) SVDQ_MAIN(false);
+    else SVDQ_MAIN(true);
+  } else {
+    SVDQ_MAIN(true);
+  }
 #undef SVDQ_MAIN
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.shares == 1) return e;
+  const long long threads = (long long)p.rows * ((a.N + 15) / 16 * 4);
+  hipLaunchKernelGGL(w4a16_sum_kernel<FP32>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, a.stream,
+                     a.partial, p.shares, a.bias, p.rows, tile0 * w4a16_rows_per_tile(FP32), a.N, a.Y);
   return hipGetLastError();
 }
 
-// Up to 4 row tiles share a pass over the weights (64 bf16 rows, 32 fp32 rows).  What a wave holds
-// of X^ is 8 registers per row tile and group, so more row tiles mean fewer groups to a chunk.
 template <bool FP32, bool RANK>
 static hipError_t launch_tiles(const W4a16Call& a) {
-  for (int t = 0; t < a.tiles; t += 4) {
+  for (int t = 0; t < a.tiles; t += kMaxTiles) {
     const int left = a.tiles - t;
-    const hipError_t e = left >= 4   ? launch_main<4, 2, FP32, RANK>(a, t)
-                         : left == 3 ? launch_main<3, 2, FP32, RANK>(a, t)
-                         : left == 2 ? launch_main<2, 4, FP32, RANK>(a, t)
-                                     : launch_main<1, 8, FP32, RANK>(a, t);
+    const hipError_t e = left >= 4   ? launch_main<4, groups_per_wave(4), FP32, RANK>(a, t)
+                         : left == 3 ? launch_main<3, groups_per_wave(3), FP32, RANK>(a, t)
+                         : left == 2 ? launch_main<2, groups_per_wave(2), FP32, RANK>(a, t)
+                                     : launch_main<1, groups_per_wave(1), FP32, RANK>(a, t);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -518,7 +613,7 @@ hipError_t launch_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const u
                              const uint8_t* container, const uint16_t* L2p, const uint16_t* bias,
                              int M, int N, int K, int r, void* Y, int out_fp32, void* workspace,
                              hipStream_t stream) {
-  const W4a16Ws w = w4a16_layout(M, K, r, out_fp32);
+  const W4a16Ws w = w4a16_layout(M, N, K, r, out_fp32);
   uint8_t* base = static_cast<uint8_t*>(workspace);
   v8h* frags = reinterpret_cast<v8h*>(base + w.frags);
   float* scales = reinterpret_cast<float*>(base + w.scales);
@@ -535,7 +630,7 @@ hipError_t launch_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const u
 #undef SVDQ_PREP
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const W4a16Call a{frags, scales, parts, slices, container, L2p, bias, M, N, K, r, tiles, Y, stream};
+  const W4a16Call a{frags, scales, parts, slices, container, L2p, bias, M, N, K, r, tiles, reinterpret_cast<float*>(base + w.partial), Y, stream};
   if (out_fp32) return r ? launch_tiles<true, true>(a) : launch_tiles<true, false>(a);
   return r ? launch_tiles<false, true>(a) : launch_tiles<false, false>(a);
 }
