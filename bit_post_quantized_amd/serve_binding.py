@@ -69,6 +69,9 @@ class _OnDevice:
 
 
 def _call(fn: str, a: _Args, args, stream) -> None:
+    for kind, v in zip(_SIGNATURES[fn][0], args):
+        if kind is _I and not -1 << 31 <= v < 1 << 31:  # (ctypes would drop the upper bits)
+            raise ValueError(f"{fn}: {v} does not fit 32 bits")
     with _OnDevice(a.device):
         status = getattr(load(), fn)(*args, a.stream(stream))
     binding._check(fn, status)

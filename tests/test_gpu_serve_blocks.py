@@ -107,6 +107,26 @@ def test_steps_in_a_row_and_release_keep_every_block_once(gpu_lib):
         assert (s[done] == 0).all() and (t[done] == -1).all()
 
 
+def test_a_plan_outlives_the_next_call(gpu_lib):
+    """Arguments of the caller's own, of the last plan, of an older one, or of two plans at once:
+    the plan before a call still holds what it held after it."""
+    i32 = lambda a: to_dev(np.asarray(a), torch.int32)  # noqa: E731
+    own = i32([3, 40]), i32([1, 1]), i32([6])
+    planner = serve.BlockPlanner(i32(np.zeros((2, 8))), i32(np.arange(6)), 16, 4)
+    plans = [planner.plan(*own)]
+    for k in range(12):
+        last, older = plans[-1], plans[-2 if k else -1]
+        lens = (own[0], last.seq_lens, older.seq_lens, last.seq_lens)[k % 4]
+        count = (own[2], last.free_count, older.free_count, older.free_count)[k % 4]
+        held = [t.clone() for t in (last.cu_rows, last.seq_lens, last.positions, last.slots, last.status, last.free_count)]
+        args = lens.clone(), count.clone()
+        plans.append(planner.plan(lens, own[1], count))
+        now = (last.cu_rows, last.seq_lens, last.positions, last.slots, last.status, last.free_count)
+        assert all(torch.equal(a, b) for a, b in zip(held, now)), k
+        assert torch.equal(args[0], lens) and torch.equal(args[1], count), k
+        assert torch.equal(plans[-1].seq_lens, args[0] + 1), k
+
+
 def test_release_keeps_to_the_free_list(gpu_lib):
     i32 = lambda a: to_dev(np.asarray(a), torch.int32)  # noqa: E731
     tables, free = i32([[1, 2, 3], [4, 5, 6], [7, 8, 9]]), i32([10, 0, 0])
