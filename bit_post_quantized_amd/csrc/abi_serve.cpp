@@ -41,6 +41,13 @@ int check_cache(int kv_heads, int dim, int bs, int num_blocks) {
   return SVDQ_OK;
 }
 
+// (a workgroup has 16 rows of a head or more, and a launch fewer than 2^24 of them)
+int check_rows(int rows, int kv_heads) {
+  if ((long long)rows * kv_heads > (1 << 27))
+    return fail(SVDQ_ESHAPE, "rows * kv_heads must be <= 2^27 (got %d * %d)", rows, kv_heads);
+  return SVDQ_OK;
+}
+
 int check_stride(const char* name, int64_t stride, long long least) {
   if (stride < least || stride % 8 != 0 || stride > (1LL << 31))
     return fail(SVDQ_ESHAPE, "%s must be a multiple of 8 elements and at least %lld (got %lld)",
@@ -154,8 +161,8 @@ int kv_block_append(const uint16_t* k, const uint16_t* v, int64_t k_stride, int6
                     int num_blocks, uint8_t* k_codes, uint8_t* v_codes, float* k_scale,
                     float* v_scale, void* stream) {
   if (rows < 0) return fail(SVDQ_EINVAL, "rows must be >= 0 (got %d)", rows);
-  if (rows > (1 << 30)) return fail(SVDQ_ESHAPE, "rows must be <= 2^30 (got %d)", rows);
   if (int s = check_cache(kv_heads, dim, block_size, num_blocks)) return s;
+  if (int s = check_rows(rows, kv_heads)) return s;
   if (int s = check_stride("k_stride", k_stride, (long long)kv_heads * dim)) return s;
   if (int s = check_stride("v_stride", v_stride, (long long)kv_heads * dim)) return s;
   if (!k_codes || !v_codes || !k_scale || !v_scale || (rows > 0 && (!k || !v || !slots)))
@@ -175,8 +182,8 @@ int kv_block_read(const int64_t* slots, int rows, int kv_heads, int dim, int blo
                   const float* k_scale, const float* v_scale, uint16_t* k_out, uint16_t* v_out,
                   void* stream) {
   if (rows < 0) return fail(SVDQ_EINVAL, "rows must be >= 0 (got %d)", rows);
-  if (rows > (1 << 30)) return fail(SVDQ_ESHAPE, "rows must be <= 2^30 (got %d)", rows);
   if (int s = check_cache(kv_heads, dim, block_size, num_blocks)) return s;
+  if (int s = check_rows(rows, kv_heads)) return s;
   if (!k_codes || !v_codes || !k_scale || !v_scale || (rows > 0 && (!slots || !k_out || !v_out)))
     return fail(SVDQ_EINVAL, "NULL pointer");
   if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_out) || !aligned16(v_out))
@@ -201,6 +208,9 @@ static int check_attention(int requests, int rows, int max_rows, int heads, int 
   if (requests > 65535 || rows > (1 << 24) || max_rows > (1 << 24))
     return fail(SVDQ_ESHAPE, "at most 65535 requests and 2^24 rows (got %d, %d, %d)", requests,
                 rows, max_rows);
+  if (!svdq::kv_block_attention_fits(requests, max_rows, heads, kv_heads, dim))
+    return fail(SVDQ_ESHAPE, "too many rows: %d requests of up to %d rows and %d heads", requests,
+                max_rows, heads);
   return SVDQ_OK;
 }
 

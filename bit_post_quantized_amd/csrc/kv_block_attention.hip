@@ -854,7 +854,7 @@ static Split split_of(int requests, int rows, int max_rows, int heads, int kv_he
   const long long tokens = (long long)width * bs;
   const int unit = s.few ? kWaves * kTile : 4 * kTile;
   long long chunks = (s.few ? 256 : s.rt == 1 ? 768 : 512) / natural;
-  if (s.few) {
+  if (s.few && natural <= 4096) {
     const long long least = (tokens + 16383) / 16384;
     if (chunks < least) chunks = least;
   }
@@ -875,6 +875,13 @@ static Split split_of(int requests, int rows, int max_rows, int heads, int kv_he
   return s;
 }
 
+// A launch has fewer than 2^32 threads: with 512 to a workgroup there is room for 2^23 (cut into
+// chunks there are 2^22 at most, and fewer joins).
+bool kv_block_attention_fits(int requests, int max_rows, int heads, int kv_heads, int dim) {
+  const long long groups = split_of(requests, 0, max_rows, heads, kv_heads, dim, 1, 16).groups;
+  return requests * groups * kv_heads < 1 << 23;
+}
+
 size_t kv_block_attention_ws_bytes(int requests, int rows, int max_rows, int heads, int kv_heads,
                                    int dim, int width, int bs) {
   if (requests <= 0 || rows <= 0) return 0;
@@ -889,8 +896,6 @@ static hipError_t launch(const BlockAttention& a, hipStream_t stream) {
   const long long joins = (long long)a.requests * a.max_rows * a.heads;
   const int each = s.chunks <= kFewChunks ? kJoinThreads / (D / 4) : 1;
   const long long join_grid = (joins + each - 1) / each;
-  // a launch has fewer than 2^32 threads
-  if (grid >= 1 << 23 || (s.chunks > 1 && join_grid >= 1 << 24)) return hipErrorInvalidConfiguration;
 #define SVDQ_ATTEND(WAVES, ...)                                                                  \
   hipLaunchKernelGGL((__VA_ARGS__), dim3((unsigned)grid), dim3(WAVES * 64), 0, stream, a,        \
                      s.chunks, s.groups, s.chunk_tokens)

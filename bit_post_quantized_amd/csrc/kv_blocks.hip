@@ -515,9 +515,7 @@ hipError_t launch_kv_block_append(const uint16_t* k, const uint16_t* v, int64_t 
                                   int64_t v_stride, const int64_t* slots, int rows,
                                   const BlockCacheView& c, hipStream_t stream) {
   const int window = append_window(rows, c.heads, c.bs);
-  const long long n = (long long)((rows + window - 1) / window) * c.heads;
-  if (n >= 1 << 24) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)n);
+  const dim3 grid((unsigned)((rows + window - 1) / window * c.heads));
   const int shift = __builtin_ctz(c.bs);
 #define SVDQ_APPEND(D, STEPS)                                                                       \
   hipLaunchKernelGGL((kv_block_append_kernel<D, STEPS>), grid, dim3(kAppendThreads), 0, stream, k, v, \
@@ -638,8 +636,7 @@ __global__ __launch_bounds__(256) void kv_block_read_kernel(const int64_t* __res
 
 hipError_t launch_kv_block_read(const int64_t* slots, int rows, const BlockCacheView& c,
                                 uint16_t* k_out, uint16_t* v_out, hipStream_t stream) {
-  const long long grid = (long long)((rows + kReadRows - 1) / kReadRows) * c.heads * 2;
-  if (grid >= 1 << 24) return hipErrorInvalidConfiguration;
+  const int grid = (rows + kReadRows - 1) / kReadRows * c.heads * 2;
   const int shift = __builtin_ctz(c.bs);
   if (c.dim == 128)
     hipLaunchKernelGGL(kv_block_read_kernel<128>, dim3((unsigned)grid), dim3(256), 0, stream,

@@ -60,6 +60,7 @@ struct BlockAttention {
   float* ws;
 };
 
+bool kv_block_attention_fits(int requests, int max_rows, int heads, int kv_heads, int dim);
 size_t kv_block_attention_ws_bytes(int requests, int rows, int max_rows, int heads, int kv_heads,
                                    int dim, int width, int bs);
 hipError_t launch_kv_block_attention(const BlockAttention& a, hipStream_t stream);

@@ -138,7 +138,8 @@ int kv_block_release(const int32_t* seq_lens, const uint8_t* done, int requests,
  *   slots    int64 [rows], as written by kv_block_plan: the rows of one block must stand
  *            together, their offsets ascending by one (otherwise that block's contents are
  *            unspecified)
- *   0 <= rows <= 2^30, 1 <= kv_heads <= 65535, num_blocks >= 1; the cache may exceed 4 GiB.
+ *   rows >= 0, 1 <= kv_heads <= 65535, rows kv_heads <= 2^27, num_blocks >= 1; the cache may
+ *   exceed 4 GiB.
  */
 int kv_block_append(const uint16_t* k, const uint16_t* v, int64_t k_stride, int64_t v_stride,
                     const int64_t* slots, int rows, int kv_heads, int dim, int block_size,
@@ -173,10 +174,13 @@ int kv_block_read(const int64_t* slots, int rows, int kv_heads, int dim, int blo
  *   out      bf16 [rows, heads, dim]  16B
  *   workspace   device scratch of kv_block_attention_workspace_bytes(...) bytes (16B; may be
  *            NULL when that is 0), no initialization needed, rewritten by every call; calls that
- *            share one workspace must not overlap in time
+ *            share one workspace must not overlap in time.  The size is that of the call's own
+ *            arguments: a smaller batch can need more (its tokens are spread over more
+ *            workgroups), so a workspace for several batches takes the largest of their sizes
  *   0 <= requests <= 65535, 0 <= rows <= 2^24, 1 <= max_rows <= 2^24, heads % kv_heads == 0,
- *   heads / kv_heads <= 128, width >= 1, requests * width < 2^31, width * bs <= 2^30, sm_scale
- *   finite.
+ *   heads / kv_heads <= 128, requests kv_heads ceil(max_rows heads / kv_heads / n) < 2^23 with
+ *   n = 16 where max_rows heads / kv_heads <= 16, else at least 32; width >= 1,
+ *   requests * width < 2^31, width * bs <= 2^30, sm_scale finite.
  */
 size_t kv_block_attention_workspace_bytes(int requests, int rows, int max_rows, int heads,
                                           int kv_heads, int dim, int width, int block_size);

@@ -90,6 +90,58 @@ def test_long_rows_split_over_workgroups(gpu_lib, bs, dim):
         check(c, run(c, causal, sm), causal, sm)
 
 
+@pytest.mark.parametrize("seq,rows,heads,kv_heads,dim,bs,width", [
+    ([20000, 77], [5, 2], 8, 1, 64, 64, 320), ([20000, 77], [5, 2], 8, 1, 128, 16, 1250),   # 40 rows: 64 to a workgroup
+    ([2100, 900], [5, 4], 8, 1, 64, 128, 17), ([2100, 900], [4, 5], 8, 1, 128, 32, 66),
+    ([5000, 64], [100, 64], 1, 1, 64, 16, 320), ([5000, 64], [100, 64], 2, 1, 128, 64, 80),  # 128
+    ([9000], [33], 34, 2, 64, 128, 71), ([4096], [150], 3, 3, 128, 16, 256),
+])
+def test_many_rows_split_over_workgroups(gpu_lib, seq, rows, heads, kv_heads, dim, bs, width):
+    from bit_post_quantized_amd import serve_binding as SB
+    assert SB.kv_block_attention_workspace_bytes(len(seq), sum(rows), max(rows), heads, kv_heads, dim, width, bs)
+    c = batch(sum(seq) + dim, seq, rows, heads, kv_heads, dim, bs, width=width)
+    sm = 1.0 / math.sqrt(dim)
+    for causal in (False, True):
+        check(c, run(c, causal, sm), causal, sm)
+
+
+def test_many_short_requests_under_a_wide_table(gpu_lib):
+    # 300 requests: no cut for the workgroups' sake, but chunks of 16384 tokens under this table
+    rng = np.random.default_rng(6)
+    seq = [int(x) for x in rng.integers(0, 40, 300)]
+    seq[17] = 17000
+    c = batch(9, seq, [1] * 300, 2, 1, 64, 128, width=400)
+    check(c, run(c, True, 0.125), True, 0.125)
+
+
+def test_split_rows_with_bad_entries_on_two_streams_and_in_a_graph(gpu_lib):
+    c = batch(91, [6000, 700], [6, 6], 8, 1, 64, 32, width=200)
+    c["tables"][0, 40:75], c["tables"][1, 3] = -1, 10 ** 6
+    cache = dev_cache(*c["cache"])
+    i32 = lambda a: to_dev(a, torch.int32)  # noqa: E731
+    q, tables, seq, cu = to_dev_bf16(c["q"]), i32(c["tables"]), i32(c["seq"]), i32(c["cu"])
+    first = cache.attention(q, tables, seq, cu, 6, sm_scale=0.125)
+    check(c, host64(first), True, 0.125)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            outs += [cache.attention(q, tables, seq, cu, 6, sm_scale=0.125) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, first) for o in outs)
+    out, g = torch.zeros_like(first), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.attention(q, tables, seq, cu, 6, sm_scale=0.125, out=out)
+    for lens in ([6000, 700], [5, 0], [700, 6000], [6000, 700]):
+        seq.copy_(i32(np.array(lens)))
+        g.replay()
+        eager = cache.attention(q, tables, seq, cu, 6, sm_scale=0.125)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), lens
+    assert torch.equal(out, first)
+
+
 def test_sharp_flat_and_signed_scores(gpu_lib):
     c = batch(77, [700, 260], [3, 1], 4, 2, 64, 16)
     for sm in (3.0, 0.0, 1e-20, -0.2):
@@ -225,6 +277,8 @@ def test_attention_refusals(gpu_lib):
         cache.attention(q, tables, seq, cu, 1, sm_scale=float("inf"))
     with pytest.raises(RuntimeError, match="max_rows"):
         cache.attention(q, tables, seq, cu, 0)
+    with pytest.raises(ValueError, match="fit 32 bits"):   # 2^32 + 1 is not 1
+        cache.attention(q, tables, seq, cu, (1 << 32) + 1)
     with pytest.raises(ValueError, match="seq_lens must be"):
         cache.attention(q, tables, seq.long(), cu, 1)
     with pytest.raises(ValueError, match="cu_rows must have shape"):

@@ -52,6 +52,10 @@ def check(y, ref, mag, K, fp32):
     (31, 128, 64, 16, False), (32, 2048, 95, 32, True), (33, 512, 16, 128, False), (48, 64, 7, 0, True),
     (49, 1088, 50, 112, True), (63, 384, 129, 32, False), (64, 4096, 72, 128, True),
     (5, 64 * 33, 4100, 32, True),
+    # K beyond what a workgroup holds of X: read again (one row tile) or cut over workgroups
+    (3, 64 * 129, 40, 32, True), (16, 64 * 150, 33, 128, False), (17, 64 * 65, 130, 48, True),
+    (24, 64 * 131, 50, 0, True), (33, 64 * 33, 600, 16, False), (40, 64 * 97, 17, 112, True),
+    (64, 64 * 1100, 20, 64, True), (64, 64 * 40, 4100, 128, False),
 ])
 def test_matches_the_layer(gpu_lib, M, K, N, r, bias, dtype):
     x, pw, ref = make(M * 7919 + K + N, M, K, N, r, bias)
@@ -130,6 +134,27 @@ def test_same_bits_every_time_on_streams_and_in_graphs(gpu_lib):
         assert torch.equal(out, eager), k
     assert lin(xd).equal(first)
     check(host64(first), *ref(x), 1024, False)
+
+
+def test_same_bits_and_guards_where_k_is_cut(gpu_lib):
+    x, pw, ref = make(24, 30, 64 * 70, 45, 32, True)
+    lin, xd = serve.DecodeLinear(pw), to_dev_bf16(x)
+    first = lin(xd)
+    check(host64(first), *ref(x), pw.K, False)
+    need = SB.svdq_w4a16_workspace_bytes(30, 45, pw.K, 32, 0)
+    ws = torch.full((need + 32,), 0x7F, dtype=torch.uint8, device="cuda")
+    guard = torch.full((32, 45), 7.0, dtype=torch.bfloat16, device="cuda")
+    buf = torch.empty_like(xd)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lin(buf, out=guard[1:31], workspace=ws[:need])
+    for k in range(3):
+        buf.copy_(xd * 2 ** k)
+        g.replay()
+        eager = lin(buf)
+        torch.cuda.synchronize()
+        assert torch.equal(guard[1:31], eager) and torch.equal(lin(xd), first), k
+    assert (guard[0] == 7).all() and (guard[31] == 7).all() and (ws[need:] == 0x7F).all()
 
 
 @pytest.mark.parametrize("N,K", [(16, 512), (1, 64), (50, 704), (33, 1024)])

@@ -97,6 +97,7 @@ def test_append_and_read_validation(lib):
     assert append(num=2 ** 31 - 1, heads=65535, ks=1 << 24, vs=1 << 24) == ESHAPE
     assert append(ks=127) == ESHAPE and append(vs=129) == ESHAPE and append(ks=120) == ESHAPE
     assert append(rows=(1 << 30) + 1) == ESHAPE
+    assert append(rows=(1 << 26) + 1) == ESHAPE and b"rows * kv_heads" in lib.svdq_last_error()
     for k in ("k", "v", "slots", "kc", "vc", "s"):
         assert append(**{k: None}) == EINVAL, k
     for k in ("k", "v", "kc", "vc"):
@@ -106,6 +107,7 @@ def test_append_and_read_validation(lib):
     def read(slots=F, rows=1, heads=2, dim=64, bs=16, num=4, kc=F, vc=F, s=F, ko=F, vo=F):
         return lib.kv_block_read(slots, rows, heads, dim, bs, num, kc, vc, s, s, ko, vo, None)
 
+    assert read(rows=(1 << 26) + 1) == ESHAPE and b"rows * kv_heads" in lib.svdq_last_error()
     assert read(rows=-1) == EINVAL and read(dim=32) == ESHAPE and read(bs=1) == ESHAPE
     for k in ("slots", "kc", "vc", "s", "ko", "vo"):
         assert read(**{k: None}) == EINVAL, k
@@ -124,6 +126,9 @@ def test_attention_validation(lib):
     assert call(heads=0) == EINVAL and call(kv=0) == EINVAL and call(width=0) == EINVAL and call(num=0) == EINVAL
     assert call(heads=7) == ESHAPE and call(heads=258) == ESHAPE and call(dim=80) == ESHAPE and call(bs=12) == ESHAPE
     assert call(n=65536) == ESHAPE and call(rows=(1 << 24) + 1) == ESHAPE and call(most=(1 << 24) + 1) == ESHAPE
+    assert call(n=65535, heads=129, kv=129, qs=129 * 64, rows=1 << 24) == ESHAPE  # 2^23 workgroups
+    assert b"too many rows" in lib.svdq_last_error()
+    assert call(n=60000, rows=1 << 24, most=1 << 24) == ESHAPE and b"too many rows" in lib.svdq_last_error()
     assert call(qs=504) == ESHAPE and call(qs=513) == ESHAPE
     assert call(sm=float("nan")) == EINVAL and call(sm=float("inf")) == EINVAL
     for k in ("q", "kc", "vc", "s", "tables", "seq", "cu", "out"):
