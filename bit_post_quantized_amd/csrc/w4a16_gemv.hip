@@ -377,8 +377,10 @@ __global__ __launch_bounds__(kWaves * 64, 1) void w4a16_kernel(
 #pragma unroll
     for (int p = 0; p < GPW / 2; ++p) w.s[p] = sp[p];
     if constexpr (RANK) {
-      const int n = min(t * 16 + c, N - 1);
-      w.l2 = *reinterpret_cast<const v8bf*>(L2p + (size_t)n * r + min(32 * wave + 8 * j, r - 8));
+      // (a wave that adds no ranks reads one address)
+      const bool adds = share == 0 && wave < steps;
+      const int n = adds ? min(t * 16 + c, N - 1) : 0, k = adds ? min(32 * wave + 8 * j, r - 8) : 0;
+      w.l2 = *reinterpret_cast<const v8bf*>(L2p + (size_t)n * r + k);
     }
   };
   // the (tile, chunk) after one
