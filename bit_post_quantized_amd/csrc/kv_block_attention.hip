@@ -17,8 +17,16 @@
 // walks over tokens of its own, straight from memory to registers, and the waves meet at the end.
 // More rows (drafts, prompts) are bound by the softmax's vector work: the waves share the tokens,
 // whose codes become fp16 once, in LDS, and own their rows.  With few workgroups the tokens are
-// split over more of them (chunks), and kv_block_combine_kernel joins the chunks' maxima, sums and
-// outputs.
+// split over more of them (chunks), whose maxima, sums and outputs a second launch joins.
+//
+// Measured (kernel times).  64 requests of up to 8192 tokens, 32 heads to 8 of 128: 138 us, 4.9 TB/s
+// of codes (equal lengths: 5.2).  1 x 10240 tokens, 32 heads: 19 us and 4 for the join; the bytes are
+// 15 at 5.5 TB/s.  2 x 5 rows, 32 heads to 4, before up to 131071 tokens: 49 us and 6; the bytes are
+// 40.  4 prompts of 475 to 1000 rows, 24 heads to 8 of 64, before up to 4096 tokens: 85 us,
+// 470 TFLOP/s: a wave's tile of 16 rows x 64 tokens is 144 vector instructions, 16 of them
+// exponentials at a quarter of the rate, against 16 matrix ones, and the longest request's 64 tiles
+// follow each other at 1.1 to 1.3 us.  4096 rows, 32 heads to 8 of 128, before 8192 tokens: 454 us,
+// 909 TFLOP/s.
 #include "serve_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -262,7 +270,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
   if (vr0 >= rg.vrows) return;
   const int top = rg.limit(a, min(vr0 + 16 * RT, rg.vrows) - 1);
   const int t0 = wk.chunk * chunk_tokens, t1 = min(t0 + chunk_tokens, top);
-  if (chunks > 1 && t0 >= t1) return;               // (the combine knows which chunks there are)
+  if (chunks > 1 && t0 >= t1) return;               // (the join knows which chunks there are)
   const int32_t* table = a.tables + (size_t)wk.b * a.width;
 
   // the table's entries for this lane's K rows (16 tokens from base + 16 (c / 4)) and for its 16

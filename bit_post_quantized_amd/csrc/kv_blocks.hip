@@ -12,22 +12,37 @@ namespace svdq {
 // those the scan left in LDS, takes the block from the table or, for a block the step adds, from
 // the free list, and writes the table entry if it is the block's first row.  Workgroup 0 also
 // writes what there is one of per request.  So no workgroup waits for another, and the launch is
-// latency: two block scans per 1024 requests.
+// latency: 5.2 us for 8 requests of a row, 5.8 for 1000 with 65536 rows together (three block scans
+// per 1024 requests, and loads that depend on each other; 6.5 and 7.2 with shuffles in the scans).
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanRows = 1024;
 
 __device__ __forceinline__ int clamp0(int x) { return x < 0 ? 0 : x; }
 
-// Inclusive sums of one value per thread over the workgroup, in 64 bits; total in `sum`.
-__device__ __forceinline__ long long block_scan(long long v, long long* lds, long long& sum) {
+// Adds the value of the lane that a DPP control names (0 where there is none, or outside ROWS).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ long long add_lane(long long v) {
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0u, (uint32_t)v, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0u, (uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
+  return v + (long long)((uint64_t)hi << 32 | lo);
+}
+
+// Inclusive sums of one value per lane: within rows of 16 lanes by shifts of 1, 2, 4 and 8, then
+// the rows before by two broadcasts of a row's last lane.
+__device__ __forceinline__ long long wave_scan(long long v) {
+  v = add_lane<0x111, 0xF>(v);
+  v = add_lane<0x112, 0xF>(v);
+  v = add_lane<0x114, 0xF>(v);
+  v = add_lane<0x118, 0xF>(v);
+  v = add_lane<0x142, 0xA>(v);  // lane 15 to the second row, 47 to the fourth
+  return add_lane<0x143, 0xC>(v);  // lane 31 to the upper half
+}
+
+// Adds what the waves before have (`total`: of this wave, in its last lane); sum: of all.  One barrier:
+// two scans that follow each other take different `lds`.
+__device__ __forceinline__ long long waves_before(long long total, long long* lds, long long& sum) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const long long u = __shfl_up(v, o);
-    if (lane >= o) v += u;
-  }
-  __syncthreads();  // (the previous scan's readers are done with lds)
-  if (lane == 63) lds[wave] = v;
+  if (lane == 63) lds[wave] = total;
   __syncthreads();
   long long before = 0;
   sum = 0;
@@ -37,7 +52,13 @@ __device__ __forceinline__ long long block_scan(long long v, long long* lds, lon
     if (w < wave) before += x;
     sum += x;
   }
-  return v + before;
+  return before;
+}
+
+// Inclusive sums of one value per thread over the workgroup, in 64 bits.
+__device__ __forceinline__ long long block_scan(long long v, long long* lds, long long& sum) {
+  v = wave_scan(v);
+  return v + waves_before(v, lds, sum);
 }
 
 __global__ __launch_bounds__(kPlanThreads) void kv_block_plan_kernel(
@@ -46,7 +67,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_block_plan_kernel(
     int capacity, const int32_t* __restrict__ free_count, int32_t* __restrict__ cu,
     int32_t* __restrict__ seq, int rows, int32_t* __restrict__ positions,
     int64_t* __restrict__ slots, int32_t* __restrict__ status, int32_t* __restrict__ free_out) {
-  __shared__ long long scan_lds[kPlanThreads / 64];
+  __shared__ long long scan_lds[3][kPlanThreads / 64];
   // the requests with rows in this workgroup's range, in order: at most one per row
   __shared__ int s_first[kPlanRows], s_ctx[kPlanRows], s_take[kPlanRows], s_req[kPlanRows];
   const int tid = threadIdx.x, bs = 1 << shift;
@@ -62,13 +83,13 @@ __global__ __launch_bounds__(kPlanThreads) void kv_block_plan_kernel(
     const int c = b < requests ? clamp0(ctx[b]) : 0;
     const int n = b < requests ? clamp0(add[b]) : 0;
     long long sum;
-    const long long cu1 = cu_base + block_scan(n, scan_lds, sum), first = cu1 - n;
+    const long long cu1 = cu_base + block_scan(n, scan_lds[0], sum), first = cu1 - n;
     cu_base += sum;
     const long long end = ((long long)c + n + bs - 1) >> shift;
     const int held = (int)(((long long)c + bs - 1) >> shift);
     int st = end > width ? 2 : cu1 > rows ? 3 : 0;
     const long long need = st ? 0 : end - held;
-    const long long incl = need_base + block_scan(need, scan_lds, sum);
+    const long long incl = need_base + block_scan(need, scan_lds[1], sum);
     need_base += sum;
     if (need > 0 && incl > have) st = 1;
     // blocks really taken: the prefix up to the first request that did not get its blocks
@@ -80,9 +101,10 @@ __global__ __launch_bounds__(kPlanThreads) void kv_block_plan_kernel(
     }
     // this range's requests (those with rows in it): compacted into LDS in order
     const bool mine = n > 0 && first < row1 && cu1 > row0;
-    const long long at = block_scan(mine ? 1 : 0, scan_lds, sum) - 1;
+    const uint64_t all = __ballot(mine);
+    const int at = __popcll(all & ((1ull << (tid & 63)) - 1)) + (int)waves_before(__popcll(all), scan_lds[2], sum);
     if (mine) {
-      const int i = found + (int)at;  // < kPlanRows: each has a row of its own in the range
+      const int i = found + at;  // < kPlanRows: each has a row of its own in the range
       s_first[i] = (int)first;
       s_ctx[i] = c;
       s_take[i] = st ? -1 : (int)(incl - need);
@@ -97,11 +119,10 @@ __global__ __launch_bounds__(kPlanThreads) void kv_block_plan_kernel(
       const long long u = __shfl_xor(taken, o);
       taken = u > taken ? u : taken;
     }
-    __syncthreads();
-    if ((tid & 63) == 0) scan_lds[tid >> 6] = taken;
+    if ((tid & 63) == 0) scan_lds[0][tid >> 6] = taken;
     __syncthreads();
     if (tid == 0) {
-      for (int w = 1; w < kPlanThreads / 64; ++w) taken = scan_lds[w] > taken ? scan_lds[w] : taken;
+      for (int w = 1; w < kPlanThreads / 64; ++w) taken = scan_lds[0][w] > taken ? scan_lds[0][w] : taken;
       free_out[0] = have - (int)taken;
       cu[0] = 0;
     }
@@ -158,21 +179,22 @@ __global__ __launch_bounds__(kPlanThreads) void kv_block_release_kernel(
     int32_t* __restrict__ tables, int width, int shift, int32_t* __restrict__ free_blocks,
     int capacity, const int32_t* __restrict__ free_count, int32_t* __restrict__ seq_out,
     int32_t* __restrict__ free_out) {
-  __shared__ long long scan_lds[kPlanThreads / 64];
+  __shared__ long long scan_lds[2][kPlanThreads / 64];
   const int me = blockIdx.x, tid = threadIdx.x, bs = 1 << shift;
   const int have = min(clamp0(free_count[0]), capacity);
   const bool last = me == requests, mine = !last && done[me];
   if (!last && tid == 0) seq_out[me] = mine ? 0 : seq[me];
   if (!last && !mine) return;
   long long before = 0;
-  for (int b0 = 0; b0 < me; b0 += kPlanThreads) {
+  int par = 0;
+  for (int b0 = 0; b0 < me; b0 += kPlanThreads, par ^= 1) {
     const int b = b0 + tid;
     long long v = 0, sum;
     if (b < me && done[b]) {
       v = ((long long)clamp0(seq[b]) + bs - 1) >> shift;
       if (v > width) v = width;
     }
-    block_scan(v, scan_lds, sum);
+    waves_before(wave_scan(v), scan_lds[par], sum);
     before += sum;
   }
   if (last) {
@@ -314,15 +336,30 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio, int n) {
   return (r & ~keep) | (w & keep);
 }
 
+// ... and of the first `n` bytes of 16.
+__device__ __forceinline__ v4u rescale16(v4u w, float ratio, int n) {
+  return v4u{rescale4(w.x, ratio, max(n, 0)), rescale4(w.y, ratio, max(n - 4, 0)),
+             rescale4(w.z, ratio, max(n - 8, 0)), rescale4(w.w, ratio, max(n - 12, 0))};
+}
+
 // The codes of a block's first `off` tokens under a grown scale: K's rows or V's rows of tokens, the
-// dwords i, i + step, ... of them.
-template <int D, bool V>
+// 16-byte pieces i, i + step, ... of them, AHEAD loads in flight.  (One token each to 64 x 8 blocks of
+// 127 that all grow: 37 us, 135 with a dword at a time; without growth 6.)
+template <int D, bool V, int AHEAD>
 __device__ __forceinline__ void rescale_block(uint8_t* codes, int bs, int off, float ratio, int i, int step) {
-  const int dw = (off + 3) / 4;  // V: dwords of a channel's earlier tokens
-  for (; i < (V ? D * dw : off * D / 4); i += step) {
-    uint32_t* p = V ? reinterpret_cast<uint32_t*>(codes + (size_t)(i / dw) * bs) + i % dw
-                    : reinterpret_cast<uint32_t*>(codes) + i;
-    *p = rescale4(*p, ratio, V ? off - 4 * (i % dw) : 4);
+  const int per = (off + 15) / 16, all = V ? D * per : off * D / 16;  // V: pieces of a channel
+  for (; i < all; i += AHEAD * step) {
+    v4u* p[AHEAD];
+    v4u w[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int at = min(i + u * step, all - 1);
+      p[u] = reinterpret_cast<v4u*>(V ? codes + (size_t)(at / per) * bs + 16 * (at % per) : codes + 16 * at);
+      w[u] = *p[u];
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (i + u * step < all) *p[u] = rescale16(w[u], ratio, V ? off - 16 * ((i + u * step) % per) : 16);
   }
 }
 
@@ -416,8 +453,8 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
       c.k_scale[bh] = ks;
       c.v_scale[bh] = vs;
     }
-    if (off > 0 && ks > k_old) rescale_block<D, false>(kc, bs, off, k_old / ks, tid, kAppendThreads);
-    if (off > 0 && vs > v_old) rescale_block<D, true>(vc, bs, off, v_old / vs, tid, kAppendThreads);
+    if (off > 0 && ks > k_old) rescale_block<D, false, 1>(kc, bs, off, k_old / ks, tid, kAppendThreads);
+    if (off > 0 && vs > v_old) rescale_block<D, true, 1>(vc, bs, off, v_old / vs, tid, kAppendThreads);
 #pragma unroll
     for (int p = 0; p < STEPS; ++p) {
       const int i = 4 * (group + GROUPS * p);
@@ -439,7 +476,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
         *reinterpret_cast<uint32_t*>(&vt[(8 * part + e) * PITCH + i]) = lo | hi;
       }
     }
-    __syncthreads();  // (the earlier tokens' rescaled dwords are written before bytes beside them)
+    __syncthreads();  // (the earlier tokens' rescaled pieces are written before bytes in them)
     // V's rows of tokens to the block: 16 bytes at a time where a chunk is whole and in step with
     // LDS (off a multiple of 4), else its bytes
     const int c0 = off >> 4, c1 = (off + n + 15) >> 4, nc = c1 - c0;
@@ -488,16 +525,20 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
       c.k_scale[bh] = ks;
       c.v_scale[bh] = vs;
     }
-    // (a lane rescales the dwords that it writes codes beside: its own channels' rows of V)
-    if (off > 0 && ks > k_old) rescale_block<D, false>(kc, bs, off, k_old / ks, part, TPR);
+    // (a lane rescales the pieces that it writes codes into: its own channels' rows of V)
+    if (off > 0 && ks > k_old) rescale_block<D, false, 4>(kc, bs, off, k_old / ks, part, TPR);
     if (off > 0 && vs > v_old) {
       const float ratio = v_old / vs;
-      for (int i = 0; i < off; i += 4)
+#pragma unroll 1
+      for (int i = 0; i < 2 * ((off + 15) / 16); ++i) {  // 16 tokens of four channels at a time
+        v4u* const p = reinterpret_cast<v4u*>(vc + (size_t)(8 * part + 4 * (i & 1)) * bs + 16 * (i >> 1));
+        const int n = off - 16 * (i >> 1);
+        v4u w[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          uint32_t* p = reinterpret_cast<uint32_t*>(vc + (size_t)(8 * part + e) * bs + i);
-          *p = rescale4(*p, ratio, off - i);
-        }
+        for (int e = 0; e < 4; ++e) w[e] = p[e * bs / 16];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e * bs / 16] = rescale16(w[e], ratio, n);
+      }
     }
 #pragma unroll
     for (int r = 0; r < kShort; ++r)
@@ -532,7 +573,8 @@ hipError_t launch_kv_block_append(const uint16_t* k, const uint16_t* v, int64_t 
 // together write whole rows between them.  K: a thread per 8 channels of a row.  V: a thread per
 // channel and 16 rows at a time; where these are 16 slots in a row from a multiple of 16 on, save
 // those without a token, their codes are one 16-byte load, otherwise a byte per row; the values go
-// through LDS to become rows of channels.
+// through LDS to become rows of channels.  20000 rows of 8 x 128 (41 MB in, 82 MB out): 22 us,
+// 5.6 TB/s, with the codes still in L2 from the append.
 constexpr int kReadRows = 64;
 
 template <int D>

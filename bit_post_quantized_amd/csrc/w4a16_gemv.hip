@@ -10,13 +10,20 @@
 // the sums are the matrix unit's fp32.
 //  1. w4a16_prep_kernel: X^ in the matrix operand's order, its scales, and T's partial sums over
 //     slices of K (bf16 MFMA on X^ split into three bf16, which keeps all 24 bits).
-//  2. w4a16_kernel: persistent workgroups of 8 waves that split K; a wave keeps its part of X^ in
-//     registers and walks over tiles of 16 columns, with the next tiles' weights in flight while
-//     it computes the current one's.  A lane turns 16 nibbles of one column into fp16 per group,
+//  2. w4a16_kernel: persistent workgroups of 8 waves that split K, or a part of it; a wave keeps
+//     its part of X^ in registers and walks over tiles of 16 columns, with the next tiles' weights
+//     in flight while it computes the current one's.  A lane turns 16 nibbles of one column into fp16 per group,
 //     one fp32 FMA per output and group applies the weight scale, the low-rank product is one more
 //     matrix step per 32 ranks, and the waves meet in LDS once per tile.
 // The weights come in a container of the matrix operand's order (svdq_pack_w4a16): in [N, K/2] a
 // wave's load takes 32 bytes of each of 16 rows, and the scales one 2-byte load per group.
+//  3. w4a16_sum_kernel, where K was cut over workgroups: the sum of their shares.
+//
+// Measured (kernel times): 1 row, 4096 x 131072: 45 us, 6.3 TB/s of weights, the memory's rate.
+// 1 row, 4096 x 4096, rank 32: 4.7 + 5.6 us, of which the weights' bytes are 1.7: two launches and
+// the latency of each one's first loads.  8 rows, 4096 x 12288: 4.8 + 10.9 us (bytes 4.9).  24 fp32
+// rows, 12288 x 4096, rank 48: 6.8 + 18 + 3.9 us; the vector work of unpacking and scaling for six
+// matrix products per group and the low-rank branch (6 us of the three) bound that.
 #include "serve_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -100,9 +107,14 @@ inline int w4a16_slices(int K) {
 constexpr int kMaxTiles = 4;
 constexpr int groups_per_wave(int tiles) { return tiles <= 2 ? 8 : 4; }
 
+// (Three row tiles with 2 groups and two workgroups to a CU: 32.6 us against 28.2 for 24 fp32 rows,
+// 12288 x 4096, rank 48.)
+
 // How a pass is cut.  One persistent workgroup per CU.  Where K is more than a workgroup's waves
-// hold of X^, it is cut into chunks: the workgroups of a column tile take one each and their sums go
-// through memory (shares), or with few rows one workgroup walks over them all and reads X^ again.
+// hold of X^, it is cut into chunks.  With one row tile a workgroup walks over them all and reads X^
+// again (12288 x 4096, rank 32: 1 row 16.1 us, cut 18.3; 16 rows 18.7, cut 20.3); with more, where
+// that is most of what it reads, the workgroups of a column tile take one chunk each and their sums
+// go through memory, shares (64 rows 31 us, read again 39).
 struct W4a16Pass {
   int rows, shares, grid;
   bool loop;
