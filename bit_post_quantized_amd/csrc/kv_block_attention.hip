@@ -14,14 +14,15 @@
 // it stands, and 8 or 16 of its scores share one pair of scales.
 //
 // Two kernels.  Few rows (one or two tiles: decoding) are bound by the codes' bytes: every wave
-// walks over tokens of its own, straight from memory to registers, and the waves meet at the end.
-// More rows (drafts, prompts) are bound by the softmax's vector work: the waves share the tokens,
-// whose codes become fp16 once, in LDS, and own their rows.  With few workgroups the tokens are
-// split over more of them (chunks), whose maxima, sums and outputs a second launch joins.
+// walks over tokens of its own, straight from memory to registers, and the waves meet at the end; the
+// workgroups take equal shares of the batch's tokens.  More rows (drafts, prompts) are bound by the
+// softmax's vector work: the waves share the tokens, whose codes become fp16 once, in LDS, and own their
+// rows; with few workgroups the tokens are split over more of them (chunks).  Where a row's tokens went
+// to several workgroups, a second launch joins their maxima, sums and outputs.
 //
-// Measured (kernel times).  64 requests of up to 8192 tokens, 32 heads to 8 of 128: 138 us, 4.9 TB/s
-// of codes (equal lengths: 5.2).  1 x 10240 tokens, 32 heads: 19 us and 4 for the join; the bytes are
-// 15 at 5.5 TB/s.  2 x 5 rows, 32 heads to 4, before up to 131071 tokens: 49 us and 6; the bytes are
+// Measured (kernel times).  64 requests of up to 8192 tokens, 32 heads to 8 of 128: 127 us, 5.3 TB/s of
+// codes, and 6 for the join (139 and none with a workgroup per request and head).  1 x 10240 tokens, 32
+// heads: 20 us and 4; the bytes are 15 at 5.5 TB/s.  2 x 5 rows, 32 heads to 4, before up to 131071 tokens: 49 us and 6; the bytes are
 // 40.  4 prompts of 475 to 1000 rows, 24 heads to 8 of 64, before up to 4096 tokens: 85 us,
 // 470 TFLOP/s: a wave's tile of 16 rows x 64 tokens is 144 vector instructions, 16 of them
 // exponentials at a quarter of the rate, against 16 matrix ones, and the longest request's 64 tiles
@@ -254,186 +255,257 @@ __device__ __forceinline__ void softmax_step(v4f (*sc)[4], const float* fac, con
 // RT tiles of 16 rows.  A wave's lane (c = l % 16, j = l / 16) scores tokens 16 j .. + 15 of its
 // tile for row c: K's row of matrix row 4 j' + i of product t is token 16 j' + 4 t + i.  The next
 // tile's codes are in flight while this one's are used.
+//
+// shares = 0: a workgroup has one request's cached head.  Otherwise the batch's tokens, in units of
+// kUnit, are one row per cached head, and a workgroup takes an equal share of it: the end of one
+// request, some whole ones, the beginning of another.  Each workgroup adds up the units itself, from the
+// lengths.  What it has of a request is a segment, kept in the workspace unless that is all of it; segment
+// (share w, request b) is number w + b of its head, since one of the two grows from each to the next.
+// The request's first and the number of its segments go to the workspace's beginning.
+constexpr int kUnit = kWaves * kTile;
+
+__device__ __forceinline__ int units_of(const BlockAttention& a, const Range& rg) {
+  return rg.vrows == 0 ? 0 : max(1, (rg.limit(a, rg.vrows - 1) + kUnit - 1) / kUnit);
+}
+
+__device__ __forceinline__ long long uniform(long long x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return (long long)((uint64_t)hi << 32 | lo);
+}
+
+__host__ __device__ inline size_t table_floats(int requests) { return ((size_t)requests * 2 + 3) / 4 * 4; }
+
 template <int D, int RT>
-__global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(BlockAttention a,
-                                                                            int chunks, int groups,
-                                                                            int chunk_tokens) {
+__global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(BlockAttention a, int shares,
+                                                                            int seg_rows) {
   constexpr int SEG = D / 64, DT = D / 16;
   __shared__ float o_lds[kWaves][16][D + 4];
   __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
-  const Work wk = work_of(a.cache.heads, chunks, groups);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, j = lane >> 4;
   const int KV = a.cache.heads, shift = __builtin_ctz(a.cache.bs);
-  const Range rg(a, wk.b);
-  const int vr0 = wk.group * 16 * RT;               // first row (row x head) of this workgroup
-  if (vr0 >= rg.vrows) return;
-  const int top = rg.limit(a, min(vr0 + 16 * RT, rg.vrows) - 1);
-  const int t0 = wk.chunk * chunk_tokens, t1 = min(t0 + chunk_tokens, top);
-  if (chunks > 1 && t0 >= t1) return;               // (the join knows which chunks there are)
-  const int32_t* table = a.tables + (size_t)wk.b * a.width;
-
-  // the table's entries for this lane's K rows (16 tokens from base + 16 (c / 4)) and for its 16
-  // scores and V columns (from base + 16 j); they are looked at one step later, so that the loads
-  // stay in flight meanwhile
-  struct Pages {
-    int k, v;
-  };
-  auto load_pages = [&](int base) {
-    return Pages{table[min(base + 16 * (c >> 2), t1 - 1) >> shift], table[min(base + 16 * j, t1 - 1) >> shift]};
-  };
-  struct Codes {
-    v4u k[4][SEG], v[DT];
-    float ks, vs;
-    bool there;  // this lane's 16 tokens
-  };
-  const int mask = a.cache.bs - 1;
-  auto load_codes = [&](int base, Pages p, Codes& w) {
-    // a block of no token, or outside the pool, is read as block 0 and left out
-    const bool k_there = base + 16 * (c >> 2) < t1 && (unsigned)p.k < (unsigned)a.cache.num_blocks;
-    w.there = base + 16 * j < t1 && (unsigned)p.v < (unsigned)a.cache.num_blocks;
-    p.k = k_there ? p.k : 0;
-    p.v = w.there ? p.v : 0;
-    const size_t bk = (size_t)p.k * KV + wk.h, bv = (size_t)p.v * KV + wk.h;
-    const int tk = (base + 16 * (c >> 2)) & mask, tv = (base + 16 * j) & mask;
-    const uint8_t* kp = a.cache.k_codes + (bk * a.cache.bs + tk + (c & 3)) * D + 16 * j;
+  const int h = blockIdx.x % KV, share = blockIdx.x / KV;
+  int b = share;
+  long long before = 0, u0 = 0, u1 = 0, all = 0;  // units before request b, of this share, of the batch
+  if (shares) {
+    __shared__ long long sums[kWaves], s_before;
+    __shared__ int s_b;
+    const int each = (a.requests + kWaves * 64 - 1) / (kWaves * 64), b0 = threadIdx.x * each;
+    long long mine = 0;
+    for (int k = 0; k < each && b0 + k < a.requests; ++k) mine += units_of(a, Range(a, b0 + k));
+    long long at = wave_scan(mine);
+    if (lane == 63) sums[wave] = at;
+    __syncthreads();
+    at -= mine;
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int s = 0; s < SEG; ++s) w.k[t][s] = *reinterpret_cast<const v4u*>(kp + 4 * t * D + 64 * s);
-    const uint8_t* vp = a.cache.v_codes + (bv * D + c) * a.cache.bs + tv;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) w.v[d] = *reinterpret_cast<const v4u*>(vp + (size_t)16 * d * a.cache.bs);
-    w.ks = a.cache.k_scale[bv];
-    w.vs = a.cache.v_scale[bv];
-  };
-
-  v8h qf[RT][SEG][2];
-  float fac[RT], m[RT], l[RT];
-  int limit[RT];
-  v4f o[RT][DT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int vr = min(vr0 + 16 * t + c, rg.vrows - 1);
-    limit[t] = rg.limit(a, vr);
-    const uint16_t* qp = a.q + (size_t)(rg.row0 + vr / rg.hg) * a.q_stride + (size_t)(wk.h * rg.hg + vr % rg.hg) * D + 16 * j;
-    float x[SEG][16];
-#pragma unroll
-    for (int s = 0; s < SEG; ++s) bf16x16(qp + 64 * s, qp + 64 * s + 8, x[s]);
-    fac[t] = scale_query<SEG>(a, x);
-#pragma unroll
-    for (int s = 0; s < SEG; ++s)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) qf[t][s][e >> 3][e & 7] = (_Float16)x[s][e];
-    m[t] = -__builtin_inff();
-    l[t] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) o[t][d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) at += sums[w];
+      all += sums[w];
+    }
+    all = uniform(all);
+    if (shares > all) shares = (int)all;  // (so that none is empty)
+    if (share >= shares) return;
+    u0 = all * share / shares;
+    u1 = all * (share + 1) / shares;
+    if (at <= u0 && u0 < at + mine)
+      for (int k = 0;; ++k) {  // (ends: u0 lies in one of this thread's requests)
+        const int n = units_of(a, Range(a, b0 + k));
+        if (u0 < at + n) {
+          s_b = b0 + k;
+          s_before = at;
+          break;
+        }
+        at += n;
+      }
+    __syncthreads();
+    b = __builtin_amdgcn_readfirstlane(s_b);
+    before = uniform(s_before);
   }
 
-  constexpr int STEP = kWaves * kTile;
-  auto step = [&](int base, const Codes& w) {
-    Runs r;
-    const float vs = w.there && w.vs != 0.0f ? w.vs : 1.0f;
-    r.ks[0] = r.ks[1] = w.there ? w.ks : 0.0f;
-    r.lv[0] = r.lv[1] = __builtin_amdgcn_logf(vs);
-    r.ivs[0] = r.ivs[1] = __builtin_amdgcn_rcpf(vs);
-    v4f sc[RT][4];
+  auto segment = [&](const Range& rg, int t0, int t1, float* seg) {
+    const int32_t* table = a.tables + (size_t)b * a.width;
+
+    // the table's entries for this lane's K rows (16 tokens from base + 16 (c / 4)) and for its 16
+    // scores and V columns (from base + 16 j); they are looked at one step later, so that the loads
+    // stay in flight meanwhile
+    struct Pages {
+      int k, v;
+    };
+    auto load_pages = [&](int base) {
+      return Pages{table[min(base + 16 * (c >> 2), t1 - 1) >> shift], table[min(base + 16 * j, t1 - 1) >> shift]};
+    };
+    struct Codes {
+      v4u k[4][SEG], v[DT];
+      float ks, vs;
+      bool there;  // this lane's 16 tokens
+    };
+    const int mask = a.cache.bs - 1;
+    auto load_codes = [&](int base, Pages p, Codes& w) {
+      // a block of no token, or outside the pool, is read as block 0 and left out
+      const bool k_there = base + 16 * (c >> 2) < t1 && (unsigned)p.k < (unsigned)a.cache.num_blocks;
+      w.there = base + 16 * j < t1 && (unsigned)p.v < (unsigned)a.cache.num_blocks;
+      p.k = k_there ? p.k : 0;
+      p.v = w.there ? p.v : 0;
+      const size_t bk = (size_t)p.k * KV + h, bv = (size_t)p.v * KV + h;
+      const int tk = (base + 16 * (c >> 2)) & mask, tv = (base + 16 * j) & mask;
+      const uint8_t* kp = a.cache.k_codes + (bk * a.cache.bs + tk + (c & 3)) * D + 16 * j;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      v8h ka[SEG][2];
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int s = 0; s < SEG; ++s) codes16_f16(w.k[t][s], ka[s][0], ka[s][1]);
+        for (int s = 0; s < SEG; ++s) w.k[t][s] = *reinterpret_cast<const v4u*>(kp + 4 * t * D + 64 * s);
+      const uint8_t* vp = a.cache.v_codes + (bv * D + c) * a.cache.bs + tv;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) w.v[d] = *reinterpret_cast<const v4u*>(vp + (size_t)16 * d * a.cache.bs);
+      w.ks = a.cache.k_scale[bv];
+      w.vs = a.cache.v_scale[bv];
+    };
+
+    v8h qf[RT][SEG][2];
+    float fac[RT], m[RT], l[RT];
+    int limit[RT];
+    v4f o[RT][DT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int vr = min(16 * t + c, rg.vrows - 1);
+      limit[t] = rg.limit(a, vr);
+      const uint16_t* qp = a.q + (size_t)(rg.row0 + vr / rg.hg) * a.q_stride + (size_t)(h * rg.hg + vr % rg.hg) * D + 16 * j;
+      float x[SEG][16];
+#pragma unroll
+      for (int s = 0; s < SEG; ++s) bf16x16(qp + 64 * s, qp + 64 * s + 8, x[s]);
+      fac[t] = scale_query<SEG>(a, x);
+#pragma unroll
+      for (int s = 0; s < SEG; ++s)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) qf[t][s][e >> 3][e & 7] = (_Float16)x[s][e];
+      m[t] = -__builtin_inff();
+      l[t] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[t][d] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    constexpr int STEP = kUnit;
+    auto step = [&](int base, const Codes& w) {
+      Runs r;
+      const float vs = w.there && w.vs != 0.0f ? w.vs : 1.0f;
+      r.ks[0] = r.ks[1] = w.there ? w.ks : 0.0f;
+      r.lv[0] = r.lv[1] = __builtin_amdgcn_logf(vs);
+      r.ivs[0] = r.ivs[1] = __builtin_amdgcn_rcpf(vs);
+      v4f sc[RT][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        v8h ka[SEG][2];
+#pragma unroll
+        for (int s = 0; s < SEG; ++s) codes16_f16(w.k[t][s], ka[s][0], ka[s][1]);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) {
+          v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int s = 0; s < SEG; ++s) {
+            x = mfma16(ka[s][0], qf[q][s][0], x);
+            x = mfma16(ka[s][1], qf[q][s][1], x);
+          }
+          sc[q][t] = x;
+        }
+      }
+      v8h pf[RT][2];
+      int seen[RT][2];
 #pragma unroll
       for (int q = 0; q < RT; ++q) {
-        v4f x = {0.0f, 0.0f, 0.0f, 0.0f};
+        const int n = w.there ? limit[q] - (base + 16 * j) : 0;  // of this lane's 16 tokens
+        seen[q][0] = n;
+        seen[q][1] = n - 8;
+      }
+      softmax_step<RT, DT>(sc, fac, r, true, seen, m, l, o, pf);
 #pragma unroll
-        for (int s = 0; s < SEG; ++s) {
-          x = mfma16(ka[s][0], qf[q][s][0], x);
-          x = mfma16(ka[s][1], qf[q][s][1], x);
+      for (int d = 0; d < DT; ++d) {
+        v8h va, vb;
+        codes16_f16(w.v[d], va, vb);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) {
+          o[q][d] = mfma16(va, pf[q][0], o[q][d]);
+          o[q][d] = mfma16(vb, pf[q][1], o[q][d]);
         }
-        sc[q][t] = x;
+      }
+    };
+    int base = t0 + wave * kTile;
+    if (base < t1) {
+      // pages two steps ahead, codes one (past the last tile block 0 is read, unused)
+      Pages p = load_pages(base);
+      Codes wa, wb;
+      load_codes(base, p, wa);
+      p = load_pages(base + STEP);
+      for (;;) {
+        load_codes(base + STEP, p, wb);
+        p = load_pages(base + 2 * STEP);
+        step(base, wa);
+        base += STEP;
+        if (base >= t1) break;
+        load_codes(base + STEP, p, wa);
+        p = load_pages(base + 2 * STEP);
+        step(base, wb);
+        base += STEP;
+        if (base >= t1) break;
       }
     }
-    v8h pf[RT][2];
-    int seen[RT][2];
+
+    // ---- the waves meet, one tile of 16 rows after the other
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
-      const int n = w.there ? limit[q] - (base + 16 * j) : 0;  // of this lane's 16 tokens
-      seen[q][0] = n;
-      seen[q][1] = n - 8;
-    }
-    softmax_step<RT, DT>(sc, fac, r, true, seen, m, l, o, pf);
-#pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      v8h va, vb;
-      codes16_f16(w.v[d], va, vb);
-#pragma unroll
-      for (int q = 0; q < RT; ++q) {
-        o[q][d] = mfma16(va, pf[q][0], o[q][d]);
-        o[q][d] = mfma16(vb, pf[q][1], o[q][d]);
+      const float ls = sum_quads(l[q]);
+      __syncthreads();
+      if (j == 0) {
+        m_lds[wave][c] = m[q];
+        l_lds[wave][c] = ls;
       }
-    }
-  };
-  int base = t0 + wave * kTile;
-  if (base < t1) {
-    // pages two steps ahead, codes one (past the last tile block 0 is read, unused)
-    Pages p = load_pages(base);
-    Codes wa, wb;
-    load_codes(base, p, wa);
-    p = load_pages(base + STEP);
-    for (;;) {
-      load_codes(base + STEP, p, wb);
-      p = load_pages(base + 2 * STEP);
-      step(base, wa);
-      base += STEP;
-      if (base >= t1) break;
-      load_codes(base + STEP, p, wa);
-      p = load_pages(base + 2 * STEP);
-      step(base, wb);
-      base += STEP;
-      if (base >= t1) break;
-    }
-  }
-
-  // ---- the waves meet, one tile of 16 rows after the other
 #pragma unroll
-  for (int q = 0; q < RT; ++q) {
-    const float ls = sum_quads(l[q]);
-    __syncthreads();
-    if (j == 0) {
-      m_lds[wave][c] = m[q];
-      l_lds[wave][c] = ls;
-    }
+      for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f*>(&o_lds[wave][c][16 * d + 4 * j]) = o[q][d];
+      __syncthreads();
+      for (int e = threadIdx.x; e < 16 * D; e += kWaves * 64) {
+        const int row = e / D, d = e % D, vr = 16 * q + row;
+        if (vr >= rg.vrows) continue;
+        float mm = -__builtin_inff();
 #pragma unroll
-    for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f*>(&o_lds[wave][c][16 * d + 4 * j]) = o[q][d];
-    __syncthreads();
-    for (int e = threadIdx.x; e < 16 * D; e += kWaves * 64) {
-      const int row = e / D, d = e % D, vr = vr0 + 16 * q + row;
-      if (vr >= rg.vrows) continue;
-      float mm = -__builtin_inff();
+        for (int w = 0; w < kWaves; ++w) mm = __builtin_fmaxf(mm, m_lds[w][row]);
+        const float off = mm == -__builtin_inff() ? 0.0f : mm;
+        float sum = 0.0f, out = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) mm = __builtin_fmaxf(mm, m_lds[w][row]);
-      const float off = mm == -__builtin_inff() ? 0.0f : mm;
-      float sum = 0.0f, out = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float f = __builtin_amdgcn_exp2f(m_lds[w][row] - off);
-        sum = __builtin_fmaf(l_lds[w][row], f, sum);
-        out = __builtin_fmaf(o_lds[w][row][d], f, out);
-      }
-      const size_t at = rg.out_row(a, wk.h, vr);
-      if (chunks == 1) {
-        a.out[at * D + d] = float_to_bf16_bits(sum == 0.0f ? 0.0f : out / sum);
-      } else {
-        float* ws = a.ws + (at * chunks + wk.chunk) * (D + 4);
-        ws[4 + d] = out;
-        if (d == 0) {
-          ws[0] = mm;
-          ws[1] = sum;
+        for (int w = 0; w < kWaves; ++w) {
+          const float f = __builtin_amdgcn_exp2f(m_lds[w][row] - off);
+          sum = __builtin_fmaf(l_lds[w][row], f, sum);
+          out = __builtin_fmaf(o_lds[w][row][d], f, out);
+        }
+        if (!seg) {
+          a.out[rg.out_row(a, h, vr) * D + d] = float_to_bf16_bits(sum == 0.0f ? 0.0f : out / sum);
+        } else {
+          float* ws = seg + (size_t)vr * (D + 4);
+          ws[4 + d] = out;
+          if (d == 0) {
+            ws[0] = mm;
+            ws[1] = sum;
+          }
         }
       }
     }
+  };
+  if (!shares) {
+    const Range rg(a, b);
+    if (rg.vrows > 0) segment(rg, 0, rg.limit(a, rg.vrows - 1), nullptr);
+    return;
+  }
+  float* const segs = a.ws + table_floats(a.requests) + (size_t)h * (gridDim.x / KV + a.requests) * seg_rows * (D + 4);
+  for (; before < u1; ++b) {
+    const Range rg(a, b);
+    const int n = units_of(a, rg);
+    if (n == 0) continue;
+    const int s0 = (int)max(u0 - before, 0ll), s1 = (int)min(u1 - before, (long long)n);
+    if (s0 == 0 && h == 0 && threadIdx.x == 0) {
+      int32_t* const info = reinterpret_cast<int32_t*>(a.ws) + 2 * (size_t)b;
+      info[0] = share;
+      info[1] = (int)(((before + n) * shares - 1) / all) - share + 1;
+    }
+    segment(rg, s0 * kUnit, min(s1 * kUnit, rg.limit(a, rg.vrows - 1)),
+            s1 - s0 == n ? nullptr : segs + (size_t)(share + b) * seg_rows * (D + 4));
+    before += n;
   }
 }
 
@@ -695,23 +767,42 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
 // --------------------------------------------------------------------------------------- join
 constexpr int kJoinThreads = 256;
 
-// The chunks that were written of row i, head h of a request: those below the tokens that the last
-// row of its group sees.
-__device__ __forceinline__ int chunks_of(const BlockAttention& a, const Range& rg, int i, int h, int chunks,
-                                         int chunk_tokens, int span) {
-  const int vr = i * rg.hg + h % rg.hg;
-  const int top = rg.limit(a, min((vr / span + 1) * span, rg.vrows) - 1);
-  return min((top + chunk_tokens - 1) / chunk_tokens, chunks);
-}
+// How a batch is cut (split_of).
+struct Cut {
+  int shares, seg_rows;             // few rows: workgroups per cached head (0: not cut), rows of a segment
+  int chunks, chunk_tokens, span;   // more rows: chunks of tokens, rows per workgroup
+};
 
-// Joins up to kFewChunks chunks: a lane adds four channels of a (row, head), and the
-// lanes of a (row, head) find its chunks' weights 2^(m_k - M) together, one chunk each.  (A workgroup
-// per (row, head), as below, takes 110 us more than this for 2 chunks of 2950 rows x 24 heads.)
-constexpr int kFewChunks = 16;
+// The parts of row i, head h of request b, `used` of them `stride` floats apart; used < 0: its output
+// is written already.
+struct Parts {
+  const float* first;
+  size_t stride;
+  int used;
+};
 
 template <int D>
-__global__ __launch_bounds__(kJoinThreads) void kv_block_join_kernel(BlockAttention a, int chunks,
-                                                                     int chunk_tokens, int span, unsigned joins) {
+__device__ __forceinline__ Parts parts_of(const BlockAttention& a, const Cut& cut, const Range& rg, int b, int i,
+                                          int h) {
+  const int vr = i * rg.hg + h % rg.hg;
+  if (cut.shares) {
+    const v2u info = reinterpret_cast<const v2u*>(a.ws)[b];
+    const size_t seg = (size_t)(h / rg.hg) * (cut.shares + a.requests) + info.x + b;
+    return Parts{a.ws + table_floats(a.requests) + (seg * cut.seg_rows + vr) * (D + 4),
+                 (size_t)cut.seg_rows * (D + 4), info.y == 1 ? -1 : (int)info.y};
+  }
+  // the chunks below the tokens that the last row of its workgroup sees
+  const int top = rg.limit(a, min((vr / cut.span + 1) * cut.span, rg.vrows) - 1);
+  return Parts{a.ws + ((size_t)(rg.row0 + i) * a.heads + h) * cut.chunks * (D + 4), D + 4,
+               min((top + cut.chunk_tokens - 1) / cut.chunk_tokens, cut.chunks)};
+}
+
+// Joins a few parts of many rows: a lane adds four channels of a (row, head), part by part.  (A
+// workgroup per (row, head), as below, takes 110 us more than this for 2 chunks of 2950 rows x 24 heads.)
+constexpr int kFewParts = 16;
+
+template <int D>
+__global__ __launch_bounds__(kJoinThreads) void kv_block_join_kernel(BlockAttention a, Cut cut, unsigned joins) {
   constexpr int LANES = D / 4;
   const int lane = threadIdx.x & (LANES - 1);
   unsigned id = blockIdx.x * (kJoinThreads / LANES) + threadIdx.x / LANES;
@@ -721,47 +812,50 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_join_kernel(BlockAttent
   const int i = id % a.max_rows, b = id / a.max_rows;
   const Range rg(a, b);
   if (i >= rg.n) return;
-  const int used = chunks_of(a, rg, i, h, chunks, chunk_tokens, span);
-  const size_t at = (size_t)(rg.row0 + i) * a.heads + h;
-  const float* ws = a.ws + at * chunks * (D + 4);
-  const v2f ms = *reinterpret_cast<const v2f*>(ws + min(lane, max(used - 1, 0)) * (D + 4));
-  const float m = lane < used ? ms.x : -__builtin_inff();
-  float mm = m;
-#pragma unroll
-  for (int x = 1; x < LANES; x <<= 1) mm = __builtin_fmaxf(mm, __shfl_xor(mm, x));
-  const float f = __builtin_amdgcn_exp2f(m - (mm == -__builtin_inff() ? 0.0f : mm));
-  float sum = lane < used ? ms.y * f : 0.0f;
-#pragma unroll
-  for (int x = 1; x < LANES; x <<= 1) sum += __shfl_xor(sum, x);
+  const Parts p = parts_of<D>(a, cut, rg, b, i, h);
+  if (p.used < 0) return;
+  float m = -__builtin_inff(), sum = 0.0f;
   v4f out = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k = 0; k < used; k += 4) {
+  for (int k = 0; k < p.used; k += 4) {
+    v2f ms[4];
     v4f v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = *reinterpret_cast<const v4f*>(ws + min(k + u, used - 1) * (D + 4) + 4 + 4 * lane);
+    for (int u = 0; u < 4; ++u) {  // (past the last part, that again)
+      const float* ws = p.first + min(k + u, p.used - 1) * p.stride;
+      ms[u] = *reinterpret_cast<const v2f*>(ws);
+      v[u] = *reinterpret_cast<const v4f*>(ws + 4 + 4 * lane);
+    }
+    float mn = m;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) mn = __builtin_fmaxf(mn, ms[u].x);
+    const float off = mn == -__builtin_inff() ? 0.0f : mn, alpha = __builtin_amdgcn_exp2f(m - off);
+    sum *= alpha;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] *= alpha;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const float w = __shfl(f, k + u, LANES);
-      if (k + u < used)
+      const float f = k + u < p.used ? __builtin_amdgcn_exp2f(ms[u].x - off) : 0.0f;
+      sum = __builtin_fmaf(ms[u].y, f, sum);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) out[e] = __builtin_fmaf(v[u][e], w, out[e]);
+      for (int e = 0; e < 4; ++e) out[e] = __builtin_fmaf(v[u][e], f, out[e]);
     }
+    m = mn;
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  *reinterpret_cast<v2u*>(a.out + at * D + 4 * lane) =
+  *reinterpret_cast<v2u*>(a.out + ((size_t)(rg.row0 + i) * a.heads + h) * D + 4 * lane) =
       v2u{pack2_bf16(out[0] * inv, out[1] * inv), pack2_bf16(out[2] * inv, out[3] * inv)};
 }
 
-// Joins more chunks of few rows, one (row, head) per workgroup (a lane of the kernel above would add
-// them one after the other).  256 threads: the chunks' weights 2^(m_k - M) go through
-// LDS, then a thread adds four channels of every PARTS-th chunk, eight loads in flight (96 chunks of
+// Joins more parts of few rows, one (row, head) per workgroup (a lane of the kernel above would add
+// them one after the other).  256 threads: the parts' weights 2^(m_k - M) go through
+// LDS, then a thread adds four channels of every PARTS-th one, eight loads in flight (96 chunks of
 // 320 rows x heads of 128: 8.7 us with one channel to a thread).
-constexpr int kMaxChunks = 1024;
+constexpr int kMaxParts = 1024;
 
 template <int D>
-__global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAttention a, int chunks,
-                                                                        int chunk_tokens, int span) {
+__global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAttention a, Cut cut) {
   constexpr int PARTS = kJoinThreads / (D / 4);
-  __shared__ float f_lds[kMaxChunks];
+  __shared__ float f_lds[kMaxParts];
   __shared__ float red[2][kJoinThreads / 64];
   __shared__ __attribute__((aligned(16))) float o_lds[PARTS][D];
   unsigned id = blockIdx.x;
@@ -771,16 +865,16 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const Range rg(a, b);
   if (i >= rg.n) return;
-  const int used = chunks_of(a, rg, i, h, chunks, chunk_tokens, span);
-  const size_t at = (size_t)(rg.row0 + i) * a.heads + h;
-  const float* ws = a.ws + at * chunks * (D + 4);
-  // four chunks to a thread at most: their maxima and sums
-  float m[kMaxChunks / kJoinThreads], s[kMaxChunks / kJoinThreads];
+  const Parts p = parts_of<D>(a, cut, rg, b, i, h);
+  const int used = p.used;
+  if (used < 0) return;
+  // four parts to a thread at most: their maxima and sums
+  float m[kMaxParts / kJoinThreads], s[kMaxParts / kJoinThreads];
   float mm = -__builtin_inff();
 #pragma unroll
-  for (int q = 0; q < kMaxChunks / kJoinThreads; ++q) {
+  for (int q = 0; q < kMaxParts / kJoinThreads; ++q) {
     const int k = tid + kJoinThreads * q;
-    const v2f ms = *reinterpret_cast<const v2f*>(ws + (size_t)min(k, max(used - 1, 0)) * (D + 4));
+    const v2f ms = *reinterpret_cast<const v2f*>(p.first + max(min(k, used - 1), 0) * p.stride);
     m[q] = k < used ? ms.x : -__builtin_inff();
     s[q] = k < used ? ms.y : 0.0f;
     mm = __builtin_fmaxf(mm, m[q]);
@@ -794,7 +888,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
   const float off = mm == -__builtin_inff() ? 0.0f : mm;
   float sum = 0.0f;
 #pragma unroll
-  for (int q = 0; q < kMaxChunks / kJoinThreads; ++q) {
+  for (int q = 0; q < kMaxParts / kJoinThreads; ++q) {
     const int k = tid + kJoinThreads * q;
     const float f = __builtin_amdgcn_exp2f(m[q] - off);
     if (k < used) f_lds[k] = f;
@@ -813,7 +907,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
     v4f v[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u)
-      v[u] = *reinterpret_cast<const v4f*>(ws + (size_t)min(k + u * PARTS, used - 1) * (D + 4) + 4 + d);
+      v[u] = *reinterpret_cast<const v4f*>(p.first + min(k + u * PARTS, used - 1) * p.stride + 4 + d);
 #pragma unroll
     for (int u = 0; u < 8; ++u)
       if (k + u * PARTS < used) {
@@ -827,8 +921,8 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
   if (tid < D) {
     float o = 0.0f;
 #pragma unroll
-    for (int p = 0; p < PARTS; ++p) o += o_lds[p][tid];
-    a.out[at * D + tid] = float_to_bf16_bits(sum == 0.0f ? 0.0f : o / sum);
+    for (int q = 0; q < PARTS; ++q) o += o_lds[q][tid];
+    a.out[((size_t)(rg.row0 + i) * a.heads + h) * D + tid] = float_to_bf16_bits(sum == 0.0f ? 0.0f : o / sum);
   }
 }
 
@@ -839,17 +933,22 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
 // hide the softmax's latency), at 128 in four waves of 32 (454 against 605 us on 4096 rows before
 // 8192 tokens: an LDS read feeds two products).
 //
-// Few rows: the codes are read at 5.2 TB/s by one workgroup on each CU, and a join costs 5 us, so
-// tokens are cut only as far as that fills (32768 tokens, 8 heads: 174 us uncut, 22.1 in 32 chunks,
-// 24.1 in 64, 30.8 in 128; 24 requests of 2048, 8 heads: 12.4 uncut, 17.5 in two).  A chunk is 16384
-// tokens at most, so that one long request among short ones does not end up in few workgroups.
+// Few rows: equal shares for 256 workgroups, up to 512 where there are as many requests (32768 tokens,
+// 8 heads: 174 us uncut, 22.1 by 256, 24.1 by 512, 30.8 by 1024; 256 requests of up to 2000 tokens, 8 heads:
+// 119 us by 512, 127 by 256, 139 by 2048).  Each adds up the lengths, some have a second request to
+// begin, and a join costs 5 us, so a batch is cut only where its workgroups leave CUs idle for longer
+// than that (1.3 us a unit; 24 requests of 2048, 8 heads: 12.4 us uncut, 17.5 cut), or where the table has
+// room for a request that would go on long after the others: 64 requests, 8 heads, one of 16384 tokens
+// and 200 in the others: 85 us uncut, 26 cut; up to 8192: 139, 133; 500 each: 16.7, 21 (1000 of up to 1000,
+// 2 heads: 29, 45, so where the requests alone fill the chip twice the room must be more).
 // More rows: cut so that the workgroups fit the chip at once, if the tiles saved (1.2 us each) take
 // longer than the join (6 us and its bytes at 4 TB/s): 2 x 5 rows before 131071 tokens 91 us in 32
 // chunks, 66 in 64, 60 in 96; 2 prompts of 1024 rows, 12 heads: 22.7 us uncut, 30 in two.
 struct Split {
   bool few;
-  int rt, groups, chunks, chunk_tokens;
-  int span() const { return (few ? 16 : 64) * rt; }
+  int rt, groups;
+  Cut cut;
+  bool joins() const { return few ? cut.shares > 0 : cut.chunks > 1; }
 };
 
 static Split split_of(int requests, int rows, int max_rows, int heads, int kv_heads, int dim, int width, int bs) {
@@ -857,19 +956,27 @@ static Split split_of(int requests, int rows, int max_rows, int heads, int kv_he
   const long long vrows = (long long)max_rows * (heads / kv_heads);
   s.few = vrows <= (dim == 64 ? 32 : 16);
   s.rt = s.few ? (vrows > 16 ? 2 : 1) : (vrows > 64 ? 2 : 1);
-  s.groups = (int)((vrows + s.span() - 1) / s.span());
+  s.cut = Cut{0, s.few ? (int)vrows : 0, 1, 0, (s.few ? 16 : 64) * s.rt};
+  s.groups = (int)((vrows + s.cut.span - 1) / s.cut.span);
   const long long natural = (long long)requests * kv_heads * s.groups;
   const long long tokens = (long long)width * bs;
-  const int unit = s.few ? kWaves * kTile : 4 * kTile;
-  long long chunks = (s.few ? 256 : s.rt == 1 ? 768 : 512) / natural;
-  if (s.few && natural <= 4096) {
-    const long long least = (tokens + 16383) / 16384;
-    if (chunks < least) chunks = least;
+  if (s.few) {
+    const long long units = (tokens + kUnit - 1) / kUnit, idle = natural < 256 ? 256 - natural : 0;
+    const bool uneven = tokens > (natural < 1024 ? 4096 : 16384);
+    const bool cut = uneven || units * idle * 1300 > 256 * 6000;  // ns
+    if (cut && requests <= 4096 && natural <= 16384) {
+      const int least = 256 / kv_heads, most = 512 / kv_heads;
+      const int shares = requests < least ? least : requests < most ? requests : most;
+      s.cut.shares = shares > 1 ? shares : 1;
+    }
+    return s;
   }
+  const int unit = 4 * kTile;
+  long long chunks = (s.rt == 1 ? 768 : 512) / natural;
   const long long most = (tokens + unit - 1) / unit;
   if (chunks > most) chunks = most;
-  if (chunks > kMaxChunks) chunks = kMaxChunks;
-  if (!s.few && chunks > 1) {
+  if (chunks > kMaxParts) chunks = kMaxParts;
+  if (chunks > 1) {
     long long joins = (long long)requests * max_rows;
     joins = (joins < rows ? joins : rows) * heads;
     const long long saved = tokens / kTile * (chunks - 1) / chunks * 1200;  // ns
@@ -878,13 +985,13 @@ static Split split_of(int requests, int rows, int max_rows, int heads, int kv_he
   if (chunks < 1) chunks = 1;
   long long per = (tokens + chunks - 1) / chunks;
   per = (per + unit - 1) / unit * unit;
-  s.chunk_tokens = (int)per;
-  s.chunks = (int)((tokens + per - 1) / per);
+  s.cut.chunk_tokens = (int)per;
+  s.cut.chunks = (int)((tokens + per - 1) / per);
   return s;
 }
 
-// A launch has fewer than 2^32 threads: with 512 to a workgroup there is room for 2^23 (cut into
-// chunks there are 2^22 at most, and fewer joins).
+// A launch has fewer than 2^32 threads: with 512 to a workgroup there is room for 2^23.  (What is cut
+// has fewer workgroups than that, and fewer joins.)
 bool kv_block_attention_fits(int requests, int max_rows, int heads, int kv_heads, int dim) {
   const long long groups = split_of(requests, 0, max_rows, heads, kv_heads, dim, 1, 16).groups;
   return requests * groups * kv_heads < 1 << 23;
@@ -894,33 +1001,38 @@ size_t kv_block_attention_ws_bytes(int requests, int rows, int max_rows, int hea
                                    int dim, int width, int bs) {
   if (requests <= 0 || rows <= 0) return 0;
   const Split s = split_of(requests, rows, max_rows, heads, kv_heads, dim, width, bs);
-  return s.chunks == 1 ? 0 : (size_t)rows * heads * s.chunks * (dim + 4) * sizeof(float);
+  if (!s.joins()) return 0;
+  const size_t parts = s.few ? (size_t)kv_heads * (s.cut.shares + requests) * s.cut.seg_rows
+                             : (size_t)rows * heads * s.cut.chunks;
+  return (parts * (dim + 4) + (s.few ? table_floats(requests) : 0)) * sizeof(float);
 }
 
 template <int D>
 static hipError_t launch(const BlockAttention& a, hipStream_t stream) {
   const Split s = split_of(a.requests, a.rows, a.max_rows, a.heads, a.cache.heads, D, a.width, a.cache.bs);
-  const long long grid = (long long)a.requests * s.groups * s.chunks * a.cache.heads;
-  const long long joins = (long long)a.requests * a.max_rows * a.heads;
-  const int each = s.chunks <= kFewChunks ? kJoinThreads / (D / 4) : 1;
-  const long long join_grid = (joins + each - 1) / each;
-#define SVDQ_ATTEND(WAVES, ...)                                                                  \
-  hipLaunchKernelGGL((__VA_ARGS__), dim3((unsigned)grid), dim3(WAVES * 64), 0, stream, a,        \
-                     s.chunks, s.groups, s.chunk_tokens)
-  if (s.few && s.rt == 1) SVDQ_ATTEND(kWaves, kv_block_attention_kernel<D, 1>);
-  else if (s.few) SVDQ_ATTEND(kWaves, kv_block_attention_kernel<D, (D == 64 ? 2 : 1)>);  // (128: never)
-  else if (s.rt == 1) SVDQ_ATTEND(4, kv_block_attention_rows_kernel<D, 1, 4>);
-  else if constexpr (D == 64) SVDQ_ATTEND(8, kv_block_attention_rows_kernel<D, 1, 8>);
-  else SVDQ_ATTEND(4, kv_block_attention_rows_kernel<D, 2, 4>);
+  const dim3 few((unsigned)a.cache.heads * (s.cut.shares ? s.cut.shares : a.requests));
+  const dim3 more((unsigned)(a.requests * s.groups * s.cut.chunks * a.cache.heads));
+#define SVDQ_ATTEND(GRID, WAVES, KERNEL, ...) \
+  hipLaunchKernelGGL(KERNEL, GRID, dim3(WAVES * 64), 0, stream, a, __VA_ARGS__)
+  if (s.few && s.rt == 1) SVDQ_ATTEND(few, kWaves, (kv_block_attention_kernel<D, 1>), s.cut.shares, s.cut.seg_rows);
+  else if (s.few)  // (128 channels: never)
+    SVDQ_ATTEND(few, kWaves, (kv_block_attention_kernel<D, (D == 64 ? 2 : 1)>), s.cut.shares, s.cut.seg_rows);
+  else if (s.rt == 1)
+    SVDQ_ATTEND(more, 4, (kv_block_attention_rows_kernel<D, 1, 4>), s.cut.chunks, s.groups, s.cut.chunk_tokens);
+  else if constexpr (D == 64)
+    SVDQ_ATTEND(more, 8, (kv_block_attention_rows_kernel<D, 1, 8>), s.cut.chunks, s.groups, s.cut.chunk_tokens);
+  else
+    SVDQ_ATTEND(more, 4, (kv_block_attention_rows_kernel<D, 2, 4>), s.cut.chunks, s.groups, s.cut.chunk_tokens);
 #undef SVDQ_ATTEND
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || s.chunks == 1) return e;
-  if (s.chunks <= kFewChunks) {
-    hipLaunchKernelGGL(kv_block_join_kernel<D>, dim3((unsigned)join_grid), dim3(kJoinThreads), 0, stream,
-                       a, s.chunks, s.chunk_tokens, s.span(), (unsigned)joins);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !s.joins()) return e;
+  const unsigned joins = (unsigned)(a.requests * a.max_rows * a.heads);
+  if ((s.few ? s.cut.shares : s.cut.chunks) <= kFewParts || joins >= 4096) {
+    const unsigned each = kJoinThreads / (D / 4);
+    hipLaunchKernelGGL(kv_block_join_kernel<D>, dim3((joins + each - 1) / each), dim3(kJoinThreads), 0, stream, a,
+                       s.cut, joins);
   } else {
-    hipLaunchKernelGGL(kv_block_combine_kernel<D>, dim3((unsigned)join_grid), dim3(kJoinThreads), 0, stream,
-                       a, s.chunks, s.chunk_tokens, s.span());
+    hipLaunchKernelGGL(kv_block_combine_kernel<D>, dim3(joins), dim3(kJoinThreads), 0, stream, a, s.cut);
   }
   return hipGetLastError();
 }

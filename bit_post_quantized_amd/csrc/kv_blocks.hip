@@ -19,25 +19,6 @@ constexpr int kPlanRows = 1024;
 
 __device__ __forceinline__ int clamp0(int x) { return x < 0 ? 0 : x; }
 
-// Adds the value of the lane that a DPP control names (0 where there is none, or outside ROWS).
-template <int CTRL, int ROWS>
-__device__ __forceinline__ long long add_lane(long long v) {
-  const uint32_t lo = __builtin_amdgcn_update_dpp(0u, (uint32_t)v, CTRL, ROWS, 0xF, false);
-  const uint32_t hi = __builtin_amdgcn_update_dpp(0u, (uint32_t)(v >> 32), CTRL, ROWS, 0xF, false);
-  return v + (long long)((uint64_t)hi << 32 | lo);
-}
-
-// Inclusive sums of one value per lane: within rows of 16 lanes by shifts of 1, 2, 4 and 8, then
-// the rows before by two broadcasts of a row's last lane.
-__device__ __forceinline__ long long wave_scan(long long v) {
-  v = add_lane<0x111, 0xF>(v);
-  v = add_lane<0x112, 0xF>(v);
-  v = add_lane<0x114, 0xF>(v);
-  v = add_lane<0x118, 0xF>(v);
-  v = add_lane<0x142, 0xA>(v);  // lane 15 to the second row, 47 to the fourth
-  return add_lane<0x143, 0xC>(v);  // lane 31 to the upper half
-}
-
 // Adds what the waves before have (`total`: of this wave, in its last lane); sum: of all.  One barrier:
 // two scans that follow each other take different `lds`.
 __device__ __forceinline__ long long waves_before(long long total, long long* lds, long long& sum) {

@@ -114,6 +114,52 @@ def test_many_short_requests_under_a_wide_table(gpu_lib):
     check(c, run(c, True, 0.125), True, 0.125)
 
 
+@pytest.mark.parametrize("seq,rows,heads,kv_heads,dim,bs,width", [
+    ([0] * 5 + [1] + [0] * 3, [1] * 9, 2, 1, 64, 16, 600),               # one unit each, mostly of nothing
+    ([5000], [0], 1, 1, 128, 16, 400), ([0], [1], 1, 1, 128, 16, 400),
+    ([300, 5000, 255, 256, 257, 0, 4000], [1, 0, 2, 0, 1, 1, 3], 8, 2, 64, 32, 256),
+    ([16384, 9, 700], [1, 1, 1], 32, 2, 64, 128, 200),                   # two row tiles
+    ([4097, 4096, 8192], [4, 4, 4], 4, 1, 128, 16, 600),
+    ([20000, 3, 3, 3, 900], [2, 1, 2, 1, 2], 6, 3, 128, 64, 400),
+    ([513] * 40, [1] * 40, 4, 4, 64, 16, 512),
+])
+def test_few_rows_in_equal_shares(gpu_lib, seq, rows, heads, kv_heads, dim, bs, width):
+    from bit_post_quantized_amd import serve_binding as SB
+    assert sum(rows) == 0 or SB.kv_block_attention_workspace_bytes(
+        len(seq), sum(rows), max(max(rows), 1), heads, kv_heads, dim, width, bs)
+    c = batch(sum(seq) + bs, seq, rows, heads, kv_heads, dim, bs, width=width, extra=2)
+    for causal in (False, True):
+        check(c, run(c, causal, 0.1), causal, 0.1)
+
+
+@pytest.mark.parametrize("n,kv_heads,width", [(700, 3, 200), (4096, 1, 300), (4097, 1, 300)])
+def test_many_uneven_requests(gpu_lib, n, kv_heads, width):
+    # shares of thousands of requests, several to a thread that adds them up; one more and none is cut
+    rng = np.random.default_rng(n)
+    seq, rows = rng.integers(0, 60, n), rng.integers(0, 3, n)
+    seq[rng.integers(0, n, 3)] = [9000, 3000, 12000]
+    c = batch(n, [int(x) for x in seq], [int(x) for x in rows], 2 * kv_heads, kv_heads, 64, 64, width=width)
+    check(c, run(c, True, 0.125), True, 0.125)
+
+
+def test_shares_follow_the_lengths_in_a_graph(gpu_lib):
+    c = batch(92, [6000, 3000, 0, 900], [1, 2, 1, 1], 8, 2, 128, 16, width=700)
+    c["tables"][3, :] = c["tables"][0, :]
+    cache = dev_cache(*c["cache"])
+    i32 = lambda a: to_dev(a, torch.int32)  # noqa: E731
+    q, tables, seq, cu = to_dev_bf16(c["q"]), i32(c["tables"]), i32(c["seq"]), i32(c["cu"])
+    out, g = torch.zeros_like(q), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.attention(q, tables, seq, cu, 2, sm_scale=0.1, out=out)
+    for lens in ([6000, 3000, 0, 900], [1, 0, 0, 0], [6000, 5, 1, 6000], [0, 0, 0, 0], [300, 3000, 4000, 1]):
+        seq.copy_(i32(np.array(lens)))
+        g.replay()
+        eager = cache.attention(q, tables, seq, cu, 2, sm_scale=0.1)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), lens
+        check(dict(c, seq=np.array(lens)), host64(eager), True, 0.1)
+
+
 def test_split_rows_with_bad_entries_on_two_streams_and_in_a_graph(gpu_lib):
     c = batch(91, [6000, 700], [6, 6], 8, 1, 64, 32, width=200)
     c["tables"][0, 40:75], c["tables"][1, 3] = -1, 10 ** 6
