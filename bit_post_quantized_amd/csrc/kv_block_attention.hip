@@ -993,7 +993,7 @@ static Split split_of(int requests, int rows, int max_rows, int heads, int kv_he
 // A launch has fewer than 2^32 threads: with 512 to a workgroup there is room for 2^23.  (What is cut
 // has fewer workgroups than that, and fewer joins.)
 bool kv_block_attention_fits(int requests, int max_rows, int heads, int kv_heads, int dim) {
-  const long long groups = split_of(requests, 0, max_rows, heads, kv_heads, dim, 1, 16).groups;
+  const long long groups = split_of(1, 0, max_rows, heads, kv_heads, dim, 1, 16).groups;
   return requests * groups * kv_heads < 1 << 23;
 }
 
