@@ -83,25 +83,6 @@ __device__ __forceinline__ float sum_quads(float x) {
   return x + __shfl_xor(x, 32);
 }
 
-// What one workgroup works on, from its linear id: cached head fastest (the workgroups of one
-// run of blocks read neighbouring memory, and with 8 heads an XCD keeps to one), then the chunk,
-// the row group, the request.
-struct Work {
-  int h, chunk, group, b;
-};
-
-__device__ __forceinline__ Work work_of(int kv_heads, int chunks, int groups) {
-  Work w;
-  unsigned id = blockIdx.x;
-  w.h = id % kv_heads;
-  id /= kv_heads;
-  w.chunk = id % chunks;
-  id /= chunks;
-  w.group = id % groups;
-  w.b = id / groups;
-  return w;
-}
-
 // The rows and tokens of a workgroup that takes `span` rows (row x head, head fastest) from
 // group * span on.
 struct Range {
@@ -121,6 +102,52 @@ struct Range {
     return (size_t)(row0 + vr / hg) * a.heads + h * hg + vr % hg;
   }
 };
+
+__device__ __forceinline__ long long uniform(long long x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return (long long)((uint64_t)hi << 32 | lo);
+}
+
+// The batch as one row of units, units(range) to a request: the request that holds unit target(all) of
+// all of them, and the units before it.  Every workgroup adds the lengths up by itself.  False: no unit
+// (target < 0).
+template <int THREADS, class Units, class Target>
+__device__ __forceinline__ bool locate(const BlockAttention& a, Units units, Target target, int& b,
+                                       long long& before, long long& all) {
+  __shared__ long long sums[THREADS / 64], s_before;
+  __shared__ int s_b;
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const int each = (a.requests + THREADS - 1) / THREADS, b0 = tid * each;
+  long long mine = 0;
+  for (int k = 0; k < each && b0 + k < a.requests; ++k) mine += units(Range(a, b0 + k));
+  long long at = wave_scan(mine);
+  if ((tid & 63) == 63) sums[wave] = at;
+  __syncthreads();
+  at -= mine;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) {
+    if (w < wave) at += sums[w];
+    all += sums[w];
+  }
+  all = uniform(all);
+  const long long u = target(all);
+  if (u < 0) return false;
+  if (at <= u && u < at + mine)
+    for (int k = 0;; ++k) {  // (ends: u lies in one of this thread's requests)
+      const int n = units(Range(a, b0 + k));
+      if (u < at + n) {
+        s_b = b0 + k;
+        s_before = at;
+        break;
+      }
+      at += n;
+    }
+  __syncthreads();
+  b = __builtin_amdgcn_readfirstlane(s_b);
+  before = uniform(s_before);
+  return true;
+}
 
 // 16 (SEG of 64 channels) of a query's channels per lane as fp16, scaled by a power of two that
 // puts the row's largest into [2^8, 2^9); returns what turns a code product into a log2 score
@@ -268,11 +295,6 @@ __device__ __forceinline__ int units_of(const BlockAttention& a, const Range& rg
   return rg.vrows == 0 ? 0 : max(1, (rg.limit(a, rg.vrows - 1) + kUnit - 1) / kUnit);
 }
 
-__device__ __forceinline__ long long uniform(long long x) {
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
-  return (long long)((uint64_t)hi << 32 | lo);
-}
-
 __host__ __device__ inline size_t table_floats(int requests) { return ((size_t)requests * 2 + 3) / 4 * 4; }
 
 template <int D, int RT>
@@ -287,40 +309,17 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
   const int h = blockIdx.x % KV, share = blockIdx.x / KV;
   int b = share;
   long long before = 0, u0 = 0, u1 = 0, all = 0;  // units before request b, of this share, of the batch
-  if (shares) {
-    __shared__ long long sums[kWaves], s_before;
-    __shared__ int s_b;
-    const int each = (a.requests + kWaves * 64 - 1) / (kWaves * 64), b0 = threadIdx.x * each;
-    long long mine = 0;
-    for (int k = 0; k < each && b0 + k < a.requests; ++k) mine += units_of(a, Range(a, b0 + k));
-    long long at = wave_scan(mine);
-    if (lane == 63) sums[wave] = at;
-    __syncthreads();
-    at -= mine;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      if (w < wave) at += sums[w];
-      all += sums[w];
-    }
-    all = uniform(all);
-    if (shares > all) shares = (int)all;  // (so that none is empty)
-    if (share >= shares) return;
-    u0 = all * share / shares;
-    u1 = all * (share + 1) / shares;
-    if (at <= u0 && u0 < at + mine)
-      for (int k = 0;; ++k) {  // (ends: u0 lies in one of this thread's requests)
-        const int n = units_of(a, Range(a, b0 + k));
-        if (u0 < at + n) {
-          s_b = b0 + k;
-          s_before = at;
-          break;
-        }
-        at += n;
-      }
-    __syncthreads();
-    b = __builtin_amdgcn_readfirstlane(s_b);
-    before = uniform(s_before);
-  }
+  if (shares &&
+      !locate<kWaves * 64>(
+          a, [&](const Range& rg) { return units_of(a, rg); },
+          [&](long long all) {
+            if (shares > all) shares = (int)all;  // (so that none is empty)
+            if (share >= shares) return -1ll;
+            u1 = all * (share + 1) / shares;
+            return u0 = all * share / shares;
+          },
+          b, before, all))
+    return;
 
   auto segment = [&](const Range& rg, int t0, int t1, float* seg) {
     const int32_t* table = a.tables + (size_t)b * a.width;
@@ -537,18 +536,38 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
   constexpr int DT = D / 16, STEPS = D / 32, THREADS = 64 * WAVES, ITEMS = 8 * D / THREADS;
   constexpr int BUFS = D == 64 ? 2 : 1;
   __shared__ __attribute__((aligned(16))) TileLds<D> lds[BUFS];
-  const Work wk = work_of(a.cache.heads, chunks, groups);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, j = lane >> 4;
   const int KV = a.cache.heads, shift = __builtin_ctz(a.cache.bs);
-  const Range rg(a, wk.b);
+  // From the linear id: cached head fastest (the workgroups of one run of blocks read neighbouring memory,
+  // and with 8 heads an XCD keeps to one), then the rows, those that see most tokens first, then the
+  // request and its chunk of tokens, only those that there are.  (Chunks without tokens between the others
+  // leave their places in the order of CUs empty: 326 us against 148 for 64 requests of 5 rows and 4096
+  // tokens with one of four chunks alive.)
   constexpr int ROWS = 16 * RT * WAVES;
-  const int vr0 = (groups - 1 - wk.group) * ROWS;  // the rows that see most tokens begin first
+  unsigned id = blockIdx.x;
+  const int h = id % KV;
+  id /= KV;
+  const int vr0 = (groups - 1 - (int)(id % groups)) * ROWS;
+  int b = id / groups, chunk = 0;
+  if (chunks > 1) {
+    long long before = 0, all = 0;
+    const int item = b;
+    if (!locate<THREADS>(
+            a,
+            [&](const Range& rg) {
+              return rg.vrows == 0 ? 0 : min(max(1, (rg.limit(a, rg.vrows - 1) + chunk_tokens - 1) / chunk_tokens), chunks);
+            },
+            [&](long long all) { return item < all ? (long long)item : -1ll; }, b, before, all))
+      return;
+    chunk = item - (int)before;
+  }
+  const Range rg(a, b);
   if (vr0 >= rg.vrows) return;
   const int top = rg.limit(a, min(vr0 + ROWS, rg.vrows) - 1);
-  const int t0 = wk.chunk * chunk_tokens, t1 = min(t0 + chunk_tokens, top);
+  const int t0 = chunk * chunk_tokens, t1 = min(t0 + chunk_tokens, top);
   if (chunks > 1 && t0 >= t1) return;
-  const int32_t* table = a.tables + (size_t)wk.b * a.width;
+  const int32_t* table = a.tables + (size_t)b * a.width;
 
   // The four 16-token parts of a tile: lane l holds the table's entry for part l % 4 and the part's
   // scales; readlane makes them uniform where they are used.  The entry is looked at one step
@@ -562,7 +581,7 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
     float ks, vs;
   };
   auto load_parts = [&](int page) {
-    const size_t at = (size_t)max(page, 0) * KV + wk.h;
+    const size_t at = (size_t)max(page, 0) * KV + h;
     return Parts{page, a.cache.k_scale[at], a.cache.v_scale[at]};
   };
   // this lane's runs of a tile, tokens 32 g + 8 j .. + 7, lie in part 2 g + j / 2
@@ -599,7 +618,7 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const int x = piece(i), token = x / (D / 16);
-    off[i] = (uint32_t)wk.h * a.cache.bs * D +
+    off[i] = (uint32_t)h * a.cache.bs * D +
              (is_k(i) ? (token & mask) * D + 16 * (x % (D / 16)) : x / 4 * a.cache.bs + (16 * (x & 3) & mask));
   }
   auto load_codes = [&](int base, int pages, Codes& w) {
@@ -638,7 +657,7 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
   for (int t = 0; t < RT; ++t) {
     const int vr = min(first + 16 * t + c, rg.vrows - 1);
     limit[t] = rg.limit(a, vr);
-    const uint16_t* qp = a.q + (size_t)(rg.row0 + vr / rg.hg) * a.q_stride + (size_t)(wk.h * rg.hg + vr % rg.hg) * D + 8 * j;
+    const uint16_t* qp = a.q + (size_t)(rg.row0 + vr / rg.hg) * a.q_stride + (size_t)(h * rg.hg + vr % rg.hg) * D + 8 * j;
     float x[STEPS / 2][16];
 #pragma unroll
     for (int s = 0; s < STEPS / 2; ++s) bf16x16(qp + 64 * s, qp + 64 * s + 32, x[s]);
@@ -745,7 +764,7 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
     const int vr = first + 16 * q + c;
     const float sum = sum_quads(l[q]);
     if (vr >= rg.vrows) continue;
-    const size_t at = rg.out_row(a, wk.h, vr);
+    const size_t at = rg.out_row(a, h, vr);
     if (chunks == 1) {
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 #pragma unroll
@@ -753,7 +772,7 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
         *reinterpret_cast<v2u*>(a.out + at * D + 16 * d + 4 * j) =
             v2u{pack2_bf16(o[q][d][0] * inv, o[q][d][1] * inv), pack2_bf16(o[q][d][2] * inv, o[q][d][3] * inv)};
     } else {
-      float* ws = a.ws + (at * chunks + wk.chunk) * (D + 4);
+      float* ws = a.ws + (at * chunks + chunk) * (D + 4);
 #pragma unroll
       for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f*>(ws + 4 + 16 * d + 4 * j) = o[q][d];
       if (j == 0) {
@@ -943,7 +962,10 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
 // 2 heads: 29, 45, so where the requests alone fill the chip twice the room must be more).
 // More rows: cut so that the workgroups fit the chip at once, if the tiles saved (1.2 us each) take
 // longer than the join (6 us and its bytes at 4 TB/s): 2 x 5 rows before 131071 tokens 91 us in 32
-// chunks, 66 in 64, 60 in 96; 2 prompts of 1024 rows, 12 heads: 22.7 us uncut, 30 in two.
+// chunks, 66 in 64, 60 in 96; 2 prompts of 1024 rows, 12 heads: 22.7 us uncut, 30 in two.  Up to 64 rows
+// (drafts) under a table of more tokens than 4096 have chunks of 4096, for the same reason as above: 64
+// requests of 5 rows, 8 heads, one of 32768 tokens and 300 in the others: 603 us uncut, 91 cut (55 by
+// 2048); 500 each: 19.8, 26.8 (32.5).  For prompts the parts would be too many bytes.
 struct Split {
   bool few;
   int rt, groups;
@@ -960,10 +982,10 @@ static Split split_of(int requests, int rows, int max_rows, int heads, int kv_he
   s.groups = (int)((vrows + s.cut.span - 1) / s.cut.span);
   const long long natural = (long long)requests * kv_heads * s.groups;
   const long long tokens = (long long)width * bs;
+  const long long uneven = natural < 1024 ? 4096 : 16384;  // of more tokens one request may outlast the others
   if (s.few) {
     const long long units = (tokens + kUnit - 1) / kUnit, idle = natural < 256 ? 256 - natural : 0;
-    const bool uneven = tokens > (natural < 1024 ? 4096 : 16384);
-    const bool cut = uneven || units * idle * 1300 > 256 * 6000;  // ns
+    const bool cut = tokens > uneven || units * idle * 1300 > 256 * 6000;  // ns
     if (cut && requests <= 4096 && natural <= 16384) {
       const int least = 256 / kv_heads, most = 512 / kv_heads;
       const int shares = requests < least ? least : requests < most ? requests : most;
@@ -976,13 +998,17 @@ static Split split_of(int requests, int rows, int max_rows, int heads, int kv_he
   const long long most = (tokens + unit - 1) / unit;
   if (chunks > most) chunks = most;
   if (chunks > kMaxParts) chunks = kMaxParts;
-  if (chunks > 1) {
+  const long long room = s.rt == 1 && tokens > uneven ? 8192 / natural : 1, capped = (tokens + 4095) / 4096;
+  const long long least = capped < room ? capped : room;
+  if (chunks < least) {
+    chunks = least;
+  } else if (chunks > 1) {
     long long joins = (long long)requests * max_rows;
     joins = (joins < rows ? joins : rows) * heads;
     const long long saved = tokens / kTile * (chunks - 1) / chunks * 1200;  // ns
     if (saved < 6000 + joins * chunks * (dim + 4) * 8 / 4000) chunks = 1;
   }
-  if (chunks < 1) chunks = 1;
+  if (chunks < 1 || requests > 4096) chunks = 1;
   long long per = (tokens + chunks - 1) / chunks;
   per = (per + unit - 1) / unit * unit;
   s.cut.chunk_tokens = (int)per;

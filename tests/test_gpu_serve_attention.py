@@ -132,6 +132,21 @@ def test_few_rows_in_equal_shares(gpu_lib, seq, rows, heads, kv_heads, dim, bs, 
         check(c, run(c, causal, 0.1), causal, 0.1)
 
 
+@pytest.mark.parametrize("n,heads,dim,bs,width", [(40, 8, 128, 16, 1500), (300, 11, 64, 64, 300), (4100, 33, 64, 128, 40)])
+def test_uneven_requests_of_drafts(gpu_lib, n, heads, dim, bs, width):
+    # more than 16 (32) rows x heads each, chunks of a long table; some without rows, some without tokens
+    rng = np.random.default_rng(n)
+    rows = rng.integers(1, 6, n) * (rng.random(n) < 0.8)
+    rows[:3] = 5 if n < 1000 else 1
+    if n > 1000:
+        rows[3:] = 0
+        rows[rng.integers(3, n, 30)] = 1
+    seq = rng.integers(0, 50, n)
+    seq[[1, n // 2]] = min(17000, width * bs), 4100
+    c = batch(n, [int(x) for x in seq], [int(x) for x in rows], heads, 1, dim, bs, width=width)
+    check(c, run(c, True, 0.1), True, 0.1)
+
+
 @pytest.mark.parametrize("n,kv_heads,width", [(700, 3, 200), (4096, 1, 300), (4097, 1, 300)])
 def test_many_uneven_requests(gpu_lib, n, kv_heads, width):
     # shares of thousands of requests, several to a thread that adds them up; one more and none is cut
