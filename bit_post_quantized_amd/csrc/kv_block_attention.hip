@@ -510,10 +510,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
 
 // ----------------------------------------------------------------------------------- more rows
 // A workgroup takes 16 RT rows per wave and walks over its tokens with them, 64 at a time.
-// Their codes come a tile or two ahead, 16 bytes per thread and load, and become fp16 in LDS: for 64
-// channels a tile ahead (double buffered, one barrier per tile), for 128 in one buffer, whose two
-// barriers cost less than a third workgroup on the CU gains (66 against 71 us for 2 x 5 rows of 32
-// heads before 131071 tokens).  K lies there as [token][D], V as [channel][token], the 16-byte slots
+// Their codes come a tile or two ahead, 16 bytes per thread and load, and become fp16 in LDS: for eight
+// waves a tile ahead (double buffered, one barrier per tile: 80 against 88 us for 4096 rows of 12 heads of
+// 64), for four in one buffer, whose two barriers cost less than more workgroups on the CU gain (66
+// against 71 us for 2 x 5 rows of 32 heads of 128 before 131071 tokens, 95 against 109 for 64 x 34 rows
+// of 12 heads of 64 before 4096).  K lies there as [token][D], V as [channel][token], the 16-byte slots
 // of both permuted within the row so that the 16 lanes which read a matrix operand, or write 16
 // pieces, meet 16 different bank groups.  Lane (c, j) scores tokens 32 g + 8 j .. + 7 (g = 0, 1) for
 // row c: K's row of matrix row 4 j' + i of product t = 2 g + e is token 32 g + 8 j' + 4 e + i.
@@ -534,7 +535,7 @@ template <int D, int RT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_attention_rows_kernel(
     BlockAttention a, int chunks, int groups, int chunk_tokens) {
   constexpr int DT = D / 16, STEPS = D / 32, THREADS = 64 * WAVES, ITEMS = 8 * D / THREADS;
-  constexpr int BUFS = D == 64 ? 2 : 1;
+  constexpr int BUFS = WAVES == 8 ? 2 : 1;
   __shared__ __attribute__((aligned(16))) TileLds<D> lds[BUFS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, j = lane >> 4;
@@ -753,7 +754,11 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
         p = load_parts(page);
         page = load_page(base + 2 * kTile);
         barrier();
+        // (a wave with products goes before those of other workgroups that still unpack codes: 510 against
+        // 530 us for 4096 rows before 8192 tokens; with two buffers 85 against 80 for 12 heads, so not there)
+        __builtin_amdgcn_s_setprio(1);
         if (base < high) products(base, now, lds[0]);
+        __builtin_amdgcn_s_setprio(0);
         barrier();
       }
     }
