@@ -26,8 +26,8 @@
 // 40.  4 prompts of 475 to 1000 rows, 24 heads to 8 of 64, before up to 4096 tokens: 85 us,
 // 470 TFLOP/s: a wave's tile of 16 rows x 64 tokens is 144 vector instructions, 16 of them
 // exponentials at a quarter of the rate, against 16 matrix ones, and the longest request's 64 tiles
-// follow each other at 1.1 to 1.3 us.  4096 rows, 32 heads to 8 of 128, before 8192 tokens: 454 us,
-// 909 TFLOP/s.
+// follow each other at 1.1 to 1.3 us.  4096 rows, 32 heads to 8 of 128, before 8192 tokens: 510 us,
+// 810 TFLOP/s.
 #include "serve_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -755,7 +755,8 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
         page = load_page(base + 2 * kTile);
         barrier();
         // (a wave with products goes before those of other workgroups that still unpack codes: 510 against
-        // 530 us for 4096 rows before 8192 tokens; with two buffers 85 against 80 for 12 heads, so not there)
+        // 530 us for 4096 rows before 8192 tokens, 107 against 116 for 64 x 5 rows before 4096, but 77
+        // against 74 for 4 x 1024 rows; with two buffers 85 against 80 for 12 heads, so not there)
         __builtin_amdgcn_s_setprio(1);
         if (base < high) products(base, now, lds[0]);
         __builtin_amdgcn_s_setprio(0);
@@ -954,7 +955,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
 // cached head (32 at 64 channels) the few-rows kernel: at 5 rows of 8 heads it would need three row
 // tiles and spill.  Above, a workgroup takes 64 rows, or 128 if there are more: at 64 channels in
 // eight waves of 16 (85 against 97 us for four of 32 on 4 prompts of 475..1000 rows: more waves to
-// hide the softmax's latency), at 128 in four waves of 32 (454 against 605 us on 4096 rows before
+// hide the softmax's latency), at 128 in four waves of 32 (535 against 605 us on 4096 rows before
 // 8192 tokens: an LDS read feeds two products).
 //
 // Few rows: equal shares for 256 workgroups, up to 512 where there are as many requests (32768 tokens,
