@@ -79,15 +79,19 @@ class DecodeLinear:
                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
         """X bf16 [M, K], M <= 64 -> [M, N], bf16 or fp32."""
         M, N, dev = X.shape[0], self.N, self.device
+        good = _is(X, _BF16, (M, self.K), dev) and _here(dev)  # (and what is allocated here with it)
         if out is None:
             out = X.new_empty((M, N), dtype=out_dtype)
+        else:
+            good = good and _is(out, out.dtype, (M, N), dev)
         code = B.SVDQ_OUT_FP32 if out.dtype is _F32 else B.SVDQ_OUT_BF16
         need = B.svdq_w4a16_workspace_bytes(M, N, self.K, self.rank, code)
         if workspace is None:
             workspace = X.new_empty(need, dtype=_U8)
-        if (_is(X, _BF16, (M, self.K), dev) and (code or out.dtype is _BF16)
-                and _is(out, out.dtype, (M, N), dev) and workspace.device == dev
-                and workspace.is_contiguous() and workspace.nbytes >= need and _here(dev)):
+        else:
+            good = good and (workspace.device == dev and workspace.is_contiguous()
+                             and workspace.nbytes >= need)
+        if good and (code or out.dtype is _BF16):
             status = self._call(X.data_ptr(), *self._weights, M, N, self.K, self.rank,
                                 out.data_ptr(), code, workspace.data_ptr(), _stream(dev))
             if status:
