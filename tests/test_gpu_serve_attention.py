@@ -157,6 +157,20 @@ def test_many_uneven_requests(gpu_lib, n, kv_heads, width):
     check(c, run(c, True, 0.125), True, 0.125)
 
 
+@pytest.mark.parametrize("seq,rows,heads,kv_heads,dim,bs,width", [
+    ([9000, 50, 4096], [1, 1, 1], 8, 2, 128, 16, 600), ([9000, 50, 4096], [4, 3, 4], 8, 2, 64, 16, 600),
+    ([300] * 70, [1] * 70, 2, 1, 64, 128, 64), ([20000, 30], [5, 5], 16, 1, 128, 64, 320),
+    ([5000, 600], [70, 64], 2, 1, 64, 16, 320), ([5000, 600], [70, 64], 2, 1, 128, 16, 320),
+])
+def test_the_workspace_holds_what_it_says(gpu_lib, seq, rows, heads, kv_heads, dim, bs, width):
+    from bit_post_quantized_amd import serve_binding as SB
+    c = batch(sum(seq) + width, seq, rows, heads, kv_heads, dim, bs, width=width)
+    need = SB.kv_block_attention_workspace_bytes(len(seq), sum(rows), max(rows), heads, kv_heads, dim, width, bs)
+    ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    check(c, run(c, True, 0.1, workspace=ws[:need]), True, 0.1)
+    assert need > 0 and (ws[need:] == 0xA5).all()
+
+
 def test_shares_follow_the_lengths_in_a_graph(gpu_lib):
     c = batch(92, [6000, 3000, 0, 900], [1, 2, 1, 1], 8, 2, 128, 16, width=700)
     c["tables"][3, :] = c["tables"][0, :]
