@@ -218,13 +218,13 @@ def test_append_many_rows_and_blocks_of_a_long_cache(gpu_lib):
 
 
 def test_cache_past_four_gib(gpu_lib):
-    # block offsets beyond 2^32 bytes: the last block of a 5.4 GB pair of code arrays
-    num, heads, bs, dim = 2 ** 15 + 8192 + 3, 8, 64, 128
+    # block offsets beyond 2^32 bytes: the last blocks of two code arrays of 8.6 GB
+    num, heads, bs, dim = 2 ** 17 + 3, 8, 64, 128
     cache = serve.BlockCache.empty(num, bs, heads, dim)
-    assert cache.k_codes.numel() > 2 ** 31
+    assert (num - 1) * heads * bs * dim > 2 ** 33
     rng = np.random.default_rng(1)
     k, v = bf16_values(rng, bs, heads, dim), bf16_values(rng, bs, heads, dim)
-    for b in (num - 1, 0, 2 ** 15):
+    for b in (num - 1, 0, 2 ** 15, 2 ** 16 + 1):
         slots = to_dev(np.arange(b * bs, b * bs + bs))
         cache.append(to_dev_bf16(k), to_dev_bf16(v), slots)
         kr, vr = cache.read(slots)
@@ -232,15 +232,19 @@ def test_cache_past_four_gib(gpu_lib):
         for got, x in ((kr, k), (vr, v)):
             off, amax = float(np.abs(host64(got) - x).max()), float(np.abs(x).max())
             assert off <= amax * (0.5 / 127 + 2.0 ** -8) * (1 + 2.0 ** -8)
-        out = cache.attention(to_dev_bf16(k[-1:]), to_dev(np.array([[b]]), torch.int32),
-                              to_dev(np.array([bs]), torch.int32), to_dev(np.array([0, 1]), torch.int32), 1)
+        i32 = lambda *v: to_dev(np.array(v), torch.int32)  # noqa: E731
+        out = cache.attention(to_dev_bf16(k[-1:]), i32([b]), i32(bs), i32(0, 1), 1)
+        # the same row in shares of a wide table, and 40 times over (the kernel of more rows)
+        wide = cache.attention(to_dev_bf16(k[-1:]), i32([b] + [-1] * 150), i32(bs), i32(0, 1), 1)
+        many = cache.attention(to_dev_bf16(k[-1:]).repeat(40, 1, 1), i32([b]), i32(bs), i32(0, 40), 40, causal=False)
         s = np.einsum("hd,thd->ht", k[-1], host64(kr)) / np.sqrt(dim)
         w = np.exp(s - s.max(1, keepdims=True))
         want = np.einsum("ht,thd->hd", w / w.sum(1, keepdims=True), host64(vr))
         # weights and values as read back, each rounded to bf16 (2^-8), against the codes' own: the
         # scores (up to 11 here) are off by 2^-8 of sum |q k|, so compare loosely, by largest value
-        off, amax = float(np.abs(host64(out)[0] - want).max()), float(np.abs(v).max())
-        assert off <= 2.0 ** -4 * amax
+        amax = float(np.abs(v).max())
+        for o in (out, wide, many):
+            assert float(np.abs(host64(o) - want).max()) <= 2.0 ** -4 * amax
     del cache
     torch.cuda.empty_cache()
 
