@@ -224,7 +224,6 @@ hipError_t launch_kv_block_release(const int32_t* seq, const uint8_t* done, int 
 // coding 45 us.
 constexpr int kAppendThreads = 256;
 constexpr int kShort = 4;
-constexpr int kMaxBlock = 128;  // tokens
 
 // Rows of a window: a block's worth (at most 64) where that makes enough workgroups, so that a
 // prompt's window begins a run; less for few rows, where a window's short runs would queue up.

@@ -147,36 +147,37 @@ class BlockPlanner:
                           p.slots.data_ptr(), p.status.data_ptr(), p.free_count.data_ptr())
             self._plans.append(p)
 
-    def _other(self, lens: torch.Tensor, free_count: torch.Tensor) -> SlotPlan:
-        """The oldest set that is not an argument's, which becomes the newest: of the three older
-        ones at most two are, so it is never the set of the call before."""
-        plans, a, b = self._plans, lens.data_ptr(), free_count.data_ptr()
+    def _other(self, a: int, b: int, some: int) -> SlotPlan:
+        """The oldest set that is not an argument's (lengths at a, free count at b), which becomes the
+        newest: of the three older ones at most two are, so it is never the set of the call before."""
+        plans = self._plans
         for i in range(3):
             o = plans[i]._outputs
-            if o[6] != b and (o[1] != a or not lens.numel()):
+            if o[6] != b and (o[1] != a or not some):
                 break
         plans.append(plans.pop(i))
         return plans[3]
 
     def plan(self, ctx_lens: torch.Tensor, new_lens: torch.Tensor,
              free_count: torch.Tensor) -> SlotPlan:
-        p = self._other(ctx_lens, free_count)
-        t, dev, n = self.block_tables, self.device, self.requests
+        ctx, count, dev, n = ctx_lens.data_ptr(), free_count.data_ptr(), self.device, self.requests
+        p = self._other(ctx, count, n)
         if (_is(ctx_lens, _I32, (n,), dev) and _is(new_lens, _I32, (n,), dev)
                 and _is(free_count, _I32, (1,), dev) and _here(dev)):
-            status = self._call(ctx_lens.data_ptr(), new_lens.data_ptr(), *self._tables,
-                                free_count.data_ptr(), *p._outputs, _stream(dev))
+            status = self._call(ctx, new_lens.data_ptr(), *self._tables, count, *p._outputs,
+                                _stream(dev))
             if status:
                 binding._check("kv_block_plan", status)
         else:
-            B.kv_block_plan(ctx_lens, new_lens, t, self.block_size, self.free_blocks, free_count,
-                            p.cu_rows, p.seq_lens, p.positions, p.slots, p.status, p.free_count)
+            B.kv_block_plan(ctx_lens, new_lens, self.block_tables, self.block_size,
+                            self.free_blocks, free_count, p.cu_rows, p.seq_lens, p.positions,
+                            p.slots, p.status, p.free_count)
         return p
 
     def release(self, seq_lens: torch.Tensor, done: torch.Tensor, free_count: torch.Tensor):
         """Gives back the blocks of the requests with ``done`` (uint8) set: (lengths, free
         count), of the set of outputs that the arguments are not part of."""
-        p = self._other(seq_lens, free_count)
+        p = self._other(seq_lens.data_ptr(), free_count.data_ptr(), self.requests)
         B.kv_block_release(seq_lens, done, self.block_tables, self.block_size, self.free_blocks,
                            free_count, p.seq_lens, p.free_count)
         return p.seq_lens, p.free_count
