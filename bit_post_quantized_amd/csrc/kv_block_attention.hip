@@ -21,7 +21,7 @@
 // to several workgroups, a second launch joins their maxima, sums and outputs.
 //
 // Measured (kernel times).  64 requests of up to 8192 tokens, 32 heads to 8 of 128: 127 us, 5.3 TB/s of
-// codes, and 6 for the join (139 and none with a workgroup per request and head).  1 x 10240 tokens, 32
+// codes, and 4 for the join (139 and none with a workgroup per request and head).  1 x 10240 tokens, 32
 // heads: 20 us and 4; the bytes are 15 at 5.5 TB/s.  2 x 5 rows, 32 heads to 4, before up to 131071 tokens: 49 us and 6; the bytes are
 // 40.  4 prompts of 475 to 1000 rows, 24 heads to 8 of 64, before up to 4096 tokens: 85 us,
 // 470 TFLOP/s: a wave's tile of 16 rows x 64 tokens is 144 vector instructions, 16 of them
@@ -964,7 +964,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
 // begin, and a join costs 5 us, so a batch is cut only where its workgroups leave CUs idle for longer
 // than that (1.3 us a unit; 24 requests of 2048, 8 heads: 12.4 us uncut, 17.5 cut), or where the table has
 // room for a request that would go on long after the others: 64 requests, 8 heads, one of 16384 tokens
-// and 200 in the others: 85 us uncut, 26 cut; up to 8192: 139, 133; 500 each: 16.7, 21 (1000 of up to 1000,
+// and 200 in the others: 85 us uncut, 28 cut; up to 8192: 139, 130; 500 each: 16.7, 19.6 (1000 of up to 1000,
 // 2 heads: 29, 45, so where the requests alone fill the chip twice the room must be more).
 // More rows: cut so that the workgroups fit the chip at once, if the tiles saved (1.2 us each) take
 // longer than the join (6 us and its bytes at 4 TB/s): 2 x 5 rows before 131071 tokens 91 us in 32
@@ -1059,7 +1059,9 @@ static hipError_t launch(const BlockAttention& a, hipStream_t stream) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || !s.joins()) return e;
   const unsigned joins = (unsigned)(a.requests * a.max_rows * a.heads);
-  if ((s.few ? s.cut.shares : s.cut.chunks) <= kFewParts || joins >= 4096) {
+  // Many rows have few parts each, most of them (64 requests of up to 8192 tokens x 32 heads: 130.5 us by
+  // lanes, 132.5 by workgroups; with one request of 60 parts 28, 25.7).
+  if ((s.few ? s.cut.shares : s.cut.chunks) <= kFewParts || joins >= 1024) {
     const unsigned each = kJoinThreads / (D / 4);
     hipLaunchKernelGGL(kv_block_join_kernel<D>, dim3((joins + each - 1) / each), dim3(kJoinThreads), 0, stream, a,
                        s.cut, joins);
