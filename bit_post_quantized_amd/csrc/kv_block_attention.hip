@@ -573,7 +573,10 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
   // The four 16-token parts of a tile: lane l holds the table's entry for part l % 4 and the part's
   // scales; readlane makes them uniform where they are used.  The entry is looked at one step
   // later, so that the load stays in flight meanwhile; -1: a block of no token, or outside the pool.
-  auto load_page = [&](int base) { return table[max(min(base + 16 * (lane & 3), t1 - 1), 0) >> shift]; };
+  auto load_page = [&](int base) {
+    const uint32_t at = (uint32_t)(max(min(base + 16 * (lane & 3), t1 - 1), 0) >> shift);
+    return *reinterpret_cast<const int32_t*>(reinterpret_cast<const char*>(table) + 4u * at);
+  };
   auto checked = [&](int base, int page) {
     return base + 16 * (lane & 3) < t1 && (unsigned)page < (unsigned)a.cache.num_blocks ? page : -1;
   };
@@ -581,9 +584,10 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
     int page;
     float ks, vs;
   };
-  auto load_parts = [&](int page) {
-    const size_t at = (size_t)max(page, 0) * KV + h;
-    return Parts{page, a.cache.k_scale[at], a.cache.v_scale[at]};
+  auto load_parts = [&](int page) {  // (a cache has at most 2^30 scales, so 32 bits hold their offsets)
+    const uint32_t at = 4u * ((uint32_t)max(page, 0) * KV + h);
+    return Parts{page, *reinterpret_cast<const float*>(reinterpret_cast<const char*>(a.cache.k_scale) + at),
+                 *reinterpret_cast<const float*>(reinterpret_cast<const char*>(a.cache.v_scale) + at)};
   };
   // this lane's runs of a tile, tokens 32 g + 8 j .. + 7, lie in part 2 g + j / 2
   struct Tile {
