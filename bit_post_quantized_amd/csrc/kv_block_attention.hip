@@ -1009,7 +1009,8 @@ static Split split_of(int requests, int rows, int max_rows, int heads, int kv_he
   if (chunks > most) chunks = most;
   if (chunks > kMaxParts) chunks = kMaxParts;
   const long long room = s.rt == 1 && tokens > uneven ? 8192 / natural : 1, capped = (tokens + 4095) / 4096;
-  const long long least = capped < room ? capped : room;
+  long long least = capped < room ? capped : room;
+  if (least > kMaxParts) least = kMaxParts;  // (then a chunk has more tokens)
   if (chunks < least) {
     chunks = least;
   } else if (chunks > 1) {

@@ -1,0 +1,47 @@
+"""The decoding step at the ends of its sizes and magnitudes."""
+import numpy as np
+import pytest
+import torch
+
+from tests.serve_cases import bf16_values, dev_cache, host64, random_cache, to_dev, to_dev_bf16
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------------------- attention
+@pytest.mark.parametrize("kv_heads,heads,rows,dim,bs", [(1, 8, 5, 64, 128), (4, 32, 5, 128, 128), (1, 1, 64, 64, 64)])
+def test_drafts_before_more_tokens_than_a_join_has_parts_for(gpu_lib, kv_heads, heads, rows, dim, bs):
+    """More than 1024 x 4096 tokens under a wider table, whose entries repeat a few blocks: equal
+    tokens count as often as the table names them.  The last blocks weigh most.  To the bounds of
+    test_gpu_serve_attention come the sums of 1024 parts and of a part's tokens, 2^-15."""
+    n, sm = 1024 * 4096 + 70001, 0.25
+    rng = np.random.default_rng(dim + kv_heads)
+    kc, ks, vc, vs = random_cache(rng, 7, kv_heads, bs, dim)
+    ks[:] = np.float32(1 / 400)
+    kc[:, :, :, 0] = 0
+    kc[4:, :, :, 0] = 127
+    used = -(-n // bs)
+    table = np.full((1, used + 9000), -1)
+    table[0, :used] = np.arange(used) % 4
+    table[0, used - 600:used] = 4 + np.arange(600) % 3
+    q = bf16_values(rng, rows, heads, dim)
+    q[:, :, 0] = 40.0
+    cache = dev_cache(kc, ks, vc, vs)
+    i32 = lambda a: to_dev(np.asarray(a), torch.int32)  # noqa: E731
+    for causal in (True, False):
+        out = cache.attention(to_dev_bf16(q), i32(table), i32([n]), i32([0, rows]), rows, causal=causal, sm_scale=sm)
+        got = host64(out)
+        for i in range(rows):
+            seen = n - rows + i + 1 if causal else n
+            count = np.zeros((7, bs))
+            np.add.at(count, table[0, :seen // bs], 1.0)
+            count[table[0, seen // bs], :seen % bs] += 1.0
+            for h in range(heads):
+                k = (kc[:, h * kv_heads // heads] * ks[:, h * kv_heads // heads, None, None].astype(np.float64)).reshape(-1, dim)
+                v = (vc[:, h * kv_heads // heads] * vs[:, h * kv_heads // heads, None, None].astype(np.float64)).reshape(-1, dim)
+                s = sm * (k @ q[i, h])
+                w = count.reshape(-1) * np.exp(s - s.max())
+                w /= w.sum()
+                top = sm * (np.abs(k) @ np.abs(q[i, h])).max()
+                err = 2 * (2 * dim + 8) * 2.0 ** -24 * top + 2.0 ** -11 + 2.0 ** -15
+                assert np.all(np.abs(got[i, h] - w @ v) <= 2.0 ** -8 * np.abs(w @ v) + err * (w @ np.abs(v))), (causal, i, h)
