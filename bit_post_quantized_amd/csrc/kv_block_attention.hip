@@ -185,14 +185,83 @@ struct Runs {
   float ks[2], lv[2], ivs[2];
 };
 
+// A weight carries its block's V scale vs, and the sum takes it out again in units of 2^-unit: it holds
+// weights times 2^unit / vs.  The unit is a wave's own and follows the largest scale that the wave has
+// met, at most 2^20 behind; a smaller scale than 2^(unit - 80), zero among them, counts as that (its
+// codes then add 127 2^-80 of the largest scale at most, and it sets no maximum that matters).  So a term
+// of the sum lies between 2^-20 and 2^80 times its weight, whatever normal or subnormal numbers the
+// scales are; the exponential, logarithm and reciprocal see normal numbers only.  Where a new unit would
+// take a sum past 2^100 (a row of tiny scales beside one that does not see the large ones), the row's
+// maximum rises instead: its weights then stand for less than 2^-64 of the largest scale.
+constexpr int kFirstUnit = -126, kLastUnit = 126;
+constexpr float kLeastScale = 0x1p-80f;
+constexpr float kFullSum = 100.0f;  // log2
+
+__device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// The largest of a wave's values, in every lane.
+__device__ __forceinline__ uint32_t max_wave(uint32_t x) {
+#define SVDQ_ROTATED(CTRL) (uint32_t) __builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, false)
+  x = max(x, SVDQ_ROTATED(0x121));  // within rows of 16 lanes by 1, 2, 4 and 8
+  x = max(x, SVDQ_ROTATED(0x122));
+  x = max(x, SVDQ_ROTATED(0x124));
+  x = max(x, SVDQ_ROTATED(0x128));
+#undef SVDQ_ROTATED
+  const auto a = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  x = max((uint32_t)a[0], (uint32_t)a[1]);
+  const auto b = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  return max((uint32_t)b[0], (uint32_t)b[1]);
+}
+
+// A unit, with what goes by it ready (each is worth several scalar instructions per tile otherwise).
+struct Unit {
+  int e;
+  float power;         // 2^e
+  uint32_t low, span;  // the normal numbers from 2^(e - 80) to 2^(e + 20)
+  __device__ __forceinline__ explicit Unit(int unit)
+      : e(unit), power(power2(unit)), low((uint32_t)(max(unit - 80, -126) + 127) << 23),
+        span(((uint32_t)(min(unit + 20, 127) + 127) << 23) - low) {}
+};
+
+// What a lane's V scale is to weights (log2) and to the sum.
+struct VScale {
+  float log2, inverse;
+};
+
+// ... where every scale of the wave is near the unit,
+__device__ __forceinline__ bool all_near(float vs, const Unit& unit) {
+  return __all(__float_as_uint(vs) - unit.low < unit.span);
+}
+
+__device__ __forceinline__ VScale near_scale(float vs, const Unit& unit) {
+  return VScale{__builtin_amdgcn_logf(vs), __builtin_amdgcn_rcpf(vs) * unit.power};
+}
+
+// ... and of any scale, after the unit has followed the wave's.
+__device__ __forceinline__ VScale any_scale(float vs, Unit& unit) {
+  const uint32_t bits = __float_as_uint(vs);
+  const int top = (int)(__builtin_amdgcn_readfirstlane(max_wave(bits < 0x7F800000u ? bits : 0u)) >> 23) - 127;
+  unit = Unit(top >= unit.e + 20 ? min(top, kLastUnit) : unit.e);
+  const float in_units = __builtin_elementwise_maximum(vs * power2(-unit.e), kLeastScale);  // (NaN stays one)
+  return VScale{__builtin_amdgcn_logf(in_units) + (float)unit.e, __builtin_amdgcn_rcpf(in_units)};
+}
+
+// How far a sum goes past 2^100 where its maximum is 2^x times the whole's and its unit `up` below the
+// whole's, and the sum on the whole's terms.  (The two go together: a scale that raises the unit raises
+// the maximum too, where its score is not far behind.)
+__device__ __forceinline__ float over_full(float l, float x, float up) {
+  return x + up + (float)((int)(__float_as_uint(l) >> 23) - 127) - kFullSum;
+}
+__device__ __forceinline__ float sum_on(float l, float x, float up) {
+  return l * __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(x + up, 126.0f));  // (0 stays 0)
+}
+
 // One softmax step of RT tiles of rows: the lane's 16 code products of each become weights (pf, the
-// second product's operand), and m, l, o follow.  A weight carries its run's V scale: it is
-// 2^(score + log2 vs), and the sum takes vs out again, so the codes of V stay codes.  (A zero V scale
-// belongs to codes that are all zero, so 1 serves for it.)  The tiles of rows go through it
-// together, with one branch for all: each is a chain of dependent operations, and two chains fill
-// each other's gaps.
+// second product's operand), and m, l, o follow.  A weight is 2^(score + log2 vs), so the codes of V
+// stay codes.  The sums' unit rises by `up` (uniform).  The tiles of rows go through it together, with
+// one branch for all: each is a chain of dependent operations, and two chains fill each other's gaps.
 template <int RT, int DT>
-__device__ __forceinline__ void softmax_step(v4f (*sc)[4], const float* fac, const Runs& r, bool masked,
+__device__ __forceinline__ void softmax_step(v4f (*sc)[4], const float* fac, const Runs& r, int up, bool masked,
                                              const int (*seen)[2], float* m, float* l, v4f (*o)[DT],
                                              v8h (*pf)[2]) {
   float f[RT][2], add[2] = {r.lv[0], r.lv[1]}, mx[RT];
@@ -238,13 +307,18 @@ __device__ __forceinline__ void softmax_step(v4f (*sc)[4], const float* fac, con
     mx[q] = max_quads(mx[q]);
     ahead = ahead || mx[q] > m[q] + kLazy;
   }
-  if (__any(ahead)) {
+  if (__any(ahead) || up) {
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
-      const float mn = __builtin_fmaxf(m[q], mx[q]);
-      const float alpha = mn == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m[q] - mn);
+      float mn = __builtin_fmaxf(m[q], mx[q]), x = mn == -__builtin_inff() ? 0.0f : m[q] - mn;
+      if (__builtin_expect(up, 0)) {
+        const float over = __builtin_fmaxf(over_full(max_quads(l[q]), x, up), 0.0f);
+        mn += over;
+        x -= over;
+      }
+      const float alpha = __builtin_amdgcn_exp2f(x);
       m[q] = mn;
-      l[q] *= alpha;
+      l[q] = sum_on(l[q], x, up);
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -302,7 +376,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
                                                                             int seg_rows) {
   constexpr int SEG = D / 64, DT = D / 16;
   __shared__ float o_lds[kWaves][16][D + 4];
-  __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
+  __shared__ float m_lds[kWaves][16], l_lds[kWaves][16], unit_lds[kWaves][16], f_lds[kWaves][16], up_lds[16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, j = lane >> 4;
   const int KV = a.cache.heads, shift = __builtin_ctz(a.cache.bs);
@@ -383,12 +457,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
     }
 
     constexpr int STEP = kUnit;
+    Unit unit(kFirstUnit);
     auto step = [&](int base, const Codes& w) {
-      Runs r;
-      const float vs = w.there && w.vs != 0.0f ? w.vs : 1.0f;
-      r.ks[0] = r.ks[1] = w.there ? w.ks : 0.0f;
-      r.lv[0] = r.lv[1] = __builtin_amdgcn_logf(vs);
-      r.ivs[0] = r.ivs[1] = __builtin_amdgcn_rcpf(vs);
       v4f sc[RT][4];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -406,6 +476,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
           sc[q][t] = x;
         }
       }
+      Runs r;  // (here: the scales are the last loads of a tile)
+      const int was = unit.e;
+      const float x = w.there ? w.vs : unit.power;
+      VScale vs = near_scale(x, unit);
+      if (__builtin_expect(!all_near(x, unit), 0)) vs = any_scale(x, unit);
+      r.ks[0] = r.ks[1] = w.there ? w.ks : 0.0f;
+      r.lv[0] = r.lv[1] = vs.log2;
+      r.ivs[0] = r.ivs[1] = vs.inverse;
       v8h pf[RT][2];
       int seen[RT][2];
 #pragma unroll
@@ -414,7 +492,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
         seen[q][0] = n;
         seen[q][1] = n - 8;
       }
-      softmax_step<RT, DT>(sc, fac, r, true, seen, m, l, o, pf);
+      softmax_step<RT, DT>(sc, fac, r, unit.e - was, true, seen, m, l, o, pf);
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         v8h va, vb;
@@ -447,7 +525,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
       }
     }
 
-    // ---- the waves meet, one tile of 16 rows after the other
+    // ---- the waves meet, one tile of 16 rows after the other.  The first wave, a lane to each wave's row,
+    // turns their maxima, units and sums into factors of their outputs (a wave that saw no token of a
+    // row has maximum -inf and the least unit).
 #pragma unroll
     for (int q = 0; q < RT; ++q) {
       const float ls = sum_quads(l[q]);
@@ -455,34 +535,34 @@ __global__ __launch_bounds__(kWaves * 64, 2) void kv_block_attention_kernel(Bloc
       if (j == 0) {
         m_lds[wave][c] = m[q];
         l_lds[wave][c] = ls;
+        unit_lds[wave][c] = m[q] == -__builtin_inff() ? kFirstUnit : unit.e;
       }
 #pragma unroll
       for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f*>(&o_lds[wave][c][16 * d + 4 * j]) = o[q][d];
       __syncthreads();
+      if (wave == 0) {
+        const float mw = m_lds[j][c], uw = unit_lds[j][c], lw = l_lds[j][c];
+        const float mm = max_quads(mw), top = max_quads(uw), off = mm == -__builtin_inff() ? 0.0f : mm;
+        const float over = max_quads(__builtin_fmaxf(over_full(lw, mw - off, top - uw), 0.0f));
+        const float x = mw - off - over, sum = sum_quads(sum_on(lw, x, top - uw));
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        // (the outputs' last factor, 2^top, goes by itself: both may be far from 1)
+        f_lds[j][c] = __builtin_amdgcn_exp2f(x) * (seg ? 1.0f : inv);
+        if (j == 0) {
+          up_lds[c] = power2((int)top);
+          if (seg && 16 * q + c < rg.vrows)
+            *reinterpret_cast<v4f*>(seg + (size_t)(16 * q + c) * (D + 4)) = v4f{mm + over, sum, top, 0.0f};
+        }
+      }
+      __syncthreads();
       for (int e = threadIdx.x; e < 16 * D; e += kWaves * 64) {
         const int row = e / D, d = e % D, vr = 16 * q + row;
         if (vr >= rg.vrows) continue;
-        float mm = -__builtin_inff();
+        float out = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) mm = __builtin_fmaxf(mm, m_lds[w][row]);
-        const float off = mm == -__builtin_inff() ? 0.0f : mm;
-        float sum = 0.0f, out = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-          const float f = __builtin_amdgcn_exp2f(m_lds[w][row] - off);
-          sum = __builtin_fmaf(l_lds[w][row], f, sum);
-          out = __builtin_fmaf(o_lds[w][row][d], f, out);
-        }
-        if (!seg) {
-          a.out[rg.out_row(a, h, vr) * D + d] = float_to_bf16_bits(sum == 0.0f ? 0.0f : out / sum);
-        } else {
-          float* ws = seg + (size_t)vr * (D + 4);
-          ws[4 + d] = out;
-          if (d == 0) {
-            ws[0] = mm;
-            ws[1] = sum;
-          }
-        }
+        for (int w = 0; w < kWaves; ++w) out = __builtin_fmaf(o_lds[w][row][d], f_lds[w][row], out);
+        if (seg) seg[(size_t)vr * (D + 4) + 4 + d] = out;
+        else a.out[rg.out_row(a, h, vr) * D + d] = float_to_bf16_bits(out * up_lds[row]);
       }
     }
   };
@@ -593,20 +673,27 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
   struct Tile {
     Runs r;
     uint32_t there;  // bit k: part k is there (uniform)
+    float vs;        // of part l % 4
+    int unit;        // that r goes by, where all scales are near it (uniform)
+  };
+  Unit unit(kFirstUnit);  // of this wave's sums
+  auto spread = [&](const VScale& vs, Runs& r) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      r.lv[g] = __shfl(vs.log2, 2 * g + (j >> 1));
+      r.ivs[g] = __shfl(vs.inverse, 2 * g + (j >> 1));
+    }
   };
   auto tile_of = [&](const Parts& p) {
     const bool there = p.page >= 0;
-    const float vs = there && p.vs != 0.0f ? p.vs : 1.0f, ks = there ? p.ks : 0.0f;
-    const float lv = __builtin_amdgcn_logf(vs), ivs = __builtin_amdgcn_rcpf(vs);
+    const float ks = there ? p.ks : 0.0f;
     Tile t;
     t.there = (uint32_t)__ballot(there) & 15u;
+    t.vs = there ? p.vs : unit.power;
+    t.unit = all_near(t.vs, unit) ? unit.e : kFirstUnit - 1;
+    spread(near_scale(t.vs, unit), t.r);
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int from = 2 * g + (j >> 1);
-      t.r.ks[g] = __shfl(ks, from);
-      t.r.lv[g] = __shfl(lv, from);
-      t.r.ivs[g] = __shfl(ivs, from);
-    }
+    for (int g = 0; g < 2; ++g) t.r.ks[g] = __shfl(ks, 2 * g + (j >> 1));
     return t;
   };
   // A tile's codes are 4 D pieces of 16 bytes each for K and V, ITEMS of them to a thread.  K: a
@@ -683,7 +770,9 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) k_at[s] = token0 * D + 8 * k_slot<D>(token0, 4 * s + j);
   const int va_at = c * kTile + 8 * v_slot(c, j), vb_at = c * kTile + 8 * v_slot(c, 4 + j);
-  auto products = [&](int base, const Tile& tl, const TileLds<D>& in) {
+  auto products = [&](int base, Tile& tl, const TileLds<D>& in) {
+    const int was = unit.e;
+    if (__builtin_expect(tl.unit != was, 0)) spread(any_scale(tl.vs, unit), tl.r);
     v4f sc[RT][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -703,7 +792,7 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
       seen[q][0] = tl.there >> (j >> 1) & 1 ? n : 0;
       seen[q][1] = tl.there >> (2 + (j >> 1)) & 1 ? n - 32 : 0;
     }
-    softmax_step<RT, DT>(sc, fac, tl.r, masked, seen, m, l, o, pf);
+    softmax_step<RT, DT>(sc, fac, tl.r, unit.e - was, masked, seen, m, l, o, pf);
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
       const v8h va = *reinterpret_cast<const v8h*>(&in.v[16 * d][0] + va_at);
@@ -739,11 +828,12 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
       int buf = 0;
       for (int base = t0; base < t1; base += kTile, buf ^= 1) {
         store_codes(w, lds[buf ^ 1]);
-        const Tile next = tile_of(p);
+        const Parts was = p;
         page = checked(base + 2 * kTile, page);
         load_codes(base + 2 * kTile, page, w);
         p = load_parts(page);
         page = load_page(base + 3 * kTile);
+        Tile next = tile_of(was);
         if (base < high) products(base, now, lds[buf]);
         now = next;
         barrier();
@@ -752,11 +842,12 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
       page = load_page(t0 + kTile);
       for (int base = t0; base < t1; base += kTile) {
         store_codes(w, lds[0]);
-        const Tile now = tile_of(p);
+        const Parts was = p;
         page = checked(base + kTile, page);
         load_codes(base + kTile, page, w);
         p = load_parts(page);
         page = load_page(base + 2 * kTile);
+        Tile now = tile_of(was);
         barrier();
         // (a wave with products goes before those of other workgroups that still unpack codes: 510 against
         // 530 us for 4096 rows before 8192 tokens, 107 against 116 for 64 x 5 rows before 4096, but 77
@@ -776,19 +867,17 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
     if (vr >= rg.vrows) continue;
     const size_t at = rg.out_row(a, h, vr);
     if (chunks == 1) {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum, up = unit.power;
 #pragma unroll
       for (int d = 0; d < DT; ++d)
         *reinterpret_cast<v2u*>(a.out + at * D + 16 * d + 4 * j) =
-            v2u{pack2_bf16(o[q][d][0] * inv, o[q][d][1] * inv), pack2_bf16(o[q][d][2] * inv, o[q][d][3] * inv)};
+            v2u{pack2_bf16(o[q][d][0] * inv * up, o[q][d][1] * inv * up),
+                pack2_bf16(o[q][d][2] * inv * up, o[q][d][3] * inv * up)};
     } else {
       float* ws = a.ws + (at * chunks + chunk) * (D + 4);
 #pragma unroll
       for (int d = 0; d < DT; ++d) *reinterpret_cast<v4f*>(ws + 4 + 16 * d + 4 * j) = o[q][d];
-      if (j == 0) {
-        ws[0] = m[q];
-        ws[1] = sum;
-      }
+      if (j == 0) *reinterpret_cast<v4f*>(ws) = v4f{m[q], sum, (float)(m[q] == -__builtin_inff() ? kFirstUnit : unit.e), 0.0f};
     }
   }
 }
@@ -843,36 +932,45 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_join_kernel(BlockAttent
   if (i >= rg.n) return;
   const Parts p = parts_of<D>(a, cut, rg, b, i, h);
   if (p.used < 0) return;
-  float m = -__builtin_inff(), sum = 0.0f;
+  float m = -__builtin_inff(), sum = 0.0f, unit = kFirstUnit;
   v4f out = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int k = 0; k < p.used; k += 4) {
-    v2f ms[4];
+    v4f ms[4];  // maximum, sum, unit
     v4f v[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {  // (past the last part, that again)
       const float* ws = p.first + min(k + u, p.used - 1) * p.stride;
-      ms[u] = *reinterpret_cast<const v2f*>(ws);
+      ms[u] = *reinterpret_cast<const v4f*>(ws);
       v[u] = *reinterpret_cast<const v4f*>(ws + 4 + 4 * lane);
     }
-    float mn = m;
+    float mn = m, top = unit;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) mn = __builtin_fmaxf(mn, ms[u].x);
-    const float off = mn == -__builtin_inff() ? 0.0f : mn, alpha = __builtin_amdgcn_exp2f(m - off);
-    sum *= alpha;
+    for (int u = 0; u < 4; ++u) {
+      mn = __builtin_fmaxf(mn, ms[u].x);
+      top = __builtin_fmaxf(top, ms[u].z);
+    }
+    const float off0 = mn == -__builtin_inff() ? 0.0f : mn;
+    float over = __builtin_fmaxf(over_full(sum, m - off0, top - unit), 0.0f);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) over = __builtin_fmaxf(over, over_full(ms[u].y, ms[u].x - off0, top - ms[u].z));
+    mn += over;
+    const float off = off0 + over, alpha = __builtin_amdgcn_exp2f(m - off);
+    sum = sum_on(sum, m - off, top - unit);
 #pragma unroll
     for (int e = 0; e < 4; ++e) out[e] *= alpha;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const float f = k + u < p.used ? __builtin_amdgcn_exp2f(ms[u].x - off) : 0.0f;
-      sum = __builtin_fmaf(ms[u].y, f, sum);
+      const float x = k + u < p.used ? ms[u].x - off : -__builtin_inff(), f = __builtin_amdgcn_exp2f(x);
+      sum += sum_on(ms[u].y, x, top - ms[u].z);
 #pragma unroll
       for (int e = 0; e < 4; ++e) out[e] = __builtin_fmaf(v[u][e], f, out[e]);
     }
     m = mn;
+    unit = top;
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum, up = power2((int)unit);
   *reinterpret_cast<v2u*>(a.out + ((size_t)(rg.row0 + i) * a.heads + h) * D + 4 * lane) =
-      v2u{pack2_bf16(out[0] * inv, out[1] * inv), pack2_bf16(out[2] * inv, out[3] * inv)};
+      v2u{pack2_bf16(out[0] * inv * up, out[1] * inv * up), pack2_bf16(out[2] * inv * up, out[3] * inv * up)};
 }
 
 // Joins more parts of few rows, one (row, head) per workgroup (a lane of the kernel above would add
@@ -885,7 +983,7 @@ template <int D>
 __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAttention a, Cut cut) {
   constexpr int PARTS = kJoinThreads / (D / 4);
   __shared__ float f_lds[kMaxParts];
-  __shared__ float red[2][kJoinThreads / 64];
+  __shared__ float red[3][kJoinThreads / 64];
   __shared__ __attribute__((aligned(16))) float o_lds[PARTS][D];
   unsigned id = blockIdx.x;
   const int h = id % a.heads;
@@ -897,31 +995,42 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
   const Parts p = parts_of<D>(a, cut, rg, b, i, h);
   const int used = p.used;
   if (used < 0) return;
-  // four parts to a thread at most: their maxima and sums
-  float m[kMaxParts / kJoinThreads], s[kMaxParts / kJoinThreads];
-  float mm = -__builtin_inff();
+  // four parts to a thread at most: their maxima, sums and units
+  float m[kMaxParts / kJoinThreads], s[kMaxParts / kJoinThreads], un[kMaxParts / kJoinThreads];
+  float mm = -__builtin_inff(), top = kFirstUnit;
 #pragma unroll
   for (int q = 0; q < kMaxParts / kJoinThreads; ++q) {
     const int k = tid + kJoinThreads * q;
-    const v2f ms = *reinterpret_cast<const v2f*>(p.first + max(min(k, used - 1), 0) * p.stride);
+    const v4f ms = *reinterpret_cast<const v4f*>(p.first + max(min(k, used - 1), 0) * p.stride);
     m[q] = k < used ? ms.x : -__builtin_inff();
     s[q] = k < used ? ms.y : 0.0f;
+    un[q] = k < used ? ms.z : (float)kFirstUnit;
     mm = __builtin_fmaxf(mm, m[q]);
+    top = __builtin_fmaxf(top, un[q]);
   }
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) mm = __builtin_fmaxf(mm, __shfl_xor(mm, x));
-  if (lane == 0) red[0][wave] = mm;
+  for (int x = 1; x < 64; x <<= 1) {
+    mm = __builtin_fmaxf(mm, __shfl_xor(mm, x));
+    top = __builtin_fmaxf(top, __shfl_xor(top, x));
+  }
+  if (lane == 0) {
+    red[0][wave] = mm;
+    red[2][wave] = top;
+  }
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kJoinThreads / 64; ++w) mm = __builtin_fmaxf(mm, red[0][w]);
+  for (int w = 0; w < kJoinThreads / 64; ++w) {
+    mm = __builtin_fmaxf(mm, red[0][w]);
+    top = __builtin_fmaxf(top, red[2][w]);
+  }
   const float off = mm == -__builtin_inff() ? 0.0f : mm;
   float sum = 0.0f;
 #pragma unroll
   for (int q = 0; q < kMaxParts / kJoinThreads; ++q) {
     const int k = tid + kJoinThreads * q;
-    const float f = __builtin_amdgcn_exp2f(m[q] - off);
-    if (k < used) f_lds[k] = f;
-    sum = __builtin_fmaf(s[q], f, sum);
+    if (k < used) f_lds[k] = __builtin_amdgcn_exp2f(m[q] - off);
+    const float up = top - un[q], over = __builtin_fmaxf(over_full(s[q], m[q] - off, up), 0.0f);
+    sum += sum_on(s[q], m[q] - off - over, up);  // (as far as it counts: the sum stays finite)
   }
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
@@ -951,7 +1060,7 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
     float o = 0.0f;
 #pragma unroll
     for (int q = 0; q < PARTS; ++q) o += o_lds[q][tid];
-    a.out[((size_t)(rg.row0 + i) * a.heads + h) * D + tid] = float_to_bf16_bits(sum == 0.0f ? 0.0f : o / sum);
+    a.out[((size_t)(rg.row0 + i) * a.heads + h) * D + tid] = float_to_bf16_bits(sum == 0.0f ? 0.0f : o / sum * power2((int)top));
   }
 }
 

@@ -166,6 +166,9 @@ int kv_block_read(const int64_t* slots, int rows, int kv_heads, int dim, int blo
  * over the tokens t < seq_lens[b], and with `causal` only t <= seq_lens[b] - n + j for the j-th
  * of the request's n rows.  A row with no token gives 0; rows at or behind cu_rows[requests] are
  * left as they were; tokens of a block whose table entry is outside [0, num_blocks) are left out.
+ * Blocks' V scales may lie as far apart as appends can make them, zero and subnormal ones among
+ * them: one under 2^-80 of the largest of the request's and head's blocks may count as that, which
+ * moves an output by less than 2^-64 of the largest |V|.
  *   q        bf16 [rows, heads, dim], 16B, rows q_stride elements apart (as k_stride)
  *   block_tables   int32 [requests, width];  seq_lens  int32 [requests] (clamped to
  *            [0, width bs]);  cu_rows  int32 [requests + 1], ascending
