@@ -234,22 +234,27 @@ inline int append_window(int rows, int heads, int bs) {
 }
 
 // What turns a value into a code + 128 under the block scale s: the correctly rounded quotient
-// (div_rn) plus 1.5 2^23 + 128, whose low byte is then the code to the nearest even.  |x / s| is at
-// most 127 (1 + 2^-23), so no code needs a clamp.  The correction step needs a normal reciprocal,
-// so a scale below 2^-80 and its values are taken 2^64 times larger (exact, the quotient is the
-// same).  s = 0: every value of the block is 0, and so is every quotient by 1.
+// (div_rn) plus 1.5 2^23 + 128, whose low byte is then the code to the nearest even.  s is amax / 127
+// rounded, by 2^-24 of it or, among the subnormal numbers, by 2^-150 of 2^-140 at least, so |x / s| is
+// at most 127 (1 + 2^-10) < 127.5 and no code needs a clamp.  The correction step needs a normal
+// reciprocal, so a scale below 2^-80 and its values are taken 2^64 times larger (exact, the quotient is
+// the same).  s = 0: every value of the block is 0, and so is every quotient by 1.  A scale that is NaN
+// or infinite gives the values `times` 0, and their codes 0, by the same branch.
 struct Coder {
-  float s, rcp;
-  bool tiny;
+  float s, rcp, times;  // values times that (1: none)
 };
 
 __device__ __forceinline__ Coder coder_of(float s) {
+  const bool tiny = s < 0x1p-80f, finite = s < __builtin_inff();
   Coder k;
-  k.tiny = s < 0x1p-80f;
-  k.s = s == 0.0f ? 1.0f : k.tiny ? s * 0x1p64f : s;
+  k.times = tiny ? 0x1p64f : finite ? 1.0f : 0.0f;
+  k.s = s == 0.0f || !finite ? 1.0f : tiny ? s * 0x1p64f : s;
   k.rcp = 1.0f / k.s;
   return k;
 }
+
+// The larger of two scales; a NaN stays one.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
 __device__ __forceinline__ uint32_t kv_code_bits(float x, Coder k) {
   return __float_as_uint(div_rn(x, k.s, k.rcp) + 12583040.0f);
@@ -265,7 +270,8 @@ __device__ __forceinline__ void bf16x8(v4u w, float* x) {
   }
 }
 
-// Largest magnitudes as bf16 bits without the sign, two to a dword (they order like integers).
+// Largest magnitudes as bf16 bits without the sign, two to a dword (they order like integers, infinity
+// and then NaN last).
 typedef uint16_t v2s __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
@@ -289,9 +295,9 @@ __device__ __forceinline__ float amax_lanes(uint32_t amax, int lanes) {
 __device__ __forceinline__ v2u codes8(v4u w, Coder k) {
   float x[8];
   bf16x8(w, x);
-  if (k.tiny)
+  if (k.times != 1.0f)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= 0x1p64f;
+    for (int e = 0; e < 8; ++e) x[e] = k.times == 0.0f ? 0.0f : x[e] * k.times;
   uint32_t b[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) b[e] = kv_code_bits(x[e], k);
@@ -424,10 +430,10 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
     __syncthreads();  // (also: every thread has read the old scales)
 #pragma unroll
     for (int q = 0; q < kAppendThreads / 64; ++q) {
-      ka = __builtin_fmaxf(ka, wmax[0][q]);
-      va = __builtin_fmaxf(va, wmax[1][q]);
+      ka = larger(ka, wmax[0][q]);
+      va = larger(va, wmax[1][q]);
     }
-    const float ks = __builtin_fmaxf(k_old, ka / 127.0f), vs = __builtin_fmaxf(v_old, va / 127.0f);
+    const float ks = larger(k_old, ka / 127.0f), vs = larger(v_old, va / 127.0f);
     const Coder kk = coder_of(ks), vk = coder_of(vs);
     if (tid == 0) {
       c.k_scale[bh] = ks;
@@ -498,8 +504,8 @@ __global__ __launch_bounds__(kAppendThreads) void kv_block_append_kernel(
       k_top = amax8(wk[r], k_top);
       v_top = amax8(wv[r], v_top);
     }
-    const float ks = __builtin_fmaxf(k_old, amax_lanes(k_top, TPR) / 127.0f);
-    const float vs = __builtin_fmaxf(v_old, amax_lanes(v_top, TPR) / 127.0f);
+    const float ks = larger(k_old, amax_lanes(k_top, TPR) / 127.0f);
+    const float vs = larger(v_old, amax_lanes(v_top, TPR) / 127.0f);
     const Coder kk = coder_of(ks), vk = coder_of(vs);
     if (part == 0) {  // (the group's lanes have read them: they are one wave's)
       c.k_scale[bh] = ks;

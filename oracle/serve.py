@@ -90,12 +90,12 @@ class Cache:
             for h in range(H):
                 v = x[t:t + n, h].astype(np.float32)
                 old = np.float32(0) if off == 0 else self.scale[b, h]
-                new = max(old, np.float32(np.abs(v).max()) / np.float32(127))
+                new = np.maximum(old, np.float32(np.abs(v).max()) / np.float32(127))  # (a NaN stays one)
                 if off > 0 and new > old:
                     ratio = np.float32(old / new)
                     was = self.codes[b, h, :off].astype(np.float32)
                     self.codes[b, h, :off] = np.rint(was * ratio).astype(np.int64)
-                if new > 0:
+                if 0 < new < np.inf:
                     q = np.clip(np.rint(v / new), -127, 127).astype(np.int64)
                 else:
                     q = np.zeros_like(v, dtype=np.int64)
