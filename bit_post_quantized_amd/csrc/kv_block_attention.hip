@@ -243,7 +243,10 @@ __device__ __forceinline__ VScale any_scale(float vs, Unit& unit) {
   const int top = (int)(__builtin_amdgcn_readfirstlane(max_wave(bits < 0x7F800000u ? bits : 0u)) >> 23) - 127;
   unit = Unit(top >= unit.e + 20 ? min(top, kLastUnit) : unit.e);
   const float in_units = __builtin_elementwise_maximum(vs * power2(-unit.e), kLeastScale);  // (NaN stays one)
-  return VScale{__builtin_amdgcn_logf(in_units) + (float)unit.e, __builtin_amdgcn_rcpf(in_units)};
+  // (the inverse is a number where the scale is not: it is multiplied by the weights of rows that do not
+  // see the block, which are 0)
+  return VScale{__builtin_amdgcn_logf(in_units) + (float)unit.e,
+                __builtin_amdgcn_rcpf(__builtin_fmaxf(in_units, kLeastScale))};
 }
 
 // How far a sum goes past 2^100 where its maximum is 2^x times the whole's and its unit `up` below the

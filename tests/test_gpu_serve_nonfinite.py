@@ -7,6 +7,7 @@ import torch
 from oracle import serve as osv
 from oracle.numerics import bf16_to_bits, decode_bf16
 from tests.serve_cases import bf16_values, dev_cache, host64, host_cache, random_cache, to_dev, to_dev_bf16
+from tests.test_gpu_serve_attention import batch, run
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,46 @@ def test_append_keeps_a_bad_value_in_its_block_and_head(gpu_lib, bs, dim, bad):
             np.testing.assert_array_equal(np.isfinite(more[b]), ~lost[b])
             cache.append(one, one, to_dev(np.array([b * bs])))      # begun anew
             assert np.isfinite(host_cache(cache)[3 if is_v else 1][b]).all()
+
+
+# --------------------------------------------------------------------------------- attention
+SHAPES = [
+    ([200, 90], [2, 2], 8, 2, 64, 16, None),            # few rows
+    ([300, 40], [1, 1], 34, 2, 64, 16, None),           # two tiles of them
+    ([9000, 50, 4096], [4, 1, 2], 8, 2, 128, 16, 600),  # in equal shares
+    ([600, 130], [300, 129], 3, 1, 64, 64, None),       # eight waves
+    ([450, 90], [450, 33], 2, 2, 128, 16, None),        # two row tiles
+    ([200, 150], [20, 17], 2, 2, 64, 32, None),         # one
+    ([20000, 77], [5, 2], 8, 1, 128, 64, 320),          # chunks, joined per row
+    ([5000, 64], [100, 64], 2, 1, 128, 16, 320),        # chunks, joined by lanes
+]
+
+
+def tolerance(c, want, mag, top):
+    D = c["q"].shape[2]
+    err = (2 * (2 * D + 8) * 2.0 ** -24 * top + 2.0 ** -11 + 2.0 ** -20)[:, :, None] * mag
+    return 2.0 ** -8 * np.abs(want) + err
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"{s[0][0]}x{s[1][0]}x{s[2]}x{s[4]}")
+@pytest.mark.parametrize("value", [np.nan, np.inf])
+def test_a_bad_block_is_seen_by_its_rows_only(gpu_lib, shape, value):
+    # the last block of each request is bad in one cached head: its last row sees it, rows whose
+    # causal limit ends before it, and the other head's, do not
+    seq, rows, heads, kv_heads, dim, bs, width = shape
+    for which in (1, 3):                              # K's scales, then V's
+        c = batch(sum(seq) + 2, seq, rows, heads, kv_heads, dim, bs, width=width)
+        kc, ks, vc, vs = c["cache"]
+        good = (kc, ks.copy(), vc, vs.copy())
+        for b, s in enumerate(seq):
+            last = c["tables"][b, -(-s // bs) - 1]
+            c["cache"][which][last, 0] = value
+            kc[last, 0], vc[last, 0] = 0, 0           # as an append leaves it: NaN whatever the code
+        got = run(c, True, 0.125)
+        want, mag, top, _ = osv.attention(c["q"], *good, c["tables"], c["seq"], c["cu"], True, 0.125, 1 << 30)
+        sees = np.zeros(got.shape[:2], bool)
+        for b, s in enumerate(seq):
+            for i in range(rows[b]):
+                sees[c["cu"][b] + i, :heads // kv_heads] = s - rows[b] + i >= (-(-s // bs) - 1) * bs
+        assert sees.any() and np.isnan(got[sees]).all()
+        assert (np.abs(got - want) <= tolerance(c, want, mag, top))[~sees].all()
