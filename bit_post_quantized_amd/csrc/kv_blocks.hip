@@ -579,7 +579,8 @@ __global__ __launch_bounds__(256) void kv_block_read_kernel(const int64_t* __res
   // Every wave holds the window's 64 slots, a row to a lane, and which rows have a token.
   const int64_t slot = slots[min(row0 + lane, rows - 1)];
   const uint64_t live = __ballot(row0 + lane < rows && slot >= 0 && slot < limit);
-  // (c - 128) s in one rounding: 128 s is exact
+  // (c - 128 is exact, so the product rounds once; 128 s, for an FMA, may be past the largest number)
+  auto value = [](uint32_t byte, float scale) { return ((float)byte - 128.0f) * scale; };
   if (!is_v) {
     v2u w[W / PER];
     float s[W / PER];
@@ -598,7 +599,7 @@ __global__ __launch_bounds__(256) void kv_block_read_kernel(const int64_t* __res
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        x[e] = __builtin_fmaf((float)(((e < 4 ? w[p].x : w[p].y) >> (8 * (e & 3))) & 0xFFu), s[p], -128.0f * s[p]);
+        x[e] = value(((e < 4 ? w[p].x : w[p].y) >> (8 * (e & 3))) & 0xFFu, s[p]);
       *reinterpret_cast<v8bf*>(k_out + ((size_t)(row0 + i) * c.heads + h) * D + 8 * part) = to_bf16x8(x);
     }
     return;
@@ -628,7 +629,7 @@ __global__ __launch_bounds__(256) void kv_block_read_kernel(const int64_t* __res
     if (!(odd >> i0 & 0xFFFF)) {
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        x[i] = __builtin_fmaf((float)((w[q][i >> 2] >> (8 * (i & 3))) & 0xFFu), s[q], -128.0f * s[q]);
+        x[i] = value((w[q][i >> 2] >> (8 * (i & 3))) & 0xFFu, s[q]);
     } else {
       uint8_t b[16];
       float t[16];
@@ -640,7 +641,7 @@ __global__ __launch_bounds__(256) void kv_block_read_kernel(const int64_t* __res
         t[i] = c.v_scale[bh];
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __builtin_fmaf((float)b[i], t[i], -128.0f * t[i]);
+      for (int i = 0; i < 16; ++i) x[i] = value(b[i], t[i]);
     }
 #pragma unroll
     for (int i = 0; i < 16; i += 8) {

@@ -134,7 +134,7 @@ int kv_block_release(const int32_t* seq_lens, const uint8_t* done, int requests,
  *     c = clamp(rne(fl32(x / s)), -127, 127), 0 where s = 0,
  * and where s > s_old the codes of the block's earlier tokens become rne(fl32(c fl32(s_old / s))).
  * A NaN among the values makes s NaN, an infinity makes it infinite (as does either in s_old); the new
- * codes are 0 then, and every value of that block and head reads as NaN until the block is begun anew.
+ * codes are 0 then, and every token of that block and head reads as NaN until the block is begun anew.
  *   k, v     bf16 [rows, kv_heads, dim], 16B, rows k_stride / v_stride elements apart (a
  *            multiple of 8, at least kv_heads dim: slices of a fused projection need no copy)
  *   slots    int64 [rows], as written by kv_block_plan: the rows of one block must stand

@@ -50,10 +50,11 @@ def test_append_keeps_a_bad_value_in_its_block_and_head(gpu_lib, bs, dim, bad):
             lost = np.zeros_like(scale, dtype=bool)
             lost[tuple(np.array(hit).T)] = True
             np.testing.assert_array_equal(np.isfinite(scale), ~lost)
-            # every value of such a block and head reads as NaN, also after another token of it
+            # every token of such a block and head reads as NaN, also after another token of it
             every = np.arange(num * bs)
             read = host64(cache.read(to_dev(every))[int(is_v)]).reshape(num, bs, heads, dim)
-            assert np.isnan(read.transpose(0, 2, 1, 3)[lost]).all()
+            for b, o, n in runs:
+                assert np.isnan(read[b, :o + n, lost[b]]).all()
             assert np.isfinite(read.transpose(0, 2, 1, 3)[~lost]).all()
             b = runs[2][0]
             one = to_dev_bf16(bf16_values(rng, 1, heads, dim))

@@ -3,9 +3,30 @@ import numpy as np
 import pytest
 import torch
 
-from tests.serve_cases import bf16_values, dev_cache, host64, random_cache, to_dev, to_dev_bf16
+from oracle.numerics import decode_bf16, round_bf16
+from tests.serve_cases import bf16_values, dev_cache, host64, host_bits, random_cache, to_dev, to_dev_bf16
+from tests.test_gpu_serve_blocks import check_append
 
 pytestmark = pytest.mark.gpu
+
+LARGEST = float(decode_bf16(np.array([0x7F7F], np.uint16))[0])
+
+
+# --------------------------------------------------------------------------------- read-back
+@pytest.mark.parametrize("peak", [2.0 ** -133, 3e-39, 1e-30, 1.0, 2.0 ** 120, 2.0 ** 127, LARGEST])
+@pytest.mark.parametrize("bs,dim", [(16, 64), (64, 128)])
+def test_read_back_of_extreme_magnitudes(gpu_lib, bs, dim, peak):
+    rng = np.random.default_rng(3)
+    x = rng.uniform(-1, 1, (3 * bs + 5, 2, dim)) * peak
+    x[::7, 0, 3], x[1::5, 1, 9] = peak, -peak
+    x = round_bf16(x)
+    slots = np.arange(bs, 4 * bs + 5)
+    cache, ok, ov = check_append(9, 6, 2, bs, dim, list(slots), x=x)
+    for order in (slots, rng.permutation(slots)):      # runs of 16 slots, and none
+        k, v = cache.read(to_dev(order))
+        np.testing.assert_array_equal(host_bits(k), ok.values(order))
+        np.testing.assert_array_equal(host_bits(v), ov.values(order))
+        assert np.isfinite(host64(k)).all() and (host64(k) != 0).any()
 
 
 # --------------------------------------------------------------------------------- attention
