@@ -87,16 +87,19 @@ __device__ __forceinline__ float sum_quads(float x) {
 // group * span on.
 struct Range {
   int row0, n, vrows, len, hg;
+  int hidden;  // tokens behind the first row's last (a request's rows past the batch's count here)
   __device__ __forceinline__ Range(const BlockAttention& a, int b) {
     row0 = min(max(a.cu[b], 0), a.rows);
-    n = min(max(a.cu[b + 1], row0), a.rows) - row0;
+    const int end = max(a.cu[b + 1], row0);
+    n = min(end, a.rows) - row0;
     hg = a.heads / a.cache.heads;
     vrows = min(n, a.max_rows) * hg;
     len = min(max(a.seq[b], 0), a.width << __builtin_ctz(a.cache.bs));
+    hidden = end - row0 - 1;
   }
   // tokens that row vr sees
   __device__ __forceinline__ int limit(const BlockAttention& a, int vr) const {
-    return a.causal ? min(len, max(len - n + vr / hg + 1, 0)) : len;
+    return a.causal ? min(len, max(len - hidden + vr / hg, 0)) : len;
   }
   __device__ __forceinline__ size_t out_row(const BlockAttention& a, int h, int vr) const {
     return (size_t)(row0 + vr / hg) * a.heads + h * hg + vr % hg;

@@ -166,8 +166,9 @@ int kv_block_read(const int64_t* slots, int rows, int kv_heads, int dim, int blo
  * h' = h kv_heads / heads the cached head of query head h,
  *     out[i, h, :] = softmax_t(sm_scale q[i, h, :] . K[t, h', :]) V[t, h', :]
  * over the tokens t < seq_lens[b], and with `causal` only t <= seq_lens[b] - n + j for the j-th
- * of the request's n rows.  A row with no token gives 0; rows at or behind cu_rows[requests] are
- * left as they were; tokens of a block whose table entry is outside [0, num_blocks) are left out.
+ * of the request's n rows (also where the batch's `rows` end before the last of them).  A row with
+ * no token gives 0; rows at or behind cu_rows[requests] are left as they were; tokens of a block whose
+ * table entry is outside [0, num_blocks) are left out.
  * Blocks' V scales may lie as far apart as appends can make them, zero and subnormal ones among
  * them: one under 2^-80 of the largest of the request's and head's blocks may count as that, which
  * moves an output by less than 2^-64 of the largest |V|.  A block that an append gave a NaN or infinite

@@ -5,6 +5,7 @@ import torch
 
 from oracle.numerics import decode_bf16, round_bf16
 from tests.serve_cases import bf16_values, dev_cache, host64, host_bits, random_cache, to_dev, to_dev_bf16
+from tests.test_gpu_serve_attention import batch, check, run
 from tests.test_gpu_serve_blocks import check_append
 
 pytestmark = pytest.mark.gpu
@@ -30,6 +31,16 @@ def test_read_back_of_extreme_magnitudes(gpu_lib, bs, dim, peak):
 
 
 # --------------------------------------------------------------------------------- attention
+def test_rows_of_a_request_that_the_batch_cuts_off(gpu_lib):
+    # the last request has more rows than q holds: those that there are keep their causal limit
+    for seq, rows, have, heads, dim in (([300, 90], [1, 9], 5, 2, 64), ([90, 500], [40, 300], 200, 1, 128)):
+        c = batch(sum(seq), seq, rows, heads, 1, dim, 16)
+        full = run(c, True, 0.125)
+        check(c, full, True, 0.125)
+        got = run(dict(c, q=c["q"][:have]), True, 0.125, max_rows=max(rows))
+        np.testing.assert_array_equal(got, full[:have])
+
+
 @pytest.mark.parametrize("kv_heads,heads,rows,dim,bs", [(1, 8, 5, 64, 128), (4, 32, 5, 128, 128), (1, 1, 64, 64, 64)])
 def test_drafts_before_more_tokens_than_a_join_has_parts_for(gpu_lib, kv_heads, heads, rows, dim, bs):
     """More than 1024 x 4096 tokens under a wider table, whose entries repeat a few blocks: equal
