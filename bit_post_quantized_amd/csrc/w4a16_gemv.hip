@@ -261,7 +261,7 @@ __global__ __launch_bounds__(kSeg * 64) void w4a16_prep_kernel(
     for (int q = 0; q < kSeg; ++q) amax = __builtin_fmaxf(amax, top[par][q][mr]);
     // 2^e with amax 2^-e in [2^10, 2^11) (e clamped so that both powers are normal; 0 keeps e = 0)
     int e = (int)(__float_as_uint(amax) >> 23) - 127 - 10;
-    e = amax == 0.0f ? 0 : max(e, -110);
+    e = amax == 0.0f ? 0 : max(e, -126);
     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
     const float up = __uint_as_float((uint32_t)(127 + e) << 23);
     _Float16 h[16];

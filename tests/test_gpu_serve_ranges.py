@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+from bit_post_quantized_amd import serve
 from oracle.numerics import decode_bf16, round_bf16
 from tests.serve_cases import bf16_values, dev_cache, host64, host_bits, random_cache, to_dev, to_dev_bf16
 from tests.test_gpu_serve_attention import batch, check, run
@@ -77,3 +78,23 @@ def test_drafts_before_more_tokens_than_a_join_has_parts_for(gpu_lib, kv_heads, 
                 top = sm * (np.abs(k) @ np.abs(q[i, h])).max()
                 err = 2 * (2 * dim + 8) * 2.0 ** -24 * top + 2.0 ** -11 + 2.0 ** -15
                 assert np.all(np.abs(got[i, h] - w @ v) <= 2.0 ** -8 * np.abs(w @ v) + err * (w @ np.abs(v))), (causal, i, h)
+
+
+# ------------------------------------------------------------------------------------ linear
+@pytest.mark.parametrize("power", [-100, -112, -118, -124])
+def test_linear_of_a_few_tiny_activations(gpu_lib, power):
+    """22 bits of every activation of a row of tiny ones (fp32 output): the bound of
+    test_gpu_serve_linear, where two terms meet eight roundings or fewer (adding zeros is exact; half of
+    the 2^-21 is theirs), each of 2^-149 at most below the normal range, where a matrix step may
+    truncate and four of them come before a sum of its own size."""
+    from tests.test_gpu_serve_linear import make
+    rng = np.random.default_rng(8)
+    K = 512
+    x = np.zeros((24, K))
+    for m in range(24):
+        x[m, rng.integers(0, K, 1 + m % 2)] = rng.uniform(1, 2, 1 + m % 2) * 2.0 ** power
+    x, pw, ref = make(power + 200, 24, K, 40, 0, False, x=round_bf16(x))
+    y = host64(serve.DecodeLinear(pw)(to_dev_bf16(x), out_dtype=torch.float32))
+    want, mag = ref(x)
+    tol = 2.0 ** -24 * np.abs(want) + (2.0 ** -21 + 4 * 2.0 ** -24) * mag + 4 * 2.0 ** -149
+    assert np.all(np.abs(y - want) <= tol), float((np.abs(y - want) / tol).max())
