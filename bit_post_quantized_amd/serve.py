@@ -117,9 +117,11 @@ class BlockPlanner:
     """Block tables and slot maps of a batch (``kv_block_plan``, ``kv_block_release``).
 
     ``block_tables`` int32 [requests, width] and ``free_blocks`` int32 [capacity] are the
-    caller's and updated in place.  ``plan`` and ``release`` write one of four sets of outputs,
-    the oldest that their own arguments are not part of, so the ``seq_lens`` and ``free_count`` of
-    one call can be the next call's arguments; a plan stays valid until the second call after it.
+    caller's and updated in place.  ``plan`` and ``release`` write one of five sets of outputs,
+    the oldest that none of their own arguments is the beginning of, so the outputs of one call can
+    be the next call's arguments; a plan stays valid until the second call after it.  A captured
+    call writes the set that its capture chose at every replay, whatever was called in between: give
+    a captured step a planner of its own.
     """
 
     def __init__(self, block_tables: torch.Tensor, free_blocks: torch.Tensor, block_size: int,
@@ -140,31 +142,35 @@ class BlockPlanner:
             return torch.empty(*shape, dtype=_I32, device=dev)
 
         self._plans = []
-        for _ in range(4):
+        for _ in range(5):
             p = SlotPlan(i32(n + 1), i32(n), i32(rows),
                          torch.empty(rows, dtype=_I64, device=dev), i32(n), i32(1))
             p._outputs = (p.cu_rows.data_ptr(), p.seq_lens.data_ptr(), rows, p.positions.data_ptr(),
                           p.slots.data_ptr(), p.status.data_ptr(), p.free_count.data_ptr())
             self._plans.append(p)
 
-    def _other(self, a: int, b: int, some: int) -> SlotPlan:
-        """The oldest set that is not an argument's (lengths at a, free count at b), which becomes the
-        newest: of the three older ones at most two are, so it is never the set of the call before."""
+    def _other(self, a: int, b: int, count: int) -> SlotPlan:
+        """The oldest set that is not an argument's (lengths at a and b, free count at count), which
+        becomes the newest: of the four older ones at most three are, so it is never the set of the
+        call before.  (Without requests the lengths are nowhere.)"""
         plans = self._plans
-        for i in range(3):
+        if not self.requests:
+            a = b = count
+        for i in range(4):
             o = plans[i]._outputs
-            if o[6] != b and (o[1] != a or not some):
+            if not (count in o or a in o or b in o):
                 break
         plans.append(plans.pop(i))
-        return plans[3]
+        return plans[4]
 
     def plan(self, ctx_lens: torch.Tensor, new_lens: torch.Tensor,
              free_count: torch.Tensor) -> SlotPlan:
-        ctx, count, dev, n = ctx_lens.data_ptr(), free_count.data_ptr(), self.device, self.requests
-        p = self._other(ctx, count, n)
+        ctx, new, dev, n = ctx_lens.data_ptr(), new_lens.data_ptr(), self.device, self.requests
+        count = free_count.data_ptr()
+        p = self._other(ctx, new, count)
         if (_is(ctx_lens, _I32, (n,), dev) and _is(new_lens, _I32, (n,), dev)
                 and _is(free_count, _I32, (1,), dev) and _here(dev)):
-            status = self._call(ctx, new_lens.data_ptr(), *self._tables, count, *p._outputs,
+            status = self._call(ctx, new, *self._tables, count, *p._outputs,
                                 _stream(dev))
             if status:
                 binding._check("kv_block_plan", status)
@@ -177,7 +183,7 @@ class BlockPlanner:
     def release(self, seq_lens: torch.Tensor, done: torch.Tensor, free_count: torch.Tensor):
         """Gives back the blocks of the requests with ``done`` (uint8) set: (lengths, free
         count), of the set of outputs that the arguments are not part of."""
-        p = self._other(seq_lens.data_ptr(), free_count.data_ptr(), self.requests)
+        p = self._other(seq_lens.data_ptr(), done.data_ptr(), free_count.data_ptr())
         B.kv_block_release(seq_lens, done, self.block_tables, self.block_size, self.free_blocks,
                            free_count, p.seq_lens, p.free_count)
         return p.seq_lens, p.free_count
