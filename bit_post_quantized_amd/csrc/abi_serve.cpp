@@ -130,6 +130,8 @@ int kv_block_plan(const int32_t* ctx_lens, const int32_t* new_lens, int requests
     return fail(SVDQ_EINVAL, "NULL pointer");
   if (free_count == free_count_out)
     return fail(SVDQ_EINVAL, "free_count_out may not be free_count");
+  if (requests > 0 && (seq_lens == ctx_lens || seq_lens == new_lens || status == ctx_lens || status == new_lens))
+    return fail(SVDQ_EINVAL, "seq_lens and status may not be ctx_lens or new_lens");
   return hip_status(
       svdq::launch_kv_block_plan(ctx_lens, new_lens, requests, block_tables, width, block_size,
                                  free_blocks, free_capacity, free_count, cu_rows, seq_lens, rows,

@@ -103,8 +103,9 @@ int svdq_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const uint16_t* 
  *                        rows do not fit `rows`
  *   free_count_out       int32 [1]: what is left
  *   0 <= requests <= 2^20, 1 <= width, requests * width < 2^31, 0 <= rows <= 2^30,
- *   free_capacity >= 0.  No output overlaps an input or another output (free_count_out may not
- *   be free_count: workgroups read it at their own time).
+ *   free_capacity >= 0.  No output overlaps an input or another output: workgroups read the lengths
+ *   and the count at their own time (free_count_out that is free_count, and seq_lens or status that is
+ *   one of the lengths, are refused).
  */
 int kv_block_plan(const int32_t* ctx_lens, const int32_t* new_lens, int requests,
                   int32_t* block_tables, int width, int block_size, const int32_t* free_blocks,
