@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 import torch
 
+from bit_post_quantized_amd import serve
 from oracle import serve as osv
 from oracle.numerics import bf16_to_bits, decode_bf16
 from tests.serve_cases import bf16_values, dev_cache, host64, host_cache, random_cache, to_dev, to_dev_bf16
@@ -85,6 +86,23 @@ def tolerance(c, want, mag, top):
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"{s[0][0]}x{s[1][0]}x{s[2]}x{s[4]}")
+def test_a_bad_query_stays_in_its_row(gpu_lib, shape):
+    seq, rows, heads, kv_heads, dim, bs, width = shape
+    c = batch(sum(seq) + 1, seq, rows, heads, kv_heads, dim, bs, width=width)
+    bits = bf16_to_bits(c["q"])
+    hit = [(0, heads - 1, NAN, 5), (rows[0] - 1, 0, NAN_ALL_ONES, 0), (rows[0], heads // 2, INF, dim - 1)]
+    for t, h, bad, d in hit:
+        bits[t, h, d] = bad
+    got = run(c, True, 0.125, q=from_bits(bits))
+    want, mag, top, _ = osv.attention(c["q"], *c["cache"], c["tables"], c["seq"], c["cu"], True, 0.125, 1 << 30)
+    keep = np.ones(got.shape[:2], bool)
+    for t, h, bad, _ in hit:
+        assert np.isnan(got[t, h]).all() if bad in (NAN, NAN_ALL_ONES) else not np.isfinite(got[t, h]).any(), (t, h)
+        keep[t, h] = False
+    assert (np.abs(got - want) <= tolerance(c, want, mag, top))[keep].all()
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"{s[0][0]}x{s[1][0]}x{s[2]}x{s[4]}")
 @pytest.mark.parametrize("value", [np.nan, np.inf])
 def test_a_bad_block_is_seen_by_its_rows_only(gpu_lib, shape, value):
     # the last block of each request is bad in one cached head: its last row sees it, rows whose
@@ -106,3 +124,27 @@ def test_a_bad_block_is_seen_by_its_rows_only(gpu_lib, shape, value):
                 sees[c["cu"][b] + i, :heads // kv_heads] = s - rows[b] + i >= (-(-s // bs) - 1) * bs
         assert sees.any() and np.isnan(got[sees]).all()
         assert (np.abs(got - want) <= tolerance(c, want, mag, top))[~sees].all()
+
+
+# ------------------------------------------------------------------------------------ linear
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bad", [NAN, 0x7FFF, NAN_ALL_ONES])
+@pytest.mark.parametrize("M,K,N,r", [(3, 256, 50, 16), (20, 64 * 70, 33, 0), (1, 64 * 129, 40, 32)])
+def test_a_nan_of_any_payload_makes_its_row_nan(gpu_lib, M, K, N, r, bad, dtype):
+    from tests.test_gpu_serve_linear import check, make
+    x, pw, ref = make(M + K, M, K, N, r, True)
+    bits = bf16_to_bits(x)
+    bits[M - 1, 7] = bad
+    y = host64(serve.DecodeLinear(pw)(from_bits(bits), out_dtype=dtype))
+    assert np.isnan(y[M - 1]).all()
+    want, mag = ref(x)
+    check(y[:M - 1], want[:M - 1], mag[:M - 1], K, dtype == torch.float32)
+
+
+def test_a_nan_bias_makes_its_column_nan(gpu_lib):
+    from tests.test_gpu_serve_linear import make
+    for K in (128, 64 * 70):
+        x, pw, _ = make(K, 20, K, 33, 16, True)
+        pw.bias[5:7] = from_bits(np.array([0x7FFF, 0xFFFF], np.uint16))
+        y = host64(serve.DecodeLinear(pw)(to_dev_bf16(x)))
+        assert np.isnan(y[:, 5:7]).all() and np.isfinite(np.delete(y, (5, 6), 1)).all()
