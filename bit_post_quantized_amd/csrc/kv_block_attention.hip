@@ -822,7 +822,10 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
     int page = checked(t0, load_page(t0));
     Codes w;
     load_codes(t0, page, w);
+    // (loads in the loop's own order: what the loop waits for is the later of both orders)
+    __builtin_amdgcn_sched_barrier(0);
     Parts p = load_parts(page);
+    __builtin_amdgcn_sched_barrier(0);
     if constexpr (BUFS == 2) {
       page = checked(t0 + kTile, load_page(t0 + kTile));
       store_codes(w, lds[0]);
@@ -848,12 +851,11 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
       page = load_page(t0 + kTile);
       for (int base = t0; base < t1; base += kTile) {
         store_codes(w, lds[0]);
-        const Parts was = p;
+        Tile now = tile_of(p);
         page = checked(base + kTile, page);
         load_codes(base + kTile, page, w);
         p = load_parts(page);
         page = load_page(base + 2 * kTile);
-        Tile now = tile_of(was);
         barrier();
         // (a wave with products goes before those of other workgroups that still unpack codes: 510 against
         // 530 us for 4096 rows before 8192 tokens, 107 against 116 for 64 x 5 rows before 4096, but 77
