@@ -20,14 +20,14 @@
 // rows; with few workgroups the tokens are split over more of them (chunks).  Where a row's tokens went
 // to several workgroups, a second launch joins their maxima, sums and outputs.
 //
-// Measured (kernel times).  64 requests of up to 8192 tokens, 32 heads to 8 of 128: 127 us, 5.3 TB/s of
-// codes, and 4 for the join (139 and none with a workgroup per request and head).  1 x 10240 tokens, 32
-// heads: 20 us and 4; the bytes are 15 at 5.5 TB/s.  2 x 5 rows, 32 heads to 4, before up to 131071 tokens: 49 us and 6; the bytes are
-// 40.  4 prompts of 475 to 1000 rows, 24 heads to 8 of 64, before up to 4096 tokens: 85 us,
-// 470 TFLOP/s: a wave's tile of 16 rows x 64 tokens is 144 vector instructions, 16 of them
-// exponentials at a quarter of the rate, against 16 matrix ones, and the longest request's 64 tiles
-// follow each other at 1.1 to 1.3 us.  4096 rows, 32 heads to 8 of 128, before 8192 tokens: 510 us,
-// 810 TFLOP/s.
+// Measured (kernel times).  64 requests of up to 8192 tokens, 32 heads to 8 of 128: 128 us, 5.3 TB/s of
+// codes, and 4.7 for the join (139 and none with a workgroup per request and head).  1 x 10240 tokens, 32
+// heads: 21 us and 4; the bytes are 15 at 5.5 TB/s.  2 x 5 rows, 32 heads to 4, before up to 131071
+// tokens: 49 us and 7; the bytes are 40.  4 prompts of 475 to 1000 rows, 24 heads to 8 of 64, before up
+// to 4096 tokens: 89 us, 450 TFLOP/s: a wave's tile of 16 rows x 64 tokens is 195 vector
+// instructions (counted, unpacking and all else among them), 16 of them exponentials at a quarter of
+// the rate, against 16 matrix ones, and the longest request's 64 tiles follow each other at 1.1 to 1.3 us.  4096 rows, 32 heads to 8 of 128,
+// before 8192 tokens, the whole call: 434 us, 950 TFLOP/s.
 #include "serve_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -857,8 +857,8 @@ __global__ __launch_bounds__(WAVES * 64, 512 / (WAVES * 64)) void kv_block_atten
         p = load_parts(page);
         page = load_page(base + 2 * kTile);
         barrier();
-        // (a wave with products goes before those of other workgroups that still unpack codes: 510 against
-        // 530 us for 4096 rows before 8192 tokens, 107 against 116 for 64 x 5 rows before 4096, but 77
+        // (a wave with products goes before those of other workgroups that still unpack codes: 4% at 4096
+        // rows before 8192 tokens, 107 against 116 us for 64 x 5 rows before 4096, but 77
         // against 74 for 4 x 1024 rows; with two buffers 85 against 80 for 12 heads, so not there)
         __builtin_amdgcn_s_setprio(1);
         if (base < high) products(base, now, lds[0]);
@@ -1072,27 +1072,26 @@ __global__ __launch_bounds__(kJoinThreads) void kv_block_combine_kernel(BlockAtt
   }
 }
 
-// How a batch is cut, from sizes the host knows (lengths are the device's).  Up to 16 query rows per
-// cached head (32 at 64 channels) the few-rows kernel: at 5 rows of 8 heads it would need three row
-// tiles and spill.  Above, a workgroup takes 64 rows, or 128 if there are more: at 64 channels in
-// eight waves of 16 (85 against 97 us for four of 32 on 4 prompts of 475..1000 rows: more waves to
-// hide the softmax's latency), at 128 in four waves of 32 (535 against 605 us on 4096 rows before
-// 8192 tokens: an LDS read feeds two products).
-//
-// Few rows: equal shares for 256 workgroups, up to 512 where there are as many requests (32768 tokens,
-// 8 heads: 174 us uncut, 22.1 by 256, 24.1 by 512, 30.8 by 1024; 256 requests of up to 2000 tokens, 8 heads:
-// 119 us by 512, 127 by 256, 139 by 2048).  Each adds up the lengths, some have a second request to
-// begin, and a join costs 5 us, so a batch is cut only where its workgroups leave CUs idle for longer
-// than that (1.3 us a unit; 24 requests of 2048, 8 heads: 12.4 us uncut, 17.5 cut), or where the table has
-// room for a request that would go on long after the others: 64 requests, 8 heads, one of 16384 tokens
-// and 200 in the others: 85 us uncut, 28 cut; up to 8192: 139, 130; 500 each: 16.7, 19.6 (1000 of up to 1000,
-// 2 heads: 29, 45, so where the requests alone fill the chip twice the room must be more).
-// More rows: cut so that the workgroups fit the chip at once, if the tiles saved (1.2 us each) take
-// longer than the join (6 us and its bytes at 4 TB/s): 2 x 5 rows before 131071 tokens 91 us in 32
-// chunks, 66 in 64, 60 in 96; 2 prompts of 1024 rows, 12 heads: 22.7 us uncut, 30 in two.  Up to 64 rows
-// (drafts) under a table of more tokens than 4096 have chunks of 4096, for the same reason as above: 64
-// requests of 5 rows, 8 heads, one of 32768 tokens and 300 in the others: 603 us uncut, 91 cut (55 by
-// 2048); 500 each: 19.8, 26.8 (32.5).  For prompts the parts would be too many bytes.
+// How a batch is cut, from sizes the host knows (lengths are the device's).  The kernel is one for the
+// whole call, by the most rows that any request has: one prompt among decoding requests takes them all
+// through the kernel of more rows, so a program calls once for each kind.
+//  - Up to 16 query rows per cached head (32 at 64 channels): the few-rows kernel; more would spill.
+//    Above, a workgroup takes 64 rows, or 128 if there are more: at 64 channels in eight waves of 16 (4
+//    prompts of 475..1000 rows 85 us, 97 in four of 32: more waves hide the softmax's latency), at 128
+//    in four waves of 32 (13% at 4096 rows before 8192 tokens: an LDS read feeds two products).
+//  - Few rows: equal shares for 256 workgroups, up to 512 where there are as many requests (one request
+//    of 32768 tokens, 8 heads: 174 us uncut, 22.1 by 256, 24.1 by 512).  A join costs 5 us, so only
+//    where uncut workgroups leave CUs idle for longer (1.3 us a unit; 24 requests of 2048, 8 heads: 12.4
+//    us uncut, 17.5 cut), or where the table has room for a request that goes on long after the others
+//    (64 requests, 8 heads, one of 16384 tokens and 200 in the others: 85 us uncut, 30 cut; 500 in all:
+//    17, 22); the room must be more where the requests alone fill the chip twice.
+//  - More rows: cut so that the workgroups fit the chip at once, if the tiles saved (1.2 us each) take
+//    longer than the join (6 us and its bytes at 4 TB/s): 2 x 5 rows before 131071 tokens 91 us in 32
+//    chunks, 60 in 96; 2 prompts of 1024 rows, 12 heads: 22.7 us uncut, 30 in two.  Up to 64 rows
+//    (drafts) under a table of more than 4096 tokens: chunks of 4096, or larger ones so that there are
+//    at most as many as a join of few rows takes (64 requests of 5 rows, 8 heads, one of 32768 tokens and
+//    300 in the others: 603 us uncut, 101 cut; 500 in all: 20, 28).  For prompts the parts would be too
+//    many bytes.
 struct Split {
   bool few;
   int rt, groups;

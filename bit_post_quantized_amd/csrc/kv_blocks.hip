@@ -218,10 +218,10 @@ hipError_t launch_kv_block_release(const int32_t* seq, const uint8_t* done, int 
 //  - A long run (a prompt's block) takes the whole workgroup: its rows are read once, 8 channels
 //    and 4 consecutive rows to a thread and step, all loads before the largest magnitude is known;
 //    K's codes are stored as they are, V's go through LDS to become rows of tokens.
-// 20000 rows of 8 x 128 (82 MB in, 41 MB out) take 31 us, 4 TB/s: the loads alone 21, the coding 2
-// of the rest.  Measured: non-temporal stores 28 us, but the read of the codes that follows takes
-// 3 us longer; K and V in workgroups of their own the same; a clamp and float conversions in the
-// coding 45 us.
+// 20000 rows of 8 x 128 (82 MB in, 41 MB out) take 33 to 35 us, 3.6 TB/s: the loads alone 21, the
+// coding 2 of the rest.  Measured: non-temporal stores 3 us less, but the read of the codes that
+// follows takes 3 us more; K and V in workgroups of their own the same; a clamp and float conversions in
+// the coding 14 us more.
 constexpr int kAppendThreads = 256;
 constexpr int kShort = 4;
 
@@ -330,7 +330,7 @@ __device__ __forceinline__ v4u rescale16(v4u w, float ratio, int n) {
 
 // The codes of a block's first `off` tokens under a grown scale: K's rows or V's rows of tokens, the
 // 16-byte pieces i, i + step, ... of them, AHEAD loads in flight.  (One token each to 64 x 8 blocks of
-// 127 that all grow: 37 us, 135 with a dword at a time; without growth 6.)
+// 127 that all grow: 42 us, 135 with a dword at a time; without growth 6.)
 template <int D, bool V, int AHEAD>
 __device__ __forceinline__ void rescale_block(uint8_t* codes, int bs, int off, float ratio, int i, int step) {
   const int per = (off + 15) / 16, all = V ? D * per : off * D / 16;  // V: pieces of a channel

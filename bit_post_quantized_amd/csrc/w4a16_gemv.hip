@@ -20,10 +20,12 @@
 //  3. w4a16_sum_kernel, where K was cut over workgroups: the sum of their shares.
 //
 // Measured (kernel times): 1 row, 4096 x 131072: 45 us, 6.3 TB/s of weights, the memory's rate.
-// 1 row, 4096 x 4096, rank 32: 4.7 + 5.6 us, of which the weights' bytes are 1.7: two launches and
-// the latency of each one's first loads.  8 rows, 4096 x 12288: 4.8 + 10.9 us (bytes 4.9).  24 fp32
-// rows, 12288 x 4096, rank 48: 6.8 + 18 + 3.9 us; the vector work of unpacking and scaling for six
-// matrix products per group and the low-rank branch (6 us of the three) bound that.
+// 1 row, 4096 x 4096, rank 32: 4.9 + 6.7 us, of which the weights' bytes are 1.7: two launches and
+// the latency of each one's first loads.  8 rows, 4096 x 12288: 4.9 + 10.7 us (bytes 4.9).  24 fp32
+// rows, 12288 x 4096, rank 48: 7.0 + 18.4 + 3.9 us, without the branch 4.7 + 14.9 + 4.0: the workgroups
+// of the first share of K add up all of T and do the branch, the others do none of it; of the rest
+// about 5 us are the instructions' issue and 5 the weights' bytes, at two waves to a SIMD that wait for
+// them on 6 or 7 tiles.  64 rows, 4096 x 12288, rank 32: 5.5 + 19.5 + 4.5 us, without 4.2 + 17.3 + 4.0.
 #include "serve_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -114,7 +116,7 @@ constexpr int groups_per_wave(int tiles) { return tiles <= 2 ? 8 : 4; }
 // hold of X^, it is cut into chunks.  With one row tile a workgroup walks over them all and reads X^
 // again (12288 x 4096, rank 32: 1 row 16.1 us, cut 18.3; 16 rows 18.7, cut 20.3); with more, where
 // that is most of what it reads, the workgroups of a column tile take one chunk each and their sums
-// go through memory, shares (64 rows 31 us, read again 39).
+// go through memory, shares (64 rows 29 us, read again 39).
 struct W4a16Pass {
   int rows, shares, grid;
   bool loop;

@@ -14,7 +14,7 @@ a graph.
 A decoding step is many small launches, so the host's share counts.  The tensors an object keeps
 are checked when it is made and their pointers kept; a call checks its own tensors in a few
 comparisons and passes them on, and whatever does not pass goes through ``serve_binding``, which
-names what is wrong.  (Plans of 8 requests one after the other: 6.8 us each, 13.3 through the
+names what is wrong.  (Plans of 8 requests one after the other: 5.9 us each, 13.3 through the
 checks of ``serve_binding``.)
 """
 from __future__ import annotations
@@ -253,7 +253,11 @@ class BlockCache:
                   cu_rows: torch.Tensor, max_rows: int, causal: bool = True,
                   sm_scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
                   workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
-        """q bf16 [rows, heads, dim] -> [rows, heads, dim]; sm_scale 1/sqrt(dim) by default."""
+        """q bf16 [rows, heads, dim] -> [rows, heads, dim]; sm_scale 1/sqrt(dim) by default.
+
+        ``max_rows`` chooses the kernel for all requests, so a batch of decoding requests and
+        prompts is faster as a call for each kind (63 requests decoding before up to 8192 tokens
+        and a prompt of 500 rows: 765 us in one call, 168 in two)."""
         shape, dev = q.shape, self.device
         rows, heads, dim = shape
         n, width = block_tables.shape

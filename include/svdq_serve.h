@@ -74,8 +74,9 @@ int svdq_pack_w4a16(const uint8_t* wq, const uint16_t* w_scales, int N, int K, u
  *   0 <= M <= 64 (more rows: svdq_w4a4_gemm), 1 <= N <= 2^24, K % 64 == 0,
  *   64 <= K <= 64 * 65535, 0 <= r <= 128, r % 16 == 0.
  * For SVDQ_OUT_BF16 an activation enters the products rounded to 11 significant bits, for
- * SVDQ_OUT_FP32 to 22 (of values within 2^24 of the largest of its row's 512); every product with
- * a 4-bit code is exact and every sum is in fp32.
+ * SVDQ_OUT_FP32 to 22 (of values within 2^24 of the largest of its row's 512), and T's sums enter
+ * the second product of the low-rank branch with 16 or 24; every product with a 4-bit code is exact
+ * and every sum is in fp32.  A row with a NaN is NaN, one with an infinity has no finite output.
  */
 size_t svdq_w4a16_workspace_bytes(int M, int N, int K, int r, int out_dtype);
 int svdq_w4a16_gemv(const uint16_t* X, const float* inv_lambda, const uint16_t* L1p,
@@ -169,7 +170,9 @@ int kv_block_read(const int64_t* slots, int rows, int kv_heads, int dim, int blo
  * over the tokens t < seq_lens[b], and with `causal` only t <= seq_lens[b] - n + j for the j-th
  * of the request's n rows (also where the batch's `rows` end before the last of them).  A row with
  * no token gives 0; rows at or behind cu_rows[requests] are left as they were; tokens of a block whose
- * table entry is outside [0, num_blocks) are left out.
+ * table entry is outside [0, num_blocks) are left out.  Scores, maxima, sums and outputs are in fp32; a
+ * weight enters the product with V rounded to fp16 (11 bits, of weights times V scale down to 2^-24 of
+ * the row's largest; what is below 2^-35 of it counts in the sum alone).
  * Blocks' V scales may lie as far apart as appends can make them, zero and subnormal ones among
  * them: one under 2^-80 of the largest of the request's and head's blocks may count as that, which
  * moves an output by less than 2^-64 of the largest |V|.  A block that an append gave a NaN or infinite
@@ -178,7 +181,8 @@ int kv_block_read(const int64_t* slots, int rows, int kv_heads, int dim, int blo
  *   block_tables   int32 [requests, width];  seq_lens  int32 [requests] (clamped to
  *            [0, width bs]);  cu_rows  int32 [requests + 1], ascending
  *   max_rows the most rows that any request has (a request's rows beyond it are left as they
- *            were); 1 for plain decoding
+ *            were); 1 for plain decoding.  It chooses the kernel for the whole batch: decoding
+ *            requests and prompts in one call cost several times what a call for each kind does
  *   out      bf16 [rows, heads, dim]  16B
  *   workspace   device scratch of kv_block_attention_workspace_bytes(...) bytes (16B; may be
  *            NULL when that is 0), no initialization needed, rewritten by every call; calls that
