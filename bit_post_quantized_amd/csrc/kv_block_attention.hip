@@ -194,8 +194,8 @@ struct Runs {
 // codes then add 127 2^-80 of the largest scale at most, and it sets no maximum that matters).  So a term
 // of the sum lies between 2^-20 and 2^80 times its weight, whatever normal or subnormal numbers the
 // scales are; the exponential, logarithm and reciprocal see normal numbers only.  Where a new unit would
-// take a sum past 2^100 (a row of tiny scales beside one that does not see the large ones), the row's
-// maximum rises instead: its weights then stand for less than 2^-64 of the largest scale.
+// take a sum past 2^100 (a row of tiny scales beside one that sees the large ones), the row's maximum
+// rises instead: its n weights of up to 2^14 then give less than n 2^-86 of the largest value.
 constexpr int kFirstUnit = -126, kLastUnit = 126;
 constexpr float kLeastScale = 0x1p-80f;
 constexpr float kFullSum = 100.0f;  // log2

@@ -175,7 +175,7 @@ int kv_block_read(const int64_t* slots, int rows, int kv_heads, int dim, int blo
  * the row's largest; what is below 2^-35 of it counts in the sum alone).
  * Blocks' V scales may lie as far apart as appends can make them, zero and subnormal ones among
  * them: one under 2^-80 of the largest of the request's and head's blocks may count as that, which
- * moves an output by less than 2^-64 of the largest |V|.  A block that an append gave a NaN or infinite
+ * moves an output by less than 2^-56 of the largest |V|.  A block that an append gave a NaN or infinite
  * scale makes the rows that see it NaN, and no others.
  *   q        bf16 [rows, heads, dim], 16B, rows q_stride elements apart (as k_stride)
  *   block_tables   int32 [requests, width];  seq_lens  int32 [requests] (clamped to
