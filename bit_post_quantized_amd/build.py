@@ -28,7 +28,8 @@ OBJDIR = os.path.join(ROOT, "_build", "obj")
 ARCH = "gfx950"
 SOURCES = ["abi.cpp", "pack_weights.hip", "act_quant.hip", "w4a4_gemm.hip", "w4a4_gemm_e3m2.hip",
            "kv_int8.hip", "kv_attention.hip", "abi_serve.cpp", "w4a16_gemv.hip", "kv_blocks.hip",
-           "kv_block_attention.hip"]
+           "kv_block_attention.hip", "abi_decoder.cpp", "norm_rows.hip", "w8a8_gemm.hip", "rope.hip",
+           "sample.hip"]
 PEAKS_SOURCES = ["peaks.hip"]
 CFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

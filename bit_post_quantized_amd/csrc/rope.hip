@@ -1,0 +1,113 @@
+// Rotary positions on the heads of q and k.
+//
+// A pair's angle is position * frequency: at position 2^20 an fp32 product is off by a sixteenth of a
+// radian, so it is formed in fp64, in half turns, and its whole turns are taken off there; what is
+// left, in [-1, 1] half turns, goes through fp32 sines and cosines.  They are the same for all heads
+// of a row, so a workgroup computes a row's pairs once into LDS, and its threads then turn the heads:
+// each takes 8 channels and, in the half layout, the 8 that they are paired with.
+#include "decoder_launch.hpp"
+#include "svdq_device.hpp"
+
+namespace svdq {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxGrid = 1 << 20;  // workgroups of a launch: fewer than 2^32 threads
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* v) {
+  if constexpr (sizeof(T) == 4) {
+    const v4f a = reinterpret_cast<const v4f*>(p)[0], b = reinterpret_cast<const v4f*>(p)[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+  } else {
+    const v4u a = *reinterpret_cast<const v4u*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(a[i] << 16);
+      v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+template <typename X, bool INTERLEAVED>
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeRows a, int group, int per_row) {
+  extern __shared__ float2 turns[];  // [group][rot / 2]: (cos, sin) times scale
+  const int half = a.rot / 2;
+  for (int64_t row0 = (int64_t)blockIdx.x * group; row0 < a.rows; row0 += (int64_t)gridDim.x * group) {
+    const int rows = (int)min((int64_t)group, a.rows - row0);
+    for (int i = threadIdx.x; i < rows * half; i += kThreads) {
+      const int r = i / half;
+      const double t = (double)a.positions[row0 + r] * (a.freqs[i - r * half] * 0.31830988618379067154);
+      float sn, cs;
+      sincospif((float)(t - 2.0 * rint(0.5 * t)), &sn, &cs);
+      turns[i] = make_float2(cs * a.scale, sn * a.scale);
+    }
+    __syncthreads();
+    // an item: 8 pairs of a head (the half layout's 8 + 8 channels, or 16 in a row), or 8 channels that
+    // are only copied; per_row items of a row, heads of q first
+    const int pairs = half / 8, rest = (a.dim - a.rot) / 8, per_head = pairs + rest;
+    for (int i = threadIdx.x; i < rows * per_row; i += kThreads) {
+      const int r = i / per_row, j = i - r * per_row;
+      const int h = j / per_head, p = j - h * per_head;
+      const int which = h >= a.heads[0];
+      const int head = which ? h - a.heads[0] : h;
+      const X* in = reinterpret_cast<const X*>(a.in[which]) + (row0 + r) * a.in_stride[which] + head * a.dim;
+      __bf16* out = reinterpret_cast<__bf16*>(a.out[which]) + (row0 + r) * a.out_stride[which] + head * a.dim;
+      float u[8], v[8];
+      if (p < pairs) {
+        const float2* cs = turns + r * half + 8 * p;
+        const int c0 = INTERLEAVED ? 16 * p : 8 * p, c1 = INTERLEAVED ? c0 + 8 : c0 + half;
+        load8(in + c0, u);
+        load8(in + c1, v);
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 t0 = cs[e], t1 = cs[4 + e];
+            const float a0 = u[2 * e], b0 = u[2 * e + 1], a1 = v[2 * e], b1 = v[2 * e + 1];
+            u[2 * e] = a0 * t0.x - b0 * t0.y;
+            u[2 * e + 1] = a0 * t0.y + b0 * t0.x;
+            v[2 * e] = a1 * t1.x - b1 * t1.y;
+            v[2 * e + 1] = a1 * t1.y + b1 * t1.x;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float2 t = cs[e];
+            const float x = u[e], y = v[e];
+            u[e] = x * t.x - y * t.y;
+            v[e] = x * t.y + y * t.x;
+          }
+        }
+        *reinterpret_cast<v8bf*>(out + c0) = to_bf16x8(u);
+        *reinterpret_cast<v8bf*>(out + c1) = to_bf16x8(v);
+      } else {
+        const int c = a.rot + 8 * (p - pairs);
+        load8(in + c, u);
+        *reinterpret_cast<v8bf*>(out + c) = to_bf16x8(u);
+      }
+    }
+    __syncthreads();  // the next rows' pairs take these ones' place
+  }
+}
+
+template <typename X, bool INTERLEAVED>
+void launch(const RopeRows& a, hipStream_t st) {
+  const int half = a.rot / 2;
+  // rows of a workgroup: one while that fills the device, else as many as its threads have pairs
+  int group = 1;
+  while (group < 8 && 2 * group * half <= kThreads && a.rows >= 4096 * group) group *= 2;
+  const int per_row = (a.heads[0] + a.heads[1]) * (half / 8 + (a.dim - a.rot) / 8);
+  hipLaunchKernelGGL((rope_kernel<X, INTERLEAVED>), dim3(min((a.rows + group - 1) / group, kMaxGrid)), dim3(kThreads),
+                     group * half * sizeof(float2), st, a, group, per_row);
+}
+
+}  // namespace
+
+hipError_t launch_rope(const RopeRows& a, int x_fp32, hipStream_t stream) {
+  if (x_fp32) a.interleaved ? launch<float, true>(a, stream) : launch<float, false>(a, stream);
+  else a.interleaved ? launch<__bf16, true>(a, stream) : launch<__bf16, false>(a, stream);
+  return hipGetLastError();
+}
+
+}  // namespace svdq
