@@ -13,6 +13,8 @@
 namespace svdq {
 namespace {
 
+typedef int v16i __attribute__((ext_vector_type(16)));
+
 constexpr int kUnit = 1024;  // 16 columns x 64 k of the container
 
 __device__ __forceinline__ v4i mfma(v4i w, v4i x, v4i acc) {
@@ -23,6 +25,15 @@ template <int N>
 struct Count {
   static constexpr int value = N;
 };
+
+// A value that is the same in every lane, in scalar registers (a buffer's base and size have to be).
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+template <typename P>
+__device__ __forceinline__ P* uniform(P* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<P*>((uint64_t)hi << 32 | lo);
+}
 
 struct Output {
   const float* sx;
@@ -156,105 +167,310 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t base, uint8_t
   __builtin_amdgcn_raw_ptr_buffer_load_lds(base, SVDQ_LDS(to), 16, offset, 0, 0, 0);
 }
 
-// s_waitcnt vmcnt(0) lgkmcnt(0): the loads into LDS have landed, the reads from it are done
-#define SVDQ_WAIT_LDS() __builtin_amdgcn_s_waitcnt(7 << 4)
+// the same with 4, and with 2 bytes (a dword each), to `to` + 4 lane
+__device__ __forceinline__ void load_to_lds4(__amdgpu_buffer_rsrc_t base, uint8_t* to, uint32_t offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(base, SVDQ_LDS(to), 4, offset, 0, 0, 0);
+}
+__device__ __forceinline__ void load_to_lds2(__amdgpu_buffer_rsrc_t base, uint8_t* to, uint32_t offset) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(base, SVDQ_LDS(to), 2, offset, 0, 0, 0);
+}
+// 16 bytes per lane, none past the buffer's end
+__device__ __forceinline__ void store_16(__amdgpu_buffer_rsrc_t base, v4u v, uint32_t offset) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, base, offset, 0, 0);
+}
 
-// A workgroup has a TM x TN tile of Y and WM x WN waves; K in stages of 128, two of them in LDS, filled
-// by loads that go straight there: while one is computed the next is on its way.
-//   X stage: rows of 128 bytes as in memory, their eight pieces of 16 bytes exchanged by the row
-//     (slot p of row r holds piece p ^ (r % 8)): a load of 64 lanes then reads eight whole rows, and an
-//     operand's read, 16 rows of the same piece, meets every bank equally.
-//   W stage: units of the container as they are, each an operand.
-// Reads past the last row or tile of columns are cut off by the buffers' sizes and give 0.
-template <int TM, int TN, int WM, int WN, bool F32>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2)))
-void w8a8_tile_kernel(const int8_t* __restrict__ qx, const int8_t* __restrict__ container, int K,
-                      Output o, int split, int32_t* __restrict__ partial) {
-  constexpr int WAVES = WM * WN, kA = TM * 128, kB = TN * 128, kStage = kA + kB;
-  constexpr int RT = TM / WM / 16, CT = TN / WN / 16;   // tiles of a wave
-  constexpr int kLoadsA = kA / 1024 / WAVES, kLoadsB = kB / 1024 / WAVES;
+// s_waitcnt vmcnt(0) lgkmcnt(0): the loads into LDS have landed, the reads from it are done
+#define SVDQ_WAIT_LDS() SVDQ_WAIT_LDS_AND(0)
+// the same but for the n newest loads; the loads alone
+#define SVDQ_WAIT_LDS_AND(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | (7 << 4))
+#define SVDQ_WAIT_LOADS(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8))
+
+// Tiles of 64 RT x 64 WN by 2 x WN waves of 32 RT x 64, persistent workgroups that go from tile to tile.
+// K in units of 64, four of them in LDS: one stream of units that runs on over the tiles, so that the next
+// tile's first units are on their way while a tile is stored.  A step computes a unit in halves of k: during
+// the first the operands of the second are read from LDS; then a barrier (unit u + 1 has landed, unit u is
+// read: its place takes u + 4); during the second those of the next unit.  The order of matrix instructions,
+// reads and loads is the written one.
+//
+// With K divided (`split` shares of a tile, in a row) the shares' sums go to `partial`, [split][M][pitch].
+constexpr int kPlaces = 4;      // units in LDS
+constexpr int kScratch = 4096;  // LDS of a wave, for scales and stores
+enum { kBf16, kFp32, kPartial };
+
+struct Problem {
+  const int8_t* qx;
+  const int8_t* container;
+  int M, N, K, split;
+  const float* sx;
+  const float* sw;
+  const uint16_t* bias;
+  void* Y;   // or the partial sums
+};
+
+// Item `l` of nx x ny tiles times `split` shares, in the order of xcd_tile_order: workgroup l runs on XCD
+// l % 8, and each XCD has a run of items, those of the first share first and, in bands of 8 row tiles, the
+// row tile fastest, so that neighbours have their weights, and then their rows, in one L2.
+struct Item {
+  int mt, nt, share, first, end;   // the tile, and the share's units
+};
+__device__ __forceinline__ Item item_at(int l, int nx, int ny, int split, int G) {
+  constexpr int kBand = 8;
+  const int tiles = nx * ny, items = tiles * split, i8 = items / 8 * 8;
+  if (l < i8) l = (l % 8) * (items / 8) + l / 8;
+  const int share = l / tiles;
+  l -= share * tiles;
+  const int b = l / (kBand * nx), rows = min(ny - b * kBand, kBand), within = l - b * kBand * nx;
+  return {uniform(b * kBand + within % rows), uniform(within / rows), uniform(share), uniform((int)((int64_t)G * share / split)),
+          uniform((int)((int64_t)G * (share + 1) / split))};
+}
+
+// What the loads bring next: a unit of an item (a share of a tile), and where it goes.  All of it is uniform.
+template <int TM, int TN>
+struct Stream {
+  const int8_t* ax;
+  const int8_t* bw;
+  int item, unit, end, place;
+  int a_left, b_left;   // bytes to the end of the operand, 0 behind the last item
+
+  __device__ __forceinline__ void start(const Problem& p, int items, int nx, int ny) {
+    a_left = b_left = unit = 0;
+    end = 1;
+    if (item >= items) return;
+    const int G = p.K / 64;
+    const Item i = item_at(item, nx, ny, p.split, G);
+    unit = i.first;
+    end = i.end;
+    ax = p.qx + (size_t)i.mt * TM * p.K + unit * 64;
+    bw = p.container + ((size_t)i.nt * (TN / 16) * G + unit) * kUnit;
+    a_left = min(p.M - i.mt * TM, TM) * p.K - unit * 64;
+    b_left = min((p.N + 15) / 16 - i.nt * (TN / 16), TN / 16) * G * kUnit - unit * kUnit;
+  }
+  __device__ __forceinline__ void advance(const Problem& p, int items, int nx, int ny) {
+    place = (place + 1) & (kPlaces - 1);
+    ax += 64;
+    bw += kUnit;
+    a_left = max(a_left - 64, 0);
+    b_left = max(b_left - kUnit, 0);
+    if (++unit == end) {
+      item += gridDim.x;
+      start(p, items, nx, ny);
+    }
+  }
+};
+
+template <int RT, int WN, int OUT>
+__global__ __launch_bounds__(128 * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void w8a8_tile_kernel(Problem p) {
+  constexpr int TM = 64 * RT, TN = 64 * WN, WAVES = 2 * WN, kA = TM * 64, kStage = kA + TN * 64;
+  constexpr int kLoadsA = TM / 16 / WAVES, kLoadsB = TN / 16 / WAVES, kLoads = kLoadsA + kLoadsB;  // of a wave
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int G = K / 64, S = (G + 1) / 2, tiles = (o.N + 15) / 16;
-  int mt, nt;
-  xcd_tile_order(8, mt, nt);
-  const int m0 = mt * TM, n0 = nt * TN;
-  const int s0 = (int)((int64_t)S * blockIdx.z / split), s1 = (int)((int64_t)S * (blockIdx.z + 1) / split);
+  const int G = p.K / 64;
+  const int nx = (p.N + TN - 1) / TN, ny = (p.M + TM - 1) / TM, items = nx * ny * p.split;
 
-  const int8_t* ax = qx + (size_t)m0 * K;
-  const int8_t* bw = container + (size_t)(n0 / 16) * G * kUnit;
-  const int a_bytes = min(o.M - m0, TM) * K, b_bytes = min(tiles - n0 / 16, TN / 16) * G * kUnit;
+  // ---- the stream of units.  X: rows of 64 bytes as in memory, a load has 16 of them; their four pieces of
+  //      16 bytes are exchanged (slot s of row r holds piece s ^ (r / 4) % 4), so that an operand's read, the
+  //      same piece of 32 rows, meets every bank equally.  W: units of the container as they are.
   uint32_t a_off[kLoadsA], b_off[kLoadsB];
 #pragma unroll
-  for (int j = 0; j < kLoadsA; ++j) {
-    const int r = 8 * (j * WAVES + wave) + lane / 8;
-    a_off[j] = (uint32_t)r * K + 16 * ((lane & 7) ^ (r & 7));
-  }
+  for (int j = 0; j < kLoadsA; ++j)
+    a_off[j] = (uint32_t)(16 * (WAVES * j + wave) + (lane >> 2)) * p.K + 16 * ((lane & 3) ^ (lane >> 4));
 #pragma unroll
-  for (int j = 0; j < kLoadsB; ++j) {
-    const int i = j * WAVES + wave;
-    b_off[j] = (uint32_t)(i / 2) * G * kUnit + (i & 1) * kUnit + lane * 16;
-  }
-  auto issue = [&](int s) {
-    uint8_t* st = lds + (s & 1) * kStage;
-    const __amdgpu_buffer_rsrc_t ra = buffer_rsrc(ax + s * 128, a_bytes - s * 128);
-    const __amdgpu_buffer_rsrc_t rb = buffer_rsrc(bw + (size_t)s * 2 * kUnit, b_bytes - s * 2 * kUnit);
-#pragma unroll
-    for (int j = 0; j < kLoadsA; ++j)
-      load_to_lds(ra, st + (j * WAVES + wave) * 1024, a_off[j]);
-#pragma unroll
-    for (int j = 0; j < kLoadsB; ++j)
-      load_to_lds(rb, st + kA + (j * WAVES + wave) * 1024, b_off[j]);
+  for (int j = 0; j < kLoadsB; ++j) b_off[j] = (uint32_t)(WAVES * j + wave) * G * kUnit + lane * 16;
+  Stream<TM, TN> next;
+  next.item = blockIdx.x;
+  next.place = 0;
+  next.start(p, items, nx, ny);
+  auto issue = [&](int j) __attribute__((always_inline)) {
+    uint8_t* st = lds + next.place * kStage;
+    if (j < kLoadsA) load_to_lds(buffer_rsrc(next.ax, next.a_left), st + (WAVES * j + wave) * 1024, a_off[j < kLoadsA ? j : 0]);
+    else load_to_lds(buffer_rsrc(next.bw, next.b_left), st + kA + (WAVES * (j - kLoadsA) + wave) * 1024,
+                     b_off[j < kLoadsA ? 0 : j - kLoadsA]);
   };
 
-  v4i acc[RT][CT] = {};
-  const int a_row = (wm * RT * 16 + (lane & 15)) * 128;
-  const int a_piece = lane >> 4, a_turn = lane & 7;
-  const int b_at = kA + wn * CT * 2 * kUnit + lane * 16;
-  auto unit = [&](const uint8_t* st, int u) {
-    v4i xf[RT], wf[CT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) wf[c] = *reinterpret_cast<const v4i*>(st + b_at + (2 * c + u) * kUnit);
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-      xf[r] = *reinterpret_cast<const v4i*>(st + a_row + r * 16 * 128 + 16 * ((4 * u + a_piece) ^ a_turn));
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int c = 0; c < CT; ++c) acc[r][c] = mfma(wf[c], xf[r], acc[r][c]);
+  // ---- operands from LDS: lane l has row l % 32 at k = 16 (l / 32) .. + 15 of 32
+  const int a0 = (wm * 32 * RT + (lane & 31)) * 64 + 16 * ((lane >> 5) ^ ((lane >> 2) & 3));
+  const int b0 = kA + (wn * 4 + ((lane >> 4) & 1)) * kUnit + ((lane & 15) + 16 * (lane >> 5)) * 16;
+  struct Frag {
+    v4i x[RT], w[2];
   };
-  if (s0 < s1) issue(s0);
-  for (int s = s0; s < s1; ++s) {
-    // stage s has landed for every wave, and every wave has read stage s - 1
-    SVDQ_WAIT_LDS();
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (s + 1 < s1) issue(s + 1);
-    const uint8_t* st = lds + (s & 1) * kStage;
-    unit(st, 0);
-    if (2 * s + 1 < G) unit(st, 1);   // (an odd number of units: the last stage has one)
-    asm volatile("" ::: "memory");
+  auto read = [&](const uint8_t* st, int h, int r, Frag& f) __attribute__((always_inline)) {
+    if (r < 2) f.w[r] = *reinterpret_cast<const v4i*>(st + b0 + 512 * h + r * 2 * kUnit);
+    else if (r < RT + 2) f.x[r - 2] = *reinterpret_cast<const v4i*>(st + (a0 ^ (32 * h)) + (r - 2) * 2048);
+  };
+  v16i acc[RT][2] = {};
+  auto product = [&](int i, int j, const Frag& f) __attribute__((always_inline)) {
+    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(f.w[j], f.x[i], acc[i][j], 0, 0, 0);
+  };
+
+  // ---- a tile's scales, into the wave's scratch: sx of its rows, sw and bias of its 64 columns
+  constexpr int kScaleLoads = OUT == kPartial ? 0 : 3 + (RT > 2);
+  uint8_t* scratch = lds + kPlaces * kStage + wave * kScratch;
+  auto issue_scales = [&](int m0, int n0, int lane) __attribute__((always_inline)) {
+    const int rows = uniform(max(min(p.M - m0, 32 * RT), 0)), columns = uniform(max(min(p.N - n0, 64), 0));
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(uniform(p.sx + min(m0, p.M)), rows * 4);
+    const __amdgpu_buffer_rsrc_t rw = buffer_rsrc(uniform(p.sw + min(n0, p.N)), columns * 4);
+    load_to_lds4(rx, scratch, lane * 4);
+    if constexpr (RT > 2) load_to_lds4(rx, scratch + 256, 256 + lane * 4);
+    load_to_lds4(rw, scratch + 512, lane * 4);
+    // (without a bias something as long is loaded, so that the loads in flight can be counted)
+    if (p.bias) load_to_lds2(buffer_rsrc(uniform(p.bias + min(n0, p.N)), columns * 2), scratch + 768, lane * 2);
+    else load_to_lds4(rw, scratch + 768, lane * 4);
+  };
+
+#pragma unroll
+  for (int u = 0; u < kPlaces; ++u) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) issue(j);
+    next.advance(p, items, nx, ny);
   }
+  Frag f0, f1;
+  static_assert((kPlaces - 1) * kLoads < 64, "loads that can be counted");
+  SVDQ_WAIT_LOADS((kPlaces - 1) * kLoads);
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int m = m0 + (wm * RT + r) * 16 + (lane & 15);
-    if (m < o.M) {
+  for (int r = 0; r < RT + 2; ++r) read(lds, 0, r, f0);
+
+  constexpr int kSize = OUT == kBf16 ? 2 : 4, kPer = 16 / kSize;   // bytes; columns of a piece of 16 bytes
+  constexpr int kPasses = OUT == kBf16 ? 1 : 2;                    // of a wave's 64 columns
+  constexpr int kStores = 4 * RT * kPasses;                        // of a tile, per wave
+  constexpr int kBehind = (kPlaces - 2) * kLoads + kScaleLoads + kStores;
+  constexpr int kPair = (kLoads + RT - 1) / RT, kReads = (RT + 2 + RT - 1) / RT;  // behind two matrix instructions
+  const int64_t pitch = OUT == kPartial ? (p.N + 15) / 16 * 16 : p.N;
+  const bool whole = pitch % kPer == 0;                            // Y's rows begin at pieces
+  int at = 0;                                                      // the place that is computed
+  int units_before = 0;
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const Item it = item_at(item, nx, ny, p.split, G);
+    const int units = it.end - it.first, m0 = it.mt * TM + wm * 32 * RT, n0 = it.nt * TN + wn * 64;
+    // a tile's first steps follow the stores of the one before, and wait for units that were sent for
+    // earlier than these
+    int behind = whole && units_before >= kPlaces && units >= kPlaces ? 3 : 0;
+    units_before = units;
+    // (kept from the compiler, which would compute the addresses of the store before the loop and keep them
+    // in registers that it does not have)
+    int lane_ = lane;
+    asm volatile("" : "+v"(lane_));
+    if constexpr (OUT != kPartial) issue_scales(m0, n0, lane_);
+    for (int u = 0; u < units; ++u) {
+      const uint8_t* st = lds + at * kStage;
+      at = (at + 1) & (kPlaces - 1);
+      const uint8_t* after = lds + at * kStage;
 #pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        const int n = n0 + (wn * CT + c) * 16 + 4 * (lane >> 4);
-        if (n < o.N) {
-          if (split == 1) {
-            store4<F32>(o, m, n, acc[r][c]);
-          } else {
-            // (partials have rows of whole tiles, so that four columns are one store)
-            const size_t pitch = (size_t)tiles * 16;
-            *reinterpret_cast<v4i*>(partial + ((size_t)blockIdx.z * o.M + m) * pitch + n) = acc[r][c];
+      for (int c = 0; c < RT; ++c) {
+        product(c, c & 1, f0);
+        product(c, 1 - (c & 1), f0);
+#pragma unroll
+        for (int r = 0; r < kReads; ++r) read(st, 1, kReads * c + r, f1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // the next unit has landed for every wave, and every wave has read this one
+      if (behind > 0) {
+        --behind;
+        SVDQ_WAIT_LDS_AND(kBehind < 63 ? kBehind : 63);
+      } else {
+        SVDQ_WAIT_LDS_AND((kPlaces - 2) * kLoads);
+      }
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = 0; c < RT; ++c) {
+        product(c, c & 1, f1);
+        product(c, 1 - (c & 1), f1);
+#pragma unroll
+        for (int r = 0; r < kReads; ++r) read(after, 0, kReads * c + r, f0);
+#pragma unroll
+        for (int j = 0; j < kPair; ++j)
+          if (kPair * c + j < kLoads) issue(kPair * c + j);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      next.advance(p, items, nx, ny);
+      asm volatile("" ::: "memory");
+    }
+
+    // ---- the tile's store.  A matrix instruction leaves four columns of one row in a lane; stored from
+    //      there, a store would touch 32 rows with 16 bytes each.  A wave turns 32 rows at a time over in
+    //      its scratch (4-byte results: 32 columns of them) and stores rows of 128 bytes; the pieces of a
+    //      row are exchanged by the row.
+    asm volatile("" : "+v"(lane_));
+    float sx[RT];
+    v4f sw[2][4];
+    v2u bias[2][4];   // packed as they are
+    if constexpr (OUT != kPartial) {
+      if (units < kPlaces) SVDQ_WAIT_LOADS(0);   // (so few steps have not waited for the scales)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) sx[i] = *reinterpret_cast<const float*>(scratch + (32 * i + (lane_ & 31)) * 4);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = 32 * j + 8 * e + 4 * (lane_ >> 5);
+          sw[j][e] = *reinterpret_cast<const v4f*>(scratch + 512 + c * 4);
+          const v4u b = *reinterpret_cast<const v4u*>(scratch + 768 + c * 4);
+          bias[j][e] = v2u{b.x | b.y << 16, b.z | b.w << 16};
+        }
+    }
+    uint8_t* base = reinterpret_cast<uint8_t*>(p.Y) + (size_t)it.share * p.M * pitch * kSize;
+    uint8_t* to = scratch + (lane_ & 31) * 128;
+    const int r8 = lane_ >> 3, p8 = lane_ & 7;   // row and piece of a store's lane
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const int m = m0 + 32 * i;
+      const __amdgpu_buffer_rsrc_t ry =
+          buffer_rsrc(uniform(base + ((size_t)min(m, p.M) * pitch + min(n0, p.N)) * kSize), 0x7FFFFFFF);
+#pragma unroll
+      for (int half = 0; half < kPasses; ++half) {
+#pragma unroll
+        for (int j = kPasses == 2 ? half : 0; j < (kPasses == 2 ? half + 1 : 2); ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const v4i sum = {acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+            if constexpr (OUT == kPartial) {
+              *reinterpret_cast<v4i*>(to + 16 * ((2 * e + (lane_ >> 5)) ^ (lane_ & 7))) = sum;
+            } else {
+              float y[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                y[q] = ((float)sum[q] * sx[i]) * sw[j][e][q];
+                const uint32_t b = bias[j][e][q >> 1];
+                if (p.bias) y[q] += __uint_as_float(q & 1 ? b & 0xFFFF0000u : b << 16);
+              }
+              if constexpr (OUT == kFp32) {
+                *reinterpret_cast<v4f*>(to + 16 * ((2 * e + (lane_ >> 5)) ^ (lane_ & 7))) = v4f{y[0], y[1], y[2], y[3]};
+              } else {
+                v2u w;
+                w.x = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{y[0], y[1]}), v2bf));
+                w.y = __builtin_bit_cast(uint32_t, __builtin_convertvector((v2f{y[2], y[3]}), v2bf));
+                *reinterpret_cast<v2u*>(to + 16 * ((4 * j + e) ^ (lane_ & 7)) + 8 * (lane_ >> 5)) = w;
+              }
+            }
+          }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int r = 8 * g + r8, n = n0 + 32 * half + p8 * kPer;
+          const v4u v = *reinterpret_cast<const v4u*>(scratch + r * 128 + 16 * (p8 ^ (r & 7)));
+          if (whole) {   // (past the end of Y: past the buffer's)
+            store_16(ry, v, m + r < p.M && n < p.N ? (uint32_t)(r * pitch + 32 * half + p8 * kPer) * kSize : ~0u);
+          } else if (m + r < p.M) {
+#pragma unroll
+            for (int q = 0; q < kPer; ++q)
+              if (n + q < p.N) {
+                if constexpr (kSize == 4) reinterpret_cast<uint32_t*>(base)[(size_t)(m + r) * pitch + n + q] = v[q];
+                else reinterpret_cast<uint16_t*>(base)[(size_t)(m + r) * pitch + n + q] = (uint16_t)(v[q / 2] >> (16 * (q & 1)));
+              }
           }
         }
       }
     }
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = v16i{};
   }
+  SVDQ_WAIT_LOADS(0);   // (the loads past the end bring nothing, but write to LDS)
 }
 
 // Y from the partial sums of `split` workgroups.
@@ -276,20 +492,36 @@ constexpr int kFewRows = 64;
 constexpr int kCus = 256;
 
 struct Plan {
-  int tile;    // 0: few rows
+  int rt, wn;   // a tile of 64 rt x 64 wn; 0: few rows
   int split;
 };
 
 Plan plan(int M, int N, int K) {
-  if (M <= kFewRows) return {0, 1};
-  const int64_t big = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
-  if (big >= kCus) return {256, 1};
-  // tiles of 128, K divided where they are fewer than two per CU and a share keeps 4 stages
-  const int64_t small = (int64_t)((M + 127) / 128) * ((N + 127) / 128);
-  const int S = (K / 64 + 1) / 2;
-  int64_t split = 2 * kCus / small;
-  if (split > S / 4) split = S / 4;
-  return {128, split < 1 ? 1 : (int)split};
+  if (M <= kFewRows) return {0, 0, 1};
+  // The tile and the division of K with the least time, by what a unit of K costs a CU with each tile (ns,
+  // measured where all CUs are busy: small tiles read LDS and L2 more often for the same products) times the
+  // items that the busiest CU has; divided sums cost a launch and are written and read once more.  Measured,
+  // us, 256 x 256 / 128 x 256 / 128 x 128 / 64 x 128, with the best division: 1000 x 4096 x 8192 (M, K, N)
+  // 52 / 38 / 43 / 51, 2000 x 8192 x 4096 89 / 67 / 78 / 104, 500 x 12288 x 4096 48 / 40 / 41 / 45 (undivided
+  // 116 / 69 / 53 / 49), 128 x 4096 x 4096 23 / 19 / 16 / 15, 300 x 8192 x 28672 107 / 111 / 108 / 123.
+  static const struct { int rt, wn; double ns; } kTiles[] = {{4, 4, 860}, {2, 4, 510}, {2, 2, 290}, {1, 2, 240}};
+  const int G = K / 64;
+  Plan best{4, 4, 1};
+  double least = 1e30;
+  for (const auto& t : kTiles) {
+    const int64_t tiles = (int64_t)((M + 64 * t.rt - 1) / (64 * t.rt)) * ((N + 64 * t.wn - 1) / (64 * t.wn));
+    for (int split = 1; split <= 8; split *= 2) {
+      if (split > 1 && (tiles * split > 2 * kCus || G < 8 * split)) break;
+      const int64_t rounds = (tiles * split + kCus - 1) / kCus;
+      double ns = (double)rounds * ((G + split - 1) / split) * t.ns;
+      if (split > 1) ns += 4000 + ((double)M * N * (8 * split + 4)) / 5500;
+      if (ns < least) {
+        least = ns;
+        best = {t.rt, t.wn, split};
+      }
+    }
+  }
+  return best;
 }
 
 template <int RT, int CT, int WAVES>
@@ -307,31 +539,31 @@ void launch_few_rows(const int8_t* qx, const int8_t* container, int K, const Out
   else launch_few<RT, 1, 16>(qx, container, K, o, f32, st);
 }
 
-template <int T, int WM, int WN, bool F32>
-hipError_t launch_tile(const int8_t* qx, const int8_t* container, int K, const Output& o, int split, int32_t* ws,
-                 hipStream_t st) {
-  constexpr int kLds = 2 * 2 * T * 128;
-  // two stages need more than the default 64 KB of LDS
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(w8a8_tile_kernel<T, T, WM, WN, F32>),
+template <int RT, int WN, int OUT>
+hipError_t launch_tile(const Problem& p, hipStream_t st) {
+  constexpr int kLds = kPlaces * (RT + WN) * 4096 + 2 * WN * kScratch;
+  constexpr int kPerCu = 160 * 1024 / kLds;
+  // more than the default 64 KB of LDS
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(w8a8_tile_kernel<RT, WN, OUT>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (e != hipSuccess) return e;
-  const dim3 grid((o.N + T - 1) / T, (o.M + T - 1) / T, split);
-  hipLaunchKernelGGL((w8a8_tile_kernel<T, T, WM, WN, F32>), grid, dim3(64 * WM * WN), kLds, st, qx, container, K, o,
-                     split, ws);
+  const int64_t items = (int64_t)((p.N + 64 * WN - 1) / (64 * WN)) * ((p.M + 64 * RT - 1) / (64 * RT)) * p.split;
+  const int grid = items < kCus * kPerCu ? (int)items : kCus * kPerCu;
+  hipLaunchKernelGGL((w8a8_tile_kernel<RT, WN, OUT>), dim3(grid), dim3(128 * WN), kLds, st, p);
   return hipGetLastError();
 }
 
-template <bool F32>
-hipError_t launch_many(const int8_t* qx, const int8_t* container, int K, const Output& o, const Plan& p, int32_t* ws,
-                 hipStream_t st) {
-  if (p.tile == 256) return launch_tile<256, 2, 4, F32>(qx, container, K, o, 1, ws, st);
-  const hipError_t e = launch_tile<128, 2, 2, F32>(qx, container, K, o, p.split, ws, st);
+template <int RT, int WN>
+hipError_t launch_many(const Problem& problem, int out_fp32, const Output& o, int32_t* ws, hipStream_t st) {
+  Problem p = problem;
+  if (p.split == 1) return out_fp32 ? launch_tile<RT, WN, kFp32>(p, st) : launch_tile<RT, WN, kBf16>(p, st);
+  p.Y = ws;
+  const hipError_t e = launch_tile<RT, WN, kPartial>(p, st);
   if (e != hipSuccess) return e;
-  if (p.split > 1) {
-    const int64_t quads = (int64_t)((o.N + 15) / 16) * 4 * o.M, blocks = (quads + 255) / 256;
-    hipLaunchKernelGGL((w8a8_join_kernel<F32>), dim3((int)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, st, ws,
-                       p.split, o);
-  }
+  const int64_t quads = (int64_t)((o.N + 15) / 16) * 4 * o.M, blocks = (quads + 255) / 256;
+  const dim3 grid((int)(blocks < 4096 ? blocks : 4096));
+  if (out_fp32) hipLaunchKernelGGL((w8a8_join_kernel<true>), grid, dim3(256), 0, st, ws, p.split, o);
+  else hipLaunchKernelGGL((w8a8_join_kernel<false>), grid, dim3(256), 0, st, ws, p.split, o);
   return hipGetLastError();
 }
 
@@ -356,19 +588,20 @@ hipError_t launch_w8a8_gemm(const int8_t* qx, const float* sx, const int8_t* con
                             hipStream_t stream) {
   const Output o{sx, sw, bias, Y, M, N};
   const Plan p = plan(M, N, K);
-  if (p.tile == 0) {
+  if (p.rt == 0) {
     switch ((M + 15) / 16) {
       case 1: launch_few_rows<1>(qx, container, K, o, out_fp32, stream); break;
       case 2: launch_few_rows<2>(qx, container, K, o, out_fp32, stream); break;
       case 3: launch_few_rows<3>(qx, container, K, o, out_fp32, stream); break;
       default: launch_few_rows<4>(qx, container, K, o, out_fp32, stream); break;
     }
-  } else if (out_fp32) {
-    return launch_many<true>(qx, container, K, o, p, static_cast<int32_t*>(workspace), stream);
-  } else {
-    return launch_many<false>(qx, container, K, o, p, static_cast<int32_t*>(workspace), stream);
+    return hipGetLastError();
   }
-  return hipGetLastError();
+  const Problem q{qx, container, M, N, K, p.split, sx, sw, bias, Y};
+  int32_t* ws = static_cast<int32_t*>(workspace);
+  if (p.rt == 4) return launch_many<4, 4>(q, out_fp32, o, ws, stream);
+  if (p.rt == 1) return launch_many<1, 2>(q, out_fp32, o, ws, stream);
+  return p.wn == 4 ? launch_many<2, 4>(q, out_fp32, o, ws, stream) : launch_many<2, 2>(q, out_fp32, o, ws, stream);
 }
 
 }  // namespace svdq

@@ -37,6 +37,7 @@ def run(case, dtype, **more):
     (65, 64, 1, True), (65, 192, 127, False), (100, 64 * 9, 128, True), (128, 128, 129, False), (129, 64 * 31, 257, True),
     (200, 64 * 64, 300, False), (257, 64 * 3, 1000, True), (500, 64 * 40, 130, True), (255, 64 * 100, 64, False),
     (3000, 64 * 3, 5000, True), (4097, 128, 4095, False), (70, 64 * 150, 20, True),
+    (4099, 64, 4104, True), (4200, 64 * 5, 4001, True), (4352, 64 * 4, 4096, False), (16400, 64 * 7, 1020, True),
 ])
 def test_matches_bit_for_bit(gpu_lib, M, K, N, bias, dtype):
     case = make(M * 7919 + K + N, M, K, N, bias)
