@@ -6,17 +6,17 @@
 //
 // The limits keep the first elements in the order of falling logits, lower indices first among equal
 // ones: with the 64-bit keys (logit's ordered bits, ~index), all different, that is "key >= cut", and
-// nothing needs to be sorted.  Four launches over (chunk of the vocabulary, row):
-//   max     the chunk's largest logit; clears what the next one adds to
-//   mass    the weights: without limits the chunk's sum, else 2048 bins over (zmax - z) / temperature,
-//           counts where top-k is on, sums where only top-p is
-//   gather  from the bins, the one that the limit falls into; the chunk's elements that may be cut go
-//           to the row's list (top-k: all down to that bin; top-p: that bin's, and the sum of what lies
-//           above it is kept per chunk)
-//   draw    a workgroup per row: the cut by bins over the list's keys, narrowed until a bin has one
-//           element; the chunk in which the drawn number falls; the element in it
+// nothing needs to be sorted.  Launches over (chunk of the vocabulary, row):
+//   max     largest logits of up to 512 parts of the row
+//   mass    top-k: the k-th largest part holds an element that k - 1 others reach or pass, so the k first are among
+//           the elements that reach it: hardly more than k, which go to the row's list with their weights.
+//           Only top-p: 2048 bins of the weights over (zmax - z) / temperature, per chunk.
+//           No limit: the weights' sum per chunk
+//   gather  only top-p: the elements of the bin that the limit falls into go to the row's list
+//   draw    a workgroup per row.  Top-k: everything from the list.  Otherwise the cut from the list, the
+//           chunk in which the drawn number falls, and the element in it
 // A list that would not fit (many equal logits, a top-k of thousands) is not used: `draw` then narrows
-// over the row itself, more slowly.
+// down the cut by bins over the row itself, more slowly.
 #include "decoder_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -27,44 +27,46 @@ typedef unsigned long long u64;
 
 constexpr int kUnitBits = 40;
 constexpr double kSpan = 28.5;        // exp(-28.5) 2^40 rounds to 0
-constexpr int kBins = 2048;
-constexpr int kCap = 2048;            // elements of a row's list
-constexpr int kMaxChunk = 16384, kMinChunk = 1024;
-constexpr int kMaxChunks = 512;       // of a row
-constexpr int kThreads = 256, kDrawThreads = 1024;
+constexpr int kBins = 2048, kCoarse = 64, kFine = kBins / kCoarse;
+constexpr int kCap = 4096;            // elements of a row's list
+constexpr int kPairs = 256;           // as many are compared each with each
+constexpr int kParts = 512;           // of a row, at most
+constexpr int kMaxChunks = 64;        // of a row
+constexpr int kThreads = 512;
+constexpr int kAhead = 2;             // pieces of 16 bytes that a thread loads before it knows the settings
 constexpr uint32_t kNanKey = 0xFFFFFFFFu, kNoneKey = 0x007FFFFFu;  // -infinity's
-
-struct Entry {
-  u64 key;
-  u64 w;
-};
 
 struct Sizes {
   int chunks, chunk;   // of a row; elements of a chunk
+  int parts;           // of a chunk: a power of two
 };
 
 Sizes sizes(int rows, int vocab) {
-  // about four workgroups per CU, chunks of 1024 to 16384 elements
+  // about four workgroups per CU, of 2048 elements or more
   int chunks = (1024 + rows - 1) / rows;
-  const int most = (vocab + kMinChunk - 1) / kMinChunk, least = (vocab + kMaxChunk - 1) / kMaxChunk;
+  const int most = (vocab + 2047) / 2048;
   if (chunks > most) chunks = most;
   if (chunks > kMaxChunks) chunks = kMaxChunks;
-  if (chunks < least) chunks = least;
   int chunk = (vocab + chunks - 1) / chunks;
-  chunk = (chunk + 7) / 8 * 8;
-  return {(vocab + chunk - 1) / chunk, chunk};
+  chunk = (chunk + 3) / 4 * 4;
+  chunks = (vocab + chunk - 1) / chunk;
+  int parts = kParts;
+  while (parts * chunks > kParts) parts /= 2;
+  return {chunks, chunk, parts};
 }
 
-// The workspace: per row and chunk a maximum and a sum, per row the bins, the list and its length.
+// The workspace of `rows` rows: per chunk its parts' maxima, a sum, the bins and the sums of each kFine of
+// them; per row the list and its length.
 struct Space {
-  uint32_t* top;     // [rows, chunks]
+  uint32_t* top;     // [rows, chunks, parts]
   u64* sum;          // [rows, chunks]
-  u64* bins;         // [rows, kBins]
-  Entry* list;       // [rows, kCap]
+  u64* bins;         // [rows, chunks, kBins]
+  u64* coarse;       // [rows, chunks, kCoarse]
+  u64* list;         // [rows, kCap], keys
   uint32_t* length;  // [rows]
 };
 
-size_t place(Space& s, void* ws, int rows, int chunks) {
+size_t place(Space& s, void* ws, int rows, const Sizes& z) {
   uint8_t* p = static_cast<uint8_t*>(ws);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -72,13 +74,20 @@ size_t place(Space& s, void* ws, int rows, int chunks) {
     at += (bytes + 15) / 16 * 16;
     return q;
   };
-  const size_t r = rows;
-  s.list = reinterpret_cast<Entry*>(take(r * kCap * sizeof(Entry)));
-  s.bins = reinterpret_cast<u64*>(take(r * kBins * 8));
-  s.sum = reinterpret_cast<u64*>(take(r * chunks * 8));
-  s.top = reinterpret_cast<uint32_t*>(take(r * chunks * 4));
+  const size_t r = rows, c = r * z.chunks;
+  s.list = reinterpret_cast<u64*>(take(r * kCap * 8));
+  s.bins = reinterpret_cast<u64*>(take(c * kBins * 8));
+  s.coarse = reinterpret_cast<u64*>(take(c * kCoarse * 8));
+  s.sum = reinterpret_cast<u64*>(take(c * 8));
+  s.top = reinterpret_cast<uint32_t*>(take(c * z.parts * 4));
   s.length = reinterpret_cast<uint32_t*>(take(r * 4));
   return at;
+}
+
+// Rows that are done at a time: their chunks' bins are 16 KB each.
+int batch(int rows, const Sizes& z) {
+  const int most = 4096 / z.chunks;
+  return rows < most ? rows : most;
 }
 
 // ---------------------------------------------------------------- values
@@ -86,6 +95,51 @@ template <typename T>
 __device__ __forceinline__ float logit(const T* p, int64_t i) {
   return (float)p[i];
 }
+
+// The elements [begin, end) of a row, 16 bytes of neighbours per thread at a time (of any alignment).  `U`
+// such pieces are loaded when the object is made, so that they are under way while other things are waited
+// for; then f(element, index) for all.
+template <int U, typename T>
+struct Elements {
+  static constexpr int E = 16 / sizeof(T);
+  struct __attribute__((packed, aligned(sizeof(T)))) Piece {
+    T v[E];
+  };
+  const T* p;
+  int begin, end;
+  Piece q[U];
+
+  __device__ __forceinline__ Elements(const T* row, int first, int last) : p(row), begin(first), end(last) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = begin + E * (threadIdx.x + u * kThreads);
+      if (i + E <= end) q[u] = *reinterpret_cast<const Piece*>(p + i);
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = begin + E * (threadIdx.x + u * kThreads);
+      if (i + E <= end) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) f((float)q[u].v[e], i + e);
+      } else {
+        for (int j = i; j < end; ++j) f((float)p[j], j);
+      }
+    }
+#pragma unroll 2
+    for (int i = begin + E * (threadIdx.x + U * kThreads); i < end; i += E * kThreads) {
+      if (i + E <= end) {
+        const Piece more = *reinterpret_cast<const Piece*>(p + i);
+#pragma unroll
+        for (int e = 0; e < E; ++e) f((float)more.v[e], i + e);
+      } else {
+        for (int j = i; j < end; ++j) f((float)p[j], j);
+      }
+    }
+  }
+};
 
 // ordered bits: greater floats have greater keys; both zeros the same
 __device__ __forceinline__ uint32_t order_key(float z) {
@@ -96,6 +150,7 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 __device__ __forceinline__ u64 full_key(float z, int i) { return (u64)order_key(z) << 32 | (uint32_t)~i; }
+__device__ __forceinline__ int index_of(u64 key) { return (int)~(uint32_t)key; }
 
 struct Row {
   double zmax, inv;       // largest logit, 1 / temperature
@@ -119,10 +174,12 @@ __device__ __forceinline__ int bin_of(double x) {   // x in [-kSpan, 0]
 }
 
 // rne(2^40 exp(x)), x in [-kSpan, 0]: x = n ln 2 + r, exp(r) by its series to r^12 (|r| < 0.347: the rest
-// is under 2^-52), and the whole number out of the sum with 2^52, whose last bit is 1.
+// is under 2^-52).  n is rounded by an addition in whose sum it is the low bits, the power of two is added to
+// the exponent, and the whole number is read out of the sum with 2^52, whose last bit is 1.
 __device__ __forceinline__ u64 weight(double x) {
-  const double n = rint(x * 1.4426950408889634074);
-  const double r = __builtin_fma(-n, 0.69314718055994530942, x);
+  constexpr double kRound = 0x1.8p52;
+  const double t = __builtin_fma(x, 1.4426950408889634074, kRound);
+  const double r = __builtin_fma(-(t - kRound), 0.69314718055994530942, x);
   double e = 1.0 / 479001600.0;
   e = __builtin_fma(e, r, 1.0 / 39916800.0);
   e = __builtin_fma(e, r, 1.0 / 3628800.0);
@@ -136,27 +193,24 @@ __device__ __forceinline__ u64 weight(double x) {
   e = __builtin_fma(e, r, 0.5);
   e = __builtin_fma(e, r, 1.0);
   e = __builtin_fma(e, r, 1.0);
-  const double v = ldexp(e, (int)n + kUnitBits) + 0x1p52;
-  return (u64)__double_as_longlong(v) & 0xFFFFFFFFFFFFFull;
+  const int n = (int)__double_as_longlong(t) + kUnitBits;   // (the sum's low word)
+  const double scaled = __longlong_as_double(__double_as_longlong(e) + ((long long)n << 52));
+  return (u64)__double_as_longlong(scaled + 0x1p52) & 0xFFFFFFFFFFFFFull;
 }
 __device__ __forceinline__ u64 weight_of(const Row& R, float z) {
   const double x = R.arg(z);
   return x < -kSpan ? 0 : weight(x);
 }
+__device__ __forceinline__ u64 weight_of(const Row& R, u64 key) { return weight_of(R, key_value((uint32_t)(key >> 32))); }
 
 // ---------------------------------------------------------------- workgroup sums
-template <int T>
-__device__ __forceinline__ uint32_t group_max(uint32_t v, uint32_t* slots) {
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
   for (int d = 32; d; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
-  __syncthreads();
-  for (int i = 0; i < T / 64; ++i) v = max(v, slots[i]);
   return v;
 }
 
-// Sum of v over the threads before this one; `all` is the whole sum.
-template <int T>
+// Sum of v over the threads before this one; `all` is the whole sum.  `slots` has kThreads / 64 places.
 __device__ __forceinline__ u64 group_scan(u64 v, u64* slots, u64& all) {
   const u64 mine = (u64)wave_scan((long long)v);
   const int w = threadIdx.x >> 6;
@@ -165,33 +219,77 @@ __device__ __forceinline__ u64 group_scan(u64 v, u64* slots, u64& all) {
   __syncthreads();
   u64 before = 0;
   all = 0;
-  for (int i = 0; i < T / 64; ++i) {
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) {
     const u64 s = slots[i];
     if (i < w) before += s;
     all += s;
   }
   return before + mine - v;
 }
+__device__ __forceinline__ u64 group_sum(u64 v, u64* slots) {
+  u64 all;
+  group_scan(v, slots, all);
+  return all;
+}
 
-// The row's settings, the same in every workgroup of the row.  T threads.
-template <int T>
-__device__ __forceinline__ Row row_of(const SampleRows& a, const Space& s, int chunks, int row, uint32_t* slots) {
-  uint32_t top = 0;
-  for (int c = threadIdx.x; c < chunks; c += T) top = max(top, s.top[(size_t)row * chunks + c]);
-  Row R;
-  R.top = group_max<T>(top, slots);
-  R.zmax = (double)key_value(R.top);
-  const float t = a.temperature[row];
-  R.greedy = !(t > 0.0f);
-  R.inv = 1.0 / (double)t;
-  R.k = a.top_k ? a.top_k[row] : 0;
+// What a workgroup shares of its row: the parts' maxima, and room to agree on one.
+struct Shared {
+  uint32_t tops[kParts], most[kThreads / 64], least;
+  u64 coarse[kThreads / 64][kCoarse];
+};
+
+// The row's settings, the same in every workgroup of the row.
+__device__ __forceinline__ Row row_of(const SampleRows& a, const Space& s, const Sizes& z, int row, Shared& L) {
+  static_assert(kThreads == kParts, "a part for each thread");
+  const int n = z.chunks * z.parts, t = threadIdx.x;
+  const uint32_t mine = t < n ? s.top[(size_t)row * n + t] : 0u;
+  const float temperature = a.temperature[row];
+  const int k = a.top_k ? a.top_k[row] : 0;
   const float p = a.top_p ? a.top_p[row] : 1.0f;
-  R.p = p;
-  R.by_count = R.k > 0;
-  R.by_mass = p < 1.0f;
   const float m = a.min_p ? a.min_p[row] : 0.0f;
+  L.tops[t] = mine;
+  const uint32_t most = wave_max(mine);
+  if ((t & 63) == 0) L.most[t >> 6] = most;
+  __syncthreads();
+  Row R;
+  R.top = 0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) R.top = max(R.top, L.most[i]);
+  R.zmax = (double)key_value(R.top);
+  R.greedy = !(temperature > 0.0f);
+  R.inv = 1.0 / (double)temperature;
+  R.k = k;
+  R.p = p;
+  R.by_count = k > 0;
+  R.by_mass = p < 1.0f;
   R.least_w = m > 0.0f ? (double)fminf(m, 1.0f) * 0x1p40 : 0.0;
   return R;
+}
+
+// What the k-th largest of a wave's 512 values reaches, and hardly more do: the 13 leading bits in which
+// the values (those that are not 0; `top` is the largest) differ, bit by bit.  0 where there are fewer than k.
+__device__ __forceinline__ uint32_t kth_largest(const uint32_t (&v)[8], uint32_t top, int k) {
+  uint32_t low = top;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (v[i]) low = min(low, v[i]);
+    n += __popcll(__ballot(v[i] != 0u));
+  }
+  if (n < k) return 0u;
+  for (int d = 32; d; d >>= 1) low = min(low, (uint32_t)__shfl_xor((int)low, d));
+  const int bits = __builtin_amdgcn_readfirstlane(32 - __clz((int)(low ^ top | 1u)));
+  uint32_t found = __builtin_amdgcn_readfirstlane(bits < 32 ? top >> bits << bits : 0u);
+#pragma unroll 1
+  for (int bit = bits - 1; bit >= max(bits - 13, 0); --bit) {
+    const uint32_t trial = found | 1u << bit;
+    n = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n += __popcll(__ballot(v[i] >= trial));
+    if (n >= k) found = trial;
+  }
+  return found;
 }
 
 // whether the limit lies at or before what sums up to `through`
@@ -202,188 +300,226 @@ __device__ __forceinline__ bool crossed(bool by_count, u64 through, int k, doubl
 // ---------------------------------------------------------------- launches
 template <typename T>
 __global__ __launch_bounds__(kThreads) void sample_max_kernel(SampleRows a, Space s, Sizes z) {
-  __shared__ uint32_t slots[kThreads / 64];
-  const int row = blockIdx.y, c = blockIdx.x;
-  if (a.top_k || a.top_p)
-    for (int b = c * kThreads + threadIdx.x; b < kBins; b += gridDim.x * kThreads) s.bins[(size_t)row * kBins + b] = 0;
-  if (c == 0 && threadIdx.x == 0) s.length[row] = 0;
+  const int row = blockIdx.y, c = blockIdx.x, t = threadIdx.x;
+  if (c == 0 && t == 0) s.length[row] = 0;
   const T* p = reinterpret_cast<const T*>(a.logits) + row * a.stride;
-  const int end = min(a.vocab, (c + 1) * z.chunk);
   uint32_t top = 0;
-#pragma unroll 8
-  for (int i = c * z.chunk + threadIdx.x; i < end; i += kThreads) {
-    const float v = logit(p, i);
-    top = max(top, v != v ? kNanKey : order_key(v));
-  }
-  top = group_max<kThreads>(top, slots);
-  if (threadIdx.x == 0) s.top[(size_t)row * z.chunks + c] = top;
+  const Elements<4, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
+  elements.each([&](float v, int) { top = max(top, v != v ? kNanKey : order_key(v)); });
+  // a part: what kThreads / parts neighbouring threads (at most a wave) have read
+  const int group = kThreads / z.parts;
+  for (int d = 1; d < group; d <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, d));
+  if (t % group == 0) s.top[((size_t)row * z.chunks + c) * z.parts + t / group] = top;
+}
+
+// Elements for a row's list, gathered in LDS first (2048 of a chunk: a chunk with more makes the list too
+// long).
+constexpr int kOfChunk = 2048;
+struct Gathered {
+  u64 key[kOfChunk];
+  uint32_t count, place;
+};
+__device__ __forceinline__ void gather(Gathered& L, float v, int i) {
+  const uint32_t at = atomicAdd(&L.count, 1u);
+  if (at < (uint32_t)kOfChunk) L.key[at] = full_key(v, i);
+}
+// (a length over kCap says that the list is not whole)
+__device__ __forceinline__ void append(Gathered& L, const Space& s, int row) {
+  __syncthreads();
+  const uint32_t n = L.count;
+  if (threadIdx.x == 0) L.place = n ? atomicAdd(&s.length[row], n > (uint32_t)kOfChunk ? kCap + 1u : n) : 0u;
+  __syncthreads();
+  const uint32_t first = L.place;
+  for (uint32_t i = threadIdx.x; i < min(n, (uint32_t)kOfChunk); i += kThreads)
+    if (first + i < (uint32_t)kCap) s.list[(size_t)row * kCap + first + i] = L.key[i];
 }
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void sample_mass_kernel(SampleRows a, Space s, Sizes z) {
-  __shared__ u64 bins[kBins];
+  __shared__ union {
+    u64 bins[kBins];
+    Gathered list;
+  } L;
   __shared__ u64 sums[kThreads / 64];
-  __shared__ uint32_t slots[kThreads / 64];
-  const int row = blockIdx.y, c = blockIdx.x;
-  const Row R = row_of<kThreads>(a, s, z.chunks, row, slots);
-  if (R.greedy || R.top == kNanKey || R.top <= kNoneKey) return;
+  __shared__ Shared S;
+  const int row = blockIdx.y, c = blockIdx.x, t = threadIdx.x;
   const T* p = reinterpret_cast<const T*>(a.logits) + row * a.stride;
-  const int end = min(a.vocab, (c + 1) * z.chunk);
-  if (!R.limited()) {
-    u64 sum = 0, all;
-#pragma unroll 4
-    for (int i = c * z.chunk + threadIdx.x; i < end; i += kThreads) {
-      const u64 w = weight_of(R, logit(p, i));
-      if ((double)w >= R.least_w) sum += w;
+  const Elements<kAhead, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
+  const Row R = row_of(a, s, z, row, S);
+  if (R.greedy || R.top == kNanKey || R.top <= kNoneKey) return;
+  const size_t at = (size_t)row * z.chunks + c;
+  if (R.by_count) {
+    if (t < 64) {
+      uint32_t tops[kParts / 64];
+#pragma unroll
+      for (int i = 0; i < kParts / 64; ++i) tops[i] = S.tops[64 * i + t];
+      const uint32_t least = kth_largest(tops, R.top, R.k);
+      if (t == 0) S.least = least, L.list.count = 0;
     }
-    group_scan<kThreads>(sum, sums, all);
-    if (threadIdx.x == 0) s.sum[(size_t)row * z.chunks + c] = all;
+    __syncthreads();
+    const uint32_t least = S.least;
+    elements.each([&](float v, int i) {
+      if (order_key(v) >= least) gather(L.list, v, i);
+    });
+    append(L.list, s, row);
     return;
   }
-  for (int b = threadIdx.x; b < kBins; b += kThreads) bins[b] = 0;
-  __syncthreads();
-#pragma unroll 4
-  for (int i = c * z.chunk + threadIdx.x; i < end; i += kThreads) {
-    const double x = R.arg(logit(p, i));
-    if (x >= -kSpan) {
-      const u64 w = weight(x);
-      if (w) atomicAdd(&bins[bin_of(x)], R.by_count ? 1ull : w);
-    }
+  if (!R.by_mass) {
+    u64 sum = 0;
+    elements.each([&](float v, int) {
+      const u64 w = weight_of(R, v);
+      sum += (double)w >= R.least_w ? w : 0;
+    });
+    sum = group_sum(sum, sums);
+    if (t == 0) s.sum[at] = sum;
+    return;
   }
+  for (int b = t; b < kBins; b += kThreads) L.bins[b] = 0;
   __syncthreads();
-  // what lies behind this chunk's own k-th element cannot hold the row's
-  u64 seen = 0, all;
-  constexpr int kPer = kBins / kThreads;
-  for (int j = 0; j < kPer; ++j) seen += bins[threadIdx.x * kPer + j];
-  seen = group_scan<kThreads>(seen, sums, all);
-  for (int j = 0; j < kPer; ++j) {
-    const int b = threadIdx.x * kPer + j;
-    const u64 n = bins[b];
-    if (n && !(R.by_count && seen >= (u64)R.k)) atomicAdd(&s.bins[(size_t)row * kBins + b], n);
-    seen += n;
-  }
-}
-
-// The first of kBins bins through which the limit is reached (kBins where none is), and what stands
-// before it, `base` and the bins in front of it.  T threads; sums has T / 64 + 1 places.
-template <int T>
-__device__ __forceinline__ int first_crossing(const u64* bins, bool by_count, int k, double least, u64 base, u64* sums,
-                                              int* found, u64& before) {
-  constexpr int kPer = kBins / T;
-  u64 n[kPer], mine = 0, all;
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) mine += n[j] = bins[threadIdx.x * kPer + j];
-  if (threadIdx.x == 0) *found = kBins;
-  u64 through = base + group_scan<T>(mine, sums, all), in_front = 0;
-  int b = kBins;
+  elements.each([&](float v, int) {
+    const double x = R.arg(v);
+    if (x >= -kSpan) atomicAdd(&L.bins[bin_of(x)], weight(x));
+  });
+  __syncthreads();
+  constexpr int kPer = kBins / kThreads;   // (kFine / kPer = 8 threads have a coarse bin)
+  u64 sum = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    if (b == kBins && n[j] && crossed(by_count, through + n[j], k, least)) {
-      b = threadIdx.x * kPer + j;
-      in_front = through;
-    }
-    through += n[j];
+    const u64 n = L.bins[t * kPer + j];
+    s.bins[at * kBins + t * kPer + j] = n;
+    sum += n;
   }
-  if (b < kBins) atomicMin(found, b);
-  __syncthreads();
-  const int first = *found;
-  if (b == first && b < kBins) sums[T / 64] = in_front;
-  __syncthreads();
-  before = sums[T / 64];
-  __syncthreads();
-  return first;
+  for (int d = 1; d < kFine / kPer; d <<= 1) sum += (u64)__shfl_xor((long long)sum, d);
+  if (t % (kFine / kPer) == 0) s.coarse[at * kCoarse + t / (kFine / kPer)] = sum;
 }
 
-// The bin that the row's limit falls into; top-p's share of the row's sum.
-template <int T>
-__device__ __forceinline__ int limit_bin(const Row& R, const u64* bins, u64* sums, int* found, double& least,
-                                         u64& before) {
-  least = 0.0;
-  if (!R.by_count) {
-    u64 mine = 0, all;
-    for (int b = threadIdx.x; b < kBins; b += T) mine += bins[b];
-    group_scan<T>(mine, sums, all);
-    least = R.p * (double)all;
+// Of a row's bins: those before `lo` stay whole, those behind `hi` go, the elements from lo to hi are looked
+// at; what stands before lo, and top-p's share of the row's sum.  The same in every thread.
+struct Limit {
+  int lo, hi;
+  u64 before;
+  double least;
+};
+__device__ __forceinline__ Limit limit_of(const Row& R, const Space& s, const Sizes& z, int row, Shared& L) {
+  constexpr int kWaves = kThreads / 64;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // sums over the chunks, each wave an eighth of them (`live`: lanes with a bin), in every wave
+  auto over_chunks = [&](const u64* first, size_t stride, bool live) {
+    u64 sum = 0;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < kMaxChunks / kWaves; ++i)
+        if (wave + i * kWaves < z.chunks) sum += first[(size_t)(wave + i * kWaves) * stride];
+    }
+    __syncthreads();
+    L.coarse[wave][lane] = sum;
+    __syncthreads();
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) sum += L.coarse[i][lane];
+    return sum;
+  };
+  u64 mine = over_chunks(s.coarse + (size_t)row * z.chunks * kCoarse + lane, kCoarse, true);
+  const u64 coarse_sum = mine, coarse_through = (u64)wave_scan((long long)mine);
+  const u64 all = (u64)__shfl((long long)coarse_through, 63);
+  // the sums of the bins of coarse bin cb, and what stands before each
+  auto fine = [&](int cb, u64& before) {
+    const u64 sum = over_chunks(s.bins + (size_t)row * z.chunks * kBins + cb * kFine + lane, kBins, lane < kFine);
+    before = (u64)__shfl((long long)(coarse_through - coarse_sum), cb) + (u64)wave_scan((long long)sum) - sum;
+    return sum;
+  };
+  Limit f{kBins, kBins, all, R.p * (double)all};
+  u64 over = __ballot(mine && !((double)coarse_through < f.least));
+  if (over) {
+    const int cb = __ffsll((unsigned long long)over) - 1;
+    u64 before;
+    mine = fine(cb, before);
+    over = __ballot(mine && !((double)(before + mine) < f.least));
+    const int b = __ffsll((unsigned long long)over) - 1;   // (there is one: the coarse bin reaches the limit)
+    f.lo = f.hi = cb * kFine + b;
+    f.before = (u64)__shfl((long long)before, b);
   }
-  return first_crossing<T>(bins, R.by_count, R.k, least, 0, sums, found, before);
+  if (R.least_w > 0.0) {
+    // min-p's border is at its logarithm: nearly always in one bin
+    const double x = fmax(log(R.least_w * 0x1p-40), -kSpan);
+    f.hi = min(f.hi, bin_of(fmax(x - 1e-6, -kSpan)));
+    const int m = bin_of(fmin(x + 1e-6, 0.0));
+    if (m < f.lo) {
+      f.lo = m;
+      u64 before;
+      fine(f.lo / kFine, before);
+      f.before = (u64)__shfl((long long)before, f.lo % kFine);
+    }
+  }
+  return f;
 }
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleRows a, Space s, Sizes z) {
-  __shared__ u64 sums[kThreads / 64 + 1];
-  __shared__ uint32_t slots[kThreads / 64];
-  __shared__ int found;
+  __shared__ Gathered L;
+  __shared__ Shared S;
   const int row = blockIdx.y, c = blockIdx.x;
-  const Row R = row_of<kThreads>(a, s, z.chunks, row, slots);
-  if (R.greedy || R.top == kNanKey || R.top <= kNoneKey || !R.limited()) return;
-  double least;
-  u64 above;
-  const int cut = limit_bin<kThreads>(R, s.bins + (size_t)row * kBins, sums, &found, least, above);
+  if (a.top_k && a.top_k[row] > 0) return;
   const T* p = reinterpret_cast<const T*>(a.logits) + row * a.stride;
-  const int end = min(a.vocab, (c + 1) * z.chunk);
-  u64 sum = 0, all;
-#pragma unroll 4
-  for (int i = c * z.chunk + threadIdx.x; i < end; i += kThreads) {
-    const float v = logit(p, i);
+  const Elements<kAhead, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
+  const Row R = row_of(a, s, z, row, S);
+  if (R.greedy || R.top == kNanKey || R.top <= kNoneKey || !R.by_mass) return;
+  const Limit f = limit_of(R, s, z, row, S);
+  if (f.lo == kBins) return;
+  if (threadIdx.x == 0) L.count = 0;
+  __syncthreads();
+  elements.each([&](float v, int i) {
     const double x = R.arg(v);
-    if (x < -kSpan) continue;
+    if (x < -kSpan) return;
     const int b = bin_of(x);
-    if (b > cut) continue;
-    const u64 w = weight(x);
-    if (!w) continue;
-    if (R.by_count || b == cut) {
-      const uint32_t at = atomicAdd(&s.length[row], 1u);
-      if (at < (uint32_t)kCap) s.list[(size_t)row * kCap + at] = Entry{full_key(v, i), w};
-    } else if ((double)w >= R.least_w) {
-      sum += w;
-    }
-  }
-  group_scan<kThreads>(sum, sums, all);
-  if (threadIdx.x == 0) s.sum[(size_t)row * z.chunks + c] = all;
+    if (b >= f.lo && b <= f.hi) gather(L, v, i);
+  });
+  append(L, s, row);
 }
 
 // ---------------------------------------------------------------- draw
-// The elements that a limit is looked for among: the row's list, or the row itself.
+struct DrawSpace {
+  union {
+    struct {
+      u64 key, w;
+    } pair[kPairs];
+    u64 list[kCap];
+  };
+  u64 bins[kBins];
+  uint32_t count[kBins];
+  u64 sums[kThreads / 64];
+  u64 chunk[kMaxChunks];
+  u64 lo, hi, before;
+  int found;
+};
+
+// The elements that a limit is looked for among: the row's list, or (list NULL) the row itself.
 template <typename T>
-struct Source {
-  const Entry* list;   // NULL: the row
+struct Among {
   const T* logits;
-  const Row* R;
+  const u64* list;
   int n;
 
   template <typename F>
   __device__ __forceinline__ void each(F f) const {
-    if (list) {
-      for (int i = threadIdx.x; i < n; i += kDrawThreads) f(list[i].key, list[i].w);
-    } else {
-      for (int i = threadIdx.x; i < n; i += kDrawThreads) {
-        const float v = logit(logits, i);
-        const u64 w = weight_of(*R, v);
-        if (w) f(full_key(v, i), w);
-      }
-    }
+    if (list)
+      for (int i = threadIdx.x; i < n; i += kThreads) f(list[i]);
+    else
+      for (int i = threadIdx.x; i < n; i += kThreads) f(full_key(logit(logits, i), i));
   }
 };
 
-struct DrawSpace {
-  u64 bins[kBins];
-  uint32_t count[kBins];
-  u64 sums[kDrawThreads / 64 + 1];
-  u64 chunk[kMaxChunks];
-  u64 lo, hi;
-  uint32_t slots[kDrawThreads / 64];
-  int found;
-};
-
-// The smallest key that stays, where those stay that come, from the greatest key down, before the
-// limit; `base` comes before all of them.  Only keys >= floor are looked at.  0 where all stay.
+// The smallest key that stays, where those stay that come, from the greatest key down, before the limit,
+// with `base` before all of them; `floor` where all that are >= floor stay (others are not looked at).
+// Bins over the keys, narrowed until the limit's bin has one element.
 template <typename T>
-__device__ u64 find_cut(const Source<T>& src, DrawSpace& L, bool by_count, int k, double least, u64 base, u64 floor) {
+__device__ __forceinline__ u64 find_cut(const Among<T>& among, const Row& R, DrawSpace& L, bool by_count, double least,
+                                     u64 base, u64 floor) {
   if (threadIdx.x == 0) L.lo = ~0ull, L.hi = 0;
   __syncthreads();
   u64 lo = ~0ull, hi = 0;
-  src.each([&](u64 key, u64) {
-    if (key >= floor) lo = min(lo, key), hi = max(hi, key);
+  among.each([&](u64 key) {
+    if (key >= floor && weight_of(R, key)) lo = min(lo, key), hi = max(hi, key);
   });
   if (lo <= hi) {
     atomicMin(&L.lo, lo);
@@ -397,21 +533,40 @@ __device__ u64 find_cut(const Source<T>& src, DrawSpace& L, bool by_count, int k
     const u64 range = hi - lo;
     const int bits = 64 - (range ? __clzll((long long)range) : 64), shift = bits > 11 ? bits - 11 : 0;
     __syncthreads();
-    for (int b = threadIdx.x; b < kBins; b += kDrawThreads) L.bins[b] = 0, L.count[b] = 0;
+    for (int b = threadIdx.x; b < kBins; b += kThreads) L.bins[b] = 0, L.count[b] = 0;
     if (threadIdx.x == 0) L.found = kBins;
     __syncthreads();
-    src.each([&](u64 key, u64 w) {
-      if (key >= lo && key <= hi) {
-        const int b = (int)((hi - key) >> shift);
-        atomicAdd(&L.bins[b], by_count ? 1ull : w);
-        atomicAdd(&L.count[b], 1u);
-      }
+    among.each([&](u64 key) {
+      if (key < lo || key > hi) return;
+      const u64 w = weight_of(R, key);
+      if (!w) return;
+      const int b = (int)((hi - key) >> shift);
+      atomicAdd(&L.bins[b], by_count ? 1ull : w);
+      atomicAdd(&L.count[b], 1u);
     });
     __syncthreads();
-    u64 before;
-    const int b = first_crossing<kDrawThreads>(L.bins, by_count, k, least, base, L.sums, &L.found, before);
+    // the first bin through which the limit is reached, and what stands before it
+    constexpr int kPer = kBins / kThreads;
+    u64 n[kPer], mine = 0, all;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) mine += n[j] = L.bins[threadIdx.x * kPer + j];
+    u64 through = base + group_scan(mine, L.sums, all), in_front = 0;
+    int first = kBins;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (first == kBins && n[j] && crossed(by_count, through + n[j], R.k, least)) {
+        first = threadIdx.x * kPer + j;
+        in_front = through;
+      }
+      through += n[j];
+    }
+    if (first < kBins) atomicMin(&L.found, first);
+    __syncthreads();
+    const int b = L.found;
     if (b == kBins) return floor;   // never reached: all stay
-    base = before;
+    if (first == b) L.before = in_front;
+    __syncthreads();
+    base = L.before;
     const uint32_t here = L.count[b];
     hi -= (u64)b << shift;
     const u64 width = (1ull << shift) - 1;
@@ -420,11 +575,23 @@ __device__ u64 find_cut(const Source<T>& src, DrawSpace& L, bool by_count, int k
   }
 }
 
+// The number that is drawn, of a sum of `total`.
+__device__ __forceinline__ u64 drawn(const SampleRows& a, int row, u64 total) {
+  const float u = a.uniform[row];
+  const u64 at = (u64)floor((double)total * (double)(u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f));
+  return at < total - 1 ? at : total - 1;
+}
+__device__ __forceinline__ void give(const SampleRows& a, int row, int token, u64 w, u64 total) {
+  a.tokens[row] = token;
+  if (a.share) a.share[row] = (float)((double)w / (double)total);
+}
+
 template <typename T>
-__global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleRows a, Space s, Sizes z) {
+__global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleRows a, Space s, Sizes z) {
   __shared__ DrawSpace L;
+  __shared__ Shared S;
   const int row = blockIdx.x, tid = threadIdx.x;
-  const Row R = row_of<kDrawThreads>(a, s, z.chunks, row, L.slots);
+  const Row R = row_of(a, s, z, row, S);
   const T* p = reinterpret_cast<const T*>(a.logits) + row * a.stride;
   if (R.top == kNanKey || R.top <= kNoneKey) {
     if (tid == 0) {
@@ -433,23 +600,22 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleRows a,
     }
     return;
   }
-  const uint32_t* tops = s.top + (size_t)row * z.chunks;
   if (R.greedy) {
     // the first chunk with the largest logit, then the first element in it
-    if (tid == 0) L.found = z.chunks;
+    if (tid == 0) L.found = kParts;
     __syncthreads();
-    for (int c = tid; c < z.chunks; c += kDrawThreads)
-      if (tops[c] == R.top) atomicMin(&L.found, c);
+    if (S.tops[tid] == R.top) atomicMin(&L.found, tid);
     __syncthreads();
-    const int c = L.found, end = min(a.vocab, (c + 1) * z.chunk);
+    const int c = L.found / z.parts;
     __syncthreads();
     if (tid == 0) L.found = a.vocab;
     __syncthreads();
-    for (int i = c * z.chunk + tid; i < end; i += kDrawThreads)
-      if (order_key(logit(p, i)) == R.top) {
-        atomicMin(&L.found, i);
-        break;
-      }
+    int least = a.vocab;
+    const Elements<kAhead, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
+    elements.each([&](float v, int i) {
+      if (order_key(v) == R.top) least = min(least, i);
+    });
+    if (least < a.vocab) atomicMin(&L.found, least);
     __syncthreads();
     if (tid == 0) {
       a.tokens[row] = L.found;
@@ -458,53 +624,113 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleRows a,
     return;
   }
 
-  // ---- the cut
   u64 cut = 0;
-  Source<T> src{nullptr, p, &R, a.vocab};
-  if (R.limited()) {
-    const uint32_t length = s.length[row];
-    const bool listed = length <= (uint32_t)kCap;
-    if (listed) {
-      src.list = s.list + (size_t)row * kCap;
-      src.n = (int)length;
+  Limit f{0, 0, 0, 0.0};
+  const uint32_t length = R.limited() ? s.length[row] : 0u;
+  const bool listed = length <= (uint32_t)kCap;
+  const int n = listed ? (int)length : a.vocab;
+  const u64* list = s.list + (size_t)row * kCap;
+  const Among<T> among{p, listed ? L.list : nullptr, n};
+  if (R.limited() && listed && !R.by_count) f = limit_of(R, s, z, row, S);
+  if (R.limited() && n <= kPairs && listed) {
+    // ---- a short list: for each element what comes before it; threads share an element where there are few
+    for (int i = tid; i < n; i += kThreads) L.pair[i] = {list[i], weight_of(R, list[i])};
+    double least = f.least;
+    __syncthreads();
+    int split = kThreads / kPairs;   // threads of an element: neighbours, a power of two
+    while (split < 64 && 2 * split * n <= kThreads) split *= 2;
+    const int i = tid / split, part = tid % split;
+    const bool first = part == 0;    // (one thread of an element counts it)
+    u64 key = 0, w = 0, mass = 0;
+    int rank = 0;
+    if (i < n) key = L.pair[i].key, w = L.pair[i].w;
+#pragma unroll 4
+    for (int j = part; j < n; j += split) {
+      const auto e = L.pair[j];
+      const bool before = e.key > key;
+      mass += before ? e.w : 0;
+      rank += before;
+    }
+    for (int d = 1; d < split; d <<= 1) {
+      mass += (u64)__shfl_xor((long long)mass, d);
+      rank += __shfl_xor(rank, d);
     }
     if (R.by_count) {
-      cut = find_cut(src, L, true, R.k, 0.0, 0, 0);
-      if (R.by_mass) {
-        u64 mass = 0, all;
-        src.each([&](u64 key, u64 w) {
-          if (key >= cut) mass += w;
-        });
-        group_scan<kDrawThreads>(mass, L.sums, all);
-        cut = find_cut(src, L, false, 0, R.p * (double)all, 0, cut);
+      if (R.by_mass) least = R.p * (double)group_sum(first && rank < R.k ? w : 0, L.sums);
+      if (!(rank < R.k && (!R.by_mass || rank == 0 || (double)mass < least) && (double)w >= R.least_w)) w = 0;
+      const u64 total = group_sum(first ? w : 0, L.sums), at = drawn(a, row, total);
+      if (first && i < n) L.pair[i].w = w;
+      __syncthreads();
+      // the weights of lower indices: those with a greater lower half of the key
+      u64 start = 0;
+#pragma unroll 4
+      for (int j = part; j < n; j += split) {
+        const auto e = L.pair[j];
+        start += (uint32_t)e.key > (uint32_t)key ? e.w : 0;
       }
-    } else {
-      double least;
-      u64 above;
-      (void)limit_bin<kDrawThreads>(R, s.bins + (size_t)row * kBins, L.sums, &L.found, least, above);
-      cut = find_cut(src, L, false, 0, least, listed ? above : 0, 0);
+      for (int d = 1; d < split; d <<= 1) start += (u64)__shfl_xor((long long)start, d);
+      if (first && w && start <= at && at < start + w) give(a, row, index_of(key), w, total);
+      return;
     }
-    // ---- the chunks' sums: what lies above the list for certain, and what of the list stays
-    const bool part = listed && !R.by_count;
+    // the least key that stays; where none of the list's does, what is greater than all of them
+    if (tid == 0) L.lo = ~0ull, L.hi = 0;
     __syncthreads();
-    for (int c = tid; c < z.chunks; c += kDrawThreads) L.chunk[c] = part ? s.sum[(size_t)row * z.chunks + c] : 0;
+    if (i < n) {
+      const u64 before = f.before + mass;
+      atomicMax(&L.hi, key);
+      if (((double)before < least || before == 0) && (double)w >= R.least_w) atomicMin(&L.lo, key);
+    }
     __syncthreads();
-    src.each([&](u64 key, u64 w) {
-      if (key >= cut && (double)w >= R.least_w) atomicAdd(&L.chunk[(uint32_t)~key / (uint32_t)z.chunk], w);
+    if (n) cut = L.lo != ~0ull ? L.lo : L.hi + 1;
+  } else if (R.limited()) {
+    if (listed) {
+      for (int i = tid; i < n; i += kThreads) L.list[i] = list[i];
+      __syncthreads();
+    }
+#pragma unroll 1
+    for (int by_count = 1; by_count >= 0; --by_count) {   // top-k first
+      if (!(by_count ? R.by_count : R.by_mass)) continue;
+      double least = f.least;
+      if (!by_count && (R.by_count || !listed)) {
+        u64 sum = 0;
+        among.each([&](u64 key) { sum += key >= cut ? weight_of(R, key) : 0; });
+        least = R.p * (double)group_sum(sum, L.sums);
+      }
+      cut = find_cut(among, R, L, by_count, least, by_count ? 0 : f.before, cut);
+    }
+  }
+
+  // ---- the chunks' sums of what stays
+  __syncthreads();
+  if (tid < kMaxChunks) L.chunk[tid] = !R.limited() && tid < z.chunks ? s.sum[(size_t)row * z.chunks + tid] : 0;
+  __syncthreads();
+  if (R.limited()) {
+    if (listed && !R.by_count) {
+      // the bins that stay whole, a wave per chunk
+      const int cb = f.lo / kFine, lane = tid & 63;
+      for (int c = tid >> 6; c < z.chunks; c += kThreads / 64) {
+        const size_t at = (size_t)row * z.chunks + c;
+        u64 sum = lane < cb ? s.coarse[at * kCoarse + lane] : 0;
+        if (f.lo < kBins && lane < f.lo % kFine) sum += s.bins[at * kBins + cb * kFine + lane];
+        sum = (u64)wave_scan((long long)sum);
+        if (lane == 63) L.chunk[c] = sum;
+      }
+      __syncthreads();
+    }
+    // (a list of top-k holds everything that stays, and f no bin then)
+    const Among<T> again{p, listed ? list : nullptr, n};   // (a short list is not in LDS as it was)
+    again.each([&](u64 key) {
+      const u64 w = key >= cut ? weight_of(R, key) : 0;
+      if (w && (double)w >= R.least_w) atomicAdd(&L.chunk[(uint32_t)index_of(key) / (uint32_t)z.chunk], w);
     });
-  } else {
-    for (int c = tid; c < z.chunks; c += kDrawThreads) L.chunk[c] = s.sum[(size_t)row * z.chunks + c];
   }
   __syncthreads();
 
   // ---- the chunk that the number falls into
   u64 total;
   const u64 mine = tid < z.chunks ? L.chunk[tid] : 0;
-  u64 before = group_scan<kDrawThreads>(mine, L.sums, total);
-  const float u = a.uniform[row];
-  const double part = (double)total * (double)(u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f);
-  u64 at = (u64)floor(part);
-  if (at > total - 1) at = total - 1;
+  u64 before = group_scan(mine, L.sums, total);
+  const u64 at = drawn(a, row, total);
   if (mine && before <= at && at < before + mine) {
     L.found = tid;
     L.lo = before;
@@ -513,39 +739,82 @@ __global__ __launch_bounds__(kDrawThreads) void sample_draw_kernel(SampleRows a,
   const int c = L.found;
   const u64 start = L.lo;
 
-  // ---- the element in it: neighbouring elements per thread, in order
-  const int first = c * z.chunk, end = min(a.vocab, first + z.chunk);
-  const int per = (z.chunk + kDrawThreads - 1) / kDrawThreads;
-  auto kept = [&](int i) {
-    const float v = logit(p, i);
-    const u64 w = weight_of(R, v);
-    return full_key(v, i) >= cut && (double)w >= R.least_w ? w : 0;
-  };
-  u64 sum = 0, all;
-  for (int i = first + tid * per; i < min(end, first + (tid + 1) * per); ++i) sum += kept(i);
-  before = start + group_scan<kDrawThreads>(sum, L.sums, all);
-  if (sum && before <= at && at < before + sum)
-    for (int i = first + tid * per;; ++i) {
-      const u64 w = kept(i);
-      if (at < before + w) {
-        a.tokens[row] = i;
-        if (a.share) a.share[row] = (float)((double)w / (double)total);
-        break;
-      }
-      before += w;
+  // ---- the element in it: each wave has a run of the chunk, and the one that the number falls into goes
+  //      through it in order, 64 x 4 elements at a time
+  constexpr int kWaves = kThreads / 64;
+  const int begin = c * z.chunk, end = min(a.vocab, begin + z.chunk);
+  const int wave = tid >> 6, lane = tid & 63, run = (z.chunk + 256 * kWaves - 1) / (256 * kWaves) * 256;
+  const int from = begin + wave * run, to = min(end, from + run);
+  auto kept = [&](int i, u64 (&w)[4]) {
+    struct __attribute__((packed, aligned(sizeof(T)))) Four {
+      T v[4];
+    } q;
+    if (i + 4 <= to) {
+      q = *reinterpret_cast<const Four*>(p + i);
+    } else {
+      for (int e = 0; e < 4; ++e) q.v[e] = i + e < to ? p[i + e] : (T)(-__builtin_inff());
     }
+    u64 sum = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float v = (float)q.v[e];
+      w[e] = full_key(v, i + e) >= cut ? weight_of(R, v) : 0;
+      if (!((double)w[e] >= R.least_w)) w[e] = 0;
+      sum += w[e];
+    }
+    return sum;
+  };
+  u64 w[4], sum = 0;
+#pragma unroll 2
+  for (int i = from + 4 * lane; i < to; i += 256) sum += kept(i, w);
+  sum = (u64)__shfl((long long)wave_scan((long long)sum), 63);
+  __syncthreads();
+  if (lane == 0) L.sums[wave] = sum;
+  __syncthreads();
+  before = start;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i)
+    if (i < wave) before += L.sums[i];
+  if (before <= at && at < before + sum) {
+    for (int first = from; first < to; first += 256) {
+      const u64 mine = kept(first + 4 * lane, w), through = before + (u64)wave_scan((long long)mine);
+      u64 in_front = through - mine;
+      if (mine && in_front <= at && at < through) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (w[e] && in_front <= at && at < in_front + w[e]) give(a, row, first + 4 * lane + e, w[e], total);
+          in_front += w[e];
+        }
+      }
+      before = (u64)__shfl((long long)through, 63);
+      if (at < before) break;
+    }
+  }
 }
 
 template <typename T>
-hipError_t launch(const SampleRows& a, hipStream_t st) {
-  const Sizes z = sizes(a.rows, a.vocab);
+hipError_t launch(const SampleRows& all, hipStream_t st) {
+  const Sizes z = sizes(all.rows, all.vocab);
+  const int most = batch(all.rows, z);
   Space s;
-  place(s, a.ws, a.rows, z.chunks);
-  const dim3 grid(z.chunks, a.rows);
-  hipLaunchKernelGGL((sample_max_kernel<T>), grid, dim3(kThreads), 0, st, a, s, z);
-  hipLaunchKernelGGL((sample_mass_kernel<T>), grid, dim3(kThreads), 0, st, a, s, z);
-  if (a.top_k || a.top_p) hipLaunchKernelGGL((sample_gather_kernel<T>), grid, dim3(kThreads), 0, st, a, s, z);
-  hipLaunchKernelGGL((sample_draw_kernel<T>), dim3(a.rows), dim3(kDrawThreads), 0, st, a, s, z);
+  place(s, all.ws, most, z);
+  for (int first = 0; first < all.rows; first += most) {
+    SampleRows a = all;
+    a.rows = all.rows - first < most ? all.rows - first : most;
+    a.logits = reinterpret_cast<const T*>(all.logits) + first * all.stride;
+    a.temperature += first;
+    a.uniform += first;
+    if (a.top_k) a.top_k += first;
+    if (a.top_p) a.top_p += first;
+    if (a.min_p) a.min_p += first;
+    a.tokens += first;
+    if (a.share) a.share += first;
+    const dim3 grid(z.chunks, a.rows);
+    hipLaunchKernelGGL((sample_max_kernel<T>), grid, dim3(kThreads), 0, st, a, s, z);
+    hipLaunchKernelGGL((sample_mass_kernel<T>), grid, dim3(kThreads), 0, st, a, s, z);
+    if (a.top_p) hipLaunchKernelGGL((sample_gather_kernel<T>), grid, dim3(kThreads), 0, st, a, s, z);
+    hipLaunchKernelGGL((sample_draw_kernel<T>), dim3(a.rows), dim3(kThreads), 0, st, a, s, z);
+  }
   return hipGetLastError();
 }
 
@@ -553,7 +822,8 @@ hipError_t launch(const SampleRows& a, hipStream_t st) {
 
 size_t sample_workspace_bytes(int rows, int vocab) {
   Space s;
-  return place(s, nullptr, rows, sizes(rows, vocab).chunks);
+  const Sizes z = sizes(rows, vocab);
+  return place(s, nullptr, batch(rows, z), z);
 }
 
 hipError_t launch_sample(const SampleRows& a, int logits_fp32, hipStream_t stream) {

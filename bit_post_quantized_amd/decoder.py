@@ -238,13 +238,13 @@ def sample(logits: torch.Tensor, temperature: torch.Tensor, uniform: torch.Tenso
         workspace = torch.empty(need, dtype=_U8, device=dev)
     else:
         good = good and workspace.device == dev and workspace.is_contiguous() and workspace.nbytes >= need
-    if (good and rows > 1 and dev.type == "cuda" and logits.dtype in _CODE and logits.stride(1) == 1
+    if (good and dev.type == "cuda" and logits.dtype in _CODE and (logits.stride(1) == 1 or vocab == 1)
             and _is(temperature, _F32, (rows,), dev) and _is(uniform, _F32, (rows,), dev)
             and (top_k is None or _is(top_k, _I32, (rows,), dev))
             and (top_p is None or _is(top_p, _F32, (rows,), dev))
             and (min_p is None or _is(min_p, _F32, (rows,), dev)) and _here(dev)):
         status = B.load().svdq_sample(
-            logits.data_ptr(), _CODE[logits.dtype], logits.stride(0), rows, vocab, temperature.data_ptr(),
+            logits.data_ptr(), _CODE[logits.dtype], logits.stride(0) if rows > 1 else vocab, rows, vocab, temperature.data_ptr(),
             uniform.data_ptr(), None if top_k is None else top_k.data_ptr(), None if top_p is None else top_p.data_ptr(),
             None if min_p is None else min_p.data_ptr(), tokens.data_ptr(), share.data_ptr(), workspace.data_ptr(),
             _stream(dev))
