@@ -33,7 +33,10 @@ constexpr int kPairs = 256;           // as many are compared each with each
 constexpr int kParts = 512;           // of a row, at most
 constexpr int kMaxChunks = 64;        // of a row
 constexpr int kThreads = 512;
-constexpr int kAhead = 2;             // pieces of 16 bytes that a thread loads before it knows the settings
+constexpr int kApart = 32;
+// pieces of 16 bytes that a thread loads before it knows the settings
+template <typename T>
+constexpr int kAhead = sizeof(T) == 4 ? 2 : 1;
 constexpr uint32_t kNanKey = 0xFFFFFFFFu, kNoneKey = 0x007FFFFFu;  // -infinity's
 
 struct Sizes {
@@ -63,7 +66,7 @@ struct Space {
   u64* bins;         // [rows, chunks, kBins]
   u64* coarse;       // [rows, chunks, kCoarse]
   u64* list;         // [rows, kCap], keys
-  uint32_t* length;  // [rows]
+  uint32_t* length;  // [rows, kApart]: a cache line each, many workgroups add to them
 };
 
 size_t place(Space& s, void* ws, int rows, const Sizes& z) {
@@ -80,7 +83,7 @@ size_t place(Space& s, void* ws, int rows, const Sizes& z) {
   s.coarse = reinterpret_cast<u64*>(take(c * kCoarse * 8));
   s.sum = reinterpret_cast<u64*>(take(c * 8));
   s.top = reinterpret_cast<uint32_t*>(take(c * z.parts * 4));
-  s.length = reinterpret_cast<uint32_t*>(take(r * 4));
+  s.length = reinterpret_cast<uint32_t*>(take(r * kApart * 4));
   return at;
 }
 
@@ -128,7 +131,7 @@ struct Elements {
         for (int j = i; j < end; ++j) f((float)p[j], j);
       }
     }
-#pragma unroll 2
+#pragma unroll 1
     for (int i = begin + E * (threadIdx.x + U * kThreads); i < end; i += E * kThreads) {
       if (i + E <= end) {
         const Piece more = *reinterpret_cast<const Piece*>(p + i);
@@ -157,16 +160,13 @@ struct Row {
   uint32_t top;           // its key
   bool greedy, by_count, by_mass;
   int k;
-  double p, least_w;      // top-p; min-p in units of the weights
+  double p;               // top-p
+  u64 least_w;            // min-p in units of the weights, the next whole number
 
   __device__ __forceinline__ bool limited() const { return by_count || by_mass; }
 
-  // (z - zmax) / temperature; far below where the weight is 0
-  __device__ __forceinline__ double arg(float z) const {
-    if (!(z > -__builtin_inff())) return -1e30;
-    if (top == 0xFF800000u) return z == __builtin_inff() ? 0.0 : -1e30;
-    return ((double)z - zmax) * inv;
-  }
+  // (z - zmax) / temperature, <= 0; far below 0 where the weight is 0
+  __device__ __forceinline__ double arg(float z) const { return fmin(((double)z - zmax) * inv, 0.0); }
 };
 
 __device__ __forceinline__ int bin_of(double x) {   // x in [-kSpan, 0]
@@ -176,20 +176,24 @@ __device__ __forceinline__ int bin_of(double x) {   // x in [-kSpan, 0]
 // rne(2^40 exp(x)), x in [-kSpan, 0]: x = n ln 2 + r, exp(r) by its series to r^12 (|r| < 0.347: the rest
 // is under 2^-52).  n is rounded by an addition in whose sum it is the low bits, the power of two is added to
 // the exponent, and the whole number is read out of the sum with 2^52, whose last bit is 1.
+__device__ __forceinline__ double fma_scalar(double a, double b, double c) {   // a b + c, c in scalar registers
+  double d;   // (left to itself the compiler copies c into the sum's registers first, for each element)
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+  return d;
+}
 __device__ __forceinline__ u64 weight(double x) {
   constexpr double kRound = 0x1.8p52;
   const double t = __builtin_fma(x, 1.4426950408889634074, kRound);
   const double r = __builtin_fma(-(t - kRound), 0.69314718055994530942, x);
-  double e = 1.0 / 479001600.0;
-  e = __builtin_fma(e, r, 1.0 / 39916800.0);
-  e = __builtin_fma(e, r, 1.0 / 3628800.0);
-  e = __builtin_fma(e, r, 1.0 / 362880.0);
-  e = __builtin_fma(e, r, 1.0 / 40320.0);
-  e = __builtin_fma(e, r, 1.0 / 5040.0);
-  e = __builtin_fma(e, r, 1.0 / 720.0);
-  e = __builtin_fma(e, r, 1.0 / 120.0);
-  e = __builtin_fma(e, r, 1.0 / 24.0);
-  e = __builtin_fma(e, r, 1.0 / 6.0);
+  double e = fma_scalar(r, 1.0 / 479001600.0, 1.0 / 39916800.0);
+  e = fma_scalar(e, r, 1.0 / 3628800.0);
+  e = fma_scalar(e, r, 1.0 / 362880.0);
+  e = fma_scalar(e, r, 1.0 / 40320.0);
+  e = fma_scalar(e, r, 1.0 / 5040.0);
+  e = fma_scalar(e, r, 1.0 / 720.0);
+  e = fma_scalar(e, r, 1.0 / 120.0);
+  e = fma_scalar(e, r, 1.0 / 24.0);
+  e = fma_scalar(e, r, 1.0 / 6.0);
   e = __builtin_fma(e, r, 0.5);
   e = __builtin_fma(e, r, 1.0);
   e = __builtin_fma(e, r, 1.0);
@@ -199,7 +203,7 @@ __device__ __forceinline__ u64 weight(double x) {
 }
 __device__ __forceinline__ u64 weight_of(const Row& R, float z) {
   const double x = R.arg(z);
-  return x < -kSpan ? 0 : weight(x);
+  return x >= -kSpan ? weight(x) : 0;
 }
 __device__ __forceinline__ u64 weight_of(const Row& R, u64 key) { return weight_of(R, key_value((uint32_t)(key >> 32))); }
 
@@ -207,6 +211,12 @@ __device__ __forceinline__ u64 weight_of(const Row& R, u64 key) { return weight_
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, d));
+  return v;
+}
+
+__device__ __forceinline__ u64 wave_max64(u64 v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v = max(v, (u64)__shfl_xor((long long)v, d));
   return v;
 }
 
@@ -256,14 +266,17 @@ __device__ __forceinline__ Row row_of(const SampleRows& a, const Space& s, const
   R.top = 0;
 #pragma unroll
   for (int i = 0; i < kThreads / 64; ++i) R.top = max(R.top, L.most[i]);
-  R.zmax = (double)key_value(R.top);
   R.greedy = !(temperature > 0.0f);
-  R.inv = 1.0 / (double)temperature;
+  // (an infinite temperature: so small that no difference is seen, but -infinity is)
+  R.zmax = (double)key_value(R.top);
+  R.inv = fmax(1.0 / (double)temperature, 1e-300);
+  // (where the largest is +infinity, a border between it and all finite logits)
+  if (R.top == 0xFF800000u) R.zmax = 1e39, R.inv = 1.0;
   R.k = k;
   R.p = p;
   R.by_count = k > 0;
   R.by_mass = p < 1.0f;
-  R.least_w = m > 0.0f ? (double)fminf(m, 1.0f) * 0x1p40 : 0.0;
+  R.least_w = m > 0.0f ? (u64)ceil((double)fminf(m, 1.0f) * 0x1p40) : 0;
   return R;
 }
 
@@ -301,7 +314,7 @@ __device__ __forceinline__ bool crossed(bool by_count, u64 through, int k, doubl
 template <typename T>
 __global__ __launch_bounds__(kThreads) void sample_max_kernel(SampleRows a, Space s, Sizes z) {
   const int row = blockIdx.y, c = blockIdx.x, t = threadIdx.x;
-  if (c == 0 && t == 0) s.length[row] = 0;
+  if (c == 0 && t == 0) s.length[(size_t)row * kApart] = 0;
   const T* p = reinterpret_cast<const T*>(a.logits) + row * a.stride;
   uint32_t top = 0;
   const Elements<4, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
@@ -327,7 +340,7 @@ __device__ __forceinline__ void gather(Gathered& L, float v, int i) {
 __device__ __forceinline__ void append(Gathered& L, const Space& s, int row) {
   __syncthreads();
   const uint32_t n = L.count;
-  if (threadIdx.x == 0) L.place = n ? atomicAdd(&s.length[row], n > (uint32_t)kOfChunk ? kCap + 1u : n) : 0u;
+  if (threadIdx.x == 0) L.place = n ? atomicAdd(&s.length[(size_t)row * kApart], n > (uint32_t)kOfChunk ? kCap + 1u : n) : 0u;
   __syncthreads();
   const uint32_t first = L.place;
   for (uint32_t i = threadIdx.x; i < min(n, (uint32_t)kOfChunk); i += kThreads)
@@ -335,7 +348,7 @@ __device__ __forceinline__ void append(Gathered& L, const Space& s, int row) {
 }
 
 template <typename T>
-__global__ __launch_bounds__(kThreads) void sample_mass_kernel(SampleRows a, Space s, Sizes z) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(8))) void sample_mass_kernel(SampleRows a, Space s, Sizes z) {
   __shared__ union {
     u64 bins[kBins];
     Gathered list;
@@ -344,7 +357,7 @@ __global__ __launch_bounds__(kThreads) void sample_mass_kernel(SampleRows a, Spa
   __shared__ Shared S;
   const int row = blockIdx.y, c = blockIdx.x, t = threadIdx.x;
   const T* p = reinterpret_cast<const T*>(a.logits) + row * a.stride;
-  const Elements<kAhead, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
+  const Elements<kAhead<T>, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
   const Row R = row_of(a, s, z, row, S);
   if (R.greedy || R.top == kNanKey || R.top <= kNoneKey) return;
   const size_t at = (size_t)row * z.chunks + c;
@@ -368,7 +381,7 @@ __global__ __launch_bounds__(kThreads) void sample_mass_kernel(SampleRows a, Spa
     u64 sum = 0;
     elements.each([&](float v, int) {
       const u64 w = weight_of(R, v);
-      sum += (double)w >= R.least_w ? w : 0;
+      sum += w >= R.least_w ? w : 0;
     });
     sum = group_sum(sum, sums);
     if (t == 0) s.sum[at] = sum;
@@ -439,9 +452,9 @@ __device__ __forceinline__ Limit limit_of(const Row& R, const Space& s, const Si
     f.lo = f.hi = cb * kFine + b;
     f.before = (u64)__shfl((long long)before, b);
   }
-  if (R.least_w > 0.0) {
+  if (R.least_w > 0) {
     // min-p's border is at its logarithm: nearly always in one bin
-    const double x = fmax(log(R.least_w * 0x1p-40), -kSpan);
+    const double x = fmax(log((double)R.least_w * 0x1p-40), -kSpan);
     f.hi = min(f.hi, bin_of(fmax(x - 1e-6, -kSpan)));
     const int m = bin_of(fmin(x + 1e-6, 0.0));
     if (m < f.lo) {
@@ -461,7 +474,7 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleRows a, S
   const int row = blockIdx.y, c = blockIdx.x;
   if (a.top_k && a.top_k[row] > 0) return;
   const T* p = reinterpret_cast<const T*>(a.logits) + row * a.stride;
-  const Elements<kAhead, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
+  const Elements<kAhead<T>, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
   const Row R = row_of(a, s, z, row, S);
   if (R.greedy || R.top == kNanKey || R.top <= kNoneKey || !R.by_mass) return;
   const Limit f = limit_of(R, s, z, row, S);
@@ -479,21 +492,20 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleRows a, S
 
 // ---------------------------------------------------------------- draw
 struct DrawSpace {
-  union {
-    struct {
-      u64 key, w;
-    } pair[kPairs];
-    u64 list[kCap];
-  };
+  struct {
+    u64 key, w;
+  } pair[kPairs];
+  u64 list[kCap];
   u64 bins[kBins];
   uint32_t count[kBins];
   u64 sums[kThreads / 64];
   u64 chunk[kMaxChunks];
+  u64 round[4][kThreads / 64];
   u64 lo, hi, before;
   int found;
 };
 
-// The elements that a limit is looked for among: the row's list, or (list NULL) the row itself.
+// The elements that a limit is looked for among: the row's list (in LDS), or (list NULL) the row itself.
 template <typename T>
 struct Among {
   const T* logits;
@@ -521,7 +533,9 @@ __device__ __forceinline__ u64 find_cut(const Among<T>& among, const Row& R, Dra
   among.each([&](u64 key) {
     if (key >= floor && weight_of(R, key)) lo = min(lo, key), hi = max(hi, key);
   });
-  if (lo <= hi) {
+  lo = ~wave_max64(~lo);
+  hi = wave_max64(hi);
+  if ((threadIdx.x & 63) == 0) {
     atomicMin(&L.lo, lo);
     atomicMax(&L.hi, hi);
   }
@@ -576,8 +590,7 @@ __device__ __forceinline__ u64 find_cut(const Among<T>& among, const Row& R, Dra
 }
 
 // The number that is drawn, of a sum of `total`.
-__device__ __forceinline__ u64 drawn(const SampleRows& a, int row, u64 total) {
-  const float u = a.uniform[row];
+__device__ __forceinline__ u64 drawn(float u, u64 total) {
   const u64 at = (u64)floor((double)total * (double)(u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f));
   return at < total - 1 ? at : total - 1;
 }
@@ -591,6 +604,10 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleRows a, Spa
   __shared__ DrawSpace L;
   __shared__ Shared S;
   const int row = blockIdx.x, tid = threadIdx.x;
+  // (asked for before the settings are there)
+  const float number = a.uniform[row];
+  const uint32_t length = s.length[(size_t)row * kApart];
+  const u64 chunk_sum = tid < z.chunks ? s.sum[(size_t)row * z.chunks + tid] : 0;
   const Row R = row_of(a, s, z, row, S);
   const T* p = reinterpret_cast<const T*>(a.logits) + row * a.stride;
   if (R.top == kNanKey || R.top <= kNoneKey) {
@@ -611,7 +628,7 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleRows a, Spa
     if (tid == 0) L.found = a.vocab;
     __syncthreads();
     int least = a.vocab;
-    const Elements<kAhead, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
+    const Elements<kAhead<T>, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
     elements.each([&](float v, int i) {
       if (order_key(v) == R.top) least = min(least, i);
     });
@@ -626,15 +643,17 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleRows a, Spa
 
   u64 cut = 0;
   Limit f{0, 0, 0, 0.0};
-  const uint32_t length = R.limited() ? s.length[row] : 0u;
   const bool listed = length <= (uint32_t)kCap;
   const int n = listed ? (int)length : a.vocab;
-  const u64* list = s.list + (size_t)row * kCap;
-  const Among<T> among{p, listed ? L.list : nullptr, n};
   if (R.limited() && listed && !R.by_count) f = limit_of(R, s, z, row, S);
+  if (R.limited() && listed) {
+    for (int i = tid; i < n; i += kThreads) L.list[i] = s.list[(size_t)row * kCap + i];
+  }
+  const Among<T> among{p, listed ? L.list : nullptr, n};
+  __syncthreads();
   if (R.limited() && n <= kPairs && listed) {
     // ---- a short list: for each element what comes before it; threads share an element where there are few
-    for (int i = tid; i < n; i += kThreads) L.pair[i] = {list[i], weight_of(R, list[i])};
+    if (tid < n) L.pair[tid] = {L.list[tid], weight_of(R, L.list[tid])};
     double least = f.least;
     __syncthreads();
     int split = kThreads / kPairs;   // threads of an element: neighbours, a power of two
@@ -657,8 +676,8 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleRows a, Spa
     }
     if (R.by_count) {
       if (R.by_mass) least = R.p * (double)group_sum(first && rank < R.k ? w : 0, L.sums);
-      if (!(rank < R.k && (!R.by_mass || rank == 0 || (double)mass < least) && (double)w >= R.least_w)) w = 0;
-      const u64 total = group_sum(first ? w : 0, L.sums), at = drawn(a, row, total);
+      if (!(rank < R.k && (!R.by_mass || rank == 0 || (double)mass < least) && w >= R.least_w)) w = 0;
+      const u64 total = group_sum(first ? w : 0, L.sums), at = drawn(number, total);
       if (first && i < n) L.pair[i].w = w;
       __syncthreads();
       // the weights of lower indices: those with a greater lower half of the key
@@ -675,18 +694,16 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleRows a, Spa
     // the least key that stays; where none of the list's does, what is greater than all of them
     if (tid == 0) L.lo = ~0ull, L.hi = 0;
     __syncthreads();
-    if (i < n) {
-      const u64 before = f.before + mass;
-      atomicMax(&L.hi, key);
-      if (((double)before < least || before == 0) && (double)w >= R.least_w) atomicMin(&L.lo, key);
+    const u64 in_front = f.before + mass;
+    const bool stays = i < n && ((double)in_front < least || in_front == 0) && w >= R.least_w;
+    const u64 lowest = ~wave_max64(stays ? ~key : 0), highest = wave_max64(key);
+    if ((tid & 63) == 0) {
+      atomicMin(&L.lo, lowest);
+      atomicMax(&L.hi, highest);
     }
     __syncthreads();
     if (n) cut = L.lo != ~0ull ? L.lo : L.hi + 1;
   } else if (R.limited()) {
-    if (listed) {
-      for (int i = tid; i < n; i += kThreads) L.list[i] = list[i];
-      __syncthreads();
-    }
 #pragma unroll 1
     for (int by_count = 1; by_count >= 0; --by_count) {   // top-k first
       if (!(by_count ? R.by_count : R.by_mass)) continue;
@@ -696,13 +713,13 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleRows a, Spa
         among.each([&](u64 key) { sum += key >= cut ? weight_of(R, key) : 0; });
         least = R.p * (double)group_sum(sum, L.sums);
       }
-      cut = find_cut(among, R, L, by_count, least, by_count ? 0 : f.before, cut);
+      cut = find_cut(among, R, L, by_count, least, listed ? f.before : 0, cut);
     }
   }
 
   // ---- the chunks' sums of what stays
   __syncthreads();
-  if (tid < kMaxChunks) L.chunk[tid] = !R.limited() && tid < z.chunks ? s.sum[(size_t)row * z.chunks + tid] : 0;
+  if (tid < kMaxChunks) L.chunk[tid] = R.limited() ? 0 : chunk_sum;
   __syncthreads();
   if (R.limited()) {
     if (listed && !R.by_count) {
@@ -718,10 +735,9 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleRows a, Spa
       __syncthreads();
     }
     // (a list of top-k holds everything that stays, and f no bin then)
-    const Among<T> again{p, listed ? list : nullptr, n};   // (a short list is not in LDS as it was)
-    again.each([&](u64 key) {
+    among.each([&](u64 key) {
       const u64 w = key >= cut ? weight_of(R, key) : 0;
-      if (w && (double)w >= R.least_w) atomicAdd(&L.chunk[(uint32_t)index_of(key) / (uint32_t)z.chunk], w);
+      if (w && w >= R.least_w) atomicAdd(&L.chunk[(uint32_t)index_of(key) / (uint32_t)z.chunk], w);
     });
   }
   __syncthreads();
@@ -730,7 +746,7 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleRows a, Spa
   u64 total;
   const u64 mine = tid < z.chunks ? L.chunk[tid] : 0;
   u64 before = group_scan(mine, L.sums, total);
-  const u64 at = drawn(a, row, total);
+  const u64 at = drawn(number, total);
   if (mine && before <= at && at < before + mine) {
     L.found = tid;
     L.lo = before;
@@ -739,56 +755,70 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleRows a, Spa
   const int c = L.found;
   const u64 start = L.lo;
 
-  // ---- the element in it: each wave has a run of the chunk, and the one that the number falls into goes
-  //      through it in order, 64 x 4 elements at a time
-  constexpr int kWaves = kThreads / 64;
-  const int begin = c * z.chunk, end = min(a.vocab, begin + z.chunk);
-  const int wave = tid >> 6, lane = tid & 63, run = (z.chunk + 256 * kWaves - 1) / (256 * kWaves) * 256;
-  const int from = begin + wave * run, to = min(end, from + run);
-  auto kept = [&](int i, u64 (&w)[4]) {
-    struct __attribute__((packed, aligned(sizeof(T)))) Four {
-      T v[4];
-    } q;
-    if (i + 4 <= to) {
-      q = *reinterpret_cast<const Four*>(p + i);
-    } else {
-      for (int e = 0; e < 4; ++e) q.v[e] = i + e < to ? p[i + e] : (T)(-__builtin_inff());
-    }
-    u64 sum = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float v = (float)q.v[e];
-      w[e] = full_key(v, i + e) >= cut ? weight_of(R, v) : 0;
-      if (!((double)w[e] >= R.least_w)) w[e] = 0;
-      sum += w[e];
-    }
-    return sum;
+  // ---- the element in it, in rounds of kRound pieces of 16 bytes per thread: the pieces' sums by wave, then
+  //      the wave that the number falls into, its lane, and the element
+  constexpr int kWaves = kThreads / 64, kRound = 4, E = 16 / sizeof(T);
+  const int wave = tid >> 6, lane = tid & 63;
+  u64 in_front = start;
+  auto kept = [&](float v, int i) {
+    const u64 w = full_key(v, i) >= cut ? weight_of(R, v) : 0;
+    return w >= R.least_w ? w : 0;
   };
-  u64 w[4], sum = 0;
-#pragma unroll 2
-  for (int i = from + 4 * lane; i < to; i += 256) sum += kept(i, w);
-  sum = (u64)__shfl((long long)wave_scan((long long)sum), 63);
-  __syncthreads();
-  if (lane == 0) L.sums[wave] = sum;
-  __syncthreads();
-  before = start;
+  const int end = min(a.vocab, (c + 1) * z.chunk);
+  for (int first = c * z.chunk; first < end; first += kRound * kThreads * E) {
+    typename Elements<1, T>::Piece q[kRound];
+    u64 through[kRound];
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i)
-    if (i < wave) before += L.sums[i];
-  if (before <= at && at < before + sum) {
-    for (int first = from; first < to; first += 256) {
-      const u64 mine = kept(first + 4 * lane, w), through = before + (u64)wave_scan((long long)mine);
-      u64 in_front = through - mine;
-      if (mine && in_front <= at && at < through) {
+    for (int u = 0; u < kRound; ++u) {
+      const int i = first + E * (u * kThreads + tid);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (w[e] && in_front <= at && at < in_front + w[e]) give(a, row, first + 4 * lane + e, w[e], total);
-          in_front += w[e];
-        }
+      for (int e = 0; e < E; ++e) q[u].v[e] = (T)(-__builtin_inff());
+      if (first + E * u * kThreads >= end) continue;   // (none for any thread)
+      if (i + E <= end) {
+        q[u] = *reinterpret_cast<const typename Elements<1, T>::Piece*>(p + i);
+      } else {
+        for (int e = 0; e < E; ++e)
+          if (i + e < end) q[u].v[e] = p[i + e];
       }
-      before = (u64)__shfl((long long)through, 63);
-      if (at < before) break;
     }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kRound; ++u) {
+      u64 sum = 0;
+      if (first + E * u * kThreads < end) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum += kept((float)q[u].v[e], first + E * (u * kThreads + tid) + e);
+      }
+      through[u] = (u64)wave_scan((long long)sum);
+      if (lane == 63) L.round[u][wave] = through[u];
+    }
+    __syncthreads();
+    // (every wave for itself: lane l has the l-th of the sums)
+    const u64 mine = lane < kRound * kWaves ? L.round[lane / kWaves][lane % kWaves] : 0;
+    const u64 upto = in_front + (u64)wave_scan((long long)mine);
+    const u64 hit = __ballot(at < upto);
+    if (hit) {
+      const int x = __ffsll((unsigned long long)hit) - 1;
+      const u64 from = (u64)__shfl((long long)(upto - mine), x);
+#pragma unroll
+      for (int u = 0; u < kRound; ++u)
+        if (x == u * kWaves + wave) {
+          // (before this lane's piece: the sum of the lanes in front)
+          u64 before = (u64)__shfl_up((long long)through[u], 1);
+          before = from + (lane ? before : 0);
+          if (before <= at && at < from + through[u]) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              const int i = first + E * (u * kThreads + tid) + e;
+              const u64 w = kept((float)q[u].v[e], i);
+              if (w && before <= at && at < before + w) give(a, row, i, w, total);
+              before += w;
+            }
+          }
+        }
+      break;
+    }
+    in_front = (u64)__shfl((long long)upto, 63);
   }
 }
 
