@@ -45,8 +45,8 @@ struct Sizes {
 };
 
 Sizes sizes(int rows, int vocab) {
-  // about four workgroups per CU, of 2048 elements or more
-  int chunks = (1024 + rows - 1) / rows;
+  // four workgroups per CU, as many as run at once, of 2048 elements or more
+  int chunks = rows < 1024 ? 1024 / rows : 1;
   const int most = (vocab + 2047) / 2048;
   if (chunks > most) chunks = most;
   if (chunks > kMaxChunks) chunks = kMaxChunks;

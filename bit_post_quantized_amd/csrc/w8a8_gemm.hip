@@ -21,11 +21,6 @@ __device__ __forceinline__ v4i mfma(v4i w, v4i x, v4i acc) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, acc, 0, 0, 0);
 }
 
-template <int N>
-struct Count {
-  static constexpr int value = N;
-};
-
 // A value that is the same in every lane, in scalar registers (a buffer's base and size have to be).
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 template <typename P>
@@ -90,72 +85,6 @@ __global__ __launch_bounds__(256) void w8a8_pack_kernel(const int8_t* codes, int
   }
 }
 
-// ---------------------------------------------------------------- few rows
-// A workgroup has CT tiles of 16 columns and all of K, dealt unit by unit to its waves; each wave
-// keeps RT x CT accumulators and the waves' sums meet in LDS.  The weights are read once, in whole
-// units; X comes from L2.
-template <int RT, int CT, int WAVES, bool F32>
-__global__ __launch_bounds__(64 * WAVES) void w8a8_few_kernel(const int8_t* __restrict__ qx,
-                                                              const int8_t* __restrict__ container,
-                                                              int K, Output o) {
-  constexpr int TILES = RT * CT, CHUNK = TILES < 4 ? TILES : 4;  // tiles exchanged at a time
-  __shared__ v4i parts[WAVES][CHUNK][64];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int G = K / 64, tiles = (o.N + 15) / 16, t0 = blockIdx.x * CT;
-  const int8_t* x[RT];
-  const int8_t* w[CT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-    x[r] = qx + (size_t)min(16 * r + (lane & 15), o.M - 1) * K + 16 * (lane >> 4);
-#pragma unroll
-  for (int c = 0; c < CT; ++c)
-    w[c] = container + (size_t)min(t0 + c, tiles - 1) * G * kUnit + lane * 16;
-  v4i acc[CT][RT] = {};
-  // U units at a time, so that their loads are in flight together (a loop around matrix instructions is
-  // not unrolled by the compiler)
-  auto step = [&](int u, auto count) {
-    constexpr int U = decltype(count)::value;
-    v4i wf[U][CT], xf[U][RT];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-        wf[i][c] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(w[c] + (size_t)(u + i * WAVES) * kUnit));
-#pragma unroll
-      for (int r = 0; r < RT; ++r) xf[i][r] = *reinterpret_cast<const v4i*>(x[r] + 64 * (u + i * WAVES));
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i)
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) acc[c][r] = mfma(wf[i][c], xf[i][r], acc[c][r]);
-  };
-  constexpr int U = RT * CT > 4 ? 2 : 4;
-  int u = wave;
-  for (; u + (U - 1) * WAVES < G; u += U * WAVES) step(u, Count<U>());
-  for (; u < G; u += WAVES) step(u, Count<1>());
-#pragma unroll
-  for (int first = 0; first < TILES; first += CHUNK) {
-    if (first) __syncthreads();
-#pragma unroll
-    for (int i = 0; i < CHUNK; ++i)
-      if (first + i < TILES) parts[wave][i][lane] = acc[(first + i) / RT][(first + i) % RT];
-    __syncthreads();
-    for (int i = wave; i < CHUNK; i += WAVES) {
-      const int tile = first + i;
-      if (tile < TILES) {
-        v4i sum = parts[0][i][lane];
-#pragma unroll
-        for (int p = 1; p < WAVES; ++p) sum += parts[p][i][lane];
-        const int m = 16 * (tile % RT) + (lane & 15), n = 16 * (t0 + tile / RT) + 4 * (lane >> 4);
-        if (m < o.M && n < o.N) store4<F32>(o, m, n, sum);
-      }
-    }
-  }
-}
-
-// ---------------------------------------------------------------- many rows
 #define SVDQ_LDS(p) ((__attribute__((address_space(3))) void*)(p))
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_rsrc(const void* base, int bytes) {
@@ -185,6 +114,112 @@ __device__ __forceinline__ void store_16(__amdgpu_buffer_rsrc_t base, v4u v, uin
 #define SVDQ_WAIT_LDS_AND(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | (7 << 4))
 #define SVDQ_WAIT_LOADS(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8))
 
+// ---------------------------------------------------------------- few rows
+// A workgroup has CT tiles of 16 columns and all of K, dealt unit by unit to its waves; each wave
+// keeps RT x CT accumulators and the waves' sums meet in LDS.  The weights are read once, in whole
+// units; X comes from L2.
+//
+// An operand of X is 16 rows with 64 bytes each, and the memory unit takes four neighbouring lanes at a
+// time: read straight into registers, where four neighbours are four rows, X costs four times what its
+// bytes do.  So rows are read piece by piece (four lanes a row) into LDS of the wave's own, and the
+// operand from there (the pieces of a row exchanged as for many rows); U units of both operands are on
+// their way while U are computed.
+template <int RT, int CT, int WAVES, int U, bool F32>
+__global__ __launch_bounds__(64 * WAVES) void w8a8_few_kernel(const int8_t* __restrict__ qx,
+                                                              const int8_t* __restrict__ container,
+                                                              int K, Output o) {
+  constexpr int TILES = RT * CT, CHUNK = TILES < 4 ? TILES : 4;  // tiles exchanged at a time
+  constexpr int kSet = U * RT * 1024;                            // X of U units
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  v4i(*parts)[CHUNK][64] = reinterpret_cast<v4i(*)[CHUNK][64]>(lds);   // (behind the loop)
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int G = K / 64, tiles = (o.N + 15) / 16, t0 = blockIdx.x * CT;
+  const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(qx, o.M * K);          // (rows past M: zeros)
+  uint8_t* mine = lds + wave * 2 * kSet;
+  uint32_t x_off[RT];
+  const int8_t* w[CT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) x_off[r] = (uint32_t)(16 * r + (lane >> 2)) * K + 16 * ((lane & 3) ^ (lane >> 4));
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+    w[c] = container + (size_t)min(t0 + c, tiles - 1) * G * kUnit + lane * 16;
+  const int x_at = (lane & 15) * 64 + 16 * ((lane >> 4) ^ ((lane >> 2) & 3));
+  v4i acc[CT][RT] = {};
+  const int units = (G - wave + WAVES - 1) / WAVES, steps = (units + U - 1) / U;   // (0 for a wave without any)
+  auto issue = [&](int s, v4i (&wf)[U][CT]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int u = min(wave + (s * U + i) * WAVES, G - 1);   // (past the end: read again, not used)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) load_to_lds(rx, mine + (s & 1) * kSet + (i * RT + r) * 1024, x_off[r] + 64 * u);
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        wf[i][c] = __builtin_nontemporal_load(reinterpret_cast<const v4i*>(w[c] + (size_t)u * kUnit));
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto compute = [&](int s, const v4i (&wf)[U][CT]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (s * U + i < units) {
+        v4i xf[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          xf[r] = *reinterpret_cast<const v4i*>(mine + (s & 1) * kSet + (i * RT + r) * 1024 + x_at);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int r = 0; r < RT; ++r) acc[c][r] = mfma(wf[i][c], xf[r], acc[c][r]);
+      }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  constexpr int kAhead = U * (RT + CT);   // loads of a step
+  v4i wa[U][CT], wb[U][CT];
+  // (a wait for all but the newest step's loads: what is computed has landed, in LDS too)
+  if (steps > 0) issue(0, wa);
+  int s = 0;
+  for (; s + 1 < steps; s += 2) {
+    issue(s + 1, wb);
+    SVDQ_WAIT_LOADS(kAhead);
+    asm volatile("" ::: "memory");
+    compute(s, wa);
+    if (s + 2 < steps) {
+      issue(s + 2, wa);
+      SVDQ_WAIT_LOADS(kAhead);
+    } else {
+      SVDQ_WAIT_LOADS(0);
+    }
+    asm volatile("" ::: "memory");
+    compute(s + 1, wb);
+  }
+  if (s < steps) {
+    SVDQ_WAIT_LOADS(0);
+    asm volatile("" ::: "memory");
+    compute(s, wa);
+  }
+  __syncthreads();   // (X's place is taken by the sums)
+#pragma unroll
+  for (int first = 0; first < TILES; first += CHUNK) {
+    if (first) __syncthreads();
+#pragma unroll
+    for (int i = 0; i < CHUNK; ++i)
+      if (first + i < TILES) parts[wave][i][lane] = acc[(first + i) / RT][(first + i) % RT];
+    __syncthreads();
+    for (int i = wave; i < CHUNK; i += WAVES) {
+      const int tile = first + i;
+      if (tile < TILES) {
+        v4i sum = parts[0][i][lane];
+#pragma unroll
+        for (int p = 1; p < WAVES; ++p) sum += parts[p][i][lane];
+        const int m = 16 * (tile % RT) + (lane & 15), n = 16 * (t0 + tile / RT) + 4 * (lane >> 4);
+        if (m < o.M && n < o.N) store4<F32>(o, m, n, sum);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- many rows
 // Tiles of 64 RT x 64 WN by 2 x WN waves of 32 RT x 64, persistent workgroups that go from tile to tile.
 // K in units of 64, four of them in LDS: one stream of units that runs on over the tiles, so that the next
 // tile's first units are on their way while a tile is stored.  A step computes a unit in halves of k: during
@@ -524,19 +559,29 @@ Plan plan(int M, int N, int K) {
   return best;
 }
 
-template <int RT, int CT, int WAVES>
-void launch_few(const int8_t* qx, const int8_t* container, int K, const Output& o, int f32, hipStream_t st) {
+template <int RT, int CT, int WAVES, int U>
+hipError_t launch_few(const int8_t* qx, const int8_t* container, int K, const Output& o, int f32, hipStream_t st) {
+  constexpr int kX = WAVES * 2 * U * RT * 1024, kParts = WAVES * (RT * CT < 4 ? RT * CT : 4) * 1024;
+  constexpr int kLds = kX > kParts ? kX : kParts;
   const dim3 grid(((o.N + 15) / 16 + CT - 1) / CT), block(64 * WAVES);
-  if (f32) hipLaunchKernelGGL((w8a8_few_kernel<RT, CT, WAVES, true>), grid, block, 0, st, qx, container, K, o);
-  else hipLaunchKernelGGL((w8a8_few_kernel<RT, CT, WAVES, false>), grid, block, 0, st, qx, container, K, o);
+  const void* fn = f32 ? reinterpret_cast<const void*>(w8a8_few_kernel<RT, CT, WAVES, U, true>)
+                       : reinterpret_cast<const void*>(w8a8_few_kernel<RT, CT, WAVES, U, false>);
+  if (kLds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+    if (e != hipSuccess) return e;
+  }
+  if (f32) hipLaunchKernelGGL((w8a8_few_kernel<RT, CT, WAVES, U, true>), grid, block, kLds, st, qx, container, K, o);
+  else hipLaunchKernelGGL((w8a8_few_kernel<RT, CT, WAVES, U, false>), grid, block, kLds, st, qx, container, K, o);
+  return hipGetLastError();
 }
 
 template <int RT>
-void launch_few_rows(const int8_t* qx, const int8_t* container, int K, const Output& o, int f32, hipStream_t st) {
+hipError_t launch_few_rows(const int8_t* qx, const int8_t* container, int K, const Output& o, int f32, hipStream_t st) {
+  constexpr int U = RT == 1 ? 4 : 2;
   const int tiles = (o.N + 15) / 16;
-  if (tiles >= 4 * 2 * kCus) launch_few<RT, 4, 8>(qx, container, K, o, f32, st);
-  else if (tiles >= 2 * 2 * kCus) launch_few<RT, 2, 8>(qx, container, K, o, f32, st);
-  else launch_few<RT, 1, 16>(qx, container, K, o, f32, st);
+  if (tiles >= 4 * kCus) return launch_few<RT, 4, 8, U>(qx, container, K, o, f32, st);
+  if (tiles >= 2 * kCus) return launch_few<RT, 2, 8, U>(qx, container, K, o, f32, st);
+  return launch_few<RT, 1, 8, RT <= 2 ? 2 * U : U>(qx, container, K, o, f32, st);
 }
 
 template <int RT, int WN, int OUT>
@@ -590,12 +635,11 @@ hipError_t launch_w8a8_gemm(const int8_t* qx, const float* sx, const int8_t* con
   const Plan p = plan(M, N, K);
   if (p.rt == 0) {
     switch ((M + 15) / 16) {
-      case 1: launch_few_rows<1>(qx, container, K, o, out_fp32, stream); break;
-      case 2: launch_few_rows<2>(qx, container, K, o, out_fp32, stream); break;
-      case 3: launch_few_rows<3>(qx, container, K, o, out_fp32, stream); break;
-      default: launch_few_rows<4>(qx, container, K, o, out_fp32, stream); break;
+      case 1: return launch_few_rows<1>(qx, container, K, o, out_fp32, stream);
+      case 2: return launch_few_rows<2>(qx, container, K, o, out_fp32, stream);
+      case 3: return launch_few_rows<3>(qx, container, K, o, out_fp32, stream);
+      default: return launch_few_rows<4>(qx, container, K, o, out_fp32, stream);
     }
-    return hipGetLastError();
   }
   const Problem q{qx, container, M, N, K, p.split, sx, sw, bias, Y};
   int32_t* ws = static_cast<int32_t*>(workspace);
