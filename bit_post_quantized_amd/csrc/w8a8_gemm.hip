@@ -577,11 +577,17 @@ hipError_t launch_few(const int8_t* qx, const int8_t* container, int K, const Ou
 
 template <int RT>
 hipError_t launch_few_rows(const int8_t* qx, const int8_t* container, int K, const Output& o, int f32, hipStream_t st) {
-  constexpr int U = RT == 1 ? 4 : 2;
+  // Columns of a workgroup: more of them read X less often, fewer leave more workgroups, and more of them on
+  // a CU.  Measured with 64 / 32 / 16 columns, us: 16 x 8192 x 28672 (rows, K, columns) 38 / 46 / 51, 32 x 8192 x
+  // 28672 43 / 55 / 71, one row of 4096 x 131072, where a wave has eight units in all, 93 / 78 / 86, of 8192 x 8192
+  // 15 / 14 / 12.
   const int tiles = (o.N + 15) / 16;
-  if (tiles >= 4 * kCus) return launch_few<RT, 4, 8, U>(qx, container, K, o, f32, st);
-  if (tiles >= 2 * kCus) return launch_few<RT, 2, 8, U>(qx, container, K, o, f32, st);
-  return launch_few<RT, 1, 8, RT <= 2 ? 2 * U : U>(qx, container, K, o, f32, st);
+  if (tiles >= 4 * kCus) {
+    if (RT == 1 && K <= 4096) return launch_few<RT, 2, 8, 2>(qx, container, K, o, f32, st);
+    return launch_few<RT, 4, 8, 2>(qx, container, K, o, f32, st);
+  }
+  if (RT > 1 && tiles >= 2 * kCus) return launch_few<RT, 2, 8, 2>(qx, container, K, o, f32, st);
+  return launch_few<RT, 1, 8, RT <= 2 ? 4 : 2>(qx, container, K, o, f32, st);
 }
 
 template <int RT, int WN, int OUT>
