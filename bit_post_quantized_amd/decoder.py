@@ -102,7 +102,15 @@ def quantize_rows(x: torch.Tensor, factor: Optional[torch.Tensor] = None, out: O
     (``svdq_quantize_rows``): activations that no norm precedes, or a weight [N, K]."""
     if out is None:
         out = Rows8(x.new_empty(x.shape, dtype=_I8), x.new_empty(x.shape[:1], dtype=_F32))
-    B.svdq_quantize_rows(x, factor, out.codes, out.scales)
+    (M, K), dev, code = x.shape, x.device, _CODE.get(x.dtype)
+    if (dev.type == "cuda" and code is not None and _is(x, x.dtype, (M, K), dev) and _is(out.codes, _I8, (M, K), dev)
+            and _is(out.scales, _F32, (M,), dev) and (factor is None or _is(factor, _F32, (K,), dev)) and _here(dev)):
+        status = B.load().svdq_quantize_rows(x.data_ptr(), code, K, None if factor is None else factor.data_ptr(), M, K,
+                                             out.codes.data_ptr(), out.scales.data_ptr(), _stream(dev))
+        if status:
+            binding._check("svdq_quantize_rows", status)
+    else:
+        B.svdq_quantize_rows(x, factor, out.codes, out.scales)
     return out
 
 
