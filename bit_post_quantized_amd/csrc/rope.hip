@@ -31,9 +31,9 @@ __device__ __forceinline__ void load8(const T* p, float* v) {
 }
 
 template <typename X, bool INTERLEAVED>
-__global__ __launch_bounds__(kThreads) void rope_kernel(RopeRows a, int group, int per_row) {
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeRows a, int group, int per_head) {
   extern __shared__ float2 turns[];  // [group][rot / 2]: (cos, sin) times scale
-  const int half = a.rot / 2;
+  const int half = a.rot / 2, per_row = (a.heads[0] + a.heads[1]) * per_head;
   for (int64_t row0 = (int64_t)blockIdx.x * group; row0 < a.rows; row0 += (int64_t)gridDim.x * group) {
     const int rows = (int)min((int64_t)group, a.rows - row0);
     for (int i = threadIdx.x; i < rows * half; i += kThreads) {
@@ -44,47 +44,53 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeRows a, int group, i
       turns[i] = make_float2(cs * a.scale, sn * a.scale);
     }
     __syncthreads();
-    // an item: 8 pairs of a head (the half layout's 8 + 8 channels, or 16 in a row), or 8 channels that
-    // are only copied; per_row items of a row, heads of q first
-    const int pairs = half / 8, rest = (a.dim - a.rot) / 8, per_head = pairs + rest;
-    for (int i = threadIdx.x; i < rows * per_row; i += kThreads) {
-      const int r = i / per_row, j = i - r * per_row;
+    // an item, of per_row of a row, heads of q first: 8 channels, turned or only copied, and in the half
+    // layout the 8 that they are paired with; the same one of several rows at a time, all loaded first
+    const int half8 = half / 8;
+    for (int j = threadIdx.x; j < per_row; j += kThreads) {
       const int h = j / per_head, p = j - h * per_head;
       const int which = h >= a.heads[0];
       const int head = which ? h - a.heads[0] : h;
-      const X* in = reinterpret_cast<const X*>(a.in[which]) + (row0 + r) * a.in_stride[which] + head * a.dim;
-      __bf16* out = reinterpret_cast<__bf16*>(a.out[which]) + (row0 + r) * a.out_stride[which] + head * a.dim;
-      float u[8], v[8];
-      if (p < pairs) {
-        const float2* cs = turns + r * half + 8 * p;
-        const int c0 = INTERLEAVED ? 16 * p : 8 * p, c1 = INTERLEAVED ? c0 + 8 : c0 + half;
-        load8(in + c0, u);
-        load8(in + c1, v);
-        if constexpr (INTERLEAVED) {
+      const X* in = reinterpret_cast<const X*>(a.in[which]) + row0 * a.in_stride[which] + head * a.dim;
+      __bf16* out = reinterpret_cast<__bf16*>(a.out[which]) + row0 * a.out_stride[which] + head * a.dim;
+      // (half layout: the first of the pairs' channels, or one that is copied)
+      const bool turned = INTERLEAVED ? 8 * p < a.rot : p < half8;
+      const int c = INTERLEAVED || turned ? 8 * p : a.rot + 8 * (p - half8);
+      constexpr int kRows = INTERLEAVED ? 4 : 2;   // (16 channels of each in the half layout)
+      for (int r0 = 0; r0 < rows; r0 += kRows) {
+        float u[kRows][8], v[kRows][8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 t0 = cs[e], t1 = cs[4 + e];
-            const float a0 = u[2 * e], b0 = u[2 * e + 1], a1 = v[2 * e], b1 = v[2 * e + 1];
-            u[2 * e] = a0 * t0.x - b0 * t0.y;
-            u[2 * e + 1] = a0 * t0.y + b0 * t0.x;
-            v[2 * e] = a1 * t1.x - b1 * t1.y;
-            v[2 * e + 1] = a1 * t1.y + b1 * t1.x;
+        for (int r = 0; r < kRows; ++r)
+          if (r0 + r < rows) {
+            load8(in + (r0 + r) * a.in_stride[which] + c, u[r]);
+            if (!INTERLEAVED && turned) load8(in + (r0 + r) * a.in_stride[which] + c + half, v[r]);
           }
-        } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float2 t = cs[e];
-            const float x = u[e], y = v[e];
-            u[e] = x * t.x - y * t.y;
-            v[e] = x * t.y + y * t.x;
+        for (int r = 0; r < kRows; ++r)
+          if (r0 + r < rows) {
+            __bf16* to = out + (r0 + r) * a.out_stride[which] + c;
+            const float2* cs = turns + (r0 + r) * half + (INTERLEAVED ? 4 * p : 8 * p);
+            if (INTERLEAVED && turned) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 t = cs[e];
+                const float x = u[r][2 * e], y = u[r][2 * e + 1];
+                u[r][2 * e] = x * t.x - y * t.y;
+                u[r][2 * e + 1] = x * t.y + y * t.x;
+              }
+            }
+            if (!INTERLEAVED && turned) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 t = cs[e];
+                const float x = u[r][e], y = v[r][e];
+                u[r][e] = x * t.x - y * t.y;
+                v[r][e] = x * t.y + y * t.x;
+              }
+              *reinterpret_cast<v8bf*>(to + half) = to_bf16x8(v[r]);
+            }
+            *reinterpret_cast<v8bf*>(to) = to_bf16x8(u[r]);
           }
-        }
-        *reinterpret_cast<v8bf*>(out + c0) = to_bf16x8(u);
-        *reinterpret_cast<v8bf*>(out + c1) = to_bf16x8(v);
-      } else {
-        const int c = a.rot + 8 * (p - pairs);
-        load8(in + c, u);
-        *reinterpret_cast<v8bf*>(out + c) = to_bf16x8(u);
       }
     }
     __syncthreads();  // the next rows' pairs take these ones' place
@@ -97,9 +103,11 @@ void launch(const RopeRows& a, hipStream_t st) {
   // rows of a workgroup: one while that fills the device, else as many as its threads have pairs
   int group = 1;
   while (group < 8 && 2 * group * half <= kThreads && a.rows >= 4096 * group) group *= 2;
-  const int per_row = (a.heads[0] + a.heads[1]) * (half / 8 + (a.dim - a.rot) / 8);
+  // (in place, the channels behind rot_dim are where they belong)
+  const bool in_place = a.in[0] == a.out[0] && (a.heads[1] == 0 || a.in[1] == a.out[1]);
+  const int rest = in_place ? 0 : (a.dim - a.rot) / 8, per_head = (INTERLEAVED ? a.rot / 8 : half / 8) + rest;
   hipLaunchKernelGGL((rope_kernel<X, INTERLEAVED>), dim3(min((a.rows + group - 1) / group, kMaxGrid)), dim3(kThreads),
-                     group * half * sizeof(float2), st, a, group, per_row);
+                     group * half * sizeof(float2), st, a, group, per_head);
 }
 
 }  // namespace

@@ -29,6 +29,12 @@ _BF16, _F32, _F64, _I8, _I32, _U8 = (torch.bfloat16, torch.float32, torch.float6
 _CODE = {_BF16: B.SVDQ_OUT_BF16, _F32: B.SVDQ_OUT_FP32}
 
 
+def _rows_of(t: torch.Tensor, dtype: torch.dtype, rows: int, heads: int, dim: int, device: torch.device) -> bool:
+    """A [rows, heads, dim] tensor whose rows may stand apart."""
+    return (t.dtype is dtype and t.shape == (rows, heads, dim) and t.device == device
+            and t.stride()[1:] == (dim, 1))
+
+
 @dataclass
 class Rows8:
     """Rows in 8 bits: the value at [m, k] is codes[m, k] scales[m]."""
@@ -51,49 +57,55 @@ class RMSNorm:
         self.device = a.device
         self._call = B.load().svdq_rms_norm
 
-    def _run(self, x, residual, residual_out, y, codes, scales):
-        M, K, dev = x.shape[0], self.K, self.device
-        kind = 0 if residual is None else _CODE.get(residual.dtype)
-        outs = ((y is None or _is(y, _BF16, (M, K), dev))
-                and (codes is None or _is(codes, _I8, (M, K), dev) and _is(scales, _F32, (M,), dev)))
-        if (_CODE.get(x.dtype) is not None and _is(x, x.dtype, (M, K), dev) and outs and kind is not None
-                and (residual is None or _is(residual, residual.dtype, (M, K), dev)
-                     and _is(residual_out, residual.dtype, (M, K), dev)) and _here(dev)):
-            status = self._call(x.data_ptr(), _CODE[x.dtype], K, None if residual is None else residual.data_ptr(),
-                                kind, None if residual is None else residual_out.data_ptr(), self._gamma, M, K,
-                                self.eps, None if y is None else y.data_ptr(),
-                                None if codes is None else codes.data_ptr(),
-                                None if scales is None else scales.data_ptr(), _stream(dev))
+    def _run(self, x, residual, residual_out, y, codes, scales, good):
+        """``good``: the outputs are as they should be."""
+        M, K, dev, code = x.shape[0], self.K, self.device, _CODE.get(x.dtype)
+        res = out = kind = 0
+        if residual is not None:
+            kind = _CODE.get(residual.dtype)
+            good = good and kind is not None and _is(residual, residual.dtype, (M, K), dev)
+            res, out = residual.data_ptr(), residual_out.data_ptr()
+        if good and code is not None and _is(x, x.dtype, (M, K), dev) and _here(dev):
+            status = self._call(x.data_ptr(), code, K, res, kind, out, self._gamma, M, K, self.eps,
+                                None if y is None else y.data_ptr(), None if codes is None else codes.data_ptr(),
+                                None if codes is None else scales.data_ptr(), _stream(dev))
             if status:
                 binding._check("svdq_rms_norm", status)
         else:
             B.svdq_rms_norm(x, residual, residual_out, self.gamma, self.eps, y, codes, scales)
 
-    @staticmethod
-    def _stream_out(residual, residual_out):
+    def _stream_out(self, x, residual, residual_out):
+        """(where x + residual goes, whether it is as it should be)"""
         if residual is None:
             if residual_out is not None:
                 raise ValueError("RMSNorm: residual_out needs a residual")
-            return None
-        return torch.empty_like(residual) if residual_out is None else residual_out
+            return None, True
+        if residual_out is None:
+            return torch.empty(residual.shape, dtype=residual.dtype, device=residual.device), True
+        return residual_out, _is(residual_out, residual.dtype, x.shape, self.device)
 
     def __call__(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
                  out: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None):
         """x bf16 or fp32 [M, K], residual bf16 or fp32 [M, K] -> (y bf16 [M, K], x + residual in the
         residual's dtype; None without one).  ``residual_out`` may be ``residual``."""
-        residual_out = self._stream_out(residual, residual_out)
+        residual_out, good = self._stream_out(x, residual, residual_out)
         if out is None:
-            out = x.new_empty(x.shape, dtype=_BF16)
-        self._run(x, residual, residual_out, out, None, None)
+            out = torch.empty(x.shape, dtype=_BF16, device=x.device)
+        else:
+            good = good and _is(out, _BF16, x.shape, self.device)
+        self._run(x, residual, residual_out, out, None, None, good)
         return out, residual_out
 
     def rows8(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, out: Optional[Rows8] = None,
               residual_out: Optional[torch.Tensor] = None):
         """The same in 8 bits: (Rows8, x + residual)."""
-        residual_out = self._stream_out(residual, residual_out)
+        residual_out, good = self._stream_out(x, residual, residual_out)
         if out is None:
-            out = Rows8(x.new_empty(x.shape, dtype=_I8), x.new_empty(x.shape[:1], dtype=_F32))
-        self._run(x, residual, residual_out, None, out.codes, out.scales)
+            out = Rows8.empty(*x.shape, device=x.device)
+        else:
+            good = (good and _is(out.codes, _I8, x.shape, self.device)
+                    and _is(out.scales, _F32, x.shape[:1], self.device))
+        self._run(x, residual, residual_out, None, out.codes, out.scales, good)
         return out, residual_out
 
 
@@ -101,7 +113,7 @@ def quantize_rows(x: torch.Tensor, factor: Optional[torch.Tensor] = None, out: O
     """x bf16 or fp32 [M, K], times factor fp32 [K], in 8 bits with a scale for each row
     (``svdq_quantize_rows``): activations that no norm precedes, or a weight [N, K]."""
     if out is None:
-        out = Rows8(x.new_empty(x.shape, dtype=_I8), x.new_empty(x.shape[:1], dtype=_F32))
+        out = Rows8.empty(*x.shape, device=x.device)
     (M, K), dev, code = x.shape, x.device, _CODE.get(x.dtype)
     if (dev.type == "cuda" and code is not None and _is(x, x.dtype, (M, K), dev) and _is(out.codes, _I8, (M, K), dev)
             and _is(out.scales, _F32, (M,), dev) and (factor is None or _is(factor, _F32, (K,), dev)) and _here(dev)):
@@ -146,14 +158,14 @@ class Linear8:
         M = codes.shape[0]
         good = _is(codes, _I8, (M, self.K), dev) and _is(x.scales, _F32, (M,), dev) and _here(dev)
         if out is None:
-            out = codes.new_empty((M, N), dtype=out_dtype)
+            out = torch.empty((M, N), dtype=out_dtype, device=codes.device)
         else:
             good = good and _is(out, out.dtype, (M, N), dev)
         need = B.svdq_w8a8_workspace_bytes(M, N, self.K)
         if workspace is not None:
             good = good and workspace.device == dev and workspace.is_contiguous() and workspace.nbytes >= need
         elif need:
-            workspace = codes.new_empty(need, dtype=_U8)
+            workspace = torch.empty(need, dtype=_U8, device=codes.device)
         code = _CODE.get(out.dtype)
         if good and code is not None:
             status = self._call(codes.data_ptr(), x.scales.data_ptr(), *self._weights, M, N, self.K, out.data_ptr(),
@@ -206,16 +218,18 @@ class Rope:
             k_out = k if k.dtype is _BF16 else torch.empty(k.shape, dtype=_BF16, device=k.device)
         rows, heads, dim = q.shape
         dev, code = self.device, _CODE.get(q.dtype)
-        if (rows > 1 and k is not None and code is not None and k.dtype is q.dtype and q_out.dtype is _BF16
-                and k_out.dtype is _BF16 and k.shape[0] == rows and k.shape[2] == dim and q_out.shape == q.shape
-                and k_out.shape == k.shape and q.device == dev and k.device == dev and q_out.device == dev
-                and k_out.device == dev and q.stride()[1:] == (dim, 1) and k.stride()[1:] == (dim, 1)
-                and q_out.stride()[1:] == (dim, 1) and k_out.stride()[1:] == (dim, 1)
+        kv = 0 if k is None else k.shape[1]
+        if (code is not None and _rows_of(q, q.dtype, rows, heads, dim, dev) and _rows_of(q_out, _BF16, rows, heads, dim, dev)
+                and (k is None or _rows_of(k, q.dtype, rows, kv, dim, dev) and _rows_of(k_out, _BF16, rows, kv, dim, dev))
                 and _is(positions, _I32, (rows,), dev) and _here(dev)):
-            status = self._call(q.data_ptr(), q.stride(0), heads, k.data_ptr(), k.stride(0), k.shape[1], code, rows,
-                                dim, self.rot_dim, 1 if self.interleaved else 0, positions.data_ptr(), self._freqs,
-                                self.scale, q_out.data_ptr(), q_out.stride(0), k_out.data_ptr(), k_out.stride(0),
-                                _stream(dev))
+            one = rows <= 1   # (the strides of a single row say nothing)
+            wide, narrow = heads * dim, kv * dim
+            status = self._call(q.data_ptr(), wide if one else q.stride(0), heads, None if k is None else k.data_ptr(),
+                                narrow if one or k is None else k.stride(0), kv, code, rows, dim, self.rot_dim,
+                                1 if self.interleaved else 0, positions.data_ptr(), self._freqs, self.scale,
+                                q_out.data_ptr(), wide if one else q_out.stride(0),
+                                None if k is None else k_out.data_ptr(),
+                                narrow if one or k is None else k_out.stride(0), _stream(dev))
             if status:
                 binding._check("svdq_rope", status)
         else:
