@@ -11,6 +11,10 @@
 // Where the sum of squares, or max |g|, leaves the middle of fp32's range (a row of zeros, of values
 // past 2^60 or under 2^-50, or one with a NaN or an infinity), the row is scaled by a power of two that
 // brings its largest |h| to [1, 2), and the exchange is made again: every row then has its 24 bits.
+//
+// Bound by memory: 16384 rows of 8192, bf16 with a residual to 8 bits, move 940 MB in 209 - 212 us (4.5 TB/s,
+// where a copy of 1 GiB reaches 5.2), to bf16 1074 MB in 200 (5.4); 4096 x 8192 to 8 bits 52 us, 16384 x 4096 88.
+// Up to a few hundred rows a call costs what its launch costs.
 #include "decoder_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -240,9 +244,8 @@ __global__ __launch_bounds__(64 * WAVES * ROWS) void norm_rows_kernel(NormRows a
   }
 }
 
-// Rows too long for registers: read three times (twice where there is no 8-bit output... the
-// maximum comes with the sum of squares, so: once for both, once more to write; a third time only
-// for rows that are scaled).
+// Rows too long for registers: read once for the sum and the maximum and once more to be written, between
+// them a third time where the row is scaled. 
 template <typename X, typename R>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormRows a) {
   constexpr int WAVES = 16, T = 1024;

@@ -2,11 +2,22 @@
 //
 //   Y[m, n] = sx[m] sw[n] sum_k qx[m, k] qw[n, k] + bias[n]
 //
-// The sums are int32 on v_mfma_i32_16x16x64_i8 and exact, so they may be divided over waves and
-// workgroups in any way.  The weight is the first operand (rows of the result) and X the second
-// (columns): a lane then holds four neighbouring columns of Y in one row.
+// The sums are int32 and exact, so they may be divided over waves and workgroups in any way.  The weight is
+// the first operand of the matrix instruction (rows of the result) and X the second (columns): a lane then
+// holds four neighbouring columns of Y in one row.  Up to 64 rows, v_mfma_i32_16x16x64_i8:
 //   operand: lane l has row l % 16, k = 16 (l / 16) .. + 15 of 64;
-//   result:  lane l has column l % 16 (a row of X), rows 4 (l / 16) + e (columns of Y).
+//   result:  lane l has column l % 16 (a row of X), rows 4 (l / 16) + e (columns of Y);
+// more rows, v_mfma_i32_32x32x32_i8:
+//   operand: lane l has row l % 32, k = 16 (l / 32) .. + 15 of 32;
+//   result:  lane l has column l % 32, rows 8 (e / 4) + 4 (l / 32) + e % 4.
+// (A loop of nothing but matrix instructions on random codes reaches 3410 TOPS with 32x32x32 and 3040 with
+// 16x16x64, 4970 on zeros: what the card's power allows, not what the instruction takes.)
+//
+// Up to 64 rows the weight is read once, and memory bounds it: 40 x 8192 x 28672 (M, K, N) 49 us, 4.8 TB/s;
+// 1 x 8192 x 28672 38 (partly from the last cache), 64 x 8192 x 28672 57, 1 x 4096 x 4096 6.  Many rows are bound by power
+// where they fill the device (8192 x 8192 x 12288 660 - 715 us from card to card, 2310 - 2500 TOPS; 530 on zeros)
+// and by the loads from L2 where they do not (500 x 12288 x 4096 40 us, of which 8 join divided sums; 2000 x 8192 x
+// 4096 67).
 #include "decoder_launch.hpp"
 #include "svdq_device.hpp"
 

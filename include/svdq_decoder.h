@@ -6,10 +6,11 @@
  * rotary positions; and sampling from logits with given random numbers.
  *
  * svdq.h's activations are quantized in groups of 64 with a low-rank branch beside them, for 4-bit
- * weights.  Layers that are kept at 8 bits on both sides (W8A8, SmoothQuant's setting in DCMP's list of
- * methods) need no branch and one scale per row, which the norm before them computes on the way; q and k are rotated by the positions that kv_block_plan wrote before
- * kv_block_append and kv_block_attention; the tokens drawn from the vocabulary projection's logits
- * are what the next kv_block_plan is called for.
+ * weights.  Layers that are kept at 8 bits on both sides (W8A8, SmoothQuant's setting in DCMP's
+ * list of methods) need no branch and one scale per row, which the norm before them computes on
+ * the way; q and k are rotated by the positions that kv_block_plan wrote before kv_block_append and
+ * kv_block_attention; the tokens drawn from the vocabulary projection's logits are what the next
+ * kv_block_plan is called for.
  *
  * The conventions are those of svdq_serve.h: device pointers owned by the caller, synchronous
  * validation with nothing launched on error, the status codes, svdq_last_error, asynchronous work
@@ -39,8 +40,9 @@ int svdq_decoder_version(void);
  * rounded to bf16, or to 8 bits with a scale for each row:
  *     s = fl32(max |y| / 127),  c = clamp(rne(fl32(y / s)), -127, 127), 0 where s = 0.
  * y is computed in fp32 from h before residual_out's rounding; a row's sum of squares neither
- * overflows nor vanishes, whatever its magnitude; a row of zeros gives zeros.  A row with a NaN or an infinity has the scale NaN
- * (infinity / infinity) and the codes 0; other rows are not touched by it.
+ * overflows nor vanishes, whatever its magnitude; a row of zeros gives zeros.  A row with a NaN or
+ * an infinity has the scale NaN (infinity / infinity) and the codes 0; other rows are not touched
+ * by it.
  *   x          [M, K] of x_dtype, 16B, rows x_stride elements apart (a multiple of 8, at least K)
  *   residual   [M, K] of residual_dtype (16B), or NULL: h = x.  residual_out likewise, or NULL
  *              where it is not needed; it may be residual itself, and is NULL without a residual
