@@ -122,3 +122,50 @@ def test_captured_and_replayed(gpu_lib):
         torch.cuda.synchronize()
         assert np.array_equal(host64(y), od.linear8(q2, sx, qw, sw, b, True)), i
         assert torch.equal(lin(x), y)
+
+
+def on_device(x, w, dtype, bias=None):
+    """The same as the oracle, with the sums from a product in 64-bit floats (whole numbers under 2^31: exact)."""
+    acc = x.codes.double() @ w.codes.double().t().contiguous()
+    y = (acc.float() * x.scales[:, None]) * w.scales[None, :]
+    if bias is not None:
+        y = y + bias.float()[None, :]
+    return y.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K,N", [
+    # each tile and division, N odd and even, the last tiles nearly empty
+    (129, 64 * 53, 4440), (144, 64 * 57, 4101), (4097, 64 * 65, 132), (4360, 64 * 66, 135), (4532, 64 * 35, 1),
+    (2196, 64 * 66, 33), (1000, 64 * 128, 1000), (4758, 64, 792), (1999, 64 * 33, 4095), (2000, 64 * 12, 4096),
+    (4101, 64 * 92, 129), (4205, 64 * 96, 132), (2337, 64, 3331), (5000, 64 * 7, 5001),
+])
+def test_tiles_and_divisions(gpu_lib, M, K, N, dtype):
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+
+    def rows(n):
+        return decoder.Rows8(torch.randint(-127, 128, (n, K), generator=g, device="cuda").to(torch.int8),
+                             0.5 + torch.rand(n, generator=g, device="cuda"))
+
+    x, w = rows(M), rows(N)
+    bias = torch.randn(N, generator=g, device="cuda").to(torch.bfloat16) * 1e4
+    guard = torch.full((M * N + 128,), 7.0, dtype=dtype, device="cuda")
+    decoder.Linear8(w.codes, w.scales, bias)(x, out=guard[64:-64].view(M, N))
+    assert torch.equal(guard[64:-64].view(M, N), on_device(x, w, dtype, bias))
+    assert (guard[:64] == 7).all() and (guard[-64:] == 7).all()
+    assert torch.equal(decoder.Linear8(w.codes, w.scales)(x, out_dtype=dtype), on_device(x, w, dtype))
+
+
+@pytest.mark.parametrize("M,N", [(66001, 33000), (40, (1 << 24) - 5), (20000, 65601)])
+def test_results_past_two_gib(gpu_lib, M, N):
+    K = 64
+    g = torch.Generator(device="cuda").manual_seed(N)
+    x = decoder.Rows8(torch.randint(-127, 128, (M, K), generator=g, device="cuda").to(torch.int8),
+                      0.5 + torch.rand(M, generator=g, device="cuda"))
+    w = decoder.Rows8(torch.randint(-127, 128, (N, K), generator=g, device="cuda").to(torch.int8),
+                      0.5 + torch.rand(N, generator=g, device="cuda"))
+    dtype = torch.float32 if M == 20000 else torch.bfloat16
+    y = decoder.Linear8(w.codes, w.scales)(x, out_dtype=dtype)
+    for first in range(0, M, 8192):
+        part = decoder.Rows8(x.codes[first:first + 8192], x.scales[first:first + 8192])
+        assert torch.equal(y[first:first + 8192], on_device(part, w, dtype)), first

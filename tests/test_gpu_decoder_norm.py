@@ -157,3 +157,20 @@ def test_no_rows_guards_and_many_rows(gpu_lib):
     n = many.shape[0] // 64
     assert torch.equal(all_.codes[:n * 64].view(n, 64, 8), few.codes[None].expand(n, 64, 8))
     assert torch.equal(all_.scales[:n * 64].view(n, 64), few.scales[None].expand(n, 64))
+
+
+def test_rows_past_two_gib(gpu_lib):
+    """[70001, 16384]: offsets past 2^31 bytes in x, the residual, the codes' 2^30 elements and y."""
+    M, K = 70001, 16384
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(M, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    gamma = torch.ones(K, device="cuda")
+    norm = decoder.RMSNorm(gamma)
+    y, _ = norm(x)
+    h8, res = norm.rows8(x, x)
+    for rows in (slice(0, 2), slice(32767, 32770), slice(65535, 65538), slice(M - 2, M)):
+        part = x[rows].contiguous()
+        assert torch.equal(y[rows], norm(part)[0])
+        p8, pres = norm.rows8(part, part)
+        assert torch.equal(h8.codes[rows], p8.codes) and torch.equal(h8.scales[rows], p8.scales)
+        assert torch.equal(res[rows], pres)

@@ -188,3 +188,53 @@ def test_captured_and_replayed(gpu_lib):
         torch.cuda.synchronize()
         want = decoder.sample(z, t, u, k, p, m)
         assert torch.equal(tokens, want[0]) and torch.equal(share, want[1]), i
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_counts_between_the_parts_and_the_list(gpu_lib, bf16):
+    """Top-k from fewer elements than a row has parts to more than its list holds, with top-p and min-p."""
+    rng = np.random.default_rng(11)
+    k = np.array([1, 63, 64, 65, 255, 256, 257, 300, 511, 512, 513, 700, 1000, 2047, 2049, 4000], np.int32)
+    z = rng.standard_normal((len(k), 40009)) * np.linspace(0.5, 4, len(k))[:, None]
+    z = round_bf16(z) if bf16 else z.astype(np.float32).astype(np.float64)
+    t, u, _, _, _ = settings(rng, len(k), "none")
+    check(z, t, u, k=k, bf16=bf16)
+    check(z, t, u, k=k, p=np.full(len(k), 0.9, np.float32), bf16=bf16)
+    check(z, t, u, k=k, p=np.full(len(k), 0.99, np.float32), m=np.full(len(k), 0.01, np.float32), bf16=bf16)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_more_rows_than_are_done_at_a_time(gpu_lib, bf16):
+    rng = np.random.default_rng(12)
+    z = rng.standard_normal((4099, 130)) * 2
+    z = round_bf16(z) if bf16 else z.astype(np.float32).astype(np.float64)
+    check(z, *settings(rng, len(z), "all"), bf16=bf16)
+
+
+def test_rows_past_two_gib(gpu_lib):
+    """Logits whose rows stand far apart: the last one begins past 2^32 bytes."""
+    far = 1 << 29
+    store = torch.full((2 * far + 1000,), float("nan"), device="cuda")
+    rng = np.random.default_rng(13)
+    z = (rng.standard_normal((3, 1000)) * 2).astype(np.float32)
+    logits = store.as_strided((3, 1000), (far, 1))
+    logits.copy_(to_dev(z))
+    t, u, k, p, m = settings(rng, 3, "both")
+    tokens, share = run(logits, t, u, k, p)
+    want, _ = run(z, t, u, k, p)
+    assert (tokens == want).all() and (tokens >= 0).all()
+
+
+def test_greedy_takes_the_first_of_the_largest(gpu_lib):
+    """In every place of chunk and part, next to one that is hardly smaller, and to its equals behind."""
+    rng = np.random.default_rng(14)
+    vocab = 9001
+    at = np.concatenate([[0, 1, 7, 8, 2047, 2048, 2049, 4095, 4096, vocab - 2, vocab - 1], rng.integers(0, vocab, 40)])
+    z = np.minimum(rng.standard_normal((len(at), vocab)), 3).astype(np.float32)
+    for b, i in enumerate(at):
+        z[b, i] = 4.0
+        z[b, min(i + 1 + b % 5, vocab - 1)] = 4.0 if i + 1 + b % 5 < vocab else z[b, vocab - 1]
+        if i:
+            z[b, i - 1] = np.nextafter(np.float32(4), np.float32(0))
+    tokens, share = run(z, np.zeros(len(at), np.float32), np.full(len(at), 0.5, np.float32))
+    assert (tokens == at).all() and (share == 1).all()
