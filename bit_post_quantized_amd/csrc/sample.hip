@@ -19,8 +19,8 @@
 // nothing) is not used: `draw` then narrows down the cut by bins over the row itself, more slowly.
 //
 // Bound by the chain of launches and exchanges, not by bytes: 64 rows of 131072 in fp32 (33 MB, 6.5 us of a copy)
-// take 27 us without a limit, 19 with top-k, 50 - 70 with top-p alone and 44 mixed; one row 13 - 17, 30 with
-// top-p alone; 300 rows of 32001 in bf16, mixed, 51; a top-k of 1000 in 64 rows of 131072 260, in one 230.
+// take 26 us without a limit, 19 with top-k and 48 - 63 with top-p alone; one row 13 - 16, 27 with
+// top-p alone; 300 rows of 32001 in bf16 36 and 56; a top-k of 1000 in 64 rows of 131072 260, in one 230.
 #include "decoder_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -470,19 +470,25 @@ __device__ __forceinline__ Limit limit_of(const Row& R, const Space& s, const Si
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleRows a, Space s, Sizes z) {
+  constexpr int kPieces = 64 / 16 * sizeof(T) / 4;   // (16 elements)
   __shared__ Gathered L;
   __shared__ Shared S;
   const int row = blockIdx.y, c = blockIdx.x;
   if (a.top_k && a.top_k[row] > 0) return;
   const T* p = reinterpret_cast<const T*>(a.logits) + row * a.stride;
-  const Elements<kAhead<T>, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
+  const Elements<kPieces, T> elements(p, c * z.chunk, min(a.vocab, (c + 1) * z.chunk));
   const Row R = row_of(a, s, z, row, S);
   if (R.greedy || R.top == kNanKey || R.top <= kNoneKey || !R.by_mass) return;
   const Limit f = limit_of(R, s, z, row, S);
   if (f.lo == kBins) return;
   if (threadIdx.x == 0) L.count = 0;
   __syncthreads();
+  // (a first look in fp32, with room for what its roundings and the bins' are off: nearly all end there)
+  const double bin = kSpan / kBins / R.inv;
+  const float below = nextafterf((float)(R.zmax - (f.hi + 1.01) * bin), -__builtin_inff());
+  const float above = nextafterf((float)(R.zmax - (f.lo - 0.01) * bin), __builtin_inff());
   elements.each([&](float v, int i) {
+    if (!(v >= below && v <= above)) return;
     const double x = R.arg(v);
     if (x < -kSpan) return;
     const int b = bin_of(x);
@@ -503,7 +509,7 @@ struct DrawSpace {
   u64 chunk[kMaxChunks];
   u64 round[4][kThreads / 64];
   u64 lo, hi, before;
-  int found;
+  int found, several;
 };
 
 // The elements that a limit is looked for among: the row's list (in LDS), or (list NULL) the row itself.
@@ -595,6 +601,75 @@ __device__ __forceinline__ u64 find_cut(const Among<T>& among, const Row& R, Dra
   }
 }
 
+// The same where the list holds the elements of the bins f.lo to f.hi and the limit is one of mass: these bins
+// are divided into kThreads, and in the one that the limit falls into few elements are left, which are
+// compared each with each.  False where they are not few.
+__device__ __forceinline__ bool cut_of_bins(const Row& R, const Limit& f, DrawSpace& L, int n, u64& cut) {
+  constexpr int kAtOnce = 128;   // so few are compared without the bins
+  const int t = threadIdx.x;
+  int m = n;
+  u64 in_front = f.before;
+  cut = 0;
+  if (t == 0) L.lo = ~0ull;
+  if (n <= kAtOnce) {
+    if (n == 0) return true;
+    if (t < n) L.pair[t] = {L.list[t], weight_of(R, L.list[t])};
+    __syncthreads();
+  } else {
+    L.bins[t] = 0;
+    if (t == 0) L.found = kBins, L.several = 0;
+    __syncthreads();
+    const float first = (float)f.lo, scale = (float)kThreads / (float)(f.hi + 1 - f.lo);
+    auto part_of = [&](u64 key) {   // (monotone, as bin_of is)
+      const float b = (float)-R.arg(key_value((uint32_t)(key >> 32))) * (float)(kBins / kSpan);
+      return max(0, min(kThreads - 1, (int)((b - first) * scale)));
+    };
+#pragma unroll 1
+    for (int i = t; i < n; i += kThreads) {
+      const u64 key = L.list[i];
+      atomicAdd(&L.bins[part_of(key)], weight_of(R, key));
+    }
+    __syncthreads();
+    const u64 mine = L.bins[t];
+    u64 all;
+    const u64 before = f.before + group_scan(mine, L.sums, all);
+    const bool here = mine && !((double)(before + mine) < f.least) && ((double)before < f.least || before == 0);
+    if (here) L.found = t, L.before = before;
+    __syncthreads();
+    const int b = L.found;
+    if (b == kBins) return true;   // not reached: all stay
+    in_front = L.before;
+#pragma unroll 1
+    for (int i = t; i < n; i += kThreads) {
+      const u64 key = L.list[i];
+      if (part_of(key) == b) {
+        const int place = atomicAdd(&L.several, 1);
+        if (place < kPairs) L.pair[place] = {key, weight_of(R, key)};
+      }
+    }
+    __syncthreads();
+    m = L.several;
+    if (m > kPairs) return false;
+  }
+  int split = kThreads / kPairs;   // threads of an element: neighbours, a power of two
+  while (split < 64 && 2 * split * m <= kThreads) split *= 2;
+  const int i = t / split;
+  u64 key = 0, mass = 0;
+  if (i < m) {
+    key = L.pair[i].key;
+#pragma unroll 2
+    for (int j = t % split; j < m; j += split) mass += L.pair[j].key > key ? L.pair[j].w : 0;
+  }
+  for (int d = 1; d < split; d <<= 1) mass += (u64)__shfl_xor((long long)mass, d);
+  in_front += mass;
+  const bool stays = i < m && ((double)in_front < f.least || in_front == 0);
+  const u64 lowest = ~wave_max64(stays ? ~key : 0);
+  if ((t & 63) == 0 && lowest != ~0ull) atomicMin(&L.lo, lowest);
+  __syncthreads();
+  cut = L.lo;
+  return true;
+}
+
 // The number that is drawn, of a sum of `total`.
 __device__ __forceinline__ u64 drawn(float u, u64 total) {
   const u64 at = (u64)floor((double)total * (double)(u > 0.0f ? fminf(u, 0x1.fffffep-1f) : 0.0f));
@@ -657,10 +732,10 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleRows a, Spa
   }
   const Among<T> among{p, listed ? L.list : nullptr, n};
   __syncthreads();
-  if (R.limited() && n <= kPairs && listed) {
+  if (R.by_count && n <= kPairs && listed) {
     // ---- a short list: for each element what comes before it; threads share an element where there are few
     if (tid < n) L.pair[tid] = {L.list[tid], weight_of(R, L.list[tid])};
-    double least = f.least;
+    double least = 0.0;
     __syncthreads();
     int split = kThreads / kPairs;   // threads of an element: neighbours, a power of two
     while (split < 64 && 2 * split * n <= kThreads) split *= 2;
@@ -680,36 +755,22 @@ __global__ __launch_bounds__(kThreads) void sample_draw_kernel(SampleRows a, Spa
       mass += (u64)__shfl_xor((long long)mass, d);
       rank += __shfl_xor(rank, d);
     }
-    if (R.by_count) {
-      if (R.by_mass) least = R.p * (double)group_sum(first && rank < R.k ? w : 0, L.sums);
-      if (!(rank < R.k && (!R.by_mass || rank == 0 || (double)mass < least) && w >= R.least_w)) w = 0;
-      const u64 total = group_sum(first ? w : 0, L.sums), at = drawn(number, total);
-      if (first && i < n) L.pair[i].w = w;
-      __syncthreads();
-      // the weights of lower indices: those with a greater lower half of the key
-      u64 start = 0;
+    if (R.by_mass) least = R.p * (double)group_sum(first && rank < R.k ? w : 0, L.sums);
+    if (!(rank < R.k && (!R.by_mass || rank == 0 || (double)mass < least) && w >= R.least_w)) w = 0;
+    const u64 total = group_sum(first ? w : 0, L.sums), at = drawn(number, total);
+    if (first && i < n) L.pair[i].w = w;
+    __syncthreads();
+    // the weights of lower indices: those with a greater lower half of the key
+    u64 start = 0;
 #pragma unroll 4
-      for (int j = part; j < n; j += split) {
-        const auto e = L.pair[j];
-        start += (uint32_t)e.key > (uint32_t)key ? e.w : 0;
-      }
-      for (int d = 1; d < split; d <<= 1) start += (u64)__shfl_xor((long long)start, d);
-      if (first && w && start <= at && at < start + w) give(a, row, index_of(key), w, total);
-      return;
+    for (int j = part; j < n; j += split) {
+      const auto e = L.pair[j];
+      start += (uint32_t)e.key > (uint32_t)key ? e.w : 0;
     }
-    // the least key that stays; where none of the list's does, what is greater than all of them
-    if (tid == 0) L.lo = ~0ull, L.hi = 0;
-    __syncthreads();
-    const u64 in_front = f.before + mass;
-    const bool stays = i < n && ((double)in_front < least || in_front == 0) && w >= R.least_w;
-    const u64 lowest = ~wave_max64(stays ? ~key : 0), highest = wave_max64(key);
-    if ((tid & 63) == 0) {
-      atomicMin(&L.lo, lowest);
-      atomicMax(&L.hi, highest);
-    }
-    __syncthreads();
-    if (n) cut = L.lo != ~0ull ? L.lo : L.hi + 1;
-  } else if (R.limited()) {
+    for (int d = 1; d < split; d <<= 1) start += (u64)__shfl_xor((long long)start, d);
+    if (first && w && start <= at && at < start + w) give(a, row, index_of(key), w, total);
+    return;
+  } else if (!(R.by_mass && !R.by_count && listed && cut_of_bins(R, f, L, n, cut)) && R.limited()) {
 #pragma unroll 1
     for (int by_count = 1; by_count >= 0; --by_count) {   // top-k first
       if (!(by_count ? R.by_count : R.by_mass)) continue;
