@@ -139,7 +139,8 @@ int svdq_rope(const void* q, int64_t q_stride, int heads, const void* k, int64_t
  *   workspace    device scratch of svdq_sample_workspace_bytes(rows, vocab) bytes (16B), no
  *                initialization needed, rewritten by every call; calls that share one workspace
  *                must not overlap in time
- *   0 <= rows <= 65535, 1 <= vocab <= 2^22.
+ *   0 <= rows <= 65535, 1 <= vocab <= 2^22.  A top-k over about 500, or a limit that falls among
+ *   thousands of equal logits, takes several times as long as a smaller one.
  */
 size_t svdq_sample_workspace_bytes(int rows, int vocab);
 int svdq_sample(const void* logits, int logits_dtype, int64_t logits_stride, int rows, int vocab,
