@@ -119,7 +119,10 @@ def test_sample_validation(lib):
     assert call(rows=0, z=None, t=None, u=None, tokens=None, ws=None) == OK
     w = lib.svdq_sample_workspace_bytes
     assert w(0, 100) == 0 and w(1, 0) == 0 and w(65536, 100) == 0 and w(2, 100) > 0
-    assert w(64, 131072) < 64 * (1 << 16)
+    # a row's list has 32 KiB, each of at most 1024 chunks (4096 where rows are done in batches) under 20 KiB of bins
+    # and maxima
+    assert w(64, 131072) <= 64 * (33 << 10) + 1024 * (20 << 10)
+    assert w(65535, 1 << 22) <= 4096 * (33 << 10) + 4096 * (20 << 10) and w(65535, 1) == w(4096, 1)
 
 
 def _cases():
