@@ -16,8 +16,7 @@
 // Up to 64 rows the weight is read once, and memory bounds it: 40 x 8192 x 28672 (M, K, N) 49 us, 4.8 TB/s;
 // 1 x 8192 x 28672 38 (partly from the last cache), 64 x 8192 x 28672 57, 1 x 4096 x 4096 6.  Many rows are bound by power
 // where they fill the device (8192 x 8192 x 12288 660 - 715 us from card to card, 2310 - 2500 TOPS; 530 on zeros)
-// and by the loads from L2 where they do not (500 x 12288 x 4096 40 us, of which 8 join divided sums; 2000 x 8192 x
-// 4096 67).
+// and by the loads from L2 where they do not (500 x 12288 x 4096 36 - 39 us; 2000 x 8192 x 4096 65).
 #include "decoder_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -238,6 +237,9 @@ __global__ __launch_bounds__(64 * WAVES) void w8a8_few_kernel(const int8_t* __re
 // read: its place takes u + 4); during the second those of the next unit.  The order of matrix instructions,
 // reads and loads is the written one.
 //
+// KS groups of 2 x WN waves take every KS-th unit each, with places of their own: a tile of few waves has one on
+// a SIMD, which waits for LDS and for its products in turn.  Their sums meet in LDS before the store.
+//
 // With K divided (`split` shares of a tile, in a row) the shares' sums go to `partial`, [split][M][pitch].
 constexpr int kPlaces = 4;      // units in LDS
 constexpr int kScratch = 4096;  // LDS of a wave, for scales and stores
@@ -270,21 +272,26 @@ __device__ __forceinline__ Item item_at(int l, int nx, int ny, int split, int G)
           uniform((int)((int64_t)G * (share + 1) / split))};
 }
 
-// What the loads bring next: a unit of an item (a share of a tile), and where it goes.  All of it is uniform.
-template <int TM, int TN>
+// What a group's loads bring next: a unit of an item (a share of a tile), every KS-th from the group's own on, and
+// where it goes.  All of it is uniform.
+template <int TM, int TN, int KS>
 struct Stream {
   const int8_t* ax;
   const int8_t* bw;
-  int item, unit, end, place;
+  int item, unit, end, place, group;
   int a_left, b_left;   // bytes to the end of the operand, 0 behind the last item
 
+  // (units are as many for every group: past the item's last, W's are zeros)
+  __device__ __forceinline__ int w_bytes() const { return KS == 1 || unit < end ? b_left : 0; }
+
   __device__ __forceinline__ void start(const Problem& p, int items, int nx, int ny) {
-    a_left = b_left = unit = 0;
+    a_left = b_left = 0;
+    unit = group;
     end = 1;
     if (item >= items) return;
     const int G = p.K / 64;
     const Item i = item_at(item, nx, ny, p.split, G);
-    unit = i.first;
+    unit = i.first + group;
     end = i.end;
     ax = p.qx + (size_t)i.mt * TM * p.K + unit * 64;
     bw = p.container + ((size_t)i.nt * (TN / 16) * G + unit) * kUnit;
@@ -293,25 +300,28 @@ struct Stream {
   }
   __device__ __forceinline__ void advance(const Problem& p, int items, int nx, int ny) {
     place = (place + 1) & (kPlaces - 1);
-    ax += 64;
-    bw += kUnit;
-    a_left = max(a_left - 64, 0);
-    b_left = max(b_left - kUnit, 0);
-    if (++unit == end) {
+    ax += 64 * KS;
+    bw += kUnit * KS;
+    a_left = max(a_left - 64 * KS, 0);
+    b_left = max(b_left - kUnit * KS, 0);
+    unit += KS;
+    if (unit - group >= end) {
       item += gridDim.x;
       start(p, items, nx, ny);
     }
   }
 };
 
-template <int RT, int WN, int OUT>
-__global__ __launch_bounds__(128 * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
+template <int RT, int WN, int KS, int OUT>
+__global__ __launch_bounds__(128 * WN * KS) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void w8a8_tile_kernel(Problem p) {
   constexpr int TM = 64 * RT, TN = 64 * WN, WAVES = 2 * WN, kA = TM * 64, kStage = kA + TN * 64;
   constexpr int kLoadsA = TM / 16 / WAVES, kLoadsB = TN / 16 / WAVES, kLoads = kLoadsA + kLoadsB;  // of a wave
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, all_waves = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = KS == 1 ? 0 : all_waves / WAVES, wave = all_waves - group * WAVES;   // (a group's waves)
   const int wm = wave / WN, wn = wave % WN;
+  uint8_t* ring = lds + group * kPlaces * kStage;
   const int G = p.K / 64;
   const int nx = (p.N + TN - 1) / TN, ny = (p.M + TM - 1) / TM, items = nx * ny * p.split;
 
@@ -324,14 +334,15 @@ void w8a8_tile_kernel(Problem p) {
     a_off[j] = (uint32_t)(16 * (WAVES * j + wave) + (lane >> 2)) * p.K + 16 * ((lane & 3) ^ (lane >> 4));
 #pragma unroll
   for (int j = 0; j < kLoadsB; ++j) b_off[j] = (uint32_t)(WAVES * j + wave) * G * kUnit + lane * 16;
-  Stream<TM, TN> next;
+  Stream<TM, TN, KS> next;
   next.item = blockIdx.x;
+  next.group = group;
   next.place = 0;
   next.start(p, items, nx, ny);
   auto issue = [&](int j) __attribute__((always_inline)) {
-    uint8_t* st = lds + next.place * kStage;
+    uint8_t* st = ring + next.place * kStage;
     if (j < kLoadsA) load_to_lds(buffer_rsrc(next.ax, next.a_left), st + (WAVES * j + wave) * 1024, a_off[j < kLoadsA ? j : 0]);
-    else load_to_lds(buffer_rsrc(next.bw, next.b_left), st + kA + (WAVES * (j - kLoadsA) + wave) * 1024,
+    else load_to_lds(buffer_rsrc(next.bw, next.w_bytes()), st + kA + (WAVES * (j - kLoadsA) + wave) * 1024,
                      b_off[j < kLoadsA ? 0 : j - kLoadsA]);
   };
 
@@ -352,7 +363,7 @@ void w8a8_tile_kernel(Problem p) {
 
   // ---- a tile's scales, into the wave's scratch: sx of its rows, sw and bias of its 64 columns
   constexpr int kScaleLoads = OUT == kPartial ? 0 : 3 + (RT > 2);
-  uint8_t* scratch = lds + kPlaces * kStage + wave * kScratch;
+  uint8_t* scratch = lds + KS * kPlaces * kStage + all_waves * kScratch;
   auto issue_scales = [&](int m0, int n0, int lane) __attribute__((always_inline)) {
     const int rows = uniform(max(min(p.M - m0, 32 * RT), 0)), columns = uniform(max(min(p.N - n0, 64), 0));
     const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(uniform(p.sx + min(m0, p.M)), rows * 4);
@@ -377,7 +388,7 @@ void w8a8_tile_kernel(Problem p) {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 #pragma unroll
-  for (int r = 0; r < RT + 2; ++r) read(lds, 0, r, f0);
+  for (int r = 0; r < RT + 2; ++r) read(ring, 0, r, f0);
 
   constexpr int kSize = OUT == kBf16 ? 2 : 4, kPer = 16 / kSize;   // bytes; columns of a piece of 16 bytes
   constexpr int kPasses = OUT == kBf16 ? 1 : 2;                    // of a wave's 64 columns
@@ -390,20 +401,21 @@ void w8a8_tile_kernel(Problem p) {
   int units_before = 0;
   for (int item = blockIdx.x; item < items; item += gridDim.x) {
     const Item it = item_at(item, nx, ny, p.split, G);
-    const int units = it.end - it.first, m0 = it.mt * TM + wm * 32 * RT, n0 = it.nt * TN + wn * 64;
+    const int units = (it.end - it.first + KS - 1) / KS, m0 = it.mt * TM + wm * 32 * RT, n0 = it.nt * TN + wn * 64;
     // a tile's first steps follow the stores of the one before, and wait for units that were sent for
     // earlier than these
-    int behind = whole && units_before >= kPlaces && units >= kPlaces ? 3 : 0;
+    int behind = group == 0 && whole && units_before >= kPlaces && units >= kPlaces ? 3 : 0;
     units_before = units;
     // (kept from the compiler, which would compute the addresses of the store before the loop and keep them
     // in registers that it does not have)
     int lane_ = lane;
     asm volatile("" : "+v"(lane_));
-    if constexpr (OUT != kPartial) issue_scales(m0, n0, lane_);
+    if constexpr (OUT != kPartial)
+      if (group == 0) issue_scales(m0, n0, lane_);
     for (int u = 0; u < units; ++u) {
-      const uint8_t* st = lds + at * kStage;
+      const uint8_t* st = ring + at * kStage;
       at = (at + 1) & (kPlaces - 1);
-      const uint8_t* after = lds + at * kStage;
+      const uint8_t* after = ring + at * kStage;
 #pragma unroll
       for (int c = 0; c < RT; ++c) {
         product(c, c & 1, f0);
@@ -437,6 +449,36 @@ void w8a8_tile_kernel(Problem p) {
       asm volatile("" ::: "memory");
     }
 
+    if constexpr (KS > 1) {
+      // ---- the groups' sums meet in the first: 32 x 32 at a time, through the second's scratch
+      static_assert(KS == 2, "one group gives, one takes");
+      v4i* give = reinterpret_cast<v4i*>(lds + KS * kPlaces * kStage + (WAVES + wave) * kScratch) + lane;
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (group == 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              give[64 * e] = v4i{acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+          }
+          SVDQ_WAIT_LDS_AND(63);
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+          if (group == 0) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const v4i v = give[64 * e];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) acc[i][j][4 * e + q] += v[q];
+            }
+          }
+          SVDQ_WAIT_LDS_AND(63);
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+        }
+    }
+    if (group == 0) {
     // ---- the tile's store.  A matrix instruction leaves four columns of one row in a lane; stored from
     //      there, a store would touch 32 rows with 16 bytes each.  A wave turns 32 rows at a time over in
     //      its scratch (4-byte results: 32 columns of them) and stores rows of 128 bytes; the pieces of a
@@ -511,6 +553,7 @@ void w8a8_tile_kernel(Problem p) {
         }
       }
     }
+    }
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -539,20 +582,23 @@ constexpr int kCus = 256;
 
 struct Plan {
   int rt, wn;   // a tile of 64 rt x 64 wn; 0: few rows
+  int groups;   // of waves in a workgroup, each with its units of K
   int split;
 };
 
 Plan plan(int M, int N, int K) {
-  if (M <= kFewRows) return {0, 0, 1};
+  if (M <= kFewRows) return {0, 0, 1, 1};
   // The tile and the division of K with the least time, by what a unit of K costs a CU with each tile (ns,
   // measured where all CUs are busy: small tiles read LDS and L2 more often for the same products) times the
   // items that the busiest CU has; divided sums cost a launch and are written and read once more.  Measured,
-  // us, 256 x 256 / 128 x 256 / 128 x 128 / 64 x 128, with the best division: 1000 x 4096 x 8192 (M, K, N)
-  // 52 / 38 / 43 / 51, 2000 x 8192 x 4096 89 / 67 / 78 / 104, 500 x 12288 x 4096 48 / 40 / 41 / 45 (undivided
-  // 116 / 69 / 53 / 49), 128 x 4096 x 4096 23 / 19 / 16 / 15, 300 x 8192 x 28672 107 / 111 / 108 / 123.
-  static const struct { int rt, wn; double ns; } kTiles[] = {{4, 4, 860}, {2, 4, 510}, {2, 2, 290}, {1, 2, 240}};
+  // us, 256 x 256 / 128 x 256 / 128 x 128 / 64 x 128, with the best division: 300 x 8192 x 28672 (M, K, N) 94 / 100 / 98 / 111,
+  // 2000 x 8192 x 4096 82 / 65 / 74 / 94, 1000 x 4096 x 8192 45 / 37 / 41 / 53, 1000 x 4096 x 4096 40 / 29 / 24 / 28, 500 x
+  // 12288 x 4096 46 / 39 / 39 / 37 (undivided 110 / 64 / 51 / 37), 256 x 4096 x 4096 26 / 21 / 18 / 14.  The smallest tile's
+  // two groups of waves against one: 500 x 12288 x 4096 37 / 44, 256 x 4096 x 4096 14.4 / 16.6, 100 x 4096 x 12288
+  // 15.3 / 17.8; for 128 x 128 no gain (39.1 / 39.0, 17.9 / 18.2, 98 / 98).
+  static const struct { int rt, wn, groups; double ns; } kTiles[] = {{4, 4, 1, 860}, {2, 4, 1, 510}, {2, 2, 1, 290}, {1, 2, 2, 180}};
   const int G = K / 64;
-  Plan best{4, 4, 1};
+  Plan best{4, 4, 1, 1};
   double least = 1e30;
   for (const auto& t : kTiles) {
     const int64_t tiles = (int64_t)((M + 64 * t.rt - 1) / (64 * t.rt)) * ((N + 64 * t.wn - 1) / (64 * t.wn));
@@ -563,7 +609,7 @@ Plan plan(int M, int N, int K) {
       if (split > 1) ns += 4000 + ((double)M * N * (8 * split + 4)) / 5500;
       if (ns < least) {
         least = ns;
-        best = {t.rt, t.wn, split};
+        best = {t.rt, t.wn, t.groups, split};
       }
     }
   }
@@ -601,26 +647,26 @@ hipError_t launch_few_rows(const int8_t* qx, const int8_t* container, int K, con
   return launch_few<RT, 1, 8, RT <= 2 ? 4 : 2>(qx, container, K, o, f32, st);
 }
 
-template <int RT, int WN, int OUT>
+template <int RT, int WN, int KS, int OUT>
 hipError_t launch_tile(const Problem& p, hipStream_t st) {
-  constexpr int kLds = kPlaces * (RT + WN) * 4096 + 2 * WN * kScratch;
+  constexpr int kLds = KS * (kPlaces * (RT + WN) * 4096 + 2 * WN * kScratch);
   constexpr int kPerCu = 160 * 1024 / kLds;
   // more than the default 64 KB of LDS
-  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(w8a8_tile_kernel<RT, WN, OUT>),
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(w8a8_tile_kernel<RT, WN, KS, OUT>),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
   if (e != hipSuccess) return e;
   const int64_t items = (int64_t)((p.N + 64 * WN - 1) / (64 * WN)) * ((p.M + 64 * RT - 1) / (64 * RT)) * p.split;
   const int grid = items < kCus * kPerCu ? (int)items : kCus * kPerCu;
-  hipLaunchKernelGGL((w8a8_tile_kernel<RT, WN, OUT>), dim3(grid), dim3(128 * WN), kLds, st, p);
+  hipLaunchKernelGGL((w8a8_tile_kernel<RT, WN, KS, OUT>), dim3(grid), dim3(128 * WN * KS), kLds, st, p);
   return hipGetLastError();
 }
 
-template <int RT, int WN>
+template <int RT, int WN, int KS>
 hipError_t launch_many(const Problem& problem, int out_fp32, const Output& o, int32_t* ws, hipStream_t st) {
   Problem p = problem;
-  if (p.split == 1) return out_fp32 ? launch_tile<RT, WN, kFp32>(p, st) : launch_tile<RT, WN, kBf16>(p, st);
+  if (p.split == 1) return out_fp32 ? launch_tile<RT, WN, KS, kFp32>(p, st) : launch_tile<RT, WN, KS, kBf16>(p, st);
   p.Y = ws;
-  const hipError_t e = launch_tile<RT, WN, kPartial>(p, st);
+  const hipError_t e = launch_tile<RT, WN, KS, kPartial>(p, st);
   if (e != hipSuccess) return e;
   const int64_t quads = (int64_t)((o.N + 15) / 16) * 4 * o.M, blocks = (quads + 255) / 256;
   const dim3 grid((int)(blocks < 4096 ? blocks : 4096));
@@ -660,9 +706,9 @@ hipError_t launch_w8a8_gemm(const int8_t* qx, const float* sx, const int8_t* con
   }
   const Problem q{qx, container, M, N, K, p.split, sx, sw, bias, Y};
   int32_t* ws = static_cast<int32_t*>(workspace);
-  if (p.rt == 4) return launch_many<4, 4>(q, out_fp32, o, ws, stream);
-  if (p.rt == 1) return launch_many<1, 2>(q, out_fp32, o, ws, stream);
-  return p.wn == 4 ? launch_many<2, 4>(q, out_fp32, o, ws, stream) : launch_many<2, 2>(q, out_fp32, o, ws, stream);
+  if (p.rt == 4) return launch_many<4, 4, 1>(q, out_fp32, o, ws, stream);
+  if (p.rt == 1) return launch_many<1, 2, 2>(q, out_fp32, o, ws, stream);
+  return p.wn == 4 ? launch_many<2, 4, 1>(q, out_fp32, o, ws, stream) : launch_many<2, 2, 1>(q, out_fp32, o, ws, stream);
 }
 
 }  // namespace svdq
