@@ -12,7 +12,7 @@
 // past 2^60 or under 2^-50, or one with a NaN or an infinity), the row is scaled by a power of two that
 // brings its largest |h| to [1, 2), and the exchange is made again: every row then has its 24 bits.
 //
-// Bound by memory: 16384 rows of 8192, bf16 with a residual to 8 bits, move 940 MB in 209 - 212 us (4.5 TB/s,
+// Bound by memory: 16384 rows of 8192, bf16 with a residual to 8 bits, move 940 MB in 196 - 212 us (4.4 - 4.8 TB/s,
 // where a copy of 1 GiB reaches 5.2), to bf16 1074 MB in 200 (5.4); 4096 x 8192 to 8 bits 52 us, 16384 x 4096 88.
 // Up to a few hundred rows a call costs what its launch costs.
 #include "decoder_launch.hpp"

@@ -4,7 +4,7 @@
 //
 // The sums are int32 and exact, so they may be divided over waves and workgroups in any way.  The weight is
 // the first operand of the matrix instruction (rows of the result) and X the second (columns): a lane then
-// holds four neighbouring columns of Y in one row.  Up to 64 rows, v_mfma_i32_16x16x64_i8:
+// holds four neighbouring columns of Y in one row.  Few rows, v_mfma_i32_16x16x64_i8:
 //   operand: lane l has row l % 16, k = 16 (l / 16) .. + 15 of 64;
 //   result:  lane l has column l % 16 (a row of X), rows 4 (l / 16) + e (columns of Y);
 // more rows, v_mfma_i32_32x32x32_i8:
@@ -13,8 +13,8 @@
 // (A loop of nothing but matrix instructions on random codes reaches 3410 TOPS with 32x32x32 and 3040 with
 // 16x16x64, 4970 on zeros: what the card's power allows, not what the instruction takes.)
 //
-// Up to 64 rows the weight is read once, and memory bounds it: 40 x 8192 x 28672 (M, K, N) 49 us, 4.8 TB/s;
-// 1 x 8192 x 28672 38 (partly from the last cache), 64 x 8192 x 28672 57, 1 x 4096 x 4096 6.  Many rows are bound by power
+// Up to 64 rows the weight is read once, and memory bounds it: 40 x 8192 x 28672 (M, K, N) 44 us, 5.4 TB/s, 64 x
+// 8192 x 28672 45, 64 x 4096 x 131072 98, 1 x 8192 x 28672 38 (partly from the last cache), 1 x 4096 x 4096 6.  Many rows are bound by power
 // where they fill the device (8192 x 8192 x 12288 660 - 715 us from card to card, 2310 - 2500 TOPS; 530 on zeros)
 // and by the loads from L2 where they do not (500 x 12288 x 4096 36 - 39 us; 2000 x 8192 x 4096 65).
 #include "decoder_launch.hpp"
@@ -586,8 +586,33 @@ struct Plan {
   int split;
 };
 
+// Tiles of 16 columns of a workgroup for `rt` tiles of 16 rows: more of them read X less often, fewer leave more
+// workgroups, and more of them on a CU.  Measured with 64 / 32 / 16 columns, us: 16 x 8192 x 28672 (rows, K, columns)
+// 38 / 46 / 51, 32 x 8192 x 28672 43 / 55 / 71, one row of 4096 x 131072, where a wave has eight units in all, 93 / 78 /
+// 86, of 8192 x 8192 15 / 14 / 12.
+int few_columns(int rt, int tiles, int K) {
+  if (tiles >= 4 * kCus) return rt == 1 && K <= 4096 ? 2 : 4;
+  return rt > 1 && tiles >= 2 * kCus ? 2 : 1;
+}
+
 Plan plan(int M, int N, int K) {
-  if (M <= kFewRows) return {0, 0, 1, 1};
+  const int G = K / 64;
+  Plan best{0, 0, 1, 1};
+  double least = 1e30;
+  const double weights = (double)N * K / 5900.0;   // ns, for memory's part
+  if (M <= kFewRows) {
+    // What a unit of 16 columns costs a CU, ns, by the rows and the columns of a workgroup: each wave brings X to LDS
+    // for itself, which from 17 rows on may take longer than the smallest tile's way.  Measured, us: 24 / 40 / 64 rows of
+    // 8192 x 28672 42 / 50 / 58 against 44 / 44 / 45 in tiles, of 4096 x 131072 101 / 121 / 136 against 92 / 93 / 98, of
+    // 16384 x 1024 17 / 23 / 30 against 14 / 14 / 15, of 8192 x 8192 16 / 19 / 23 against 20 / 20 / 21, of 4096 x 4096
+    // 7 / 9 / 10 against 12 / 12 / 13.
+    const int rt = (M + 15) / 16, tiles = (N + 15) / 16, columns = few_columns(rt, tiles, K);
+    if (rt == 1) return best;
+    const double groups = (double)((tiles + columns - 1) / columns) / kCus;
+    const double unit = columns == 4 ? 30 + 0.53 * M : columns == 2 ? 25 + 0.85 * M : 20 + 1.3 * M;
+    const double few = groups > 1.0 ? groups * (columns * G * unit + 1000.0) : columns * G * unit;
+    least = 0.97 * (few > weights ? few : weights);
+  }
   // The tile and the division of K with the least time, by what a unit of K costs a CU with each tile (ns,
   // measured where all CUs are busy: small tiles read LDS and L2 more often for the same products) times the
   // items that the busiest CU has; divided sums cost a launch and are written and read once more.  Measured,
@@ -597,16 +622,15 @@ Plan plan(int M, int N, int K) {
   // two groups of waves against one: 500 x 12288 x 4096 37 / 44, 256 x 4096 x 4096 14.4 / 16.6, 100 x 4096 x 12288
   // 15.3 / 17.8; for 128 x 128 no gain (39.1 / 39.0, 17.9 / 18.2, 98 / 98).
   static const struct { int rt, wn, groups; double ns; } kTiles[] = {{4, 4, 1, 860}, {2, 4, 1, 510}, {2, 2, 1, 290}, {1, 2, 2, 180}};
-  const int G = K / 64;
-  Plan best{4, 4, 1, 1};
-  double least = 1e30;
   for (const auto& t : kTiles) {
+    if (M <= 64 * (t.rt - 1)) continue;   // (a tile half empty)
     const int64_t tiles = (int64_t)((M + 64 * t.rt - 1) / (64 * t.rt)) * ((N + 64 * t.wn - 1) / (64 * t.wn));
     for (int split = 1; split <= 8; split *= 2) {
       if (split > 1 && (tiles * split > 2 * kCus || G < 8 * split)) break;
       const int64_t rounds = (tiles * split + kCus - 1) / kCus;
-      double ns = (double)rounds * ((G + split - 1) / split) * t.ns;
-      if (split > 1) ns += 4000 + ((double)M * N * (8 * split + 4)) / 5500;
+      double ns = (double)rounds * ((G + split - 1) / split) * (M <= kFewRows ? 150 + 1.4 * M : t.ns);
+      if (split > 1) ns += (M <= kFewRows ? 6500 : 4000) + ((double)M * N * (8 * split + 4)) / 5500;
+      if (M <= kFewRows && ns < weights) ns = weights;
       if (ns < least) {
         least = ns;
         best = {t.rt, t.wn, t.groups, split};
@@ -634,16 +658,12 @@ hipError_t launch_few(const int8_t* qx, const int8_t* container, int K, const Ou
 
 template <int RT>
 hipError_t launch_few_rows(const int8_t* qx, const int8_t* container, int K, const Output& o, int f32, hipStream_t st) {
-  // Columns of a workgroup: more of them read X less often, fewer leave more workgroups, and more of them on
-  // a CU.  Measured with 64 / 32 / 16 columns, us: 16 x 8192 x 28672 (rows, K, columns) 38 / 46 / 51, 32 x 8192 x
-  // 28672 43 / 55 / 71, one row of 4096 x 131072, where a wave has eight units in all, 93 / 78 / 86, of 8192 x 8192
-  // 15 / 14 / 12.
-  const int tiles = (o.N + 15) / 16;
-  if (tiles >= 4 * kCus) {
-    if (RT == 1 && K <= 4096) return launch_few<RT, 2, 8, 2>(qx, container, K, o, f32, st);
-    return launch_few<RT, 4, 8, 2>(qx, container, K, o, f32, st);
-  }
-  if (RT > 1 && tiles >= 2 * kCus) return launch_few<RT, 2, 8, 2>(qx, container, K, o, f32, st);
+  const int columns = few_columns(RT, (o.N + 15) / 16, K);
+  if constexpr (RT == 1)
+    if (columns == 2) return launch_few<1, 2, 8, 2>(qx, container, K, o, f32, st);
+  if (columns == 4) return launch_few<RT, 4, 8, 2>(qx, container, K, o, f32, st);
+  if constexpr (RT > 1)
+    if (columns == 2) return launch_few<RT, 2, 8, 2>(qx, container, K, o, f32, st);
   return launch_few<RT, 1, 8, RT <= 2 ? 4 : 2>(qx, container, K, o, f32, st);
 }
 

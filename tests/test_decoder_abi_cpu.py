@@ -77,7 +77,7 @@ def test_product_validation(lib):
     assert call(M=200, K=64 * 64, ws=None) == EINVAL and b"workspace" in lib.svdq_last_error()
     assert call(M=0, qx=None, sx=None, Y=None, ws=None) == OK
     w, c, p = lib.svdq_w8a8_workspace_bytes, lib.svdq_w8a8_container_bytes, lib.svdq_pack_w8a8
-    assert w(0, 16, 64) == 0 and w(64, 16, 1 << 16) == 0 and w(1, 16, 65) == 0 and w(200, 16, 64 * 64) > 0
+    assert w(0, 16, 64) == 0 and w(16, 16, 1 << 16) == 0 and w(1, 16, 65) == 0 and w(200, 16, 64 * 64) > 0
     assert c(16, 64) == 1024 and c(17, 128) == 4096 and c(0, 64) == 0 and c(16, 100) == 0 and c(1, 64 * 2048) == 0
     assert p(F, 0, 64, F, None) == EINVAL and p(F, 16, 65, F, None) == ESHAPE and p(None, 16, 64, F, None) == EINVAL
     assert p(F, 16, 64, None, None) == EINVAL and p(ODD, 16, 64, F, None) == EALIGN and p(F, 16, 64, ODD, None) == EALIGN
