@@ -454,8 +454,8 @@ __device__ __forceinline__ Limit limit_of(const Row& R, const Space& s, const Si
     f.before = (u64)__shfl((long long)before, b);
   }
   if (R.least_w > 0) {
-    // min-p's border is at its logarithm: nearly always in one bin
-    const double x = fmax(log((double)R.least_w * 0x1p-40), -kSpan);
+    // min-p's border, where what rounds up to least_w begins (so x > log(2^-41) > -kSpan): nearly always in one bin
+    const double x = log(((double)R.least_w - 0.5) * 0x1p-40);
     f.hi = min(f.hi, bin_of(fmax(x - 1e-6, -kSpan)));
     const int m = bin_of(fmin(x + 1e-6, 0.0));
     if (m < f.lo) {
