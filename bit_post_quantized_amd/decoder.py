@@ -48,14 +48,23 @@ class Rows8:
 
 class RMSNorm:
     """y = h / sqrt(mean(h^2) + eps) gamma of h = x + residual (``svdq_rms_norm``); gamma fp32 [K].
-    A smoothing factor of the projection behind it is folded into gamma."""
+    A smoothing factor of the projection behind it is folded into gamma.  Gamma's memory is checked and bound
+    when the object is made, and anew when another tensor is assigned to ``gamma``."""
 
     def __init__(self, gamma: torch.Tensor, eps: float = 1e-6):
-        a = binding._Args("RMSNorm")
-        self.K, self.eps, self.gamma = gamma.shape[0], float(eps), gamma
-        self._gamma = a(gamma, 4 * self.K, "gamma", _F32, (self.K,))
-        self.device = a.device
+        self.gamma, self.eps = gamma, float(eps)
         self._call = B.load().svdq_rms_norm
+
+    @property
+    def gamma(self) -> torch.Tensor:
+        return self._gamma
+
+    @gamma.setter
+    def gamma(self, gamma: torch.Tensor):
+        a, K = binding._Args("RMSNorm"), gamma.shape[0]
+        self._pointer = a(gamma, 4 * K, "gamma", _F32, (K,))
+        self._gamma = gamma.detach()   # (holds the memory, whatever becomes of the tensor's own)
+        self.K, self.device = K, a.device
 
     def _run(self, x, residual, residual_out, y, codes, scales, good):
         """``good``: the outputs are as they should be."""
@@ -66,13 +75,13 @@ class RMSNorm:
             good = good and kind is not None and _is(residual, residual.dtype, (M, K), dev)
             res, out = residual.data_ptr(), residual_out.data_ptr()
         if good and code is not None and _is(x, x.dtype, (M, K), dev) and _here(dev):
-            status = self._call(x.data_ptr(), code, K, res, kind, out, self._gamma, M, K, self.eps,
+            status = self._call(x.data_ptr(), code, K, res, kind, out, self._pointer, M, K, self.eps,
                                 None if y is None else y.data_ptr(), None if codes is None else codes.data_ptr(),
                                 None if codes is None else scales.data_ptr(), _stream(dev))
             if status:
                 binding._check("svdq_rms_norm", status)
         else:
-            B.svdq_rms_norm(x, residual, residual_out, self.gamma, self.eps, y, codes, scales)
+            B.svdq_rms_norm(x, residual, residual_out, self._gamma, self.eps, y, codes, scales)
 
     def _stream_out(self, x, residual, residual_out):
         """(where x + residual goes, whether it is as it should be)"""
@@ -139,7 +148,8 @@ class Linear8:
         B.svdq_pack_w8a8(codes, self.container)
         self._weights = (a(self.container, 0, "container"), a(scales, 4 * N, "sw", _F32, (N,)),
                          a(bias, 2 * N, "bias", _BF16, (N,)))
-        self._held = (self.container, scales, bias)
+        # (detached: holds the memory, whatever becomes of the tensors' own)
+        self._held = (self.container.detach(), scales.detach(), None if bias is None else bias.detach())
         self.device = a.device
         self._call = B.load().svdq_w8a8_gemm
 
@@ -197,15 +207,25 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, factor: float = 1.0, o
 
 class Rope:
     """Rotary positions (``svdq_rope``) with the frequencies fp64 [rot_dim / 2]; channels from rot_dim on
-    are left as they are.  ``scale`` multiplies what is rotated (a factor of a scheme for long contexts)."""
+    are left as they are.  ``scale`` multiplies what is rotated (a factor of a scheme for long contexts).
+    The frequencies' memory is checked and bound when the object is made, and anew when another tensor is
+    assigned to ``freqs``."""
 
     def __init__(self, freqs: torch.Tensor, interleaved: bool = False, scale: float = 1.0):
-        a = binding._Args("Rope")
-        self.freqs, self.rot_dim = freqs, 2 * freqs.shape[0]
+        self.freqs = freqs
         self.interleaved, self.scale = bool(interleaved), float(scale)
-        self._freqs = a(freqs, 8 * freqs.shape[0], "freqs", _F64, (freqs.shape[0],))
-        self.device = a.device
         self._call = B.load().svdq_rope
+
+    @property
+    def freqs(self) -> torch.Tensor:
+        return self._freqs
+
+    @freqs.setter
+    def freqs(self, freqs: torch.Tensor):
+        a, pairs = binding._Args("Rope"), freqs.shape[0]
+        self._pointer = a(freqs, 8 * pairs, "freqs", _F64, (pairs,))
+        self._freqs = freqs.detach()   # (holds the memory, whatever becomes of the tensor's own)
+        self.rot_dim, self.device = 2 * pairs, a.device
 
     def __call__(self, q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
                  q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None):
@@ -226,14 +246,14 @@ class Rope:
             wide, narrow = heads * dim, kv * dim
             status = self._call(q.data_ptr(), wide if one else q.stride(0), heads, None if k is None else k.data_ptr(),
                                 narrow if one or k is None else k.stride(0), kv, code, rows, dim, self.rot_dim,
-                                1 if self.interleaved else 0, positions.data_ptr(), self._freqs, self.scale,
+                                1 if self.interleaved else 0, positions.data_ptr(), self._pointer, self.scale,
                                 q_out.data_ptr(), wide if one else q_out.stride(0),
                                 None if k is None else k_out.data_ptr(),
                                 narrow if one or k is None else k_out.stride(0), _stream(dev))
             if status:
                 binding._check("svdq_rope", status)
         else:
-            B.svdq_rope(q, k, positions, self.freqs, self.interleaved, self.scale, q_out, k_out)
+            B.svdq_rope(q, k, positions, self._freqs, self.interleaved, self.scale, q_out, k_out)
         return q_out, k_out
 
 
