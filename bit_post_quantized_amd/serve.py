@@ -126,7 +126,6 @@ class BlockPlanner:
 
     def __init__(self, block_tables: torch.Tensor, free_blocks: torch.Tensor, block_size: int,
                  rows: int):
-        self.block_tables, self.free_blocks = block_tables, free_blocks
         self.block_size, self.rows = block_size, rows
         self.requests, self.width = n, width = block_tables.shape
         self.device = dev = block_tables.device
@@ -134,6 +133,8 @@ class BlockPlanner:
         cap = free_blocks.shape[0]
         self._tables = (n, a(block_tables, 4 * n * width, "block_tables", _I32), width, block_size,
                         a(free_blocks, 4 * cap, "free_blocks", _I32, (cap,)), cap)
+        # (detached: holds the memory, whatever becomes of the tensors' own)
+        self._bound = block_tables.detach(), free_blocks.detach()
         self._call = B.load().kv_block_plan
         if max(rows, n, width, cap) >= 1 << 30:
             raise ValueError(f"BlockPlanner: {rows} rows, tables of {n} x {width} or {cap} free blocks are too many")
@@ -148,6 +149,15 @@ class BlockPlanner:
             p._outputs = (p.cu_rows.data_ptr(), p.seq_lens.data_ptr(), rows, p.positions.data_ptr(),
                           p.slots.data_ptr(), p.status.data_ptr(), p.free_count.data_ptr())
             self._plans.append(p)
+
+    @property
+    def block_tables(self) -> torch.Tensor:
+        """The tables that every call reads and writes; another one takes another planner."""
+        return self._bound[0]
+
+    @property
+    def free_blocks(self) -> torch.Tensor:
+        return self._bound[1]
 
     def _other(self, a: int, b: int, count: int) -> SlotPlan:
         """The oldest set that is not an argument's (lengths at a and b, free count at count), which

@@ -115,3 +115,31 @@ def test_the_linears_scales_and_bias_are_kept(calls, monkeypatch):
     gc.collect()
     assert [t.data_ptr() for t in linear._held[1:]] == want == list(linear._weights[1:])
     assert set(want) <= Memory.alive
+
+
+def test_the_planners_tables_are_kept_and_the_same_for_plan_and_release(monkeypatch):
+    from bit_post_quantized_amd import serve
+    empty, seen = torch.empty, []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *args: seen.append(args) or 0
+
+    monkeypatch.setattr(serve.B, "load", lambda: Lib())
+    monkeypatch.setattr(serve.B._Args, "stream", lambda self, stream: 0)
+    monkeypatch.setattr(torch, "empty", lambda *n, dtype, device=None: empty(*n, dtype=dtype) if device is None
+                        else Held(n, dtype))
+    for name, value in (("_here", True), ("_stream", 0)):
+        monkeypatch.setattr(serve, name, lambda dev, value=value: value)
+    tables, free = Held([4, 8], I32), Held([32], I32)
+    want = [tables.memory.pointer, free.memory.pointer]
+    planner = serve.BlockPlanner(tables, free, 16, 40)
+    for name in ("block_tables", "free_blocks"):
+        with pytest.raises(AttributeError):
+            setattr(planner, name, Held([4, 8], I32))
+    tables.memory, free.memory = Memory(), Memory()
+    gc.collect()
+    planner.plan(Held([4], I32), Held([4], I32), Held([1], I32))
+    planner.release(Held([4], I32), Held([4], torch.uint8), Held([1], I32))
+    assert set(want) <= Memory.alive and len(seen) == 2
+    assert all(pointer in call for call in seen for pointer in want)
