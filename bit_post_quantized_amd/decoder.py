@@ -240,7 +240,8 @@ class Rope:
         dev, code = self.device, _CODE.get(q.dtype)
         kv = 0 if k is None else k.shape[1]
         if (code is not None and _rows_of(q, q.dtype, rows, heads, dim, dev) and _rows_of(q_out, _BF16, rows, heads, dim, dev)
-                and (k is None or _rows_of(k, q.dtype, rows, kv, dim, dev) and _rows_of(k_out, _BF16, rows, kv, dim, dev))
+                and (k_out is None if k is None else
+                     _rows_of(k, q.dtype, rows, kv, dim, dev) and _rows_of(k_out, _BF16, rows, kv, dim, dev))
                 and _is(positions, _I32, (rows,), dev) and _here(dev)):
             one = rows <= 1   # (the strides of a single row say nothing)
             wide, narrow = heads * dim, kv * dim

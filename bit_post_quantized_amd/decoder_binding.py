@@ -171,6 +171,8 @@ def svdq_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tenso
     kp = kop = None
     kv = ks = kos = 0
     outs = [("q_out", q_out)]
+    if k is None and k_out is not None:
+        raise ValueError(f"{fn}: k_out needs k")
     if k is not None:
         if k_out is None:
             raise ValueError(f"{fn}: k needs k_out")

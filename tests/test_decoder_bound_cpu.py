@@ -143,3 +143,12 @@ def test_the_planners_tables_are_kept_and_the_same_for_plan_and_release(monkeypa
     planner.release(Held([4], I32), Held([4], torch.uint8), Held([1], I32))
     assert set(want) <= Memory.alive and len(seen) == 2
     assert all(pointer in call for call in seen for pointer in want)
+
+
+def test_an_output_of_keys_without_keys_is_refused(calls, fast):
+    rope = decoder.Rope(Held([32], F64))
+    q, pos = Held([3, 4, 64], BF16), Held([3], I32)
+    with pytest.raises(ValueError, match="k_out needs k"):
+        rope(q, None, pos, q, Held([3, 2, 64], BF16))
+    assert not calls
+    assert rope(q, None, pos) == (q, None) and len(calls) == 1
