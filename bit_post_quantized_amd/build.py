@@ -7,7 +7,7 @@ Flags: -O3, -ffp-contract=off (the kernels place every fused multiply-add explic
 correctly rounded fp32 division, packed-fp32 instruction generation turned off for the device
 pass (a device feature; the host pass warns that it does not know it, harmlessly), and MFMA
 results kept in VGPRs (-amdgpu-mfma-vgpr-form): the kernels consume every MFMA result with
-VALU instructions, which cannot read AGPRs without a copy (but for AGPR_SOURCES).
+VALU instructions, which cannot read AGPRs without a copy.
 """
 from __future__ import annotations
 
@@ -35,12 +35,10 @@ CFLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",
     "-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+    "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-Wall", "-Wno-unused-function",
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
-VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-# one wave per SIMD with 256 accumulators: these are in AGPRs
-AGPR_SOURCES = ("w8a8_gemm.hip",)
 
 
 def hipcc() -> str:
@@ -51,8 +49,7 @@ def hipcc() -> str:
 
 def _compile(src: str) -> str:
     obj = os.path.join(OBJDIR, os.path.splitext(src)[0] + ".o")
-    form = [] if src in AGPR_SOURCES else VGPR_FORM
-    cmd = [hipcc(), *CFLAGS, *form, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [hipcc(), *CFLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
