@@ -12,9 +12,11 @@
 // past 2^60 or under 2^-50, or one with a NaN or an infinity), the row is scaled by a power of two that
 // brings its largest |h| to [1, 2), and the exchange is made again: every row then has its 24 bits.
 //
-// Bound by memory: 16384 rows of 8192, bf16 with a residual to 8 bits, move 940 MB in 196 - 212 us (4.4 - 4.8 TB/s,
-// where a copy of 1 GiB reaches 5.2), to bf16 1074 MB in 200 (5.4); 4096 x 8192 to 8 bits 52 us, 16384 x 4096 88.
-// Up to a few hundred rows a call costs what its launch costs.
+// Bound by memory: 16384 rows of 8192, bf16 with a residual to 8 bits, move 940 MB in 193 - 212 us (4.4 - 4.9 TB/s,
+// where torch's copy of 1 GiB reaches 5.1 - 5.2 and one in runs of 16 KiB 6.2), to bf16 1074 MB in 197 (5.4), all of it
+// in fp32 to bf16 1879 MB in 360 (5.2); 4096 x 8192 to 8 bits 52 - 57 us, in fp32 to bf16 92; 16384 x 4096 88.  Without the
+// norm 16384 x 8192 take 77 us (5.2 TB/s), in fp32 111.  Rows that are read twice, 2048 x 32768: to bf16 135 us (4.0 TB/s of
+// one reading), to 8 bits 127, in fp32 239, without the norm 51.  Up to a few hundred rows a call costs what its launch costs.
 #include "decoder_launch.hpp"
 #include "svdq_device.hpp"
 
@@ -245,7 +247,7 @@ __global__ __launch_bounds__(64 * WAVES * ROWS) void norm_rows_kernel(NormRows a
 }
 
 // Rows too long for registers: read once for the sum and the maximum and once more to be written, between
-// them a third time where the row is scaled. 
+// them a third time where the row is scaled.
 template <typename X, typename R>
 __global__ __launch_bounds__(1024) void norm_long_kernel(NormRows a) {
   constexpr int WAVES = 16, T = 1024;

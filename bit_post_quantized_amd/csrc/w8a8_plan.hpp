@@ -45,7 +45,11 @@ inline Plan plan(int M, int N, int K) {
   }
   // The tile and the division of K with the least time, by what a unit of K costs a CU with each tile (ns,
   // measured where all CUs are busy: small tiles read LDS and L2 more often for the same products) times the
-  // items that the busiest CU has; divided sums cost a launch and are written and read once more.  Measured,
+  // items that the busiest CU has; divided sums cost a launch (the join takes 3.6 - 4.6 us for 39 x 40 to 20 x 15563
+  // sums, 6.8 for 113 x 15747) and are written and read once more.  Up to 64 rows 2.5 us more are asked for.  Measured, us,
+  // with 6.5 / with 4: 24 x 6144 x 14000 19.8 / 22.4, 32 x 8192 x 8192 17.5 / 20.2, 20 x 16384 x 4096 18.6 / 20.7, 64 x 4096 x 512
+  // 9.1 / 10.4; the other way 40 x 8192 x 5120 24.1 / 17.4, 48 x 6144 x 6144 21.2 / 16.1, 64 x 4096 x 6144 17.0 / 14.8, where the
+  // first kind has a few workgroups more than there are CUs, which its estimate does not see.  Measured,
   // us, 256 x 256 / 128 x 256 / 128 x 128 / 64 x 128, with the best division: 300 x 8192 x 28672 (M, K, N) 94 / 100 / 98 / 111,
   // 2000 x 8192 x 4096 82 / 65 / 74 / 94, 1000 x 4096 x 8192 45 / 37 / 41 / 53, 1000 x 4096 x 4096 40 / 29 / 24 / 28, 500 x
   // 12288 x 4096 46 / 39 / 39 / 37 (undivided 110 / 64 / 51 / 37), 256 x 4096 x 4096 26 / 21 / 18 / 14.  The smallest tile's

@@ -194,7 +194,9 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, factor: float = 1.0, o
     """Frequencies fp64 [rot_dim / 2] in radians per position, base^(-2 i / rot_dim), for contexts
     ``factor`` times as long as trained: all divided by it (positions interpolated), or, with the trained
     length ``original``, by parts as in YaRN (Peng et al. 2023): those that make at least ``high`` turns
-    in it stay, those of at most ``low`` turns are divided, in between linearly in the turns."""
+    in it stay, those of at most ``low`` turns are divided, in between linearly in the turns.  (A model whose
+    configuration goes linearly over the channels in between, not over their turns, needs frequencies of its
+    own: ``Rope`` takes any.)"""
     i = torch.arange(rot_dim // 2, dtype=_F64)
     f = float(base) ** (-2.0 * i / rot_dim)
     if original is None:

@@ -42,11 +42,12 @@ int svdq_decoder_version(void);
  * y is computed in fp32 from h before residual_out's rounding; a row's sum of squares neither
  * overflows nor vanishes, whatever its magnitude; a row of zeros gives zeros.  A row with a NaN or
  * an infinity has the scale NaN (infinity / infinity) and the codes 0; other rows are not touched
- * by it.
- *   x          [M, K] of x_dtype, 16B, rows x_stride elements apart (a multiple of 8, at least K)
+ * by it.  (h gamma is rounded to fp32 before it is divided; where that leaves fp32's range for all of a row, the row
+ * is scaled by a power of two first.)
+ *   x          [M, K] of x_dtype, 16B, rows x_stride elements apart (a multiple of 8, from K to 2^31)
  *   residual   [M, K] of residual_dtype (16B), or NULL: h = x.  residual_out likewise, or NULL
  *              where it is not needed; it may be residual itself, and is NULL without a residual
- *   gamma      fp32 [K] 16B, or NULL for ones;  eps >= 0, finite
+ *   gamma      fp32 [K] 16B, or NULL for ones;  0 <= eps <= 3e38
  *   y          bf16 [M, K] 16B;  codes  int8 [M, K] 16B, scales  fp32 [M]: y or NULL, codes and
  *              scales or both NULL, at least one of the two
  *   0 <= M <= 2^24, 8 <= K <= 2^20, K % 8 == 0.  Nothing else overlaps.
@@ -107,10 +108,10 @@ int svdq_w8a8_gemm(const int8_t* qx, const float* sx, const int8_t* container, c
  *           where x_dtype is SVDQ_OUT_BF16 and the strides agree, otherwise they do not overlap it
  *   positions  int32 [rows] (as written by kv_block_plan);  freqs  fp64 [rot_dim / 2], in radians
  *           per position, finite
- *   scale   finite; 1, or the factor of a scheme for long contexts
+ *   scale   at most 3e38 either way; 1, or the factor of a scheme for long contexts
  *   rows >= 0, heads >= 1, kv_heads >= 0, (heads + kv_heads) rows <= 2^27, heads and kv_heads
  *   <= 65535; dim % 8 == 0, dim <= 1024; rot_dim % 16 == 0, 16 <= rot_dim <= dim; strides a multiple
- *   of 8, at least heads * dim; all pointers but positions 16B.
+ *   of 8, from heads * dim to 2^31; all pointers but positions 16B.
  */
 int svdq_rope(const void* q, int64_t q_stride, int heads, const void* k, int64_t k_stride,
               int kv_heads, int x_dtype, int rows, int dim, int rot_dim, int interleaved,
@@ -131,16 +132,22 @@ int svdq_rope(const void* q, int64_t q_stride, int heads, const void* k, int64_t
  * is not > 0 means the largest logit (the first of equal ones), with the share 1.
  * Logits of -infinity are never drawn; where the largest is +infinity, only such logits are.  A row
  * with a NaN, or with nothing above -infinity, gets the token -1 and the share 0.
- *   logits       [rows, vocab] of logits_dtype, rows logits_stride >= vocab elements apart, aligned
- *                to an element
+ *   logits       [rows, vocab] of logits_dtype, rows logits_stride elements apart (from vocab to 2^31),
+ *                aligned to an element
  *   temperature  fp32 [rows];  uniform  fp32 [rows], in [0, 1) (clamped to it; NaN counts as 0)
  *   top_k        int32 [rows] or NULL;  top_p, min_p  fp32 [rows] or NULL (NaN: no limit)
  *   tokens       int32 [rows];  share  fp32 [rows] or NULL
  *   workspace    device scratch of svdq_sample_workspace_bytes(rows, vocab) bytes (16B), no
  *                initialization needed, rewritten by every call; calls that share one workspace
  *                must not overlap in time
- *   0 <= rows <= 65535, 1 <= vocab <= 2^22.  A top-k over about 500, or a limit that falls among
- *   thousands of equal logits, takes several times as long as a smaller one.
+ *   0 <= rows <= 65535, 1 <= vocab <= 2^22.
+ * Over a vocabulary of more than 2048, some rows are searched by one workgroup, which takes 6 to 20 times
+ * as long (64 rows of 131072: 126 - 467 us instead of 15 - 47):
+ *   - a top-k of more than 512, or of more than the row has parts (512 at most, of neighbouring logits) with
+ *     anything above -infinity in them: a mask that leaves fewer than top_k tokens is such a row;
+ *   - a limit that falls among thousands of equal logits;
+ *   - a top-p, without a top-k, with more than 4096 logits (2048 in a chunk of the row) in the bin that its
+ *     limit falls into.  A bin is 1/72 of the temperature wide: flat rows at high temperatures have such bins.
  */
 size_t svdq_sample_workspace_bytes(int rows, int vocab);
 int svdq_sample(const void* logits, int logits_dtype, int64_t logits_stride, int rows, int vocab,
